@@ -350,6 +350,140 @@ aqfq_status aqfq_kd_loss(int kd_type, const void* student, const void* teacher,
                          void* dstudent, int32_t* topk_idx, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ---- the layer around the fake-quantized weight ------------------------------
+ * Layer norm with its gradient, activation checkpoints in 8 bits, and the
+ * matrix product with bias, activation and residual with its gradient products:
+ * what a training step of a block runs next to the fake-quant of its weights
+ * (AngelSlim mcore_qad article, sections 1 and 2.3: frozen weights, activations
+ * and gradients in BF16, and the gradient with respect to a fake-quantized
+ * weight that aqfq_scale_grad takes as dy).
+ *
+ * Tensors of these calls are views [rows, cols] with contiguous columns and
+ * rows `ld` elements apart (ld >= cols).  Unless stated, a tensor may start at
+ * any element; rows that allow wide accesses (16-byte aligned starts) take them.
+ * Any number of rows and columns is accepted, zero and odd ones among them.
+ * Sums are held in binary32; stored values are rounded to their type once.
+ * Results do not depend on the launch's timing: no floating-point atomics.
+ * Non-finite values follow the formulas' arithmetic and stay in the rows (or
+ * column sums) they belong to.  Outputs must not overlap inputs or each other. */
+typedef enum aqfq_dtype { AQFQ_BF16 = 0, AQFQ_F32 = 1 } aqfq_dtype;
+
+/* act(p): p | max(p, 0) | p Phi(p) | p (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))) / 2
+ * | p / (1 + exp(-p)).  The derivative of relu at 0 is 0. */
+typedef enum aqfq_act {
+  AQFQ_ACT_NONE = 0,
+  AQFQ_ACT_RELU = 1,
+  AQFQ_ACT_GELU = 2,
+  AQFQ_ACT_GELU_TANH = 3,
+  AQFQ_ACT_SILU = 4
+} aqfq_act;
+
+/* An activation kept in 8 bits between the forward and the backward pass.
+ * Each row is cut into groups of `group` columns (the last one may be shorter);
+ * per group, in binary32: scale = amax / qmax (qmax 127 or 448), code =
+ * grid(x / scale) on INT8 [-127, 127] or E4M3 with the rounding of
+ * aqfq_qdq_fwd, and the kept value is code * scale.  A group of zeros has scale
+ * 0 and codes 0 (as has one so small that its scale underflows); a group with
+ * a NaN or an infinity has scale NaN and codes 0, so all of it comes back NaN.
+ *   fmt    AQFQ_INT8 | AQFQ_FP8_E4M3      group  32, 64 or 128
+ *   codes  device, [rows, cols] bytes, contiguous
+ *   scale  device float, [rows, ceil(cols / group)], contiguous */
+typedef struct aqfq_ckpt8 {
+  int32_t fmt;
+  int32_t group;
+  void* codes;
+  float* scale;
+} aqfq_ckpt8;
+
+/* Writes the checkpoint of x [rows, cols] (dtype BF16 or F32). */
+aqfq_status aqfq_ckpt8_pack(const aqfq_ckpt8* ckpt, int dtype, const void* x, int64_t ldx,
+                            int64_t rows, int64_t cols, void* stream);
+
+/* y = act(kept values): the activation, or what follows it, recomputed from the
+ * checkpoint (AQFQ_ACT_NONE: the kept values themselves). */
+aqfq_status aqfq_ckpt8_unpack(const aqfq_ckpt8* ckpt, int act, int dtype, void* y, int64_t ldy,
+                              int64_t rows, int64_t cols, void* stream);
+
+/* Gradient of an activation whose input p was kept in 8 bits:
+ *   dx = dy act'(p);  y = act(p) (optional);  dbias[c] = sum over rows of dx
+ *   (optional, float [cols], added to with accumulate).
+ * With ckpt NULL and AQFQ_ACT_NONE, dx = dy (the call then gives the column
+ * sums of dy: the bias gradient of a layer without activation).  dx, y and
+ * dbias may each be NULL, not all of them; dbias sums the unrounded dx.
+ *   workspace  device, aqfq_ckpt8_act_bwd_workspace_bytes(rows, cols) bytes,
+ *              8-byte aligned; needed with dbias only */
+size_t aqfq_ckpt8_act_bwd_workspace_bytes(int64_t rows, int64_t cols);
+aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int dtype, const void* dy,
+                               int64_t lddy, int64_t rows, int64_t cols, void* dx, int64_t lddx,
+                               void* y, int64_t ldy, float* dbias, int accumulate,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm over the last axis: y = (x - mean) rstd gamma + beta per row, with
+ * rstd = 1 / sqrt(var + eps), var the mean of (x - mean)^2.
+ *   x, y         [rows, cols] of dtype, cols >= 1
+ *   gamma, beta  [cols] of param_dtype; NULL = ones / zeros
+ *   eps          finite, >= 0
+ *   mean, rstd   float [rows], optional (the backward needs them)
+ *   ckpt         optional: also writes the 8-bit checkpoint of x */
+aqfq_status aqfq_layernorm_fwd(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                               int param_dtype, const void* gamma, const void* beta, float eps,
+                               void* y, int64_t ldy, float* mean, float* rstd,
+                               const aqfq_ckpt8* ckpt, void* stream);
+
+/* Its gradient, h = (x - mean) rstd and u = dy gamma:
+ *   dx = rstd (u - mean(u) - h mean(u h)) + dres;  dgamma = sum over rows of
+ *   dy h;  dbeta = sum over rows of dy
+ *   x | ckpt     the forward's input, or its 8-bit checkpoint; not both
+ *   mean, rstd   the forward's
+ *   dres         optional [rows, cols] of dtype: added to dx (the gradient of a
+ *                residual branch around the norm)
+ *   dx           optional [rows, cols] of dtype
+ *   dgamma, dbeta  optional float [cols], added to with accumulate
+ *   workspace    device, aqfq_layernorm_bwd_workspace_bytes(rows, cols) bytes,
+ *                8-byte aligned; needed with dgamma or dbeta only */
+size_t aqfq_layernorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+aqfq_status aqfq_layernorm_bwd(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               const aqfq_ckpt8* ckpt, int64_t rows, int64_t cols,
+                               const float* mean, const float* rstd, int param_dtype,
+                               const void* gamma, const void* dres, int64_t lddres, void* dx,
+                               int64_t lddx, float* dgamma, float* dbeta, int accumulate,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Matrix products of a linear layer y = x W^T + b, W [N, K], x [M, K] (BF16,
+ * products accumulated in FP32).
+ *   forward      p = x W^T + bias;  y = act(p) + residual (BF16 [M, N]); with
+ *                ckpt, p (unrounded) is also kept in 8 bits
+ *   input grad   dx = (dy W) act'(p') + residual (BF16 [M, K]), p' [M, K] the
+ *                8-bit checkpoint of the activation's input that made x (ckpt
+ *                NULL and AQFQ_ACT_NONE: no activation)
+ *   weight grad  dw = dy^T x (dtype BF16 or F32 [N, K]), added to with
+ *                accumulate
+ *   x, w, dy     16-byte aligned, leading dimension a multiple of 8 elements
+ *                (M, N and K themselves are free, also 0: an empty sum is 0)
+ *   bias         optional [N] of bias_dtype;  residual  optional BF16
+ *   workspace    device, aqfq_linear_workspace_bytes(pass, M, N, K) bytes,
+ *                16-byte aligned (0 bytes for many sizes: partial sums of a
+ *                product that is split along its inner axis)
+ *   error_flag   optional device int32, set to 1 if a pipeline wait of the
+ *                kernel timed out (the output is then incomplete); never cleared
+ * Limits: M, N, K < 2^30. */
+enum { AQFQ_LINEAR_FWD = 0, AQFQ_LINEAR_DGRAD = 1, AQFQ_LINEAR_WGRAD = 2 };
+size_t aqfq_linear_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K);
+aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
+                            int64_t N, int64_t K, int bias_dtype, const void* bias, int act,
+                            const void* residual, int64_t ldr, void* y, int64_t ldy,
+                            const aqfq_ckpt8* ckpt, void* workspace, size_t workspace_bytes,
+                            int32_t* error_flag, void* stream);
+aqfq_status aqfq_linear_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t M,
+                              int64_t N, int64_t K, int act, const aqfq_ckpt8* ckpt,
+                              const void* residual, int64_t ldr, void* dx, int64_t lddx,
+                              void* workspace, size_t workspace_bytes, int32_t* error_flag,
+                              void* stream);
+aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t M,
+                              int64_t N, int64_t K, int dtype, void* dw, int64_t lddw,
+                              int accumulate, void* workspace, size_t workspace_bytes,
+                              int32_t* error_flag, void* stream);
+
 /* Diagnostic (the pages have no counterpart): checks the bounded-wait path
  * that the GEMM's pipeline uses when a stage never arrives.  One thread waits
  * on an mbarrier phase that nothing completes, polling at most `polls` times

@@ -23,6 +23,9 @@ INT8, INT4, FP8_E4M3, NVFP4 = 0, 1, 2, 3
 PER_TENSOR, PER_CHANNEL, PER_GROUP, PER_HEAD = 0, 1, 2, 3
 SCALE_LEARNED, SCALE_DYNAMIC_BLOCK = 0, 1
 KD_KL, KD_RKL, KD_CAKLD, KD_MSE = 0, 1, 2, 3
+BF16, F32 = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+LINEAR_FWD, LINEAR_DGRAD, LINEAR_WGRAD = 0, 1, 2
 
 STATUS = {0: "AQFQ_OK", 1: "AQFQ_ERR_NULL", 2: "AQFQ_ERR_SHAPE", 3: "AQFQ_ERR_ALIGN",
           4: "AQFQ_ERR_UNSUPPORTED", 5: "AQFQ_ERR_WORKSPACE", 6: "AQFQ_ERR_CUDA"}
@@ -32,6 +35,10 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_qdq_fwd_grad", "aqfq_scale_grad_noalloc",
            "aqfq_scale_grad_workspace_bytes", "aqfq_observer_minmax", "aqfq_minmax_scale",
            "aqfq_scale_init", "aqfq_kd_loss", "aqfq_kd_workspace_bytes",
+           "aqfq_ckpt8_pack", "aqfq_ckpt8_unpack", "aqfq_ckpt8_act_bwd",
+           "aqfq_ckpt8_act_bwd_workspace_bytes", "aqfq_layernorm_fwd", "aqfq_layernorm_bwd",
+           "aqfq_layernorm_bwd_workspace_bytes", "aqfq_linear_fwd", "aqfq_linear_dgrad",
+           "aqfq_linear_wgrad", "aqfq_linear_workspace_bytes",
            "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_status_string",
            "aqfq_version")
 
@@ -42,6 +49,12 @@ class QSpec(ctypes.Structure):
 
 def qspec(fmt, gran, group=0, qmin=0, qmax=0, mode=SCALE_LEARNED) -> QSpec:
     return QSpec(fmt, gran, group, qmin, qmax, mode)
+
+
+class Ckpt8(ctypes.Structure):
+    """An activation checkpoint in 8 bits (keeps its tensors alive)."""
+    _fields_ = [("fmt", ctypes.c_int32), ("group", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
 
 
 class AqfqError(RuntimeError):
@@ -81,6 +94,23 @@ def lib():
                 "aqfq_kd_loss": (i32, [i32, P, P, P, i64, i64, ctypes.c_int32, ctypes.c_float,
                                        ctypes.c_float, P, P, P, P, P, sz, P]),
                 "aqfq_kd_workspace_bytes": (sz, [i64]),
+                "aqfq_ckpt8_pack": (i32, [P, i32, P, i64, i64, i64, P]),
+                "aqfq_ckpt8_unpack": (i32, [P, i32, i32, P, i64, i64, i64, P]),
+                "aqfq_ckpt8_act_bwd": (i32, [P, i32, i32, P, i64, i64, i64, P, i64, P, i64, P, i32,
+                                             P, sz, P]),
+                "aqfq_ckpt8_act_bwd_workspace_bytes": (sz, [i64, i64]),
+                "aqfq_layernorm_fwd": (i32, [i32, P, i64, i64, i64, i32, P, P, ctypes.c_float, P,
+                                             i64, P, P, P, P]),
+                "aqfq_layernorm_bwd": (i32, [i32, P, i64, P, i64, P, i64, i64, P, P, i32, P, P, i64,
+                                             P, i64, P, P, i32, P, sz, P]),
+                "aqfq_layernorm_bwd_workspace_bytes": (sz, [i64, i64]),
+                "aqfq_linear_fwd": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, i32, P, i64, P, i64,
+                                          P, P, sz, P, P]),
+                "aqfq_linear_dgrad": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, P, i64, P, i64, P,
+                                            sz, P, P]),
+                "aqfq_linear_wgrad": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, i64, i32, P, sz, P,
+                                            P]),
+                "aqfq_linear_workspace_bytes": (sz, [i32, i64, i64, i64]),
                 "aqfq_selftest_wait_timeout": (i32, [P, ctypes.c_uint32, P]),
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
                 "aqfq_status_string": (ctypes.c_char_p, [i32]),
@@ -288,6 +318,204 @@ def aqfq_scale_init(spec, x, scale, tensor_scale, stream=None):
     st = lib().aqfq_scale_init(ctypes.byref(spec), _ptr(x), B, R, K, _ptr(scale),
                                _ptr(tensor_scale), _stream(stream))
     _check("aqfq_scale_init", st)
+
+
+# ---- the layer around the fake-quantized weight ---------------------------------------
+# Matrices are 2D tensors with contiguous columns; the row stride is passed on.
+
+def _mat(t, name, dtypes, shape=None):
+    """(address, leading dimension) of a matrix; None gives (None, 0)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("aqfq works on CUDA tensors only")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous columns")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    rows, cols = t.shape
+    return t.data_ptr(), t.stride(0) if rows > 1 else _ld_of_one_row(cols)
+
+
+def _ld_of_one_row(cols):
+    """A single row has no second one: a leading dimension that every check accepts."""
+    return (cols + 7) // 8 * 8
+
+
+def _vec(t, name, dtypes, n):
+    """Address of a contiguous vector of n elements, or None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("aqfq works on CUDA tensors only")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must have {n} contiguous elements")
+    return t.data_ptr()
+
+
+_ROWS = (torch.bfloat16, torch.float32)
+_BF = (torch.bfloat16,)
+_FL = (torch.float32,)
+_I32 = (torch.int32,)
+
+
+def _dt(t):
+    return F32 if t is not None and t.dtype == torch.float32 else BF16
+
+
+def _ws(workspace):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _flag(t):
+    return _vec(t, "error_flag", _I32, 1)
+
+
+def ckpt8(fmt, group, codes, scale) -> Ckpt8:
+    """The 8-bit checkpoint held in codes (uint8 [rows, cols]) and scale (float32
+    [rows, ceil(cols / group)])."""
+    _u8(codes, "codes"), _f32(scale, "scale")
+    if codes.dim() != 2 or group <= 0:
+        raise ValueError("codes must be [rows, cols] and group positive")
+    rows, cols = codes.shape
+    if tuple(scale.shape) != (rows, -(-cols // group)):
+        raise ValueError("scale must be [rows, ceil(cols / group)]")
+    c = Ckpt8(fmt, group, _ptr(codes), _ptr(scale))
+    c.tensors = (codes, scale)
+    return c
+
+
+def _ck(c, rows, cols):
+    """Pointer to the checkpoint of a [rows, cols] matrix, or None."""
+    if c is None:
+        return None
+    if tuple(c.tensors[0].shape) != (rows, cols):
+        raise ValueError(f"the checkpoint must be of a [{rows}, {cols}] matrix")
+    return ctypes.byref(c)
+
+
+def aqfq_ckpt8_pack(ckpt, x, stream=None):
+    p, ld = _mat(x, "x", _ROWS)
+    R, C = x.shape
+    _check("aqfq_ckpt8_pack",
+           lib().aqfq_ckpt8_pack(_ck(ckpt, R, C), _dt(x), p, ld, R, C, _stream(stream)))
+
+
+def aqfq_ckpt8_unpack(ckpt, y, act=ACT_NONE, stream=None):
+    p, ld = _mat(y, "y", _ROWS)
+    R, C = y.shape
+    _check("aqfq_ckpt8_unpack",
+           lib().aqfq_ckpt8_unpack(_ck(ckpt, R, C), int(act), _dt(y), p, ld, R, C, _stream(stream)))
+
+
+def aqfq_ckpt8_act_bwd_workspace_bytes(rows, cols) -> int:
+    return int(lib().aqfq_ckpt8_act_bwd_workspace_bytes(int(rows), int(cols)))
+
+
+def aqfq_ckpt8_act_bwd(ckpt, act, dy, dx=None, y=None, dbias=None, accumulate=False, workspace=None,
+                       stream=None):
+    """dx = dy act'(p), y = act(p) and dbias = column sums of dx for the p kept in ckpt."""
+    pd, ldd = _mat(dy, "dy", _ROWS)
+    R, C = dy.shape
+    px, ldx = _mat(dx, "dx", (dy.dtype,), (R, C))
+    py, ldy = _mat(y, "y", (dy.dtype,), (R, C))
+    ws, wsb = _ws(workspace)
+    _check("aqfq_ckpt8_act_bwd",
+           lib().aqfq_ckpt8_act_bwd(_ck(ckpt, R, C), int(act), _dt(dy), pd, ldd, R, C, px, ldx, py,
+                                    ldy, _vec(dbias, "dbias", _FL, C), int(bool(accumulate)), ws, wsb,
+                                    _stream(stream)))
+
+
+def aqfq_layernorm_fwd(x, gamma, beta, eps, y, mean=None, rstd=None, ckpt=None, stream=None):
+    """y = (x - mean) rstd gamma + beta per row of x [rows, cols]."""
+    px, ldx = _mat(x, "x", _ROWS)
+    R, C = x.shape
+    py, ldy = _mat(y, "y", (x.dtype,), (R, C))
+    par = gamma if gamma is not None else beta
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one type")
+    _check("aqfq_layernorm_fwd",
+           lib().aqfq_layernorm_fwd(_dt(x), px, ldx, R, C, _dt(par), _vec(gamma, "gamma", _ROWS, C),
+                                    _vec(beta, "beta", _ROWS, C), float(eps), py, ldy,
+                                    _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
+                                    _ck(ckpt, R, C), _stream(stream)))
+
+
+def aqfq_layernorm_bwd_workspace_bytes(rows, cols) -> int:
+    return int(lib().aqfq_layernorm_bwd_workspace_bytes(int(rows), int(cols)))
+
+
+def aqfq_layernorm_bwd(dy, x, mean, rstd, gamma, dx=None, dgamma=None, dbeta=None, dres=None,
+                       ckpt=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of aqfq_layernorm_fwd from its input x, or (x None) from ckpt."""
+    pd, ldd = _mat(dy, "dy", _ROWS)
+    R, C = dy.shape
+    dt = (dy.dtype,)
+    px, ldx = _mat(x, "x", dt, (R, C))
+    pr, ldr = _mat(dres, "dres", dt, (R, C))
+    po, ldo = _mat(dx, "dx", dt, (R, C))
+    ws, wsb = _ws(workspace)
+    _check("aqfq_layernorm_bwd",
+           lib().aqfq_layernorm_bwd(_dt(dy), pd, ldd, px, ldx, _ck(ckpt, R, C), R, C,
+                                    _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
+                                    _dt(gamma), _vec(gamma, "gamma", _ROWS, C), pr, ldr, po, ldo,
+                                    _vec(dgamma, "dgamma", _FL, C), _vec(dbeta, "dbeta", _FL, C),
+                                    int(bool(accumulate)), ws, wsb, _stream(stream)))
+
+
+def aqfq_linear_workspace_bytes(kind, M, N, K) -> int:
+    return int(lib().aqfq_linear_workspace_bytes(int(kind), int(M), int(N), int(K)))
+
+
+def aqfq_linear_fwd(x, w, y, bias=None, act=ACT_NONE, residual=None, ckpt=None, workspace=None,
+                    error_flag=None, stream=None):
+    """y = act(x @ w.T + bias) + residual; ckpt keeps x @ w.T + bias in 8 bits."""
+    px, ldx = _mat(x, "x", _BF)
+    M, K = x.shape
+    N = w.shape[0]
+    pw, ldw = _mat(w, "w", _BF, (N, K))
+    pr, ldr = _mat(residual, "residual", _BF, (M, N))
+    py, ldy = _mat(y, "y", _BF, (M, N))
+    ws, wsb = _ws(workspace)
+    _check("aqfq_linear_fwd",
+           lib().aqfq_linear_fwd(px, ldx, pw, ldw, M, N, K, _dt(bias), _vec(bias, "bias", _ROWS, N),
+                                 int(act), pr, ldr, py, ldy, _ck(ckpt, M, N), ws, wsb,
+                                 _flag(error_flag), _stream(stream)))
+
+
+def aqfq_linear_dgrad(dy, w, dx, act=ACT_NONE, ckpt=None, residual=None, workspace=None,
+                      error_flag=None, stream=None):
+    """dx = (dy @ w) act'(p) + residual, p [M, K] kept in ckpt."""
+    pd, ldd = _mat(dy, "dy", _BF)
+    M, N = dy.shape
+    K = w.shape[1]
+    pw, ldw = _mat(w, "w", _BF, (N, K))
+    pr, ldr = _mat(residual, "residual", _BF, (M, K))
+    po, ldo = _mat(dx, "dx", _BF, (M, K))
+    ws, wsb = _ws(workspace)
+    _check("aqfq_linear_dgrad",
+           lib().aqfq_linear_dgrad(pd, ldd, pw, ldw, M, N, K, int(act), _ck(ckpt, M, K), pr, ldr, po,
+                                   ldo, ws, wsb, _flag(error_flag), _stream(stream)))
+
+
+def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=None, stream=None):
+    """dw (+)= dy.T @ x."""
+    pd, ldd = _mat(dy, "dy", _BF)
+    M, N = dy.shape
+    K = x.shape[1]
+    px, ldx = _mat(x, "x", _BF, (M, K))
+    po, ldo = _mat(dw, "dw", _ROWS, (N, K))
+    ws, wsb = _ws(workspace)
+    _check("aqfq_linear_wgrad",
+           lib().aqfq_linear_wgrad(pd, ldd, px, ldx, M, N, K, _dt(dw), po, ldo,
+                                   int(bool(accumulate)), ws, wsb, _flag(error_flag),
+                                   _stream(stream)))
 
 
 def aqfq_status_string(status: int) -> str:
