@@ -466,7 +466,8 @@ aqfq_status aqfq_layernorm_bwd(int dtype, const void* dy, int64_t lddy, const vo
  *                product that is split along its inner axis)
  *   error_flag   optional device int32, set to 1 if a pipeline wait of the
  *                kernel timed out (the output is then incomplete); never cleared
- * Limits: M, N, K < 2^30. */
+ * Limits: M, N, K < 2^30, the axis that is summed over at most 2^26, leading
+ * dimensions of x, w and dy below 2^38. */
 enum { AQFQ_LINEAR_FWD = 0, AQFQ_LINEAR_DGRAD = 1, AQFQ_LINEAR_WGRAD = 2 };
 size_t aqfq_linear_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K);
 aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,

@@ -9,8 +9,13 @@
 //   forward       r = m, c = n, k = k:  A = x (k contiguous), B = W (k contiguous)
 //   input grad    r = m, c = k, k = n:  A = dy (n contiguous), B = W (c contiguous)
 //   weight grad   r = n, c = k, k = m:  A = dy (r contiguous), B = x (c contiguous)
+#include <cuda.h>
+
+#include <mutex>
+
 #include "aqfq_internal.h"
 #include "aqfq_layer.cuh"
+#include "aqfq_sm100_pair.cuh"
 
 namespace aqfq {
 namespace layer {
@@ -19,7 +24,7 @@ namespace {
 enum Pass { P_FWD = AQFQ_LINEAR_FWD, P_DGRAD = AQFQ_LINEAR_DGRAD, P_WGRAD = AQFQ_LINEAR_WGRAD };
 
 // ---------------------------------------------------------------------------
-// epilogue: a warp holds 128 columns of one row, a lane 4 of them, so an 8-bit
+// epilogue: a warp holds 128 columns of a row, a lane 4 of them, so an 8-bit
 // group of 32, 64 or 128 columns is 8, 16 or 32 neighbouring lanes
 // ---------------------------------------------------------------------------
 struct Epi {
@@ -34,135 +39,512 @@ struct Epi {
   Ckpt c;               // forward: written; input gradient: read
 };
 
-// v: the sums of row r, columns [col, col + 4); every lane of the warp calls it
-template <int PASS>
-__device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col, float (&v)[4]) {
+// the bias of columns [col, col + 4)
+__device__ __forceinline__ void load_bias4(const Epi& e, int64_t col, float (&b)[4]) {
   const int n = e.cols - col > 4 ? 4 : int(e.cols - col);
-  const bool in = r < e.rows && n > 0, full = n == 4;
-  if constexpr (PASS == P_FWD) {
-    if (e.bias && in) {
-      float b[4];
-      if (e.bias_dtype == AQFQ_BF16)
-        load_row(static_cast<const bf16*>(e.bias) + col, e.vec_bias && full, n, b);
-      else
-        load_row(static_cast<const float*>(e.bias) + col, e.vec_bias && full, n, b);
+  if (e.bias && n > 0) {
+    if (e.bias_dtype == AQFQ_BF16)
+      load_row(static_cast<const bf16*>(e.bias) + col, e.vec_bias && n == 4, n, b);
+    else
+      load_row(static_cast<const float*>(e.bias) + col, e.vec_bias && n == 4, n, b);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += b[i];
-    }
-    if (e.c.codes) {
+    for (int i = 0; i < 4; ++i) b[i] = 0.0f;
+  }
+}
+
+// v[j]: the sums of row r + j, columns [col, col + 4); every lane of the warp
+// calls it.  What the rows read is fetched for all of them first.
+template <int PASS, int R>
+__device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col,
+                                          const float (&bias)[4], float (&v)[R][4]) {
+  const int n = e.cols - col > 4 ? 4 : int(e.cols - col);
+  const bool full = n == 4;
+  bool in[R];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = i < n ? v[i] : 0.0f;  // beyond the row: no share in amax
-      uint32_t m = amax_bits(v);
-      for (int o = 1; o < (1 << (e.c.lg - 2)); o <<= 1)
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const Divisor d = make_divisor(ckpt_scale(m, e.c.fmt));
-      if (in) {
-        const uint32_t w[1] = {ckpt_codes4(v, d, e.c.fmt)};
-        store_bytes<4>(e.c.codes + r * e.cols + col, e.vec_codes && full, n, w);
-        if ((col & ((1 << e.c.lg) - 1)) == 0) e.c.scale[r * e.c.groups + (col >> e.c.lg)] = d.s;
+  for (int j = 0; j < R; ++j) in[j] = r + j < e.rows && n > 0;
+  float add[R][4];
+  uint32_t code[R][1];
+  float cs[R];
+  const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
+  if (adds) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (!in[j]) continue;
+      if constexpr (PASS == P_WGRAD) {
+        if (e.out_dtype == AQFQ_BF16)
+          load_row(static_cast<const bf16*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, add[j]);
+        else
+          load_row(static_cast<const float*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, add[j]);
+      } else {
+        load_row(e.res + (r + j) * e.ldr + col, e.vec_res && full, n, add[j]);
       }
     }
-    act_apply(e.act, v);
   }
-  if (!in) return;
   if constexpr (PASS == P_DGRAD) {
     if (e.c.codes) {
-      uint32_t w[1];
-      load_bytes<4>(e.c.codes + r * e.cols + col, e.vec_codes && full, n, w);
-      float p[4];
-      ckpt_values4(w[0], e.c.scale[r * e.c.groups + (col >> e.c.lg)], e.c.fmt, p);
-      slope_apply(e.act, p, v);
-    }
-  }
-  if constexpr (PASS != P_WGRAD) {
-    if (e.res) {
-      float b[4];
-      load_row(e.res + r * e.ldr + col, e.vec_res && full, n, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += b[i];
-    }
-    store_row(static_cast<bf16*>(e.out) + r * e.ldo + col, e.vec_out && full, n, v);
-  } else if (e.out_dtype == AQFQ_BF16) {
-    bf16* o = static_cast<bf16*>(e.out) + r * e.ldo + col;
-    if (e.accumulate) {
-      float b[4];
-      load_row(o, e.vec_out && full, n, b);
+      for (int j = 0; j < R; ++j) {
+        if (!in[j]) continue;
+        load_bytes<4>(e.c.codes + (r + j) * e.cols + col, e.vec_codes && full, n, code[j]);
+        cs[j] = e.c.scale[(r + j) * e.c.groups + (col >> e.c.lg)];
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += b[i];
-    }
-    store_row(o, e.vec_out && full, n, v);
-  } else {
-    float* o = static_cast<float*>(e.out) + r * e.ldo + col;
-    if (e.accumulate) {
-      float b[4];
-      load_row(o, e.vec_out && full, n, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += b[i];
-    }
-    store_row(o, e.vec_out && full, n, v);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// product: 64 x 128 outputs per CTA, 16 of k at a time through shared memory;
-// a warp computes 8 rows, a lane 4 columns of each
-// ---------------------------------------------------------------------------
-struct Operands {
-  const bf16 *a, *b;
-  int64_t ars, aks, brs, bks;  // element strides along r / c and k
-  int64_t rows, cols, depth;
-};
-
-constexpr int BM = 64, BN = 128, BK = 16;
-
-template <int PASS>
-__global__ void __launch_bounds__(256) linear_kernel(const Operands o, const Epi e) {
-  __shared__ float sa[BK][BM + 1];
-  __shared__ __align__(16) float sb[BK][BN + 4];
-  const int64_t r0 = int64_t(blockIdx.y) * BM, c0 = int64_t(blockIdx.x) * BN;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float acc[8][4] = {};
-  for (int64_t k0 = 0; k0 < o.depth; k0 += BK) {
-    for (int i = threadIdx.x; i < BM * BK; i += 256) {
-      // consecutive threads along the contiguous axis
-      const int k = o.aks == 1 ? i % BK : i / BM, r = o.aks == 1 ? i / BK : i % BM;
-      sa[k][r] = (r0 + r < o.rows && k0 + k < o.depth)
-                     ? to_f(o.a[(r0 + r) * o.ars + (k0 + k) * o.aks]) : 0.0f;
-    }
-    for (int i = threadIdx.x; i < BN * BK; i += 256) {
-      const int k = o.bks == 1 ? i % BK : i / BN, c = o.bks == 1 ? i / BK : i % BN;
-      sb[k][c] = (c0 + c < o.cols && k0 + k < o.depth)
-                     ? to_f(o.b[(c0 + c) * o.brs + (k0 + k) * o.bks]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < BK; ++k) {
-      const float4 b = *reinterpret_cast<const float4*>(&sb[k][lane * 4]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = sa[k][warp * 8 + i];
-        acc[i][0] = fmaf(a, b.x, acc[i][0]);
-        acc[i][1] = fmaf(a, b.y, acc[i][1]);
-        acc[i][2] = fmaf(a, b.z, acc[i][2]);
-        acc[i][3] = fmaf(a, b.w, acc[i][3]);
+      for (int j = 0; j < R; ++j) {
+        if (!in[j]) continue;
+        float p[4];
+        ckpt_values4(code[j][0], cs[j], e.c.fmt, p);
+        slope_apply(e.act, p, v[j]);
       }
     }
-    __syncthreads();
+  }
+  if constexpr (PASS == P_FWD) {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] += bias[i];
+    if (e.c.codes) {
+      uint32_t m[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = i < n ? v[j][i] : 0.0f;  // no share beyond the row
+        m[j] = amax_bits(v[j]);
+      }
+      for (int o = 1; o < (1 << (e.c.lg - 2)); o <<= 1)
+#pragma unroll
+        for (int j = 0; j < R; ++j) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (!in[j]) continue;
+        const Divisor d = make_divisor(ckpt_scale(m[j], e.c.fmt));
+        const uint32_t w[1] = {ckpt_codes4(v[j], d, e.c.fmt)};
+        store_bytes<4>(e.c.codes + (r + j) * e.cols + col, e.vec_codes && full, n, w);
+        if ((col & ((1 << e.c.lg) - 1)) == 0) e.c.scale[(r + j) * e.c.groups + (col >> e.c.lg)] = d.s;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) act_apply(e.act, v[j]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) epilogue4<PASS>(e, r0 + warp * 8 + i, c0 + lane * 4, acc[i]);
+  for (int j = 0; j < R; ++j) {
+    if (!in[j]) continue;
+    if (adds) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] += add[j][i];
+    }
+    if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32)
+      store_row(static_cast<float*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, v[j]);
+    else
+      store_row(static_cast<bf16*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, v[j]);
+  }
 }
 
+// ---------------------------------------------------------------------------
+// product on a pair of CTAs: tiles of 256 rows x BN columns, 64 of k per stage.
+// Each CTA loads 128 rows of A and BN / 2 of B by TMA; one thread of the leader
+// issues the MMAs for both (tcgen05, cta_group::2); the accumulators (128 rows
+// x BN columns per CTA) are double-buffered in tensor memory, so the epilogue of
+// a tile runs under the next tile's MMAs.  Ragged edges and the tail of k are
+// zeros from the TMA's fill.
+//   warp 0  TMA producer    warp 1  MMA issuer (leader)    warp 2  tensor memory
+//   warps 4-7  epilogue: TMEM -> shared memory -> rows of 128 columns
+// Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
+// raises the caller's flag and returns.
+// ---------------------------------------------------------------------------
+using namespace sm100;
+
+constexpr int kRows = 256, kHalf = 128, kBK = 64;
+constexpr int kThreadsP = 256;
+constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
+constexpr int kStage32 = 32 * 128 * 4;         // 16 KiB per epilogue warp
+
+template <int BN>
+struct Cfg {
+  static constexpr int STAGES = BN == 256 ? 5 : 6;
+  static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
+  static constexpr uint32_t STAGE = kABytes + B_BYTES;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 4 * kStage32 + 256;
+};
+
+struct __align__(8) PairShared {
+  uint64_t full[6], empty[6];  // TMA bytes of both CTAs (leader) / MMA commit
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int32_t abort;
+};
+
+struct PairArgs {
+  int nr, nc;        // tiles
+  int splits;        // slices of the inner axis
+  int ksteps;        // 64-element steps of the inner axis
+  float* part;       // [splits][rows][cols4] partial sums when splits > 1
+  int64_t cols4;     // cols rounded up to 4
+  int32_t* err;
+};
+
+// tile t of nr x nc: groups of 8 tile rows, column by column, so that the tiles in
+// flight share their operands in L2
+__device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& tc) {
+  const int width = 8 * a.nc, g = t / width, first = g * 8;
+  const int gm = a.nr - first < 8 ? a.nr - first : 8;
+  const int in = t - g * width;
+  tr = first + in % gm;
+  tc = in / gm;
+}
+
+template <int PASS, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const PairArgs a, const Epi e) {
+  using C = Cfg<BN>;
+  constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sb = smem + C::STAGES * kABytes;
+  uint8_t* stg = sb + C::STAGES * C::B_BYTES;
+  PairShared* sh = reinterpret_cast<PairShared*>(stg + 4 * kStage32);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int tiles = a.nr * a.nc, units = tiles * a.splits;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->tfull[b], 1);
+      mbar_init(&sh->tempty[b], 8);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+  }
+  if (warp == 2) tmem_alloc_pair(&sh->tmem, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  volatile int32_t* abort = &sh->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += npairs) {
+        int tr, tc;
+        tile_of(a, u % tiles, tr, tc);
+        const int sp = u / tiles;
+        const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
+        const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
+        const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
+        for (int k = k0; k < k1; ++k, ++it) {
+          const int s = it % C::STAGES;
+          if (*abort || (it >= C::STAGES &&
+                         !mbar_wait_suspend(&sh->empty[s], ((it / C::STAGES) & 1) ^ 1))) {
+            *abort = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t bar = peer_addr(smem_u32(&sh->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * C::STAGE);
+          const uint32_t da = smem_u32(smem + s * kABytes), db = smem_u32(sb + s * C::B_BYTES);
+          if constexpr (A_MN) {
+            tma_load_2d_pair(da, &ta, bar, r0, k * kBK);
+            tma_load_2d_pair(da + kABytes / 2, &ta, bar, r0 + 64, k * kBK);
+          } else {
+            tma_load_2d_pair(da, &ta, bar, k * kBK, r0);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_2d_pair(db + j * 8192, &tb, bar, c0 + 64 * j, k * kBK);
+          } else {
+            tma_load_2d_pair(db, &tb, bar, k * kBK, c0);
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // let the copies already issued (the peer's among them) land
+        for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+          mbar_wait_suspend(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kRows, BN) | (A_MN ? kIdescTransA : 0) |
+                                 (B_MN ? kIdescTransB : 0);
+      const uint64_t da0 = A_MN ? smem_desc_mn_sw128(smem_u32(smem), 8192)
+                                : smem_desc_sw128(smem_u32(smem));
+      const uint64_t db0 = B_MN ? smem_desc_mn_sw128(smem_u32(sb), 8192)
+                                : smem_desc_sw128(smem_u32(sb));
+      // 16 of k: 32 bytes along a row, or two atoms of 8
+      constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += npairs, ++n) {
+        const int sp = u / tiles;
+        const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
+        const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
+        const int buf = n & 1;
+        if (n >= 2 && !mbar_wait_suspend(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
+          *abort = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + uint32_t(buf * 256);
+        for (int k = k0; k < k1; ++k, ++it) {
+          const int s = it % C::STAGES;
+          if (*abort || !mbar_wait_suspend(&sh->full[s], (it / C::STAGES) & 1)) {
+            *abort = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t da = da0 + ((s * kABytes) >> 4), db = db0 + ((s * C::B_BYTES) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, (k > k0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(&sh->empty[s]);
+        }
+        if (ok) tc_commit_pair(&sh->tfull[buf]);
+      }
+      if (!ok) {  // drain the MMAs already issued
+        tc_commit_pair(&sh->drain);
+        mbar_wait_suspend(&sh->drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    float* my = reinterpret_cast<float*>(stg + q * kStage32);
+    int n = 0;
+    for (int u = pair; u < units; u += npairs, ++n) {
+      int tr, tc;
+      tile_of(a, u % tiles, tr, tc);
+      const int buf = n & 1;
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait_suspend(&sh->tfull[buf], (n >> 1) & 1) && !*abort;
+        if (!ok) *abort = 1;
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      tc_fence_after_sync();
+      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32;
+      const int nrows = e.rows - r0 < 32 ? int(e.rows - r0) : 32;  // <= 0: nothing of this warp
+#pragma unroll 1
+      for (int h = 0; h < BN / 128; ++h) {
+        const int64_t col = int64_t(tc) * BN + h * 128 + lane * 4;
+        const bool live = nrows > 0 && int64_t(tc) * BN + h * 128 < e.cols;
+        if (live) {
+          // 32 rows x 128 columns into shared memory; 16-byte unit c of row r at c ^ r
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[32];
+            tc_ld_32x32b_x32(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + h * 128 + cc * 32), v);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(my + lane * 128 + (((cc * 8 + i) ^ lane) * 4)) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        if (h == BN / 128 - 1) {  // this warp is done with the accumulator
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), 0));
+        }
+        __syncwarp();
+        if (live) {
+          if (a.splits > 1) {
+            float* dst = a.part + (int64_t(u / tiles) * e.rows + r0) * a.cols4 + col;
+            if (col < a.cols4)
+#pragma unroll 4
+              for (int j = 0; j < nrows; ++j)
+                *reinterpret_cast<float4*>(dst + j * a.cols4) =
+                    *reinterpret_cast<const float4*>(my + j * 128 + ((lane ^ j) * 4));
+          } else {
+            float bias[4];
+            load_bias4(e, col, bias);
+#pragma unroll 1
+            for (int j = 0; j < nrows; j += 4) {
+              float v[4][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(my + (j + i) * 128 + ((lane ^ (j + i)) * 4));
+                v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+              }
+              epilogue4<PASS, 4>(e, r0 + j, col, bias, v);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the peer's MMAs and arrivals into this CTA are done
+  if (warp == 2) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
+}
+
+// out = epilogue(sum of the slices' partial sums, in order); also the empty
+// product (splits 0): a warp takes 128 columns of a row
 template <int PASS>
-cudaError_t launch(const Operands& o, const Epi& e, cudaStream_t st) {
-  const int64_t gx = (o.cols + BN - 1) / BN, gy = (o.rows + BM - 1) / BM;
-  linear_kernel<PASS><<<dim3(unsigned(gx), unsigned(gy)), 256, 0, st>>>(o, e);
+__global__ void __launch_bounds__(256)
+    finish_kernel(const float* part, int splits, int64_t cols4, const Epi e) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = int64_t(blockIdx.x) * 128 + lane * 4;
+  float bias[4];
+  if (PASS == P_FWD) load_bias4(e, col, bias);
+  for (int64_t r = int64_t(blockIdx.y) * 8 + warp; r < e.rows; r += int64_t(gridDim.y) * 8) {
+    float v[1][4] = {};
+    if (col < cols4) {
+      const float* p = part + r * cols4 + col;
+      for (int s = 0; s < splits; ++s) {
+        const float4 f = *reinterpret_cast<const float4*>(p + int64_t(s) * e.rows * cols4);
+        v[0][0] += f.x, v[0][1] += f.y, v[0][2] += f.z, v[0][3] += f.w;
+      }
+    }
+    epilogue4<PASS, 1>(e, r, col, bias, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+struct Operand {
+  const void* p;
+  int64_t inner, outer, ld;  // contiguous axis, the other one, its stride
+};
+
+bool encode(CUtensorMap* tm, const Operand& o, unsigned box0, unsigned box1) {
+  const cuuint64_t dims[2] = {cuuint64_t(o.inner), cuuint64_t(o.outer)};
+  const int64_t ld = o.outer > 1 ? o.ld : (o.inner + 7) / 8 * 8;  // a single row has no stride
+  const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  const cuuint32_t box[2] = {box0, box1};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(o.p), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// How a product of rows x cols over `depth` is cut.
+struct Plan {
+  int bn;         // columns per tile
+  int nr, nc;     // tiles
+  int ksteps;
+  int splits;
+  int64_t cols4;
+  size_t bytes;   // partial sums
+};
+
+constexpr int kPairs = 76;  // SM pairs
+
+Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
+  Plan p;
+  p.bn = 256;
+  p.nr = int((rows + kRows - 1) / kRows);
+  p.nc = int((cols + p.bn - 1) / p.bn);
+  p.ksteps = int((depth + kBK - 1) / kBK);
+  p.splits = p.ksteps > 0 ? 1 : 0;
+  const int64_t tiles = int64_t(p.nr) * p.nc;
+  if (tiles * 2 <= kPairs && p.ksteps >= 16) {
+    int64_t s = kPairs / tiles;
+    if (s > p.ksteps / 8) s = p.ksteps / 8;
+    if (s > 8) s = 8;
+    p.splits = int(s);
+  }
+  p.cols4 = (cols + 3) / 4 * 4;
+  p.bytes = p.splits > 1 ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
+  return p;
+}
+
+template <int PASS, int BN>
+cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
+                        cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(pair_kernel<PASS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(Cfg<BN>::SMEM));
+  });
+  if (attr != cudaSuccess) return attr;
+  const int64_t units = int64_t(a.nr) * a.nc * a.splits;
+  const unsigned pairs = unsigned(units < kPairs ? units : kPairs);
+  pair_kernel<PASS, BN><<<2 * pairs, kThreadsP, Cfg<BN>::SMEM, st>>>(ta, tb, a, e);
   return cudaGetLastError();
 }
 
-// sizes of one product; operands that the tensor memory accelerator can read
-// (16-byte base, rows a multiple of 16 bytes apart)
+// out[r, c] = epilogue(sum over k of A(r, k) B(c, k)); A, B as stored
+template <int PASS>
+aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi& e, void* workspace,
+                    size_t workspace_bytes, int32_t* err, cudaStream_t st) {
+  const Plan p = make_plan(e.rows, e.cols, depth);
+  if (p.bytes > 0) {
+    if (!workspace || workspace_bytes < p.bytes) return AQFQ_ERR_WORKSPACE;
+    if (!al(workspace, 16)) return AQFQ_ERR_ALIGN;
+  }
+  float* part = static_cast<float*>(workspace);
+  if (p.splits > 0) {
+    if (!encode_fn()) return AQFQ_ERR_CUDA;
+    CUtensorMap ta, tb;
+    constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+    if (!encode(&ta, A, kBK, A_MN ? kBK : kHalf) ||
+        !encode(&tb, B, kBK, B_MN ? kBK : unsigned(p.bn / 2)))
+      return AQFQ_ERR_CUDA;
+    PairArgs a = {p.nr, p.nc, p.splits, p.ksteps, part, p.cols4, err};
+    if (launch_pair<PASS, 256>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
+  }
+  if (p.splits != 1) {
+    const int64_t gy = (e.rows + 7) / 8;
+    finish_kernel<PASS><<<dim3(unsigned((e.cols + 127) / 128), unsigned(gy > 65535 ? 65535 : gy)), 256,
+                          0, st>>>(part, p.splits, p.cols4, e);
+    if (cudaGetLastError() != cudaSuccess) return AQFQ_ERR_CUDA;
+  }
+  return AQFQ_OK;
+}
+
+// Sizes of one product.  The inner axis is bounded so that no tile's sum takes
+// longer than a bounded wait (2^20 steps of about 0.35 us).
 bool size_ok(int64_t v) { return v >= 0 && v <= 0x3FFFFFFF; }
+bool inner_ok(int64_t v, int64_t lda, int64_t ldb) {
+  return v <= (1 << 26) && lda < (int64_t(1) << 38) && ldb < (int64_t(1) << 38);
+}
+// operands that the tensor memory accelerator can read: 16-byte base, rows a
+// multiple of 16 bytes (and less than 2^40 bytes) apart
 bool operand_ok(const void* p, int64_t ld) { return al(p, 16) && ld % 8 == 0; }
 
 void finish_epi(Epi& e, int es) {
@@ -180,8 +562,13 @@ using namespace aqfq;
 using namespace aqfq::layer;
 
 extern "C" size_t aqfq_linear_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K) {
-  (void)pass, (void)M, (void)N, (void)K;
-  return 0;
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return 0;
+  switch (pass) {
+    case AQFQ_LINEAR_FWD: return make_plan(M, N, K).bytes;
+    case AQFQ_LINEAR_DGRAD: return make_plan(M, K, N).bytes;
+    case AQFQ_LINEAR_WGRAD: return make_plan(N, K, M).bytes;
+    default: return 0;
+  }
 }
 
 extern "C" aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -190,9 +577,8 @@ extern "C" aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w
                                        int64_t ldr, void* y, int64_t ldy, const aqfq_ckpt8* ckpt,
                                        void* workspace, size_t workspace_bytes,
                                        int32_t* error_flag, void* stream) {
-  (void)workspace, (void)workspace_bytes, (void)error_flag;
   if (!size_ok(M) || !size_ok(N) || !size_ok(K) || !view_ok(M, K, ldx) || !view_ok(N, K, ldw) ||
-      !view_ok(M, N, ldy) || (residual && !view_ok(M, N, ldr)))
+      !view_ok(M, N, ldy) || (residual && !view_ok(M, N, ldr)) || !inner_ok(K, ldx, ldw))
     return AQFQ_ERR_SHAPE;
   if (!act_ok(act) || !dtype_ok(bias_dtype)) return AQFQ_ERR_UNSUPPORTED;
   Epi e = {};
@@ -210,8 +596,8 @@ extern "C" aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w
   e.res = static_cast<const bf16*>(residual), e.ldr = ldr;
   e.out = y, e.ldo = ldy, e.out_dtype = AQFQ_BF16, e.act = act;
   finish_epi(e, 2);
-  const Operands o = {static_cast<const bf16*>(x), static_cast<const bf16*>(w), ldx, 1, ldw, 1, M, N, K};
-  return launch<P_FWD>(o, e, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
+  return product<P_FWD>({x, K, M, ldx}, {w, K, N, ldw}, K, e, workspace, workspace_bytes, error_flag,
+                        static_cast<cudaStream_t>(stream));
 }
 
 extern "C" aqfq_status aqfq_linear_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw,
@@ -220,9 +606,8 @@ extern "C" aqfq_status aqfq_linear_dgrad(const void* dy, int64_t lddy, const voi
                                          int64_t ldr, void* dx, int64_t lddx, void* workspace,
                                          size_t workspace_bytes, int32_t* error_flag,
                                          void* stream) {
-  (void)workspace, (void)workspace_bytes, (void)error_flag;
   if (!size_ok(M) || !size_ok(N) || !size_ok(K) || !view_ok(M, N, lddy) || !view_ok(N, K, ldw) ||
-      !view_ok(M, K, lddx) || (residual && !view_ok(M, K, ldr)))
+      !view_ok(M, K, lddx) || (residual && !view_ok(M, K, ldr)) || !inner_ok(N, lddy, ldw))
     return AQFQ_ERR_SHAPE;
   if (!act_ok(act)) return AQFQ_ERR_UNSUPPORTED;
   Epi e = {};
@@ -241,8 +626,8 @@ extern "C" aqfq_status aqfq_linear_dgrad(const void* dy, int64_t lddy, const voi
   e.res = static_cast<const bf16*>(residual), e.ldr = ldr;
   e.out = dx, e.ldo = lddx, e.out_dtype = AQFQ_BF16, e.act = act;
   finish_epi(e, 2);
-  const Operands o = {static_cast<const bf16*>(dy), static_cast<const bf16*>(w), lddy, 1, 1, ldw, M, K, N};
-  return launch<P_DGRAD>(o, e, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
+  return product<P_DGRAD>({dy, N, M, lddy}, {w, K, N, ldw}, N, e, workspace, workspace_bytes,
+                          error_flag, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -250,9 +635,8 @@ extern "C" aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const voi
                                          int64_t lddw, int accumulate, void* workspace,
                                          size_t workspace_bytes, int32_t* error_flag,
                                          void* stream) {
-  (void)workspace, (void)workspace_bytes, (void)error_flag;
   if (!size_ok(M) || !size_ok(N) || !size_ok(K) || !view_ok(M, N, lddy) || !view_ok(M, K, ldx) ||
-      !view_ok(N, K, lddw))
+      !view_ok(N, K, lddw) || !inner_ok(M, lddy, ldx))
     return AQFQ_ERR_SHAPE;
   if (!dtype_ok(dtype)) return AQFQ_ERR_UNSUPPORTED;
   if (N > 0 && K > 0 && (!dw || (M > 0 && (!dy || !x)))) return AQFQ_ERR_NULL;
@@ -263,6 +647,6 @@ extern "C" aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const voi
   e.rows = N, e.cols = K;
   e.out = dw, e.ldo = lddw, e.out_dtype = dtype, e.accumulate = accumulate;
   finish_epi(e, esize(dtype));
-  const Operands o = {static_cast<const bf16*>(dy), static_cast<const bf16*>(x), 1, lddy, 1, ldx, N, K, M};
-  return launch<P_WGRAD>(o, e, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
+  return product<P_WGRAD>({dy, N, M, lddy}, {x, K, M, ldx}, M, e, workspace, workspace_bytes,
+                          error_flag, static_cast<cudaStream_t>(stream));
 }
