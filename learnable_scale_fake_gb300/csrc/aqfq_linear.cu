@@ -141,6 +141,243 @@ __device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col,
 }
 
 // ---------------------------------------------------------------------------
+// epilogue from tensor memory: a lane holds one row, 16 columns at a time, so a
+// checkpoint group is a run of one lane's values (no exchange between lanes, one
+// division per group) and every access is a whole 32-byte sector.
+// ---------------------------------------------------------------------------
+// 16 BF16 at p; a16 / a32: p is 16- / 32-byte aligned (all 16 in the row), else n single ones
+__device__ __forceinline__ void ld16(const bf16* p, bool a32, bool a16, int n, uint32_t (&w)[8]) {
+  if (a32) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else if (a16) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = 2 * i < n ? p[2 * i].b : 0u;
+      w[i] |= 2 * i + 1 < n ? uint32_t(p[2 * i + 1].b) << 16 : 0u;
+    }
+  }
+}
+__device__ __forceinline__ void st16(bf16* p, bool a32, bool a16, int n, const uint32_t (&w)[8]) {
+  if (a32) {
+    st_256(p, w);
+  } else if (a16) {
+    st_128(p, w[0], w[1], w[2], w[3]);
+    st_128(p + 8, w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (2 * i < n) p[2 * i].b = uint16_t(w[i]);
+      if (2 * i + 1 < n) p[2 * i + 1].b = uint16_t(w[i] >> 16);
+    }
+  }
+}
+
+// alignment of a row segment of 16 columns that lies in the row
+struct Seg {
+  bool a32, a16;
+};
+__device__ __forceinline__ Seg seg(const void* p, bool whole) {
+  const uint32_t a = uint32_t(reinterpret_cast<uintptr_t>(p));
+  return {whole && (a & 31) == 0, whole && (a & 15) == 0};
+}
+
+// 16 columns of a bias vector (the same for every lane)
+__device__ __forceinline__ void bias16(const Epi& e, int64_t col, int n, float (&b)[16]) {
+  if (e.bias_dtype == AQFQ_BF16) {
+    const bf16* p = static_cast<const bf16*>(e.bias) + col;
+    uint32_t w[8];
+    ld16(p, false, seg(p, n >= 16).a16, n, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[2 * i] = bf_lo(w[i]), b[2 * i + 1] = bf_hi(w[i]);
+  } else {
+    const float* p = static_cast<const float*>(e.bias) + col;
+    const bool a16 = seg(p, n >= 16).a16;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      if (a16) {
+        const float4 f = *reinterpret_cast<const float4*>(p + i);
+        b[i] = f.x, b[i + 1] = f.y, b[i + 2] = f.z, b[i + 3] = f.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[i + j] = i + j < n ? p[i + j] : 0.0f;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  __syncwarp();  // the load is a warp-wide instruction
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  sm100::tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Columns [col, col + 16 * chunks) of row r (one row per lane of the warp; chunks
+// * 16 a multiple of the checkpoint's group), sums at taddr.  `in`: the row
+// exists.  Every lane of the warp calls it.
+template <int PASS, int ACT>
+__device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col, int chunks,
+                                             uint32_t taddr) {
+  const int gch = PASS == P_FWD && e.c.codes ? 1 << (e.c.lg - 4) : 1;  // chunks per group
+  const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
+#pragma unroll 1
+  for (int g = 0; g < chunks && col + g * 16 < e.cols; g += gch) {
+    Divisor div = {};
+    if (PASS == P_FWD && e.c.codes) {
+      uint32_t m = 0;
+#pragma unroll 1
+      for (int c = g; c < g + gch; ++c) {
+        float v[16], b[16];
+        tmem16(taddr + uint32_t(c * 16), v);
+        const int64_t left = e.cols - (col + c * 16);
+        const int n = left > 16 ? 16 : int(left);
+        if (n <= 0) break;  // uniform
+        if (e.bias) {
+          bias16(e, col + c * 16, n, b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += b[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = i < n ? max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu) : m;
+      }
+      div = make_divisor(ckpt_scale(m, e.c.fmt));
+      if (in) e.c.scale[r * e.c.groups + ((col + g * 16) >> e.c.lg)] = div.s;
+    }
+#pragma unroll 1
+    for (int c = g; c < g + gch; ++c) {
+      const int64_t cc = col + c * 16;
+      const int64_t left = e.cols - cc;
+      const int n = left > 16 ? 16 : int(left);
+      if (n <= 0) break;  // uniform
+      // what the row reads, before the accumulators are waited for
+      uint32_t aw[8], cw[4];
+      float af[PASS == P_WGRAD ? 16 : 1], cs = 0.0f;
+      if (adds && in) {
+        if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
+          const float* p = static_cast<const float*>(e.out) + r * e.ldo + cc;
+          const bool a16 = seg(p, n == 16).a16;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            if (a16) {
+              const float4 f = *reinterpret_cast<const float4*>(p + i);
+              if constexpr (PASS == P_WGRAD) af[i] = f.x, af[i + 1] = f.y, af[i + 2] = f.z, af[i + 3] = f.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if constexpr (PASS == P_WGRAD) af[i + j] = i + j < n ? p[i + j] : 0.0f;
+            }
+          }
+        } else {
+          const bf16* p = PASS == P_WGRAD ? static_cast<const bf16*>(e.out) + r * e.ldo + cc
+                                          : e.res + r * e.ldr + cc;
+          const Seg s = seg(p, n == 16);
+          ld16(p, s.a32, s.a16, n, aw);
+        }
+      }
+      if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE && in) {
+        const uint8_t* p = e.c.codes + r * e.cols + cc;
+        if (seg(p, n == 16).a16) {
+          const uint4 u = *reinterpret_cast<const uint4*>(p);
+          cw[0] = u.x, cw[1] = u.y, cw[2] = u.z, cw[3] = u.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cw[i] = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < n) cw[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+        }
+        cs = e.c.scale[r * e.c.groups + (cc >> e.c.lg)];
+      }
+      float v[16];
+      tmem16(taddr + uint32_t(c * 16), v);
+      if (PASS == P_FWD) {
+        if (e.bias) {
+          float b[16];
+          bias16(e, cc, n, b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += b[i];
+        }
+        if (e.c.codes && in) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = ckpt_codes4(v + 4 * i, div, e.c.fmt);
+          uint8_t* p = e.c.codes + r * e.cols + cc;
+          if (seg(p, n == 16).a16) {
+            st_128(p, w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < n) p[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = act_f<ACT>(v[i]);
+      }
+      if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float p[4];
+          ckpt_values4(cw[i], cs, e.c.fmt, p);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float d;
+            act_fd<ACT>(p[j], d);
+            v[4 * i + j] *= d;
+          }
+        }
+      }
+      if (!in) continue;
+      if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
+        float* p = static_cast<float*>(e.out) + r * e.ldo + cc;
+        const bool a16 = seg(p, n == 16).a16;
+        if constexpr (PASS == P_WGRAD) {
+          if (adds) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += af[i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          if (a16) {
+            *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i + j < n) p[i + j] = v[i + j];
+          }
+        }
+      } else {
+        if (adds) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(aw[i]), v[2 * i + 1] += bf_hi(aw[i]);
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+        bf16* p = static_cast<bf16*>(e.out) + r * e.ldo + cc;
+        const Seg s = seg(p, n == 16);
+        st16(p, s.a32, s.a16, n, w);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // product on a pair of CTAs: tiles of 256 rows x BN columns, 64 of k per stage.
 // Each CTA loads 128 rows of A and BN / 2 of B by TMA; one thread of the leader
 // issues the MMAs for both (tcgen05, cta_group::2); the accumulators (128 rows
@@ -148,27 +385,27 @@ __device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col,
 // a tile runs under the next tile's MMAs.  Ragged edges and the tail of k are
 // zeros from the TMA's fill.
 //   warp 0  TMA producer    warp 1  MMA issuer (leader)    warp 2  tensor memory
-//   warps 4-7  epilogue: TMEM -> shared memory -> rows of 128 columns
+//   warps 4-11  epilogue, two per quarter of the rows, half of the columns each
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
 using namespace sm100;
 
 constexpr int kRows = 256, kHalf = 128, kBK = 64;
-constexpr int kThreadsP = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kThreadsP = 128 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
-constexpr int kStage32 = 32 * 128 * 4;         // 16 KiB per epilogue warp
 
 template <int BN>
 struct Cfg {
-  static constexpr int STAGES = BN == 256 ? 5 : 6;
+  static constexpr int STAGES = BN == 256 ? 7 : 9;
   static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
   static constexpr uint32_t STAGE = kABytes + B_BYTES;
-  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 4 * kStage32 + 256;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 256;
 };
 
 struct __align__(8) PairShared {
-  uint64_t full[6], empty[6];  // TMA bytes of both CTAs (leader) / MMA commit
+  uint64_t full[9], empty[9];  // TMA bytes of both CTAs (leader) / MMA commit
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -194,7 +431,7 @@ __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& 
   tc = in / gm;
 }
 
-template <int PASS, int BN>
+template <int PASS, int ACT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
@@ -204,8 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sb = smem + C::STAGES * kABytes;
-  uint8_t* stg = sb + C::STAGES * C::B_BYTES;
-  PairShared* sh = reinterpret_cast<PairShared*>(stg + 4 * kStage32);
+  PairShared* sh = reinterpret_cast<PairShared*>(sb + C::STAGES * C::B_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int tiles = a.nr * a.nc, units = tiles * a.splits;
@@ -218,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->tfull[b], 1);
-      mbar_init(&sh->tempty[b], 8);
+      mbar_init(&sh->tempty[b], 2 * kEpiWarps);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -278,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kRows, BN) | (A_MN ? kIdescTransA : 0) |
                                  (B_MN ? kIdescTransB : 0);
       const uint64_t da0 = A_MN ? smem_desc_mn_sw128(smem_u32(smem), 8192)
@@ -287,7 +523,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
                                 : smem_desc_sw128(smem_u32(sb));
       // 16 of k: 32 bytes along a row, or two atoms of 8
       constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
-      int it = 0, n = 0;
+      int s = 0, n = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += npairs, ++n) {
         const int sp = u / tiles;
@@ -295,36 +532,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
         const int buf = n & 1;
         if (n >= 2 && !mbar_wait_suspend(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
-          *abort = 1;
           ok = false;
           break;
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + uint32_t(buf * 256);
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % C::STAGES;
-          if (*abort || !mbar_wait_suspend(&sh->full[s], (it / C::STAGES) & 1)) {
-            *abort = 1;
+        for (int k = k0; k < k1; ++k) {
+          if (!mbar_wait_suspend(&sh->full[s], phase)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint64_t da = da0 + ((s * kABytes) >> 4), db = db0 + ((s * C::B_BYTES) >> 4);
+          if (elect_one()) {
+            tc_mma_f16_pair(d, da, db, idesc, k > k0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, (k > k0 || kk > 0) ? 1u : 0u);
-          tc_commit_pair(&sh->empty[s]);
+            for (int kk = 1; kk < kBK / 16; ++kk) tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, 1u);
+            tc_commit_pair(&sh->empty[s]);
+            if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf]);
+          }
+          __syncwarp();
+          if (++s == C::STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) tc_commit_pair(&sh->tfull[buf]);
       }
-      if (!ok) {  // drain the MMAs already issued
-        tc_commit_pair(&sh->drain);
+      if (!ok) {  // a wait timed out: drain the MMAs already issued
+        *abort = 1;
+        if (elect_one()) tc_commit_pair(&sh->drain);
+        __syncwarp();
         mbar_wait_suspend(&sh->drain, 0);
       }
     }
   } else if (warp >= 4) {
-    const int q = warp & 3;
-    float* my = reinterpret_cast<float*>(stg + q * kStage32);
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    constexpr int W = BN / 2;  // columns of this warp
     int n = 0;
     for (int u = pair; u < units; u += npairs, ++n) {
       int tr, tc;
@@ -338,56 +581,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       tc_fence_after_sync();
-      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32;
-      const int nrows = e.rows - r0 < 32 ? int(e.rows - r0) : 32;  // <= 0: nothing of this warp
+      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
+      const int64_t col = int64_t(tc) * BN + half * W;
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + half * W);
+      if (r0 < e.rows && col < e.cols) {
+        if (a.splits > 1) {
+          float* dst = a.part + (int64_t(u / tiles) * e.rows + r) * a.cols4 + col;
 #pragma unroll 1
-      for (int h = 0; h < BN / 128; ++h) {
-        const int64_t col = int64_t(tc) * BN + h * 128 + lane * 4;
-        const bool live = nrows > 0 && int64_t(tc) * BN + h * 128 < e.cols;
-        if (live) {
-          // 32 rows x 128 columns into shared memory; 16-byte unit c of row r at c ^ r
-#pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t v[32];
-            tc_ld_32x32b_x32(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + h * 128 + cc * 32), v);
-            tc_wait_ld();
+          for (int c = 0; c < W / 16 && col + c * 16 < e.cols; ++c) {
+            float v[16];
+            tmem16(taddr + uint32_t(c * 16), v);
+            if (r < e.rows) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(my + lane * 128 + (((cc * 8 + i) ^ lane) * 4)) =
-                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-        if (h == BN / 128 - 1) {  // this warp is done with the accumulator
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), 0));
-        }
-        __syncwarp();
-        if (live) {
-          if (a.splits > 1) {
-            float* dst = a.part + (int64_t(u / tiles) * e.rows + r0) * a.cols4 + col;
-            if (col < a.cols4)
-#pragma unroll 4
-              for (int j = 0; j < nrows; ++j)
-                *reinterpret_cast<float4*>(dst + j * a.cols4) =
-                    *reinterpret_cast<const float4*>(my + j * 128 + ((lane ^ j) * 4));
-          } else {
-            float bias[4];
-            load_bias4(e, col, bias);
-#pragma unroll 1
-            for (int j = 0; j < nrows; j += 4) {
-              float v[4][4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 f = *reinterpret_cast<const float4*>(my + (j + i) * 128 + ((lane ^ (j + i)) * 4));
-                v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-              }
-              epilogue4<PASS, 4>(e, r0 + j, col, bias, v);
+              for (int i = 0; i < 16; i += 4)
+                if (col + c * 16 + i < a.cols4)
+                  *reinterpret_cast<float4*>(dst + c * 16 + i) =
+                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
+        } else {
+          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr);
         }
-        __syncwarp();
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), 0));
     }
   }
   tc_fence_before_sync();
@@ -492,19 +710,19 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   return p;
 }
 
-template <int PASS, int BN>
+template <int PASS, int ACT, int BN>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(pair_kernel<PASS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr = cudaFuncSetAttribute(pair_kernel<PASS, ACT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 int(Cfg<BN>::SMEM));
   });
   if (attr != cudaSuccess) return attr;
   const int64_t units = int64_t(a.nr) * a.nc * a.splits;
   const unsigned pairs = unsigned(units < kPairs ? units : kPairs);
-  pair_kernel<PASS, BN><<<2 * pairs, kThreadsP, Cfg<BN>::SMEM, st>>>(ta, tb, a, e);
+  pair_kernel<PASS, ACT, BN><<<2 * pairs, kThreadsP, Cfg<BN>::SMEM, st>>>(ta, tb, a, e);
   return cudaGetLastError();
 }
 
@@ -526,7 +744,18 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
         !encode(&tb, B, kBK, B_MN ? kBK : unsigned(p.bn / 2)))
       return AQFQ_ERR_CUDA;
     PairArgs a = {p.nr, p.nc, p.splits, p.ksteps, part, p.cols4, err};
-    if (launch_pair<PASS, 256>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
+    cudaError_t r;
+    // split products leave the epilogue to finish_kernel
+    switch (PASS == P_WGRAD || p.splits > 1 ? AQFQ_ACT_NONE : e.act) {
+      case AQFQ_ACT_RELU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_RELU, 256>(ta, tb, a, e, st); break;
+      case AQFQ_ACT_GELU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_GELU, 256>(ta, tb, a, e, st); break;
+      case AQFQ_ACT_GELU_TANH:
+        r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_GELU_TANH, 256>(ta, tb, a, e, st);
+        break;
+      case AQFQ_ACT_SILU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_SILU, 256>(ta, tb, a, e, st); break;
+      default: r = launch_pair<PASS, AQFQ_ACT_NONE, 256>(ta, tb, a, e, st); break;
+    }
+    if (r != cudaSuccess) return AQFQ_ERR_CUDA;
   }
   if (p.splits != 1) {
     const int64_t gy = (e.rows + 7) / 8;

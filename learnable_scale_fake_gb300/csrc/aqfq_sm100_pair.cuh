@@ -10,6 +10,19 @@
 namespace aqfq {
 namespace sm100 {
 
+// true in one lane of a converged warp.  The tcgen05 and TMA instructions take
+// uniform registers: issued under this predicate in a warp-uniform loop they need
+// no per-lane serialisation.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{ .reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
