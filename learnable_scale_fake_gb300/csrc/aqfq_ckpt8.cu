@@ -18,126 +18,193 @@ namespace layer {
 namespace {
 
 constexpr int kWarps = 8;
+// rows in flight per lane
+constexpr int kU = 2, kUB = 2;
 
-// lanes per row: a whole group at least, 32 at most
+// How a [rows, cols] matrix is covered.  V = 8 (rows allow 16-byte accesses): a
+// lane holds 8 columns, 2^lr lanes share a row (narrow rows: several per warp).
+// V = 1: a warp holds 128 columns of one row as four vectors of 32.
 struct Map {
   int lr;          // log2 of the lanes that share a row
   unsigned gx;     // column segments
   unsigned gy;     // row slices
 };
 
-inline Map make_map(int64_t rows, int64_t cols, int lg, int64_t max_parts) {
+// Enough blocks for eight per SM; the bias gradient's partial sums bound the slices.
+inline Map make_map(int64_t rows, int64_t cols, int lg, bool wide, int64_t max_parts) {
   Map m;
-  m.lr = lg - 3;
+  m.lr = wide ? lg - 3 : 5;
   while (m.lr < 5 && (int64_t(8) << m.lr) < cols) ++m.lr;
-  m.gx = unsigned((cols + (int64_t(8) << m.lr) - 1) / (int64_t(8) << m.lr));
+  const int64_t seg = wide ? int64_t(8) << m.lr : 128;
+  m.gx = unsigned((cols + seg - 1) / seg);
   const int64_t per = int64_t(kWarps) << (5 - m.lr);  // rows of one block step
   int64_t gy = (rows + per - 1) / per;
-  const int64_t fill = (int64_t(sm_count()) * 16 + m.gx - 1) / m.gx;
+  const int64_t fill = (int64_t(sm_count()) * 8 + m.gx - 1) / m.gx;
   if (gy > fill) gy = fill;
   if (gy > max_parts) gy = max_parts;
   m.gy = unsigned(gy < 1 ? 1 : gy);
   return m;
 }
 
+template <int V>
 struct Lane {
+  static constexpr int NV = V == 8 ? 1 : 4;
   int64_t row, step;  // first row, rows between two of this lane's rows
-  int64_t col;
-  int n;              // columns in range (<= 0: none)
+  int64_t base;       // first row of the warp (the same trip count in every lane)
+  int64_t col0;       // first column of the warp
+  int64_t col[NV];    // this lane's vectors, clamped into the row
+  bool in[NV];
 };
-__device__ __forceinline__ Lane lane_of(int lr, int64_t cols) {
+template <int V>
+__device__ __forceinline__ Lane<V> lane_of(int lr, int64_t cols) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Lane l;
-  const int sub = lane >> lr, rpw = 32 >> lr;
-  l.row = (int64_t(blockIdx.y) * kWarps + warp) * rpw + sub;
+  Lane<V> l;
+  const int rpw = 32 >> lr;
+  l.base = (int64_t(blockIdx.y) * kWarps + warp) * rpw;
+  l.row = l.base + (lane >> lr);
   l.step = int64_t(gridDim.y) * kWarps * rpw;
-  l.col = ((int64_t(blockIdx.x) << lr) + (lane & ((1 << lr) - 1))) * 8;
-  const int64_t left = cols - l.col;
-  l.n = left > 8 ? 8 : int(left);
+  l.col0 = V == 8 ? (int64_t(blockIdx.x) << lr) * 8 : int64_t(blockIdx.x) * 128;
+#pragma unroll
+  for (int j = 0; j < Lane<V>::NV; ++j) {
+    const int64_t c = l.col0 + (V == 8 ? (lane & ((1 << lr) - 1)) * 8 : j * 32 + lane);
+    l.in[j] = c < cols;
+    l.col[j] = l.in[j] ? c : 0;
+  }
   return l;
 }
 
-template <typename T>
+// Rows in flight per lane: loads of all of them are issued before the first is
+// used.  Rows past the end reread the last row and store nothing.
+template <typename T, int V, int U>
 __global__ void __launch_bounds__(kWarps * 32)
-    pack_kernel(const T* x, int64_t ldx, int64_t rows, int64_t cols, int lr, bool vec, bool cvec,
-                const Ckpt c) {
-  const Lane l = lane_of(lr, cols);
-  const int64_t last = l.row - (l.row % (32 >> lr));  // warp-uniform trip count
-  for (int64_t r0 = last, r = l.row; r0 < rows; r0 += l.step, r += l.step) {
-    const bool in = r < rows;
-    float v[8];
-    load_row(x + r * ldx + l.col, vec && in && l.n == 8, in ? l.n : 0, v);
-    uint32_t m = amax_bits(v);
-    for (int o = 1; o < (1 << (c.lg - 3)); o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const Divisor d = make_divisor(ckpt_scale(m, c.fmt));
-    if (in && l.n > 0) {
-      const uint32_t w[2] = {ckpt_codes4(v, d, c.fmt), ckpt_codes4(v + 4, d, c.fmt)};
-      store_bytes<8>(c.codes + r * cols + l.col, cvec && l.n == 8, l.n, w);
-      if ((l.col & ((1 << c.lg) - 1)) == 0) c.scale[r * c.groups + (l.col >> c.lg)] = d.s;
+    pack_kernel(const T* x, int64_t ldx, int64_t rows, int64_t cols, int lr, const Ckpt c) {
+  constexpr int NV = Lane<V>::NV;
+  const Lane<V> l = lane_of<V>(lr, cols);
+  for (int64_t b = l.base, r = l.row; b < rows; b += l.step * U, r += l.step * U) {
+    Vec<T, V> raw[U][NV];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) raw[u][j].load(x + ru * ldx + l.col[j]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step;
+      float v[NV * V];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!l.in[j]) raw[u][j].zero();
+        raw[u][j].get(v + j * V);
+      }
+      if constexpr (V == 8) {
+        uint32_t m = amax_bits(v);
+        for (int o = 1; o < (1 << (c.lg - 3)); o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const Divisor d = make_divisor(ckpt_scale(m, c.fmt));
+        if (ru < rows && l.in[0]) {
+          st_64(c.codes + ru * cols + l.col[0], ckpt_codes4(v, d, c.fmt), ckpt_codes4(v + 4, d, c.fmt));
+          if ((l.col[0] & ((1 << c.lg) - 1)) == 0) c.scale[ru * c.groups + (l.col[0] >> c.lg)] = d.s;
+        }
+      } else if (ru < rows) {  // uniform: one row per warp
+        ckpt_row<V, NV>(c, ru, cols, l.col0, v);
+      }
     }
   }
 }
 
-template <typename T, int ACT>
+template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
-    unpack_kernel(const Ckpt c, int64_t rows, int64_t cols, int lr, bool cvec, T* y, int64_t ldy,
-                  bool vec) {
-  const Lane l = lane_of(lr, cols);
-  if (l.n <= 0) return;
-  for (int64_t r = l.row; r < rows; r += l.step) {
-    uint32_t w[2];
-    load_bytes<8>(c.codes + r * cols + l.col, cvec && l.n == 8, l.n, w);
-    const float s = c.scale[r * c.groups + (l.col >> c.lg)];
-    float v[8];
-    ckpt_values4(w[0], s, c.fmt, v);
-    ckpt_values4(w[1], s, c.fmt, v + 4);
+    unpack_kernel(const Ckpt c, int64_t rows, int64_t cols, int lr, T* y, int64_t ldy) {
+  constexpr int NV = Lane<V>::NV;
+  const Lane<V> l = lane_of<V>(lr, cols);
+  for (int64_t r = l.row; r < rows; r += l.step * U) {
+    CodeVec<V> w[U][NV];
+    float s[U][NV];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_f<ACT>(v[i]);
-    store_row(y + r * ldy + l.col, vec && l.n == 8, l.n, v);
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        w[u][j].load(c.codes + ru * cols + l.col[j]);
+        s[u][j] = __ldg(c.scale + ru * c.groups + (l.col[j] >> c.lg));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step;
+      float v[NV * V];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) w[u][j].values(s[u][j], c.fmt, v + j * V);
+      act_all<ACT>(v);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (ru < rows && l.in[j]) put<T, V>(y + ru * ldy + l.col[j], v + j * V);
+    }
   }
 }
 
-template <typename T, int ACT>
+template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
-    act_bwd_kernel(const Ckpt c, const T* dy, int64_t lddy, int64_t rows, int64_t cols, int lr,
-                   bool vec, bool cvec, T* dx, int64_t lddx, T* y, int64_t ldy, float* part) {
-  const Lane l = lane_of(lr, cols);
-  float sum[8] = {};
-  if (l.n > 0) {
-    for (int64_t r = l.row; r < rows; r += l.step) {
-      float v[8];
-      load_row(dy + r * lddy + l.col, vec && l.n == 8, l.n, v);
-      if (c.codes) {
-        uint32_t w[2];
-        load_bytes<8>(c.codes + r * cols + l.col, cvec && l.n == 8, l.n, w);
-        const float s = c.scale[r * c.groups + (l.col >> c.lg)];
-        float p[8];
-        ckpt_values4(w[0], s, c.fmt, p);
-        ckpt_values4(w[1], s, c.fmt, p + 4);
+    act_bwd_kernel(const Ckpt c, const T* dy, int64_t lddy, int64_t rows, int64_t cols, int lr, T* dx,
+                   int64_t lddx, T* y, int64_t ldy, float* part) {
+  constexpr int NV = Lane<V>::NV, E = NV * V;
+  const Lane<V> l = lane_of<V>(lr, cols);
+  float sum[E] = {};
+  for (int64_t r = l.row; r < rows; r += l.step * U) {
+    Vec<T, V> raw[U][NV];
+    CodeVec<V> w[U][NV];
+    float s[U][NV];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float d;
-          p[i] = act_fd<ACT>(p[i], d);
-          v[i] *= d;
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        raw[u][j].load(dy + ru * lddy + l.col[j]);
+        if (c.codes) {
+          w[u][j].load(c.codes + ru * cols + l.col[j]);
+          s[u][j] = __ldg(c.scale + ru * c.groups + (l.col[j] >> c.lg));
         }
-        if (y) store_row(y + r * ldy + l.col, vec && l.n == 8, l.n, p);
       }
-      if (dx) store_row(dx + r * lddx + l.col, vec && l.n == 8, l.n, v);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * l.step;
+      if (ru >= rows) break;
+      float v[E];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) raw[u][j].get(v + j * V);
+      if (c.codes) {
+        float p[E];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) w[u][j].values(s[u][j], c.fmt, p + j * V);
+        slope_all<ACT>(p, v);
+        if (y) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (l.in[j]) put<T, V>(y + ru * ldy + l.col[j], p + j * V);
+        }
+      }
+      if (dx) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (l.in[j]) put<T, V>(dx + ru * lddx + l.col[j], v + j * V);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum[i] += v[i];
     }
   }
   if (part) {
-    __shared__ float red[kWarps][256];
+    // the lanes of a column, then the eight warps, in a fixed order
+    __shared__ float red[kWarps][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < E; ++i) {
       for (int o = 16; o >= (1 << lr); o >>= 1) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
-      if (lane < (1 << lr)) red[warp][lane * 8 + i] = sum[i];
+      if (lane < (1 << lr)) red[warp][V == 8 ? lane * 8 + i : i * 32 + lane] = sum[i];
     }
     __syncthreads();
-    const int64_t col = (int64_t(blockIdx.x) << lr) * 8 + threadIdx.x;
-    if (int(threadIdx.x) < (8 << lr) && col < cols) {
+    const int64_t col = l.col0 + threadIdx.x;
+    if (int(threadIdx.x) < (V == 8 ? 8 << lr : 128) && col < cols) {
       float t = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) t += red[w][threadIdx.x];
@@ -173,6 +240,25 @@ size_t act_bwd_ws(int64_t rows, int64_t cols) {
   int64_t parts = (rows + kWarps - 1) / kWarps;
   if (parts > kMaxParts) parts = kMaxParts;
   return size_t(parts) * size_t(cols) * 4;
+}
+
+template <typename T>
+struct Type {
+  using type = T;
+};
+
+// f(tag of the element type, columns per vector)
+template <typename F>
+void by_type(int dtype, bool wide, F f) {
+  using V8 = std::integral_constant<int, 8>;
+  using V1 = std::integral_constant<int, 1>;
+  if (dtype == AQFQ_BF16) {
+    if (wide) f(Type<bf16>(), V8());
+    else f(Type<bf16>(), V1());
+  } else {
+    if (wide) f(Type<float>(), V8());
+    else f(Type<float>(), V1());
+  }
 }
 
 // f(tag of the activation)
@@ -220,16 +306,14 @@ extern "C" aqfq_status aqfq_ckpt8_pack(const aqfq_ckpt8* ckpt, int dtype, const 
   if (!x) return AQFQ_ERR_NULL;
   if (!al(x, esize(dtype))) return AQFQ_ERR_ALIGN;
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
-  const Map m = make_map(rows, cols, c.lg, 65535);
-  const bool vec = rows_aligned<8>(x, ldx, esize(dtype)), cvec = rows_aligned<8>(c.codes, cols, 1);
-  const dim3 grid(m.gx, m.gy);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == AQFQ_BF16)
-    pack_kernel<<<grid, kWarps * 32, 0, st>>>(static_cast<const bf16*>(x), ldx, rows, cols, m.lr,
-                                              vec, cvec, c);
-  else
-    pack_kernel<<<grid, kWarps * 32, 0, st>>>(static_cast<const float*>(x), ldx, rows, cols, m.lr,
-                                              vec, cvec, c);
+  const bool wide = cols % 8 == 0 && rows_aligned<8>(x, ldx, esize(dtype)) && al(c.codes, 8);
+  const Map m = make_map(rows, cols, c.lg, wide, 65535);
+  by_type(dtype, wide, [&](auto t, auto v) {
+    using T = typename decltype(t)::type;
+    constexpr int V = decltype(v)::value;
+    pack_kernel<T, V, kU><<<dim3(m.gx, m.gy), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const T*>(x), ldx, rows, cols, m.lr, c);
+  });
   return done();
 }
 
@@ -244,18 +328,17 @@ extern "C" aqfq_status aqfq_ckpt8_unpack(const aqfq_ckpt8* ckpt, int act, int dt
   if (!y) return AQFQ_ERR_NULL;
   if (!al(y, esize(dtype))) return AQFQ_ERR_ALIGN;
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
-  const Map m = make_map(rows, cols, c.lg, 65535);
-  const bool vec = rows_aligned<8>(y, ldy, esize(dtype)), cvec = rows_aligned<8>(c.codes, cols, 1);
-  const dim3 grid(m.gx, m.gy);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool wide = cols % 8 == 0 && rows_aligned<8>(y, ldy, esize(dtype)) && al(c.codes, 8);
+  const Map m = make_map(rows, cols, c.lg, wide, 65535);
   by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    if (dtype == AQFQ_BF16)
-      unpack_kernel<bf16, ACT><<<grid, kWarps * 32, 0, st>>>(c, rows, cols, m.lr, cvec,
-                                                             static_cast<bf16*>(y), ldy, vec);
-    else
-      unpack_kernel<float, ACT><<<grid, kWarps * 32, 0, st>>>(c, rows, cols, m.lr, cvec,
-                                                              static_cast<float*>(y), ldy, vec);
+    by_type(dtype, wide, [&](auto t, auto v) {
+      using T = typename decltype(t)::type;
+      constexpr int V = decltype(v)::value;
+      unpack_kernel<T, V, ACT, kU>
+          <<<dim3(m.gx, m.gy), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+              c, rows, cols, m.lr, static_cast<T*>(y), ldy);
+    });
   });
   return done();
 }
@@ -299,22 +382,19 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
     return AQFQ_OK;
   }
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
-  const Map m = make_map(rows, cols, c.lg, dbias ? kMaxParts : 65535);
-  const bool vec = rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dx, lddx, es) &&
-                   rows_aligned<8>(y, ldy, es);
-  const bool cvec = rows_aligned<8>(c.codes, cols, 1);
-  const dim3 grid(m.gx, m.gy);
+  const bool wide = cols % 8 == 0 && rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dx, lddx, es) &&
+                    rows_aligned<8>(y, ldy, es) && al(c.codes, 8);
+  const Map m = make_map(rows, cols, c.lg, wide, dbias ? kMaxParts : 65535);
   float* part = dbias ? static_cast<float*>(workspace) : nullptr;
   by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    if (dtype == AQFQ_BF16)
-      act_bwd_kernel<bf16, ACT><<<grid, kWarps * 32, 0, st>>>(
-          c, static_cast<const bf16*>(dy), lddy, rows, cols, m.lr, vec, cvec,
-          static_cast<bf16*>(dx), lddx, static_cast<bf16*>(y), ldy, part);
-    else
-      act_bwd_kernel<float, ACT><<<grid, kWarps * 32, 0, st>>>(
-          c, static_cast<const float*>(dy), lddy, rows, cols, m.lr, vec, cvec,
-          static_cast<float*>(dx), lddx, static_cast<float*>(y), ldy, part);
+    by_type(dtype, wide, [&](auto t, auto v) {
+      using T = typename decltype(t)::type;
+      constexpr int V = decltype(v)::value;
+      act_bwd_kernel<T, V, ACT, kUB><<<dim3(m.gx, m.gy), kWarps * 32, 0, st>>>(
+          c, static_cast<const T*>(dy), lddy, rows, cols, m.lr, static_cast<T*>(dx), lddx,
+          static_cast<T*>(y), ldy, part);
+    });
   });
   if (cudaGetLastError() != cudaSuccess) return AQFQ_ERR_CUDA;
   if (dbias &&

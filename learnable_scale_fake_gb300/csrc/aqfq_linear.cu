@@ -253,7 +253,8 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
           for (int i = 0; i < 16; ++i) v[i] += b[i];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = i < n ? max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu) : m;
+        for (int i = 0; i < 16; ++i) v[i] = i < n ? v[i] : 0.0f;
+        m = max(m, amax_bits(v));
       }
       div = make_divisor(ckpt_scale(m, e.c.fmt));
       if (in) e.c.scale[r * e.c.groups + ((col + g * 16) >> e.c.lg)] = div.s;
@@ -325,21 +326,13 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
               if (i < n) p[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
           }
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = act_f<ACT>(v[i]);
+        act_all<ACT>(v);
       }
       if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) {
+        float p[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float p[4];
-          ckpt_values4(cw[i], cs, e.c.fmt, p);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d;
-            act_fd<ACT>(p[j], d);
-            v[4 * i + j] *= d;
-          }
-        }
+        for (int i = 0; i < 4; ++i) ckpt_values4(cw[i], cs, e.c.fmt, p + 4 * i);
+        slope_all<ACT>(p, v);
       }
       if (!in) continue;
       if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
