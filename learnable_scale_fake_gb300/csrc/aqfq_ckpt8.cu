@@ -75,39 +75,32 @@ __device__ __forceinline__ Lane<V> lane_of(int lr, int64_t cols) {
 
 // Rows in flight per lane: loads of all of them are issued before the first is
 // used.  Rows past the end reread the last row and store nothing.
-template <typename T, int V, int U>
+template <typename T, int V, int FMT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
     pack_kernel(const T* x, int64_t ldx, int64_t rows, int64_t cols, int lr, const Ckpt c) {
-  constexpr int NV = Lane<V>::NV;
+  constexpr int NV = Lane<V>::NV, P = NV * V / 2;
   const Lane<V> l = lane_of<V>(lr, cols);
   for (int64_t b = l.base, r = l.row; b < rows; b += l.step * U, r += l.step * U) {
-    Vec<T, V> raw[U][NV];
+    Row<T, V, NV> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) raw[u][j].load(x + ru * ldx + l.col[j]);
+      for (int j = 0; j < NV; ++j) raw[u].load(j, x + ru * ldx + l.col[j]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step;
-      float v[NV * V];
+      bool in[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (!l.in[j]) raw[u][j].zero();
-        raw[u][j].get(v + j * V);
+        if (!l.in[j]) raw[u].zero(j);
+        in[j] = l.in[j] && ru < rows;
       }
-      if constexpr (V == 8) {
-        uint32_t m = amax_bits(v);
-        for (int o = 1; o < (1 << (c.lg - 3)); o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const Divisor d = make_divisor(ckpt_scale(m, c.fmt));
-        if (ru < rows && l.in[0]) {
-          st_64(c.codes + ru * cols + l.col[0], ckpt_codes4(v, d, c.fmt), ckpt_codes4(v + 4, d, c.fmt));
-          if ((l.col[0] & ((1 << c.lg) - 1)) == 0) c.scale[ru * c.groups + (l.col[0] >> c.lg)] = d.s;
-        }
-      } else if (ru < rows) {  // uniform: one row per warp
-        ckpt_row<V, NV>(c, ru, cols, l.col0, v);
-      }
+      f2 v[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = raw[u].pair_at(i);
+      ckpt_write<FMT, V, NV>(c, ru, cols, l.col, in, v);
     }
   }
 }
@@ -115,30 +108,25 @@ __global__ void __launch_bounds__(kWarps * 32)
 template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
     unpack_kernel(const Ckpt c, int64_t rows, int64_t cols, int lr, T* y, int64_t ldy) {
-  constexpr int NV = Lane<V>::NV;
+  constexpr int NV = Lane<V>::NV, P = NV * V / 2;
   const Lane<V> l = lane_of<V>(lr, cols);
   for (int64_t r = l.row; r < rows; r += l.step * U) {
-    CodeVec<V> w[U][NV];
-    float s[U][NV];
+    CodeRow<V, NV> w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        w[u][j].load(c.codes + ru * cols + l.col[j]);
-        s[u][j] = __ldg(c.scale + ru * c.groups + (l.col[j] >> c.lg));
-      }
+      for (int j = 0; j < NV; ++j) w[u].load(j, c, ru, cols, l.col[j]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step;
-      float v[NV * V];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) w[u][j].values(s[u][j], c.fmt, v + j * V);
+      f2 v[P];
+      w[u].values(c.fmt, v);
       act_all<ACT>(v);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (ru < rows && l.in[j]) put<T, V>(y + ru * ldy + l.col[j], v + j * V);
+        if (ru < rows && l.in[j]) put<T, V>(y + ru * ldy + l.col[j], v, j);
     }
   }
 }
@@ -147,56 +135,54 @@ template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
     act_bwd_kernel(const Ckpt c, const T* dy, int64_t lddy, int64_t rows, int64_t cols, int lr, T* dx,
                    int64_t lddx, T* y, int64_t ldy, float* part) {
-  constexpr int NV = Lane<V>::NV, E = NV * V;
+  constexpr int NV = Lane<V>::NV, E = NV * V, P = E / 2;
   const Lane<V> l = lane_of<V>(lr, cols);
-  float sum[E] = {};
+  f2 sum2[P] = {};
   for (int64_t r = l.row; r < rows; r += l.step * U) {
-    Vec<T, V> raw[U][NV];
-    CodeVec<V> w[U][NV];
-    float s[U][NV];
+    Row<T, V, NV> raw[U];
+    CodeRow<V, NV> w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step < rows ? r + u * l.step : rows - 1;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        raw[u][j].load(dy + ru * lddy + l.col[j]);
-        if (c.codes) {
-          w[u][j].load(c.codes + ru * cols + l.col[j]);
-          s[u][j] = __ldg(c.scale + ru * c.groups + (l.col[j] >> c.lg));
-        }
+        raw[u].load(j, dy + ru * lddy + l.col[j]);
+        if (c.codes) w[u].load(j, c, ru, cols, l.col[j]);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t ru = r + u * l.step;
       if (ru >= rows) break;
-      float v[E];
+      f2 v[P];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) raw[u][j].get(v + j * V);
+      for (int i = 0; i < P; ++i) v[i] = raw[u].pair_at(i);
       if (c.codes) {
-        float p[E];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) w[u][j].values(s[u][j], c.fmt, p + j * V);
+        f2 p[P];
+        w[u].values(c.fmt, p);
         slope_all<ACT>(p, v);
         if (y) {
 #pragma unroll
           for (int j = 0; j < NV; ++j)
-            if (l.in[j]) put<T, V>(y + ru * ldy + l.col[j], p + j * V);
+            if (l.in[j]) put<T, V>(y + ru * ldy + l.col[j], p, j);
         }
       }
       if (dx) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          if (l.in[j]) put<T, V>(dx + ru * lddx + l.col[j], v + j * V);
+          if (l.in[j]) put<T, V>(dx + ru * lddx + l.col[j], v, j);
       }
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[i] += v[i];
+      for (int i = 0; i < P; ++i) sum2[i] = add2(sum2[i], v[i]);
     }
   }
   if (part) {
     // the lanes of a column, then the eight warps, in a fixed order
     __shared__ float red[kWarps][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float sum[E];
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum[2 * i] = lo2(sum2[i]), sum[2 * i + 1] = hi2(sum2[i]);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       for (int o = 16; o >= (1 << lr); o >>= 1) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
@@ -311,8 +297,13 @@ extern "C" aqfq_status aqfq_ckpt8_pack(const aqfq_ckpt8* ckpt, int dtype, const 
   by_type(dtype, wide, [&](auto t, auto v) {
     using T = typename decltype(t)::type;
     constexpr int V = decltype(v)::value;
-    pack_kernel<T, V, kU><<<dim3(m.gx, m.gy), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const T*>(x), ldx, rows, cols, m.lr, c);
+    const dim3 grid(m.gx, m.gy);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const T* in = static_cast<const T*>(x);
+    if (c.fmt == AQFQ_INT8)
+      pack_kernel<T, V, AQFQ_INT8, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, c);
+    else
+      pack_kernel<T, V, AQFQ_FP8_E4M3, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, c);
   });
   return done();
 }

@@ -219,6 +219,24 @@ __device__ __forceinline__ void slope_all(float (&p)[V], float (&v)[V]) {
   }
 }
 
+// the same for pairs
+template <int ACT, int P>
+__device__ __forceinline__ void act_all(f2 (&v)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = act2<ACT>(v[i]);
+}
+template <int ACT, int P>
+__device__ __forceinline__ void slope_all(f2 (&p)[P], f2 (&v)[P]) {
+  if constexpr (ACT != AQFQ_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f2 d;
+      p[i] = act_fd2<ACT>(p[i], d);
+      v[i] = mul2(v[i], d);
+    }
+  }
+}
+
 // the activation chosen at run time (uniform)
 template <int V>
 __device__ __forceinline__ void act_apply(int act, float (&v)[V]) {
@@ -256,38 +274,65 @@ struct Ckpt {
   int lg;          // log2 of the group
 };
 
-__device__ __forceinline__ float ckpt_scale(uint32_t amax_bits, int fmt) {
-  if (amax_bits >= 0x7F800000u) return __int_as_float(0x7FC00000);
-  return __fdiv_rn(__uint_as_float(amax_bits), fmt == AQFQ_INT8 ? 127.0f : 448.0f);
+// The group's divisor: s = RN(amax / qmax) and RN(1 / s).  The quotient by the
+// constant is Markstein's correction with RN(1 / qmax) (equal to the IEEE quotient
+// for every binary32 mantissa; checked for both constants); tiny amax divides.
+template <int FMT>
+__device__ __forceinline__ Divisor ckpt_divisor(uint32_t amax_bits) {
+  constexpr float qm = FMT == AQFQ_INT8 ? 127.0f : 448.0f, rc = 1.0f / qm;
+  const float a = __uint_as_float(amax_bits);
+  const float q0 = __fmul_rn(a, rc);
+  float s = __fmaf_rn(__fmaf_rn(-q0, qm, a), rc, q0);
+  if (!(a >= 0x1p-90f && a < 0x1p127f))  // rare: tiny, huge, infinite or NaN
+    s = amax_bits >= 0x7F800000u ? __int_as_float(0x7FC00000) : __fdiv_rn(a, qm);
+  return make_divisor(s);
 }
 
 // four codes of x / s, element 0 in the low byte; a scale of zero or NaN gives zeros
-__device__ __forceinline__ uint32_t ckpt_codes4(const float* x, const Divisor& d, int fmt) {
-  if (!(d.s > 0.0f)) return 0u;
-  f2 v[2];
-  if (d.fast) {
-    v[0] = mdiv2(mk2(x[0], x[1]), d), v[1] = mdiv2(mk2(x[2], x[3]), d);
-  } else {  // a quotient may leave the grid here (a rounded subnormal scale)
-    float q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[i] = __fdiv_rn(x[i], d.s);
-      if (fmt == AQFQ_INT8) q[i] = fminf(fmaxf(q[i], -127.0f), 127.0f);
-    }
-    v[0] = mk2(q[0], q[1]), v[1] = mk2(q[2], q[3]);
-  }
-  if (fmt == AQFQ_INT8) {
+template <int FMT>
+__device__ __forceinline__ uint32_t grid_codes4(f2 a, f2 b) {
+  if constexpr (FMT == AQFQ_INT8) {
     // |x / s| <= 127 (1 + 2^-23) rounds to at most 127: no clamp.  The sum with 1.5 * 2^23
     // holds the rounded integer in its low bits.
-    const f2 a = add2(v[0], pair(12582912.0f)), b = add2(v[1], pair(12582912.0f));
+    a = add2(a, pair(12582912.0f)), b = add2(b, pair(12582912.0f));
     return __byte_perm(__byte_perm(uint32_t(a), uint32_t(a >> 32), 0x0040),
                        __byte_perm(uint32_t(b), uint32_t(b >> 32), 0x0040), 0x5410);
+  } else {
+    return cvt_e4m3x2(hi2(a), lo2(a)) | (cvt_e4m3x2(hi2(b), lo2(b)) << 16);
   }
-  return cvt_e4m3x2(hi2(v[0]), lo2(v[0])) | (cvt_e4m3x2(hi2(v[1]), lo2(v[1])) << 16);
+}
+// x: 2 P pairs; w: P words of codes
+template <int FMT, int P>
+__device__ __forceinline__ void ckpt_codes(const f2* x, const Divisor& d, uint32_t (&w)[P]) {
+  if (d.fast) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = grid_codes4<FMT>(mdiv2(x[2 * i], d), mdiv2(x[2 * i + 1], d));
+  } else {  // zero, NaN, or beyond the fast range (a rounded subnormal scale may leave the grid)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2 p = x[2 * i + (j >> 1)];
+        q[j] = d.s > 0.0f ? __fdiv_rn(j & 1 ? hi2(p) : lo2(p), d.s) : 0.0f;
+        if (FMT == AQFQ_INT8) q[j] = fminf(fmaxf(q[j], -127.0f), 127.0f);
+      }
+      w[i] = grid_codes4<FMT>(mk2(q[0], q[1]), mk2(q[2], q[3]));
+    }
+  }
+}
+// the format chosen at run time (uniform)
+__device__ __forceinline__ Divisor ckpt_divisor(uint32_t amax_bits, int fmt) {
+  return fmt == AQFQ_INT8 ? ckpt_divisor<AQFQ_INT8>(amax_bits) : ckpt_divisor<AQFQ_FP8_E4M3>(amax_bits);
+}
+template <int P>
+__device__ __forceinline__ void ckpt_codes(const f2* x, const Divisor& d, int fmt, uint32_t (&w)[P]) {
+  if (fmt == AQFQ_INT8) ckpt_codes<AQFQ_INT8>(x, d, w);
+  else ckpt_codes<AQFQ_FP8_E4M3>(x, d, w);
 }
 
-// four stored values (code * s, rounded to binary32)
-__device__ __forceinline__ void ckpt_values4(uint32_t c, float s, int fmt, float* v) {
+// four stored values (code * s, rounded to binary32) as two pairs
+__device__ __forceinline__ void ckpt_values4(uint32_t c, float s, int fmt, f2* v) {
   f2 a, b;
   if (fmt == AQFQ_INT8) {
     // byte + 128 in the low mantissa bits of 2^23: exact
@@ -301,18 +346,31 @@ __device__ __forceinline__ void ckpt_values4(uint32_t c, float s, int fmt, float
     const float2 p = dec_e4m3x2(c & 0xFFFFu), q = dec_e4m3x2(c >> 16);
     a = mk2(p.x, p.y), b = mk2(q.x, q.y);
   }
-  a = mul2(a, pair(s)), b = mul2(b, pair(s));
-  v[0] = lo2(a), v[1] = hi2(a), v[2] = lo2(b), v[3] = hi2(b);
+  v[0] = mul2(a, pair(s)), v[1] = mul2(b, pair(s));
+}
+__device__ __forceinline__ void ckpt_values4(uint32_t c, float s, int fmt, float* v) {
+  f2 p[2];
+  ckpt_values4(c, s, fmt, p);
+  v[0] = lo2(p[0]), v[1] = hi2(p[0]), v[2] = lo2(p[1]), v[3] = hi2(p[1]);
 }
 
 // bits of the largest |x|, at or above those of infinity when one is NaN
+__device__ __forceinline__ void amax_step(float& m, f2 p) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(lo2(p)), "f"(hi2(p)));
+}
 template <int V>
 __device__ __forceinline__ uint32_t amax_bits(const float (&v)[V]) {
   static_assert(V % 2 == 0, "pairs");
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; i += 2)
-    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
+  for (int i = 0; i < V; i += 2) amax_step(m, mk2(v[i], v[i + 1]));
+  return __float_as_uint(m) & 0x7FFFFFFFu;
+}
+template <int P>
+__device__ __forceinline__ uint32_t amax_bits(const f2 (&v)[P]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) amax_step(m, v[i]);
   return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
@@ -346,92 +404,130 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, bool vec, int n, ui
   }
 }
 
-// V consecutive elements as they are in memory (V = 8: rows allow 16-byte accesses;
-// V = 1: any row), so that loads can be in flight before anything is converted
-template <typename T, int V>
-struct Vec {
+// ---------------------------------------------------------------------------
+// A lane's share of a row: NV vectors of V consecutive elements, kept as they are
+// in memory until all loads are under way.  V = 8 where rows allow 16-byte
+// accesses; V = 1 (neighbouring lanes on neighbouring columns) where they do not.
+// In arithmetic the E = NV V elements are E / 2 pairs: neighbours within a vector
+// (V = 8), or the same lane's elements of vectors 2k and 2k + 1 (V = 1).
+// ---------------------------------------------------------------------------
+template <typename T, int V, int NV>
+struct Row {
   static constexpr int W = V == 1 ? 1 : V * int(sizeof(T)) / 4;
-  uint32_t w[W];
-  __device__ __forceinline__ void load(const T* p) {
+  uint32_t w[NV][W];
+  __device__ __forceinline__ void load(int j, const T* p) {
     if constexpr (V == 1) {
-      if constexpr (sizeof(T) == 2) w[0] = reinterpret_cast<const uint16_t*>(p)[0];
-      else w[0] = __float_as_uint(*reinterpret_cast<const float*>(p));
+      if constexpr (sizeof(T) == 2) w[j][0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+      else w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     } else {
 #pragma unroll
-      for (int i = 0; i < W; i += 4) ld_stream_v4(reinterpret_cast<const uint32_t*>(p) + i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+      for (int i = 0; i < W; i += 4)
+        ld_stream_v4(reinterpret_cast<const uint32_t*>(p) + i, w[j][i], w[j][i + 1], w[j][i + 2], w[j][i + 3]);
     }
   }
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ void zero(int j) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = 0;
+    for (int i = 0; i < W; ++i) w[j][i] = 0;
   }
-  __device__ __forceinline__ void get(float* v) const {
+  __device__ __forceinline__ f2 pair_at(int i) const {  // 0 <= i < E / 2
     if constexpr (V == 1) {
-      v[0] = sizeof(T) == 2 ? __uint_as_float(w[0] << 16) : __uint_as_float(w[0]);
+      const uint32_t a = w[2 * i][0], b = w[2 * i + 1][0];
+      return sizeof(T) == 2 ? mk2(__uint_as_float(a << 16), __uint_as_float(b << 16))
+                            : mk2(__uint_as_float(a), __uint_as_float(b));
     } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[2 * i] = bf_lo(w[i]), v[2 * i + 1] = bf_hi(w[i]);
+      return bf2(w[i / 4][i % 4]);
     } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] = __uint_as_float(w[i]);
+      return mk2(__uint_as_float(w[i / 4][2 * (i % 4)]), __uint_as_float(w[i / 4][2 * (i % 4) + 1]));
     }
   }
 };
+// stores vector j of a lane's pairs
 template <typename T, int V>
-__device__ __forceinline__ void put(T* p, const float* v) {
+__device__ __forceinline__ void put(T* p, const f2* v, int j) {
   if constexpr (V == 1) {
-    from_f(v[0], *p);
+    from_f(j & 1 ? hi2(v[j / 2]) : lo2(v[j / 2]), *p);
+  } else if constexpr (sizeof(T) == 2) {
+    const f2* q = v + 4 * j;
+    st_128(p, pack2(q[0]), pack2(q[1]), pack2(q[2]), pack2(q[3]));
   } else {
-    float t[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) t[i] = v[i];
-    store_row(p, true, V, t);
+    const f2* q = v + 4 * j;
+    const uint32_t w[8] = {uint32_t(q[0]), uint32_t(q[0] >> 32), uint32_t(q[1]), uint32_t(q[1] >> 32),
+                           uint32_t(q[2]), uint32_t(q[2] >> 32), uint32_t(q[3]), uint32_t(q[3] >> 32)};
+    st_128(p, w[0], w[1], w[2], w[3]);
+    st_128(p + 4, w[4], w[5], w[6], w[7]);
   }
 }
-template <int V>
-struct CodeVec {
-  uint32_t w[2];
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (V == 8) {
-      asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-    } else {
-      w[0] = __ldg(p);
-    }
+// the codes of a lane's vectors
+template <int V, int NV>
+struct CodeRow {
+  uint32_t w[NV][V == 8 ? 2 : 1];
+  float s[NV];
+  __device__ __forceinline__ void load(int j, const Ckpt& c, int64_t r, int64_t cols, int64_t col) {
+    const uint8_t* p = c.codes + r * cols + col;
+    if constexpr (V == 8)
+      asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[j][0]), "=r"(w[j][1]) : "l"(p));
+    else
+      w[j][0] = __ldg(p);
+    s[j] = __ldg(c.scale + r * c.groups + (col >> c.lg));
   }
-  __device__ __forceinline__ void values(float s, int fmt, float* v) const {
+  __device__ __forceinline__ void zero(int j) {
+#pragma unroll
+    for (int i = 0; i < (V == 8 ? 2 : 1); ++i) w[j][i] = 0;
+    s[j] = 0.0f;
+  }
+  __device__ __forceinline__ void values(int fmt, f2 (&v)[NV * V / 2]) const {
     if constexpr (V == 8) {
-      ckpt_values4(w[0], s, fmt, v);
-      ckpt_values4(w[1], s, fmt, v + 4);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        ckpt_values4(w[j][0], s[j], fmt, v + 4 * j);
+        ckpt_values4(w[j][1], s[j], fmt, v + 4 * j + 2);
+      }
     } else {
-      float t[4];
-      ckpt_values4(w[0], s, fmt, t);
-      v[0] = t[0];
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) {
+        f2 a[2], b[2];
+        ckpt_values4(w[j][0], s[j], fmt, a);
+        ckpt_values4(w[j + 1][0], s[j + 1], fmt, b);
+        v[j / 2] = mk2(lo2(a[0]), lo2(b[0]));
+      }
     }
   }
 };
 
-// the 8-bit checkpoint of a warp's columns from col0 on; v: the lane's values,
-// zero beyond the row.  V = 8: a group is a run of lanes; V = 1: one, two or four
-// whole vectors (NV is a multiple of four or a vector a whole group).
-template <int V, int NV>
-__device__ __forceinline__ void ckpt_row(const Ckpt& c, int64_t r, int64_t cols, int64_t col0,
-                                         const float* v) {
-  const int lane = threadIdx.x & 31;
+// Writes the 8-bit checkpoint of a warp's share of row r.  v: pairs, zero beyond
+// the row; col[j] the first column of vector j, in[j] whether it is stored.
+// V = 8: a group is a run of lanes; V = 1: one, two or four whole vectors, vector j
+// a multiple of four ones starting a multiple of 128 columns.
+template <int FMT, int V, int NV>
+__device__ __forceinline__ void ckpt_write(const Ckpt& c, int64_t r, int64_t cols,
+                                           const int64_t (&col)[NV], const bool (&in)[NV],
+                                           const f2 (&v)[NV * V / 2]) {
   uint8_t* codes = c.codes + r * cols;
   float* scale = c.scale + r * c.groups;
+  const int mask = (1 << c.lg) - 1;
   if constexpr (V == 8) {
+    uint32_t m[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * 8;
-      float t[8];
+      const f2 t[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+      m[j] = amax_bits(t);
+    }
+    // a group is at least four lanes
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[j * 8 + i];
-      uint32_t m = amax_bits(t);
-      for (int o = 1; o < (1 << (c.lg - 3)); o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const Divisor d = make_divisor(ckpt_scale(m, c.fmt));
-      if (col < cols) {
-        st_64(codes + col, ckpt_codes4(v + j * 8, d, c.fmt), ckpt_codes4(v + j * 8 + 4, d, c.fmt));
-        if ((col & ((1 << c.lg) - 1)) == 0) scale[col >> c.lg] = d.s;
+    for (int o = 1; o < 16; o <<= 1) {
+      if (o < 4 || o < (1 << (c.lg - 3))) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Divisor d = ckpt_divisor<FMT>(m[j]);
+      uint32_t w[2];
+      ckpt_codes<FMT>(v + 4 * j, d, w);
+      if (in[j]) {
+        st_64(codes + col[j], w[0], w[1]);
+        if ((int(col[j]) & mask) == 0) scale[col[j] >> c.lg] = d.s;
       }
     }
   } else {
@@ -440,18 +536,22 @@ __device__ __forceinline__ void ckpt_row(const Ckpt& c, int64_t r, int64_t cols,
     for (int j = 0; j < NV; j += 4) {
       uint32_t m[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m[i] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[j + i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        const f2 p = v[(j + i) / 2];
+        m[i] = __reduce_max_sync(0xFFFFFFFFu, uint32_t(i & 1 ? p >> 32 : p) & 0x7FFFFFFFu);
+      }
       if (c.lg > 5) m[0] = m[1] = max(m[0], m[1]), m[2] = m[3] = max(m[2], m[3]);
       if (c.lg > 6) m[0] = m[1] = m[2] = m[3] = max(m[0], m[2]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t col = col0 + (j + i) * 32 + lane;
-        const Divisor d = make_divisor(ckpt_scale(m[i], c.fmt));
-        if (col < cols) {
-          const float one[4] = {v[j + i], 0.0f, 0.0f, 0.0f};
-          codes[col] = uint8_t(ckpt_codes4(one, d, c.fmt));
-          if ((col & ((1 << c.lg) - 1)) == 0) scale[col >> c.lg] = d.s;
+        const Divisor d = ckpt_divisor<FMT>(m[i]);
+        const f2 p = v[(j + i) / 2];
+        const f2 one[2] = {mk2(i & 1 ? hi2(p) : lo2(p), 0.0f), 0ull};
+        uint32_t w[1];
+        ckpt_codes<FMT>(one, d, w);
+        if (in[j + i]) {
+          codes[col[j + i]] = uint8_t(w[0]);
+          if ((int(col[j + i]) & mask) == 0) scale[col[j + i] >> c.lg] = d.s;
         }
       }
     }

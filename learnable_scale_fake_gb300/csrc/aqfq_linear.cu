@@ -117,8 +117,10 @@ __device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col,
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         if (!in[j]) continue;
-        const Divisor d = make_divisor(ckpt_scale(m[j], e.c.fmt));
-        const uint32_t w[1] = {ckpt_codes4(v[j], d, e.c.fmt)};
+        const Divisor d = ckpt_divisor(m[j], e.c.fmt);
+        const f2 x[2] = {mk2(v[j][0], v[j][1]), mk2(v[j][2], v[j][3])};
+        uint32_t w[1];
+        ckpt_codes(x, d, e.c.fmt, w);
         store_bytes<4>(e.c.codes + (r + j) * e.cols + col, e.vec_codes && full, n, w);
         if ((col & ((1 << e.c.lg) - 1)) == 0) e.c.scale[(r + j) * e.c.groups + (col >> e.c.lg)] = d.s;
       }
@@ -256,7 +258,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
         for (int i = 0; i < 16; ++i) v[i] = i < n ? v[i] : 0.0f;
         m = max(m, amax_bits(v));
       }
-      div = make_divisor(ckpt_scale(m, e.c.fmt));
+      div = ckpt_divisor(m, e.c.fmt);
       if (in) e.c.scale[r * e.c.groups + ((col + g * 16) >> e.c.lg)] = div.s;
     }
 #pragma unroll 1
@@ -315,8 +317,10 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
         }
         if (e.c.codes && in) {
           uint32_t w[4];
+          f2 x[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ckpt_codes4(v + 4 * i, div, e.c.fmt);
+          for (int i = 0; i < 8; ++i) x[i] = mk2(v[2 * i], v[2 * i + 1]);
+          ckpt_codes(x, div, e.c.fmt, w);
           uint8_t* p = e.c.codes + r * e.cols + cc;
           if (seg(p, n == 16).a16) {
             st_128(p, w[0], w[1], w[2], w[3]);

@@ -7,8 +7,11 @@
 //   dgamma = sum over rows of dy h,   dbeta = sum over rows of dy
 // with x as it was, or as its 8-bit checkpoint gives it back (then mu and r
 // are still those of the exact x).
+#include <type_traits>
+
 #include "aqfq_internal.h"
 #include "aqfq_layer.cuh"
+#include "aqfq_sm100.cuh"
 
 namespace aqfq {
 namespace layer {
@@ -97,9 +100,11 @@ __global__ void __launch_bounds__(kT) norm_fwd_kernel(const T* x, T* y, const Fw
         uint32_t m = amax_bits(v);
         for (int o = 1; o < (1 << (a.c.lg - 3)); o <<= 1)
           m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const Divisor d = make_divisor(ckpt_scale(m, a.c.fmt));
+        const Divisor d = ckpt_divisor(m, a.c.fmt);
         if (n > 0) {
-          const uint32_t w[2] = {ckpt_codes4(v, d, a.c.fmt), ckpt_codes4(v + 4, d, a.c.fmt)};
+          const f2 t[4] = {mk2(v[0], v[1]), mk2(v[2], v[3]), mk2(v[4], v[5]), mk2(v[6], v[7])};
+          uint32_t w[2];
+          ckpt_codes(t, d, a.c.fmt, w);
           store_bytes<8>(a.c.codes + r * a.cols + col, a.cvec && n == 8, n, w);
           if ((col & ((1 << a.c.lg) - 1)) == 0) a.c.scale[r * a.c.groups + (col >> a.c.lg)] = d.s;
         }
@@ -118,94 +123,149 @@ __global__ void __launch_bounds__(kT) norm_fwd_kernel(const T* x, T* y, const Fw
 // ---------------------------------------------------------------------------
 // Rows held in registers.  A row belongs to G warps; warp w of it holds columns
 // [w 32 NV V, ...): NV vectors of V consecutive columns per lane, vector j of the
-// lane at ((w NV + j) 32 + lane) V.  V = 8 where the rows allow 16-byte accesses;
-// V = 1 where they do not: neighbouring lanes on neighbouring columns.
+// lane at ((w NV + j) 32 + lane) V.  A block takes R rows at a time (G = 1: each of
+// its four warps does): their loads are all under way before the first sum, they
+// share the barriers of the two reductions and the conversion of gamma and beta.
 // ---------------------------------------------------------------------------
-// V parameters at column col
-template <int V>
-__device__ __forceinline__ void params(const void* p, int pdtype, int64_t col, float def, float* v) {
+// V parameters as pairs
+template <int V, int NV>
+__device__ __forceinline__ void params(const void* p, int pdtype, const int64_t (&col)[NV],
+                                       const bool (&in)[NV], float def, f2 (&v)[NV * V / 2]) {
   if (!p) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = def;
-  } else if constexpr (V == 1) {
-    v[0] = pdtype == AQFQ_BF16 ? to_f(static_cast<const bf16*>(p)[col]) : static_cast<const float*>(p)[col];
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = pair(def);
+  } else if (pdtype == AQFQ_BF16) {
+    Row<bf16, V, NV> w;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j]) w.load(j, static_cast<const bf16*>(p) + col[j]);
+      else w.zero(j);
+    }
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
   } else {
-    float t[V];
-    if (pdtype == AQFQ_BF16) load_row(static_cast<const bf16*>(p) + col, true, V, t);
-    else load_row(static_cast<const float*>(p) + col, true, V, t);
+    Row<float, V, NV> w;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = t[i];
+    for (int j = 0; j < NV; ++j) {
+      if (in[j]) w.load(j, static_cast<const float*>(p) + col[j]);
+      else w.zero(j);
+    }
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
   }
 }
-
-
-// sum over the G warps of a row; G > 1: one barrier (named `bar`, of the row's
-// warps) through red[G], which the caller alternates between two calls
-template <int G>
-__device__ __forceinline__ float row_sum(float v, float* red, int bar) {
-  v = warp_sum(v);
-  if constexpr (G > 1) {
-    if ((threadIdx.x & 31) == 0) red[(threadIdx.x >> 5) % G] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(32 * G) : "memory");
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < G; ++w) v += red[w];
-  }
-  return v;
+// whether pair i's elements lie in the row (V = 1: each on its own)
+template <int V, int NV>
+__device__ __forceinline__ f2 masked(f2 v, int i, const bool (&in)[NV]) {
+  if constexpr (V == 8) return in[i / 4] ? v : 0ull;
+  else return mk2(in[2 * i] ? lo2(v) : 0.0f, in[2 * i + 1] ? hi2(v) : 0.0f);
 }
 
-template <typename T, int V, int NV, int G>
+template <typename T, int V, int NV, int G, int R>
 __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
     norm_fwd_rows(const T* x, T* y, const FwdArgs a) {
-  constexpr int RB = G == 1 ? 4 : 1;  // rows per block
-  __shared__ float red[2][G];
+  constexpr int RB = G == 1 ? 4 : 1, P = NV * V / 2;
+  __shared__ float red[2][R][G];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col0 = G == 1 ? 0 : int64_t(warp) * (NV * 32 * V);
   const float inv = 1.0f / float(a.cols);
-  for (int64_t r = int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0); r < a.rows;
-       r += int64_t(gridDim.x) * RB) {
-    const T* row = x + r * a.ldx;
-    Vec<T, V> raw[NV];
+  const int64_t r0 = (int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0)) * R;
+  if (G == 1 && r0 >= a.rows) return;
+  int64_t col[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col[j] = ((G == 1 ? 0 : int64_t(warp) * (NV * 32)) + j * 32 + lane) * V;
+    in[j] = col[j] < a.cols;
+  }
+  Row<T, V, NV> raw[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const T* row = x + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldx;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * V;
-      if (col < a.cols) raw[j].load(row + col);
-      else raw[j].zero();
+      if (in[j]) raw[k].load(j, row + col[j]);
+      else raw[k].zero(j);
     }
-    float v[NV * V], s = 0.0f;
+  }
+  f2 v[R][P];
+  float s[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) raw[j].get(v + j * V);
-    if (a.c.codes) ckpt_row<V, NV>(a.c, r, a.cols, col0, v);
+  for (int k = 0; k < R; ++k) {
+    f2 t = 0;
 #pragma unroll
-    for (int i = 0; i < NV * V; ++i) s += v[i];
-    const float mu = row_sum<G>(s, red[0], 1) * inv;
-    s = 0.0f;
+    for (int i = 0; i < P; ++i) {
+      v[k][i] = raw[k].pair_at(i);
+      t = add2(t, v[k][i]);
+    }
+    s[k] = lo2(t) + hi2(t);
+  }
+  if (a.c.codes) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = col0 + (j * 32 + lane) * V < a.cols;
+    for (int k = 0; k < R; ++k) {
+      bool ink[NV];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[j * V + i] -= mu;
-        if (in) s = fmaf(v[j * V + i], v[j * V + i], s);
+      for (int j = 0; j < NV; ++j) ink[j] = in[j] && r0 + k < a.rows;
+      if (a.c.fmt == AQFQ_INT8) ckpt_write<AQFQ_INT8, V, NV>(a.c, r0 + k, a.cols, col, ink, v[k]);
+      else ckpt_write<AQFQ_FP8_E4M3, V, NV>(a.c, r0 + k, a.cols, col, ink, v[k]);
+    }
+  }
+  // two passes over the registers: mean, then the sum of squared deviations
+  float mu[R], rs[R];
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < R; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+    if constexpr (G > 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) red[pass][k][warp] = s[k];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        s[k] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < G; ++w) s[k] += red[pass][k][w];
       }
     }
-    const float rs = rsqrtf(row_sum<G>(s, red[1], 1) * inv + a.eps);
-    if (lane == 0 && col0 == 0) {
-      if (a.mean) a.mean[r] = mu;
-      if (a.rstd) a.rstd[r] = rs;
-    }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * V;
-      if (col < a.cols) {
-        float g[V], b[V];
-        params<V>(a.gamma, a.pdtype, col, 1.0f, g);
-        params<V>(a.beta, a.pdtype, col, 0.0f, b);
+    for (int k = 0; k < R; ++k) {
+      if (pass == 0) {
+        mu[k] = s[k] * inv;
+        f2 t = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = fmaf(v[j * V + i] * rs, g[i], b[i]);
-        put<T, V>(y + r * a.ldy + col, g);
+        for (int i = 0; i < P; ++i) {
+          v[k][i] = sub2(v[k][i], pair(mu[k]));
+          const f2 d = masked<V, NV>(v[k][i], i, in);
+          t = fma2(d, d, t);
+        }
+        s[k] = lo2(t) + hi2(t);
+      } else {
+        rs[k] = rsqrtf(fmaf(s[k], inv, a.eps));
       }
     }
+  }
+  if (lane == 0 && (G == 1 || warp == 0)) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (r0 + k < a.rows) {
+        if (a.mean) a.mean[r0 + k] = mu[k];
+        if (a.rstd) a.rstd[r0 + k] = rs[k];
+      }
+  }
+  f2 g[P], b[P];
+  params<V, NV>(a.gamma, a.pdtype, col, in, 1.0f, g);
+  params<V, NV>(a.beta, a.pdtype, col, in, 0.0f, b);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (r0 + k >= a.rows) break;
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[k][i] = fma2(mul2(v[k][i], pair(rs[k])), g[i], b[i]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in[j]) put<T, V>(y + (r0 + k) * a.ldy + col[j], v[k], j);
   }
 }
 
@@ -310,143 +370,451 @@ __global__ void __launch_bounds__(kT)
 // backward with the row in registers: dx and the column sums in one pass.  A block
 // is NG rows' worth of warps (blockDim / 32 G) that walk down the rows; a lane
 // keeps its columns' sums for gamma and beta, and the next row's loads are in
-// flight while this one is reduced.
+// flight while this one is reduced (one barrier per row).
 // ---------------------------------------------------------------------------
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool CK>
 struct RowRegs {
-  Vec<T, V> dy[NV], x[NV], res[NV];  // x: or, in its first words, the codes
-  float s[NV];                       // scale of the codes
+  Row<T, V, NV> dy, res;
+  typename std::conditional<CK, CodeRow<V, NV>, Row<T, V, NV>>::type x;
   float mu, rs;
+  // r: a row that exists
   __device__ __forceinline__ void load(const T* pdy, const T* px, const T* pres, const BwdArgs& a,
-                                       int64_t r, int64_t col0) {
-    const int lane = threadIdx.x & 31;
-    if (r >= a.rows) return;
+                                       int64_t r, const int64_t (&col)[NV], const bool (&in)[NV]) {
     mu = __ldg(a.mean + r), rs = __ldg(a.rstd + r);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * V;
-      s[j] = 0.0f;
-      if (col < a.cols) {
-        dy[j].load(pdy + r * a.lddy + col);
-        if (px) {
-          x[j].load(px + r * a.ldx + col);
-        } else {
-          const uint8_t* c = a.c.codes + r * a.cols + col;
-          if constexpr (V == 8) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(c));
-            x[j].w[0] = u.x, x[j].w[1] = u.y;
-          } else {
-            x[j].w[0] = __ldg(c);
-          }
-          s[j] = __ldg(a.c.scale + r * a.c.groups + (col >> a.c.lg));
-        }
-        if (pres) res[j].load(pres + r * a.lddres + col);
+      if (in[j]) {
+        dy.load(j, pdy + r * a.lddy + col[j]);
+        if constexpr (CK) x.load(j, a.c, r, a.cols, col[j]);
+        else x.load(j, px + r * a.ldx + col[j]);
+        if (pres) res.load(j, pres + r * a.lddres + col[j]);
       } else {
-        dy[j].zero(), x[j].zero(), res[j].zero();
+        dy.zero(j), x.zero(j), res.zero(j);
       }
     }
-  }
-  // h of vector j
-  __device__ __forceinline__ void hat(const T* px, const BwdArgs& a, int j, float* h) const {
-    if (px) {
-      x[j].get(h);
-    } else if constexpr (V == 8) {
-      ckpt_values4(x[j].w[0], s[j], a.c.fmt, h);
-      ckpt_values4(x[j].w[1], s[j], a.c.fmt, h + 4);
-    } else {
-      float t[4];
-      ckpt_values4(x[j].w[0], s[j], a.c.fmt, t);
-      h[0] = t[0];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = (h[i] - mu) * rs;
   }
 };
 
-template <typename T, int V, int NV, int G, bool PF>
-__global__ void __launch_bounds__(512, 1)
+template <typename T, int V, int NV, int G, bool CK, bool PF>
+__global__ void __launch_bounds__(1024, 1)
     norm_bwd_rows(const T* dy, const T* x, const T* dres, T* dx, float* pg, float* pb,
                   const BwdArgs a) {
-  constexpr int C = 32 * G * NV * V;  // columns a row may have
+  constexpr int C = 32 * G * NV * V, P = NV * V / 2;  // columns a row may have
   extern __shared__ float sums[];     // [2][C] when several rows share the block
-  __shared__ float red[16][2][2];     // [warp][parity][sum]
+  __shared__ float2 red[32][2];       // [warp][parity]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ng = int(blockDim.x) / (32 * G), grp = warp / G, wr = warp % G;
-  const int64_t col0 = int64_t(wr) * (NV * 32 * V);
   const float inv = 1.0f / float(a.cols);
-  float ag[NV * V] = {}, ab[NV * V] = {};
+  int64_t col[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col[j] = (int64_t(wr) * (NV * 32) + j * 32 + lane) * V;
+    in[j] = col[j] < a.cols;
+  }
+  f2 g[P], ag[P] = {}, ab[P] = {};
+  params<V, NV>(a.gamma, a.pdtype, col, in, 1.0f, g);
   const int64_t step = int64_t(gridDim.x) * ng;
   int64_t r = int64_t(blockIdx.x) * ng + grp;
-  RowRegs<T, V, NV> cur;
-  cur.load(dy, x, dres, a, r, col0);
+  RowRegs<T, V, NV, CK> cur;
+  if (r < a.rows) cur.load(dy, x, dres, a, r, col, in);
   int par = 0;
   for (; r < a.rows; r += step, par ^= 1) {
-    RowRegs<T, V, NV> nxt;
-    if constexpr (PF) nxt.load(dy, x, dres, a, r + step, col0);
-    float s1 = 0.0f, s2 = 0.0f;
+    RowRegs<T, V, NV, CK> nxt;
+    if constexpr (PF) nxt.load(dy, x, dres, a, r + step < a.rows ? r + step : r, col, in);
+    f2 h[P], t1 = 0, t2 = 0;
+    if constexpr (CK) {
+      cur.x.values(a.c.fmt, h);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * V;
-      if (col < a.cols) {
-        float h[V], d[V], g[V];
-        cur.hat(x, a, j, h);
-        cur.dy[j].get(d);
-        params<V>(a.gamma, a.pdtype, col, 1.0f, g);
+      for (int i = 0; i < P; ++i) h[i] = cur.x.pair_at(i);
+    }
+    const f2 mu = pair(cur.mu), rs = pair(cur.rs);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          ag[j * V + i] = fmaf(d[i], h[i], ag[j * V + i]);
-          ab[j * V + i] += d[i];
-          const float u = d[i] * g[i];
-          s1 += u;
-          s2 = fmaf(u, h[i], s2);
-        }
-      }
+    for (int i = 0; i < P; ++i) {
+      const f2 d = cur.dy.pair_at(i);  // zero beyond the row, so h there does not count
+      h[i] = mul2(sub2(h[i], mu), rs);
+      if constexpr (V == 1) h[i] = masked<V, NV>(h[i], i, in);
+      ag[i] = fma2(d, h[i], ag[i]);
+      ab[i] = add2(ab[i], d);
+      const f2 u = mul2(d, g[i]);
+      t1 = add2(t1, u);
+      t2 = fma2(u, h[i], t2);
     }
     if (dx) {
-      s1 = warp_sum(s1), s2 = warp_sum(s2);
+      float s1 = lo2(t1) + hi2(t1), s2 = lo2(t2) + hi2(t2);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+        s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+      }
       if constexpr (G > 1) {
-        if (lane == 0) red[warp][par][0] = s1, red[warp][par][1] = s2;
+        if (lane == 0) red[warp][par] = make_float2(s1, s2);
         asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * G) : "memory");
         s1 = s2 = 0.0f;
 #pragma unroll
-        for (int w = 0; w < G; ++w) s1 += red[grp * G + w][par][0], s2 += red[grp * G + w][par][1];
-      }
-      const float m1 = s1 * inv, m2 = s2 * inv;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int64_t col = col0 + (j * 32 + lane) * V;
-        if (col < a.cols) {
-          float h[V], d[V], g[V], e[V];
-          cur.hat(x, a, j, h);
-          cur.dy[j].get(d);
-          params<V>(a.gamma, a.pdtype, col, 1.0f, g);
-          if (dres) {
-            cur.res[j].get(e);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) e[i] = 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) d[i] = fmaf(cur.rs, fmaf(-h[i], m2, fmaf(d[i], g[i], -m1)), e[i]);
-          put<T, V>(dx + r * a.lddx + col, d);
+        for (int w = 0; w < G; ++w) {
+          const float2 p = red[grp * G + w][par];
+          s1 += p.x, s2 += p.y;
         }
       }
+      const f2 m1 = pair(-s1 * inv), m2 = pair(-s2 * inv);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const f2 t = fma2(h[i], m2, fma2(cur.dy.pair_at(i), g[i], m1));
+        h[i] = dres ? fma2(rs, t, cur.res.pair_at(i)) : mul2(rs, t);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (in[j]) put<T, V>(dx + r * a.lddx + col[j], h, j);
     }
     if constexpr (PF) cur = nxt;
-    else cur.load(dy, x, dres, a, r + step, col0);
+    else if (r + step < a.rows) cur.load(dy, x, dres, a, r + step, col, in);
   }
   if (!pg) return;
   // the block's column sums: group after group into shared memory, in order
   if (ng > 1) {
-    for (int g = 0; g < ng; ++g) {
-      if (g == grp) {
+    for (int k = 0; k < ng; ++k) {
+      if (k == grp) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c0 = V == 8 ? int(col[i / 4]) + 2 * (i % 4) : int(col[2 * i % NV]);
+          const int c1 = V == 8 ? c0 + 1 : int(col[(2 * i + 1) % NV]);
+          sums[c0] = (k ? sums[c0] : 0.0f) + lo2(ag[i]);
+          sums[c1] = (k ? sums[c1] : 0.0f) + hi2(ag[i]);
+          sums[C + c0] = (k ? sums[C + c0] : 0.0f) + lo2(ab[i]);
+          sums[C + c1] = (k ? sums[C + c1] : 0.0f) + hi2(ab[i]);
+        }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      pg[int64_t(blockIdx.x) * a.cols + c] = sums[c];
+      pb[int64_t(blockIdx.x) * a.cols + c] = sums[C + c];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j]) {
+        put<float, V>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
+        put<float, V>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: persistent blocks whose rows arrive by bulk asynchronous copies.  A
+// group of G warps owns a ring of stages in shared memory, one row (x; or dy, the
+// kept input and the residual's gradient) per stage; a lane works on NV vectors of 8
+// columns.  The copies need no registers, so the bytes in flight per SM (the
+// rings, about 200 KB) cover the memory latency whatever the row's arithmetic
+// holds.  The barrier of a row's reduction also says that the row before it has been
+// read by every warp, so one thread refills that stage right after it.
+// A wait gives up after about a second; the rows left are then written as NaN.
+// ---------------------------------------------------------------------------
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 200 * 1024;  // per SM
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+template <int G>
+__device__ __forceinline__ void group_sync(int grp) {
+  if constexpr (G == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * G) : "memory");
+}
+// sums of K values over a group: every warp's totals through red[G][K]
+template <int G, int K>
+__device__ __forceinline__ void group_sum(float (&s)[K], float* red, int grp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+  if constexpr (G > 1) {
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) red[((threadIdx.x >> 5) % G) * K + k] = s[k];
+    }
+  }
+  group_sync<G>(grp);
+  if constexpr (G > 1) {
+    // pairs of totals, added two at a time
+    static_assert(G * K % 2 == 0, "pairs");
+    const f2* p = reinterpret_cast<const f2*>(red);
+    f2 t = p[0];
+#pragma unroll
+    for (int w = 1; w < G * K / 2; ++w) t = add2(t, p[w]);
+    if constexpr (K == 1) s[0] = lo2(t) + hi2(t);
+    else s[0] = lo2(t), s[1] = hi2(t);
+  }
+}
+
+// pairs of V = 8 vectors of a row in shared memory
+// (MASK: zeros where the vector lies beyond the row)
+template <bool MASK, typename T, int NV>
+__device__ __forceinline__ void smem_pairs(const uint8_t* row, const int (&col)[NV], const bool (&in)[NV],
+                                           f2 (&v)[NV * 4]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + col[j] * int(sizeof(T)));
+    uint4 a = p[0];
+    if (MASK && !in[j]) a = make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(T) == 2) {
+      v[4 * j] = bf2(a.x), v[4 * j + 1] = bf2(a.y), v[4 * j + 2] = bf2(a.z), v[4 * j + 3] = bf2(a.w);
+    } else {
+      uint4 b = p[1];
+      if (MASK && !in[j]) b = make_uint4(0, 0, 0, 0);
+      v[4 * j] = mk2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[4 * j + 1] = mk2(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[4 * j + 2] = mk2(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[4 * j + 3] = mk2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+  }
+}
+
+// after a timeout at row r (stage st): waits, bounded, for the copies that may still be
+// on their way into the block's memory
+__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int st, uint32_t phase, int64_t r,
+                                           int64_t step, int64_t rows) {
+  for (int i = 0; i < stages && r < rows; ++i, r += step) {
+    sm100::mbar_wait_suspend(&full[st], phase);
+    if (++st == stages) st = 0, phase ^= 1;
+  }
+}
+
+struct RingArgs {
+  int stages, stage_bytes;  // per group
+  int row_bytes;            // of a tensor's row; a multiple of 16
+};
+
+// NW warps per block, MB blocks per SM
+template <typename T, int NV, int G, int NW, int MB>
+__global__ void __launch_bounds__(32 * NW, MB)
+    norm_fwd_ring(const T* x, T* y, const FwdArgs a, const RingArgs q) {
+  constexpr int NG = NW / G, P = NV * 4;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[NG][kMaxStages];
+  __shared__ __align__(8) float red[NG][2][G];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / G, wr = warp % G;
+  uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < NG; ++g)
+      for (int i = 0; i < q.stages; ++i) sm100::mbar_init(&full[g][i], 1);
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t step = int64_t(gridDim.x) * NG;
+  int64_t r = int64_t(blockIdx.x) * NG + grp;
+  const bool loader = wr == 0 && lane == 0;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      sm100::mbar_arrive_expect_tx(&full[grp][st], uint32_t(q.row_bytes));
+      bulk_load(sm100::smem_u32(mine + st * q.stage_bytes), x + row * a.ldx, uint32_t(q.row_bytes),
+                &full[grp][st]);
+    }
+  };
+  if (loader)
+    for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
+  const float inv = 1.0f / float(a.cols);
+  int col[NV];
+  int64_t col64[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col64[j] = (wr * NV * 32 + j * 32 + lane) * 8;
+    in[j] = col64[j] < a.cols;
+    col[j] = in[j] ? int(col64[j]) : 0;
+  }
+  f2 g[P], b[P];
+  params<8, NV>(a.gamma, a.pdtype, col64, in, 1.0f, g);
+  params<8, NV>(a.beta, a.pdtype, col64, in, 0.0f, b);
+  int st = 0, prev = q.stages - 1;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (bool first = true; r < a.rows; r += step, first = false) {
+    if (ok) {
+      ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
+      if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
+    }
+    f2 v[P], t = 0;
+    smem_pairs<true, T, NV>(mine + st * q.stage_bytes, col, in, v);
+    if (!ok) v[0] = pair(__int_as_float(0x7FC00000));
+#pragma unroll
+    for (int i = 0; i < P; ++i) t = add2(t, v[i]);
+    if (a.c.codes) {
+      if (a.c.fmt == AQFQ_INT8) ckpt_write<AQFQ_INT8, 8, NV>(a.c, r, a.cols, col64, in, v);
+      else ckpt_write<AQFQ_FP8_E4M3, 8, NV>(a.c, r, a.cols, col64, in, v);
+    }
+    float s[1] = {lo2(t) + hi2(t)};
+    group_sum<G, 1>(s, red[grp][0], grp);
+    // every warp has read the row before this one
+    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+    const float mu = s[0] * inv;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      t = 0;
+#pragma unroll
+      for (int i = 4 * j; i < 4 * j + 4; ++i) {
+        v[i] = sub2(v[i], pair(mu));
+        t = fma2(v[i], v[i], t);
+      }
+      s[0] += in[j] ? lo2(t) + hi2(t) : 0.0f;
+    }
+    group_sum<G, 1>(s, red[grp][1], grp);
+    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
+    if (loader) {
+      if (a.mean) a.mean[r] = mu;
+      if (a.rstd) a.rstd[r] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = fma2(mul2(v[i], pair(rs)), g[i], b[i]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in[j]) put<T, 8>(y + r * a.ldy + col[j], v, j);
+    prev = st;
+    if (++st == q.stages) st = 0, phase ^= 1;
+  }
+}
+
+template <typename T, int NV, int G, bool CK>
+__global__ void __launch_bounds__(512, 1)
+    norm_bwd_ring(const T* dy, const T* x, const T* dres, T* dx, float* pg, float* pb, const BwdArgs a,
+                  const RingArgs q) {
+  constexpr int NG = 16 / G, P = NV * 4, C = 32 * G * NV * 8;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[NG][kMaxStages];
+  __shared__ __align__(8) float red[NG][2][G * 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / G, wr = warp % G;
+  uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < NG; ++g)
+      for (int i = 0; i < q.stages; ++i) sm100::mbar_init(&full[g][i], 1);
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t step = int64_t(gridDim.x) * NG;
+  int64_t r = int64_t(blockIdx.x) * NG + grp;
+  const bool loader = wr == 0 && lane == 0;
+  const uint32_t xbytes = CK ? uint32_t(a.cols) : uint32_t(q.row_bytes);
+  // a stage: dy, the residual's gradient, the kept input
+  const int off_res = q.row_bytes, off_x = dres ? 2 * q.row_bytes : q.row_bytes;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      uint64_t* bar = &full[grp][st];
+      const uint32_t dst = sm100::smem_u32(mine + st * q.stage_bytes);
+      sm100::mbar_arrive_expect_tx(bar, uint32_t(off_x) + xbytes);
+      bulk_load(dst, dy + row * a.lddy, uint32_t(q.row_bytes), bar);
+      if (dres) bulk_load(dst + off_res, dres + row * a.lddres, uint32_t(q.row_bytes), bar);
+      if (CK) bulk_load(dst + off_x, a.c.codes + row * a.cols, xbytes, bar);
+      else bulk_load(dst + off_x, x + row * a.ldx, xbytes, bar);
+    }
+  };
+  if (loader)
+    for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
+  const float inv = 1.0f / float(a.cols);
+  int col[NV];
+  int64_t col64[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col64[j] = (wr * NV * 32 + j * 32 + lane) * 8;
+    in[j] = col64[j] < a.cols;
+    col[j] = in[j] ? int(col64[j]) : 0;
+  }
+  f2 g[P], ag[P] = {}, ab[P] = {};
+  params<8, NV>(a.gamma, a.pdtype, col64, in, 1.0f, g);
+  // the row's scalars are fetched one row ahead
+  float mu_n = 0.0f, rs_n = 0.0f, sc_n[NV];
+  auto scalars = [&](int64_t row) {
+    if (row < a.rows) {
+      mu_n = __ldg(a.mean + row), rs_n = __ldg(a.rstd + row);
+      if constexpr (CK) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) sc_n[j] = __ldg(a.c.scale + row * a.c.groups + (col[j] >> a.c.lg));
+      }
+    }
+  };
+  scalars(r);
+  int st = 0, prev = q.stages - 1, par = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (bool first = true; r < a.rows; r += step, first = false, par ^= 1) {
+    const f2 mu = pair(mu_n), rs = pair(rs_n);
+    float sc[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) sc[j] = CK ? sc_n[j] : 0.0f;
+    scalars(r + step);
+    if (ok) {
+      ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
+      if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
+    }
+    const uint8_t* stage = mine + st * q.stage_bytes;
+    f2 d[P], h[P], t1 = 0, t2 = 0;
+    smem_pairs<true, T, NV>(stage, col, in, d);  // zero beyond the row: nothing there counts
+    if constexpr (CK) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint2 w = *reinterpret_cast<const uint2*>(stage + off_x + col[j]);
+        ckpt_values4(w.x, sc[j], a.c.fmt, h + 4 * j);
+        ckpt_values4(w.y, sc[j], a.c.fmt, h + 4 * j + 2);
+      }
+    } else {
+      smem_pairs<false, T, NV>(stage + off_x, col, in, h);
+    }
+    if (!ok) h[0] = d[0] = pair(__int_as_float(0x7FC00000));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      h[i] = mul2(sub2(h[i], mu), rs);
+      ag[i] = fma2(d[i], h[i], ag[i]);
+      ab[i] = add2(ab[i], d[i]);
+      d[i] = mul2(d[i], g[i]);
+      t1 = add2(t1, d[i]);
+      t2 = fma2(d[i], h[i], t2);
+    }
+    float s[2] = {lo2(t1) + hi2(t1), lo2(t2) + hi2(t2)};
+    group_sum<G, 2>(s, red[grp][par], grp);
+    // every warp has read the row before this one
+    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+    if (dx) {
+      const f2 m1 = pair(-s[0] * inv), m2 = pair(-s[1] * inv);
+      f2 e[P];
+      if (dres) smem_pairs<false, T, NV>(stage + off_res, col, in, e);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const f2 t = fma2(h[i], m2, add2(d[i], m1));
+        h[i] = dres ? fma2(rs, t, e[i]) : mul2(rs, t);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (in[j]) put<T, 8>(dx + r * a.lddx + col[j], h, j);
+    }
+    prev = st;
+    if (++st == q.stages) st = 0, phase ^= 1;
+  }
+  if (!pg) return;
+  float* sums = reinterpret_cast<float*>(ring);
+  if constexpr (NG > 1) {
+    // group after group into shared memory (every copy has landed and been read), in order
+    __syncthreads();
+    for (int k = 0; k < NG; ++k) {
+      if (k == grp) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int c = int(col0) + (j * 32 + lane) * V + i;
-            sums[c] = (g ? sums[c] : 0.0f) + ag[j * V + i];
-            sums[C + c] = (g ? sums[C + c] : 0.0f) + ab[j * V + i];
+          for (int i = 0; i < 4; ++i) {
+            float2* p = reinterpret_cast<float2*>(sums + col64[j] + 2 * i);
+            float2* p2 = reinterpret_cast<float2*>(sums + C + col64[j] + 2 * i);
+            const float2 o = k ? *p : make_float2(0.0f, 0.0f), o2 = k ? *p2 : make_float2(0.0f, 0.0f);
+            *p = make_float2(o.x + lo2(ag[4 * j + i]), o.y + hi2(ag[4 * j + i]));
+            *p2 = make_float2(o2.x + lo2(ab[4 * j + i]), o2.y + hi2(ab[4 * j + i]));
           }
       }
       __syncthreads();
@@ -458,10 +826,9 @@ __global__ void __launch_bounds__(512, 1)
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t col = col0 + (j * 32 + lane) * V;
-      if (col < a.cols) {
-        put<float, V>(pg + int64_t(blockIdx.x) * a.cols + col, ag + j * V);
-        put<float, V>(pb + int64_t(blockIdx.x) * a.cols + col, ab + j * V);
+      if (in[j]) {
+        put<float, 8>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
+        put<float, 8>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
       }
     }
   }
@@ -476,35 +843,79 @@ int bwd_parts(int64_t rows) {
   return int(m > kMaxParts ? kMaxParts : m);
 }
 
-template <typename T, int V, int NV, int G>
+template <typename T, int V, int NV, int G, int R>
 cudaError_t run_fwd(const void* x, void* y, const FwdArgs& a, cudaStream_t st) {
-  constexpr int RB = G == 1 ? 4 : 1;
-  const int64_t blocks = (a.rows + RB - 1) / RB;
-  const unsigned grid = unsigned(blocks > 0x7FFFFFFF ? 0x7FFFFFFF : blocks);
-  norm_fwd_rows<T, V, NV, G><<<grid, G == 1 ? 128 : 32 * G, 0, st>>>(static_cast<const T*>(x),
-                                                                    static_cast<T*>(y), a);
+  constexpr int RB = G == 1 ? 4 * R : R;
+  norm_fwd_rows<T, V, NV, G, R><<<unsigned((a.rows + RB - 1) / RB), G == 1 ? 128 : 32 * G, 0, st>>>(
+      static_cast<const T*>(x), static_cast<T*>(y), a);
   return cudaGetLastError();
 }
+
+// the ring's stages for `groups` groups in `bytes` of shared memory; fewer than 3: no ring
+inline RingArgs make_ring(int stage_bytes, int row_bytes, int groups, int bytes) {
+  RingArgs q;
+  q.stage_bytes = (stage_bytes + 127) / 128 * 128;
+  q.row_bytes = row_bytes;
+  q.stages = bytes / (groups * q.stage_bytes);
+  if (q.stages > kMaxStages) q.stages = kMaxStages;
+  return q;
+}
+
+template <typename K>
+cudaError_t ring_smem(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+}
+
+template <typename T, int NV, int G, int NW, int MB>
+cudaError_t run_fwd_ring(const void* x, void* y, const FwdArgs& a, const RingArgs& q, cudaStream_t st) {
+  constexpr int NG = NW / G;
+  static const cudaError_t attr = ring_smem(norm_fwd_ring<T, NV, G, NW, MB>);
+  if (attr != cudaSuccess) return attr;
+  int64_t blocks = (a.rows + NG - 1) / NG;
+  if (blocks > MB * kSms) blocks = MB * kSms;
+  norm_fwd_ring<T, NV, G, NW, MB><<<unsigned(blocks), 32 * NW, size_t(NG) * q.stages * q.stage_bytes, st>>>(
+      static_cast<const T*>(x), static_cast<T*>(y), a, q);
+  return cudaGetLastError();
+}
+
+// Whether a ring serves [rows, cols]: enough rows that every group has several.
+// fwd: groups on the GPU; the ring's set-up costs about a microsecond
+inline bool ring_rows(int64_t rows, int64_t groups) { return rows >= 4 * groups; }
 
 template <typename T>
 cudaError_t launch_fwd(const void* x, void* y, const FwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
+  if (a.vec && a.pvec && c % 8 == 0 && a.cvec && c > 256 && c <= 8192) {
+    // 16 columns per lane; blocks of 8 warps, three per SM, or of 16 for the widest rows
+    const int G = c <= 512 ? 1 : c <= 1024 ? 2 : c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
+    const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : 3, row = int(c) * int(sizeof(T));
+    const RingArgs q = make_ring(row, row, nw / G, kRingBytes / mb);
+    if (q.stages >= 3 && ring_rows(a.rows, kSms * mb * (nw / G))) {
+      if (G == 1) return run_fwd_ring<T, 2, 1, 8, 3>(x, y, a, q, st);
+      if (G == 2) return run_fwd_ring<T, 2, 2, 8, 3>(x, y, a, q, st);
+      if (G == 4) return run_fwd_ring<T, 2, 4, 8, 3>(x, y, a, q, st);
+      if (G == 8) return run_fwd_ring<T, 2, 8, 8, 3>(x, y, a, q, st);
+      return run_fwd_ring<T, 2, 16, 16, 1>(x, y, a, q, st);
+    }
+  }
+  // one block per (few) rows: the grid has to hold them
+  const bool regs = a.rows <= 0x7FFFFFFF;
   // wide accesses need whole vectors: columns a multiple of 8 and every row aligned
-  if (a.vec && a.pvec && c % 8 == 0 && a.cvec) {
-    if (c <= 256) return run_fwd<T, 8, 1, 1>(x, y, a, st);
-    if (c <= 512) return run_fwd<T, 8, 2, 1>(x, y, a, st);
-    if (c <= 1024) return run_fwd<T, 8, 4, 1>(x, y, a, st);
-    if (c <= 2048) return run_fwd<T, 8, 2, 4>(x, y, a, st);
-    if (c <= 4096) return run_fwd<T, 8, 2, 8>(x, y, a, st);
-    if (c <= 8192) return run_fwd<T, 8, 4, 8>(x, y, a, st);
-    if (c <= 16384) return run_fwd<T, 8, 4, 16>(x, y, a, st);
-  } else {
-    if (c <= 256) return run_fwd<T, 1, 8, 1>(x, y, a, st);
-    if (c <= 512) return run_fwd<T, 1, 16, 1>(x, y, a, st);
-    if (c <= 1024) return run_fwd<T, 1, 16, 2>(x, y, a, st);
-    if (c <= 2048) return run_fwd<T, 1, 16, 4>(x, y, a, st);
-    if (c <= 4096) return run_fwd<T, 1, 16, 8>(x, y, a, st);
-    if (c <= 8192) return run_fwd<T, 1, 16, 16>(x, y, a, st);
+  if (regs && a.vec && a.pvec && c % 8 == 0 && a.cvec) {
+    if (c <= 256) return run_fwd<T, 8, 1, 1, 2>(x, y, a, st);
+    if (c <= 512) return run_fwd<T, 8, 2, 1, 1>(x, y, a, st);
+    if (c <= 1024) return run_fwd<T, 8, 2, 2, 2>(x, y, a, st);
+    if (c <= 2048) return run_fwd<T, 8, 2, 4, 2>(x, y, a, st);
+    if (c <= 4096) return run_fwd<T, 8, 2, 8, 2>(x, y, a, st);
+    if (c <= 8192) return run_fwd<T, 8, 2, 16, 2>(x, y, a, st);
+    if (c <= 16384) return run_fwd<T, 8, 4, 16, 1>(x, y, a, st);
+  } else if (regs) {
+    if (c <= 256) return run_fwd<T, 1, 8, 1, 2>(x, y, a, st);
+    if (c <= 512) return run_fwd<T, 1, 8, 2, 2>(x, y, a, st);
+    if (c <= 1024) return run_fwd<T, 1, 8, 4, 2>(x, y, a, st);
+    if (c <= 2048) return run_fwd<T, 1, 8, 8, 2>(x, y, a, st);
+    if (c <= 4096) return run_fwd<T, 1, 8, 16, 2>(x, y, a, st);
+    if (c <= 8192) return run_fwd<T, 1, 16, 16, 1>(x, y, a, st);
   }
   const unsigned grid = unsigned(a.rows > 0x7FFFFFFF ? 0x7FFFFFFF : a.rows);
   norm_fwd_kernel<T><<<grid, kT, 0, st>>>(static_cast<const T*>(x), static_cast<T*>(y), a);
@@ -520,15 +931,17 @@ struct BwdOut {
 template <typename T, int V, int NV, int G, bool PF>
 cudaError_t run_bwd(const void* dy, const void* x, const void* dres, const BwdOut& o, const BwdArgs& a,
                     cudaStream_t st) {
-  // rows per block: up to 16 warps, fewer when there are few rows
+  // rows per block: up to 32 warps (and 15 named barriers), fewer when there are few rows
+  constexpr int most = G == 1 ? 32 : (32 / G < 15 ? 32 / G : 15);
   int64_t ng = (a.rows + kSms - 1) / kSms;
-  if (ng > 16 / G) ng = 16 / G;
+  if (ng > most) ng = most;
   int64_t parts = (a.rows + ng - 1) / ng;
   if (parts > kSms) parts = kSms;
   const bool cols = o.dgamma || o.dbeta;
   float* pb = cols ? o.ws + size_t(parts) * size_t(a.cols) : nullptr;
   const size_t smem = ng > 1 && cols ? size_t(2) * 32 * G * NV * V * 4 : 0;  // 32 KiB at most
-  norm_bwd_rows<T, V, NV, G, PF><<<unsigned(parts), unsigned(32 * G * ng), smem, st>>>(
+  auto kernel = x ? norm_bwd_rows<T, V, NV, G, false, PF> : norm_bwd_rows<T, V, NV, G, true, PF>;
+  kernel<<<unsigned(parts), unsigned(32 * G * ng), smem, st>>>(
       static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const T*>(dres),
       static_cast<T*>(o.dx), cols ? o.ws : nullptr, pb, a);
   const cudaError_t e = cudaGetLastError();
@@ -536,22 +949,65 @@ cudaError_t run_bwd(const void* dy, const void* x, const void* dres, const BwdOu
   return launch_part_sums(o.ws, pb, int(parts), a.cols, o.dgamma, o.dbeta, o.accumulate, st);
 }
 
+template <typename T, int NV, int G, bool CK>
+cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const BwdOut& o,
+                         const BwdArgs& a, const RingArgs& q, cudaStream_t st) {
+  constexpr int NG = 16 / G;
+  static const cudaError_t attr = ring_smem(norm_bwd_ring<T, NV, G, CK>);
+  if (attr != cudaSuccess) return attr;
+  const bool cols = o.dgamma || o.dbeta;
+  int64_t parts = (a.rows + NG - 1) / NG;
+  if (parts > kSms) parts = kSms;
+  float* pb = cols ? o.ws + size_t(parts) * size_t(a.cols) : nullptr;
+  size_t smem = size_t(NG) * q.stages * q.stage_bytes;
+  if (NG > 1 && smem < size_t(2) * 32 * G * NV * 8 * 4) smem = size_t(2) * 32 * G * NV * 8 * 4;
+  norm_bwd_ring<T, NV, G, CK><<<unsigned(parts), 512, smem, st>>>(
+      static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const T*>(dres),
+      static_cast<T*>(o.dx), cols ? o.ws : nullptr, pb, a, q);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !cols) return e;
+  return launch_part_sums(o.ws, pb, int(parts), a.cols, o.dgamma, o.dbeta, o.accumulate, st);
+}
+
+template <typename T, int NV, int G>
+cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const BwdOut& o,
+                         const BwdArgs& a, const RingArgs& q, cudaStream_t st) {
+  return x ? run_bwd_ring<T, NV, G, false>(dy, x, dres, o, a, q, st)
+           : run_bwd_ring<T, NV, G, true>(dy, x, dres, o, a, q, st);
+}
+
 template <typename T>
 cudaError_t launch_bwd(const void* dy, const void* x, const void* dres, const BwdOut& o,
                        const BwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
+  // bulk copies: every row's bytes and its start a multiple of 16 (codes: columns)
+  if (a.vec && a.pvec && c % (x ? 8 : 16) == 0 && (x || al(a.c.codes, 16)) && c > 256 && c <= 8192) {
+    const int G = c <= 512 ? 1 : c <= 1024 ? 2 : c <= 2048 ? 4 : c <= 4096 ? 8 : 16;  // 16 columns per lane
+    const int row = int(c) * int(sizeof(T));
+    const RingArgs q = make_ring(row * (dres ? 2 : 1) + (x ? row : int(c)), row, 16 / G, kRingBytes);
+    if (q.stages >= 3 && ring_rows(a.rows, kSms * (16 / G))) {
+      if (G == 1) return run_bwd_ring<T, 2, 1>(dy, x, dres, o, a, q, st);
+      if (G == 2) return run_bwd_ring<T, 2, 2>(dy, x, dres, o, a, q, st);
+      if (G == 4) return run_bwd_ring<T, 2, 4>(dy, x, dres, o, a, q, st);
+      if (G == 8) return run_bwd_ring<T, 2, 8>(dy, x, dres, o, a, q, st);
+      return run_bwd_ring<T, 2, 16>(dy, x, dres, o, a, q, st);
+    }
+  }
   if (a.vec && a.pvec && c % 8 == 0 && a.cvec) {
-    if (c <= 512) return run_bwd<T, 8, 2, 1, sizeof(T) == 2>(dy, x, dres, o, a, st);
-    if (c <= 1024) return run_bwd<T, 8, 2, 2, sizeof(T) == 2>(dy, x, dres, o, a, st);
-    if (c <= 2048) return run_bwd<T, 8, 2, 4, sizeof(T) == 2>(dy, x, dres, o, a, st);
-    if (c <= 4096) return run_bwd<T, 8, 2, 8, sizeof(T) == 2>(dy, x, dres, o, a, st);
-    if (c <= 8192) return run_bwd<T, 8, 2, 16, sizeof(T) == 2>(dy, x, dres, o, a, st);
+    constexpr bool PF = sizeof(T) == 2;  // two binary32 rows do not fit the registers
+    if (c <= 256) return run_bwd<T, 8, 1, 1, PF>(dy, x, dres, o, a, st);
+    if (c <= 512) return run_bwd<T, 8, 1, 2, PF>(dy, x, dres, o, a, st);
+    if (c <= 1024) return run_bwd<T, 8, 1, 4, PF>(dy, x, dres, o, a, st);
+    if (c <= 2048) return run_bwd<T, 8, 1, 8, PF>(dy, x, dres, o, a, st);
+    if (c <= 4096) return run_bwd<T, 8, 1, 16, PF>(dy, x, dres, o, a, st);
+    if (c <= 8192) return run_bwd<T, 8, 1, 32, PF>(dy, x, dres, o, a, st);
   } else {
-    if (c <= 256) return run_bwd<T, 1, 8, 1, true>(dy, x, dres, o, a, st);
-    if (c <= 512) return run_bwd<T, 1, 8, 2, true>(dy, x, dres, o, a, st);
-    if (c <= 1024) return run_bwd<T, 1, 8, 4, true>(dy, x, dres, o, a, st);
-    if (c <= 2048) return run_bwd<T, 1, 8, 8, true>(dy, x, dres, o, a, st);
-    if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(dy, x, dres, o, a, st);
+    if (c <= 128) return run_bwd<T, 1, 4, 1, true>(dy, x, dres, o, a, st);
+    if (c <= 512) return run_bwd<T, 1, 4, 4, true>(dy, x, dres, o, a, st);
+    if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(dy, x, dres, o, a, st);
+    if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(dy, x, dres, o, a, st);
+    if (c <= 4096) return run_bwd<T, 1, 4, 32, true>(dy, x, dres, o, a, st);
+    if (c <= 8192) return run_bwd<T, 1, 8, 32, false>(dy, x, dres, o, a, st);
   }
   const T *tdy = static_cast<const T*>(dy), *tx = static_cast<const T*>(x);
   if (o.dx) {
