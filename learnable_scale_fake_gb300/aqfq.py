@@ -134,10 +134,16 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it, where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(fn, status):
@@ -327,34 +333,36 @@ def _mat(t, name, dtypes, shape=None):
     """(address, leading dimension) of a matrix; None gives (None, 0)."""
     if t is None:
         return None, 0
+    size = t.shape
+    if t.dtype in dtypes and t.is_cuda and len(size) == 2 and (shape is None or size == shape):
+        ld, inner = t.stride()
+        if inner == 1 or size[1] <= 1:
+            # a single row has no second one: a leading dimension that every check accepts
+            return t.data_ptr(), ld if size[0] > 1 else (size[1] + 7) // 8 * 8
+    _refuse_mat(t, name, dtypes, shape)
+
+
+def _refuse_mat(t, name, dtypes, shape):
     if not t.is_cuda:
         raise ValueError("aqfq works on CUDA tensors only")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a matrix with contiguous columns")
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    rows, cols = t.shape
-    return t.data_ptr(), t.stride(0) if rows > 1 else _ld_of_one_row(cols)
-
-
-def _ld_of_one_row(cols):
-    """A single row has no second one: a leading dimension that every check accepts."""
-    return (cols + 7) // 8 * 8
+    raise ValueError(f"{name} must be a matrix with contiguous columns")
 
 
 def _vec(t, name, dtypes, n):
     """Address of a contiguous vector of n elements, or None."""
     if t is None:
         return None
+    if t.dtype in dtypes and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("aqfq works on CUDA tensors only")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must have {n} contiguous elements")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have {n} contiguous elements")
 
 
 _ROWS = (torch.bfloat16, torch.float32)
@@ -370,7 +378,9 @@ def _dt(t):
 def _ws(workspace):
     if workspace is None:
         return None, 0
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        _ptr(workspace)  # refuses
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _flag(t):
@@ -384,10 +394,11 @@ def ckpt8(fmt, group, codes, scale) -> Ckpt8:
     if codes.dim() != 2 or group <= 0:
         raise ValueError("codes must be [rows, cols] and group positive")
     rows, cols = codes.shape
-    if tuple(scale.shape) != (rows, -(-cols // group)):
+    if scale.shape != (rows, -(-cols // group)):
         raise ValueError("scale must be [rows, ceil(cols / group)]")
     c = Ckpt8(fmt, group, _ptr(codes), _ptr(scale))
     c.tensors = (codes, scale)
+    c.size = (rows, cols)
     return c
 
 
@@ -395,7 +406,7 @@ def _ck(c, rows, cols):
     """Pointer to the checkpoint of a [rows, cols] matrix, or None."""
     if c is None:
         return None
-    if tuple(c.tensors[0].shape) != (rows, cols):
+    if c.size != (rows, cols):
         raise ValueError(f"the checkpoint must be of a [{rows}, {cols}] matrix")
     return ctypes.byref(c)
 
