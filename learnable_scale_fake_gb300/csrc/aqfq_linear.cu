@@ -53,16 +53,16 @@ __device__ __forceinline__ void load_bias4(const Epi& e, int64_t col, float (&b)
   }
 }
 
-// v[j]: the sums of row r + j, columns [col, col + 4); every lane of the warp
+// v[j]: the sums of row r + j < rend, columns [col, col + 4); every lane of the warp
 // calls it.  What the rows read is fetched for all of them first.
 template <int PASS, int R>
-__device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t col,
+__device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t rend, int64_t col,
                                           const float (&bias)[4], float (&v)[R][4]) {
   const int n = e.cols - col > 4 ? 4 : int(e.cols - col);
   const bool full = n == 4;
   bool in[R];
 #pragma unroll
-  for (int j = 0; j < R; ++j) in[j] = r + j < e.rows && n > 0;
+  for (int j = 0; j < R; ++j) in[j] = r + j < rend && n > 0;
   float add[R][4];
   uint32_t code[R][1];
   float cs[R];
@@ -189,32 +189,8 @@ __device__ __forceinline__ Seg seg(const void* p, bool whole) {
   return {whole && (a & 31) == 0, whole && (a & 15) == 0};
 }
 
-// 16 columns of a bias vector (the same for every lane)
-__device__ __forceinline__ void bias16(const Epi& e, int64_t col, int n, float (&b)[16]) {
-  if (e.bias_dtype == AQFQ_BF16) {
-    const bf16* p = static_cast<const bf16*>(e.bias) + col;
-    uint32_t w[8];
-    ld16(p, false, seg(p, n >= 16).a16, n, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[2 * i] = bf_lo(w[i]), b[2 * i + 1] = bf_hi(w[i]);
-  } else {
-    const float* p = static_cast<const float*>(e.bias) + col;
-    const bool a16 = seg(p, n >= 16).a16;
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      if (a16) {
-        const float4 f = *reinterpret_cast<const float4*>(p + i);
-        b[i] = f.x, b[i + 1] = f.y, b[i + 2] = f.z, b[i + 3] = f.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[i + j] = i + j < n ? p[i + j] : 0.0f;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void tmem16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 16 accumulator columns of the lane's row: issued, then waited for
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[16]) {
   __syncwarp();  // the load is a warp-wide instruction
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -224,98 +200,126 @@ __device__ __forceinline__ void tmem16(uint32_t taddr, float (&v)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-  sm100::tc_wait_ld();
+}
+// (the registers pass through, so that no use moves above the wait)
+__device__ __forceinline__ void tmem_take(uint32_t (&r)[16], float (&v)[16]) {
+  __syncwarp();
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Columns [col, col + 16 * chunks) of row r (one row per lane of the warp; chunks
+// What 16 columns of a row read besides the sums: the residual, the previous
+// output of an accumulation, or the checkpoint's codes.
+template <int PASS>
+struct ChunkIn {
+  uint32_t w[PASS == P_WGRAD ? 16 : 8];
+  uint32_t code[4];
+  float scale;
+  __device__ __forceinline__ void load(const Epi& e, int64_t r, int64_t cc, bool codes) {
+    const int64_t left = e.cols - cc;
+    const int n = left > 16 ? 16 : int(left);
+    if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
+      if (e.accumulate) {
+        const float* p = static_cast<const float*>(e.out) + r * e.ldo + cc;
+        const bool a16 = seg(p, n == 16).a16;
+#pragma unroll
+        for (int i = 0; i < (PASS == P_WGRAD ? 16 : 0); i += 4) {
+          if (a16) {
+            const uint4 f = *reinterpret_cast<const uint4*>(p + i);
+            w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i + j] = i + j < n ? __float_as_uint(p[i + j]) : 0u;
+          }
+        }
+      }
+    } else if (PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr) {
+      const bf16* p = PASS == P_WGRAD ? static_cast<const bf16*>(e.out) + r * e.ldo + cc
+                                      : e.res + r * e.ldr + cc;
+      const Seg s = seg(p, n == 16);
+      uint32_t t[8];
+      ld16(p, s.a32, s.a16, n, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = t[i];
+    }
+    if (codes) {
+      const uint8_t* p = e.c.codes + r * e.cols + cc;
+      if (seg(p, n == 16).a16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        code[0] = u.x, code[1] = u.y, code[2] = u.z, code[3] = u.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) code[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+      }
+      scale = e.c.scale[r * e.c.groups + (cc >> e.c.lg)];
+    }
+  }
+};
+
+// Columns [col, col + 16 chunks) of row r (one row per lane of the warp; chunks
 // * 16 a multiple of the checkpoint's group), sums at taddr.  `in`: the row
-// exists.  Every lane of the warp calls it.
+// exists.  Every lane of the warp calls it.  sb: the columns' bias in shared
+// memory.  nx holds the first chunk's inputs (loaded before the accumulators were
+// waited for); the next chunk's inputs and sums are under way while one is computed.
 template <int PASS, int ACT>
 __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col, int chunks,
-                                             uint32_t taddr) {
-  const int gch = PASS == P_FWD && e.c.codes ? 1 << (e.c.lg - 4) : 1;  // chunks per group
+                                             uint32_t taddr, const float* sb, ChunkIn<PASS>& nx) {
+  constexpr bool CODES_IN = PASS == P_DGRAD && ACT != AQFQ_ACT_NONE;
+  const bool codes_out = PASS == P_FWD && e.c.codes;
   const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
+  const int64_t avail = (e.cols - col + 15) / 16;
+  const int nch = avail < chunks ? int(avail) : chunks;
+  const int gch = codes_out ? 1 << (e.c.lg - 4) : nch;  // chunks per group
+  uint32_t t[16];
+  float v[16];
 #pragma unroll 1
-  for (int g = 0; g < chunks && col + g * 16 < e.cols; g += gch) {
+  for (int g = 0; g < nch; g += gch) {
+    const int end = g + gch < nch ? g + gch : nch;
     Divisor div = {};
-    if (PASS == P_FWD && e.c.codes) {
+    if (codes_out) {
       uint32_t m = 0;
+      tmem_issue(taddr + uint32_t(g * 16), t);
 #pragma unroll 1
-      for (int c = g; c < g + gch; ++c) {
-        float v[16], b[16];
-        tmem16(taddr + uint32_t(c * 16), v);
+      for (int c = g; c < end; ++c) {
+        tmem_take(t, v);
+        if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
         const int64_t left = e.cols - (col + c * 16);
-        const int n = left > 16 ? 16 : int(left);
-        if (n <= 0) break;  // uniform
         if (e.bias) {
-          bias16(e, col + c * 16, n, b);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += b[i];
+          for (int i = 0; i < 16; ++i) v[i] += sb[c * 16 + i];
         }
+        if (left < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? v[i] : 0.0f;
+          for (int i = 0; i < 16; ++i) v[i] = i < left ? v[i] : 0.0f;
+        }
         m = max(m, amax_bits(v));
       }
       div = ckpt_divisor(m, e.c.fmt);
       if (in) e.c.scale[r * e.c.groups + ((col + g * 16) >> e.c.lg)] = div.s;
     }
+    tmem_issue(taddr + uint32_t(g * 16), t);
 #pragma unroll 1
-    for (int c = g; c < g + gch; ++c) {
+    for (int c = g; c < end; ++c) {
       const int64_t cc = col + c * 16;
       const int64_t left = e.cols - cc;
       const int n = left > 16 ? 16 : int(left);
-      if (n <= 0) break;  // uniform
-      // what the row reads, before the accumulators are waited for
-      uint32_t aw[8], cw[4];
-      float af[PASS == P_WGRAD ? 16 : 1], cs = 0.0f;
-      if (adds && in) {
-        if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
-          const float* p = static_cast<const float*>(e.out) + r * e.ldo + cc;
-          const bool a16 = seg(p, n == 16).a16;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            if (a16) {
-              const float4 f = *reinterpret_cast<const float4*>(p + i);
-              if constexpr (PASS == P_WGRAD) af[i] = f.x, af[i + 1] = f.y, af[i + 2] = f.z, af[i + 3] = f.w;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if constexpr (PASS == P_WGRAD) af[i + j] = i + j < n ? p[i + j] : 0.0f;
-            }
-          }
-        } else {
-          const bf16* p = PASS == P_WGRAD ? static_cast<const bf16*>(e.out) + r * e.ldo + cc
-                                          : e.res + r * e.ldr + cc;
-          const Seg s = seg(p, n == 16);
-          ld16(p, s.a32, s.a16, n, aw);
-        }
-      }
-      if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE && in) {
-        const uint8_t* p = e.c.codes + r * e.cols + cc;
-        if (seg(p, n == 16).a16) {
-          const uint4 u = *reinterpret_cast<const uint4*>(p);
-          cw[0] = u.x, cw[1] = u.y, cw[2] = u.z, cw[3] = u.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cw[i] = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < n) cw[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
-        }
-        cs = e.c.scale[r * e.c.groups + (cc >> e.c.lg)];
-      }
-      float v[16];
-      tmem16(taddr + uint32_t(c * 16), v);
+      const ChunkIn<PASS> cur = nx;
+      if (c + 1 < nch && in) nx.load(e, r, cc + 16, CODES_IN);
+      tmem_take(t, v);
+      if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
       if (PASS == P_FWD) {
         if (e.bias) {
-          float b[16];
-          bias16(e, cc, n, b);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += b[i];
+          for (int i = 0; i < 16; ++i) v[i] += sb[c * 16 + i];
         }
-        if (e.c.codes && in) {
+        if (codes_out && in) {
           uint32_t w[4];
           f2 x[8];
 #pragma unroll
@@ -332,43 +336,44 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
         }
         act_all<ACT>(v);
       }
-      if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) {
+      if (CODES_IN) {
         float p[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ckpt_values4(cw[i], cs, e.c.fmt, p + 4 * i);
+        for (int i = 0; i < 4; ++i) ckpt_values4(cur.code[i], cur.scale, e.c.fmt, p + 4 * i);
         slope_all<ACT>(p, v);
       }
-      if (!in) continue;
-      if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
-        float* p = static_cast<float*>(e.out) + r * e.ldo + cc;
-        const bool a16 = seg(p, n == 16).a16;
-        if constexpr (PASS == P_WGRAD) {
+      if (in) {
+        if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
+          float* p = static_cast<float*>(e.out) + r * e.ldo + cc;
+          const bool a16 = seg(p, n == 16).a16;
+          if constexpr (PASS == P_WGRAD) {
+            if (adds) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(cur.w[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            if (a16) {
+              *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (i + j < n) p[i + j] = v[i + j];
+            }
+          }
+        } else {
           if (adds) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += af[i];
+            for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(cur.w[i]), v[2 * i + 1] += bf_hi(cur.w[i]);
           }
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+          bf16* p = static_cast<bf16*>(e.out) + r * e.ldo + cc;
+          const Seg q = seg(p, n == 16);
+          st16(p, q.a32, q.a16, n, w);
         }
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          if (a16) {
-            *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (i + j < n) p[i + j] = v[i + j];
-          }
-        }
-      } else {
-        if (adds) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(aw[i]), v[2 * i + 1] += bf_hi(aw[i]);
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
-        bf16* p = static_cast<bf16*>(e.out) + r * e.ldo + cc;
-        const Seg s = seg(p, n == 16);
-        st16(p, s.a32, s.a16, n, w);
       }
     }
   }
@@ -395,14 +400,18 @@ constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
 template <int BN>
 struct Cfg {
-  static constexpr int STAGES = BN == 256 ? 7 : 9;
+  static constexpr int STAGES = 6;
   static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
   static constexpr uint32_t STAGE = kABytes + B_BYTES;
-  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 256;
+  static constexpr uint32_t BIAS = kEpiWarps * (BN / 2) * 4;  // a warp's columns
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + BIAS + 256;
+  // a split tile's partial sums (one row per 16-byte odd stride) reuse the stages
+  static constexpr int PSTRIDE = BN + 4;
+  static_assert(size_t(kHalf) * PSTRIDE * 4 <= size_t(STAGES) * STAGE, "partial sums fit the stages");
 };
 
 struct __align__(8) PairShared {
-  uint64_t full[9], empty[9];  // TMA bytes of both CTAs (leader) / MMA commit
+  uint64_t full[6], empty[6];  // TMA bytes of both CTAs (leader) / MMA commit
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -428,8 +437,11 @@ __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& 
   tc = in / gm;
 }
 
-template <int PASS, int ACT, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
+// SPLIT: a cluster of S pairs takes one tile, pair i the i-th slice of the inner
+// axis; the partial sums meet through distributed shared memory, each CTA finishing
+// its share of the rows (one launch, no scratch; the sums in the slices' order).
+template <int PASS, int ACT, int BN, bool SPLIT>
+__global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
   using C = Cfg<BN>;
@@ -438,11 +450,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sb = smem + C::STAGES * kABytes;
-  PairShared* sh = reinterpret_cast<PairShared*>(sb + C::STAGES * C::B_BYTES);
+  float* sbias = reinterpret_cast<float*>(sb + C::STAGES * C::B_BYTES);
+  PairShared* sh = reinterpret_cast<PairShared*>(reinterpret_cast<uint8_t*>(sbias) + C::BIAS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int tiles = a.nr * a.nc, units = tiles * a.splits;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
+  const int tiles = a.nr * a.nc, units = SPLIT ? tiles : tiles * a.splits;
+  // one unit per cluster, or a strided share of the units per pair
+  const int pair = SPLIT ? blockIdx.x / (2 * a.splits) : blockIdx.x >> 1;
+  const int npairs = SPLIT ? units : gridDim.x >> 1;
+  const int slice = int(crank >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -474,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       for (int u = pair; u < units && ok; u += npairs) {
         int tr, tc;
         tile_of(a, u % tiles, tr, tc);
-        const int sp = u / tiles;
+        const int sp = SPLIT ? slice : u / tiles;
         const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
         const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
@@ -486,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
             ok = false;
             break;
           }
-          const uint32_t bar = peer_addr(smem_u32(&sh->full[s]), 0);
+          const uint32_t bar = peer_addr(smem_u32(&sh->full[s]), lead);
           if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * C::STAGE);
           const uint32_t da = smem_u32(smem + s * kABytes), db = smem_u32(sb + s * C::B_BYTES);
           if constexpr (A_MN) {
@@ -524,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += npairs, ++n) {
-        const int sp = u / tiles;
+        const int sp = SPLIT ? slice : u / tiles;
         const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
         const int buf = n & 1;
@@ -545,8 +561,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
             tc_mma_f16_pair(d, da, db, idesc, k > k0 ? 1u : 0u);
 #pragma unroll
             for (int kk = 1; kk < kBK / 16; ++kk) tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, 1u);
-            tc_commit_pair(&sh->empty[s]);
-            if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf]);
+            tc_commit_pair(&sh->empty[s], lead);
+            if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf], lead);
           }
           __syncwarp();
           if (++s == C::STAGES) {
@@ -557,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       }
       if (!ok) {  // a wait timed out: drain the MMAs already issued
         *abort = 1;
-        if (elect_one()) tc_commit_pair(&sh->drain);
+        if (elect_one()) tc_commit_pair(&sh->drain, lead);
         __syncwarp();
         mbar_wait_suspend(&sh->drain, 0);
       }
@@ -565,11 +581,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     constexpr int W = BN / 2;  // columns of this warp
+    float* mybias = sbias + (warp - 4) * W;
     int n = 0;
     for (int u = pair; u < units; u += npairs, ++n) {
       int tr, tc;
       tile_of(a, u % tiles, tr, tc);
       const int buf = n & 1;
+      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
+      const int64_t col = int64_t(tc) * BN + half * W;
+      const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
+      ChunkIn<PASS> first;
+      if (live && whole) {
+        if (PASS == P_FWD && e.bias) {
+          float b[4];
+          __syncwarp();
+          if (lane * 4 < W) {
+            load_bias4(e, col + lane * 4, b);
+            *reinterpret_cast<float4*>(mybias + lane * 4) = make_float4(b[0], b[1], b[2], b[3]);
+          }
+          __syncwarp();
+        }
+        if (r < e.rows) first.load(e, r, col, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
+      }
       bool ok = true;
       if (lane == 0) {
         ok = mbar_wait_suspend(&sh->tfull[buf], (n >> 1) & 1) && !*abort;
@@ -578,16 +611,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
       ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       tc_fence_after_sync();
-      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
-      const int64_t col = int64_t(tc) * BN + half * W;
       const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + half * W);
-      if (r0 < e.rows && col < e.cols) {
-        if (a.splits > 1) {
+      if (live) {
+        if (SPLIT) {
+          // into this CTA's shared memory (its stages are all consumed)
+          float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * C::PSTRIDE + half * W;
+          uint32_t t[16];
+          float v[16];
+          tmem_issue(taddr, t);
+#pragma unroll 1
+          for (int c = 0; c < W / 16; ++c) {
+            tmem_take(t, v);
+            if (c + 1 < W / 16) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        } else if (a.splits > 1) {
           float* dst = a.part + (int64_t(u / tiles) * e.rows + r) * a.cols4 + col;
+          uint32_t t[16];
+          float v[16];
 #pragma unroll 1
           for (int c = 0; c < W / 16 && col + c * 16 < e.cols; ++c) {
-            float v[16];
-            tmem16(taddr + uint32_t(c * 16), v);
+            tmem_issue(taddr + uint32_t(c * 16), t);
+            tmem_take(t, v);
             if (r < e.rows) {
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
@@ -597,12 +644,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
             }
           }
         } else {
-          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr);
+          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr, mybias, first);
         }
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), 0));
+      if (!SPLIT && lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), lead));
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync();  // every slice's partial sums are in shared memory
+    if (warp >= 4) {
+      int tr, tc;
+      tile_of(a, pair, tr, tc);
+      const int half = (warp - 4) & 1, rend = kHalf * (slice + 1) / a.splits;
+      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
+      const int64_t col = int64_t(tc) * BN + half * (BN / 2) + lane * 4;
+      float bias[4] = {};
+      if (PASS == P_FWD) load_bias4(e, col, bias);
+      const int64_t last = r0 + rend < e.rows ? r0 + rend : e.rows;
+      if (int64_t(tc) * BN + half * (BN / 2) < e.cols) {
+        // four rows of 128 columns per warp and turn
+        for (int row = kHalf * slice / a.splits + ((warp - 4) >> 1) * 4; row < rend && r0 + row < last;
+             row += 4 * (kEpiWarps / 2)) {
+          float v[4][4] = {};
+          const uint32_t mine = smem_u32(smem) + uint32_t(row * C::PSTRIDE + half * (BN / 2) + lane * 4) * 4;
+          for (int sl = 0; sl < a.splits; ++sl) {
+            const uint32_t base = peer_addr(mine, uint32_t(2 * sl) + rank);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (row + j >= rend) continue;
+              float4 f;
+              asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                           : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                           : "r"(base + uint32_t(j * C::PSTRIDE * 4)));
+              v[j][0] += f.x, v[j][1] += f.y, v[j][2] += f.z, v[j][3] += f.w;
+            }
+          }
+          epilogue4<PASS, 4>(e, r0 + row, last, col, bias, v);
+        }
+      }
     }
   }
   tc_fence_before_sync();
@@ -633,7 +715,7 @@ __global__ void __launch_bounds__(256)
         v[0][0] += f.x, v[0][1] += f.y, v[0][2] += f.z, v[0][3] += f.w;
       }
     }
-    epilogue4<PASS, 1>(e, r, col, bias, v);
+    epilogue4<PASS, 1>(e, r, e.rows, col, bias, v);
   }
 }
 
@@ -678,49 +760,59 @@ bool encode(CUtensorMap* tm, const Operand& o, unsigned box0, unsigned box1) {
 
 // How a product of rows x cols over `depth` is cut.
 struct Plan {
-  int bn;         // columns per tile
   int nr, nc;     // tiles
   int ksteps;
-  int splits;
+  int splits;     // slices of the inner axis
+  bool cluster;   // joined in a cluster; else through scratch and finish_kernel
   int64_t cols4;
-  size_t bytes;   // partial sums
+  size_t bytes;   // scratch
 };
 
 constexpr int kPairs = 76;  // SM pairs
+constexpr int kBN = 256;
 
+// Fewer tiles than half the SM pairs: the inner axis is split.  Up to four slices
+// join in a cluster (8 CTAs, the portable size); a long inner axis with very few
+// tiles takes more slices through scratch.
 Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   Plan p;
-  p.bn = 256;
   p.nr = int((rows + kRows - 1) / kRows);
-  p.nc = int((cols + p.bn - 1) / p.bn);
+  p.nc = int((cols + kBN - 1) / kBN);
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
+  p.cluster = false;
   const int64_t tiles = int64_t(p.nr) * p.nc;
-  if (tiles * 2 <= kPairs && p.ksteps >= 16) {
-    int64_t s = kPairs / tiles;
-    if (s > p.ksteps / 8) s = p.ksteps / 8;
-    if (s > 8) s = 8;
-    p.splits = int(s);
+  if (tiles <= 9 && p.ksteps >= 128) {
+    p.splits = int(kPairs / tiles < p.ksteps / 16 ? kPairs / tiles : p.ksteps / 16);
+  } else if (tiles <= kPairs / 2 && p.ksteps >= 4) {
+    p.splits = tiles <= 16 ? 4 : tiles <= 24 ? 3 : 2;
+    if (p.splits > p.ksteps / 2) p.splits = p.ksteps / 2;
+    p.cluster = p.splits > 1;
   }
   p.cols4 = (cols + 3) / 4 * 4;
-  p.bytes = p.splits > 1 ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
+  p.bytes = p.splits > 1 && !p.cluster ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
   return p;
 }
 
-template <int PASS, int ACT, int BN>
+template <int PASS, int ACT, bool SPLIT>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(pair_kernel<PASS, ACT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(Cfg<BN>::SMEM));
-  });
+  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
   if (attr != cudaSuccess) return attr;
-  const int64_t units = int64_t(a.nr) * a.nc * a.splits;
-  const unsigned pairs = unsigned(units < kPairs ? units : kPairs);
-  pair_kernel<PASS, ACT, BN><<<2 * pairs, kThreadsP, Cfg<BN>::SMEM, st>>>(ta, tb, a, e);
-  return cudaGetLastError();
+  const int64_t tiles = int64_t(a.nr) * a.nc, units = tiles * a.splits;
+  cudaLaunchConfig_t cfg = {};
+  const int csize = SPLIT ? 2 * a.splits : 2;
+  cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < kPairs ? units : kPairs));
+  cfg.blockDim = dim3(kThreadsP);
+  cfg.dynamicSmemBytes = Cfg<kBN>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(csize), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, a, e);
 }
 
 // out[r, c] = epilogue(sum over k of A(r, k) B(c, k)); A, B as stored
@@ -738,23 +830,29 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     CUtensorMap ta, tb;
     constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
     if (!encode(&ta, A, kBK, A_MN ? kBK : kHalf) ||
-        !encode(&tb, B, kBK, B_MN ? kBK : unsigned(p.bn / 2)))
+        !encode(&tb, B, kBK, B_MN ? kBK : unsigned(kBN / 2)))
       return AQFQ_ERR_CUDA;
     PairArgs a = {p.nr, p.nc, p.splits, p.ksteps, part, p.cols4, err};
     cudaError_t r;
-    // split products leave the epilogue to finish_kernel
-    switch (PASS == P_WGRAD || p.splits > 1 ? AQFQ_ACT_NONE : e.act) {
-      case AQFQ_ACT_RELU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_RELU, 256>(ta, tb, a, e, st); break;
-      case AQFQ_ACT_GELU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_GELU, 256>(ta, tb, a, e, st); break;
-      case AQFQ_ACT_GELU_TANH:
-        r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_GELU_TANH, 256>(ta, tb, a, e, st);
-        break;
-      case AQFQ_ACT_SILU: r = launch_pair<PASS, PASS == P_WGRAD ? 0 : AQFQ_ACT_SILU, 256>(ta, tb, a, e, st); break;
-      default: r = launch_pair<PASS, AQFQ_ACT_NONE, 256>(ta, tb, a, e, st); break;
+    if (p.cluster) {
+      r = launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st);
+    } else if (PASS == P_WGRAD || p.splits > 1) {  // finish_kernel has the epilogue, or it is plain
+      r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
+    } else {
+      constexpr bool W = PASS == P_WGRAD;  // (instantiated once)
+      switch (e.act) {
+        case AQFQ_ACT_RELU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_RELU, false>(ta, tb, a, e, st); break;
+        case AQFQ_ACT_GELU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_GELU, false>(ta, tb, a, e, st); break;
+        case AQFQ_ACT_GELU_TANH:
+          r = launch_pair<PASS, W ? 0 : AQFQ_ACT_GELU_TANH, false>(ta, tb, a, e, st);
+          break;
+        case AQFQ_ACT_SILU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_SILU, false>(ta, tb, a, e, st); break;
+        default: r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st); break;
+      }
     }
     if (r != cudaSuccess) return AQFQ_ERR_CUDA;
   }
-  if (p.splits != 1) {
+  if (p.splits != 1 && !p.cluster) {
     const int64_t gy = (e.rows + 7) / 8;
     finish_kernel<PASS><<<dim3(unsigned((e.cols + 127) / 128), unsigned(gy > 65535 ? 65535 : gy)), 256,
                           0, st>>>(part, p.splits, p.cols4, e);

@@ -78,12 +78,12 @@ __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t a_desc
       : "memory");
 }
 // when the prior MMAs are complete: one arrival on the mbarrier at this offset in
-// both CTAs
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+// both CTAs of the pair whose leader has cluster rank `lead`
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint32_t lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(uint16_t(3))
+      "h"(uint16_t(3u << lead))
       : "memory");
 }
 
