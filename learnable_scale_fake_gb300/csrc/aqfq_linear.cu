@@ -653,37 +653,47 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
   }
   if constexpr (SPLIT) {
+    // this CTA's rows of the tile; a warp takes half the columns of R rows per turn
+    constexpr int R = 2, NW = kThreadsP / 32;
+    int tr, tc;
+    tile_of(a, pair, tr, tc);
+    const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
+    const int nrows = e.rows - r0 > kHalf ? kHalf : (e.rows > r0 ? int(e.rows - r0) : 0);
+    const int half = warp & 1, rend = nrows * (slice + 1) / a.splits;
+    const int64_t col = int64_t(tc) * BN + half * (BN / 2) + lane * 4;
+    float bias[4] = {};
+    if (PASS == P_FWD) load_bias4(e, col, bias);
     __syncwarp();
     cluster_sync();  // every slice's partial sums are in shared memory
-    if (warp >= 4) {
-      int tr, tc;
-      tile_of(a, pair, tr, tc);
-      const int half = (warp - 4) & 1, rend = kHalf * (slice + 1) / a.splits;
-      const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
-      const int64_t col = int64_t(tc) * BN + half * (BN / 2) + lane * 4;
-      float bias[4] = {};
-      if (PASS == P_FWD) load_bias4(e, col, bias);
-      const int64_t last = r0 + rend < e.rows ? r0 + rend : e.rows;
-      if (int64_t(tc) * BN + half * (BN / 2) < e.cols) {
-        // four rows of 128 columns per warp and turn
-        for (int row = kHalf * slice / a.splits + ((warp - 4) >> 1) * 4; row < rend && r0 + row < last;
-             row += 4 * (kEpiWarps / 2)) {
-          float v[4][4] = {};
-          const uint32_t mine = smem_u32(smem) + uint32_t(row * C::PSTRIDE + half * (BN / 2) + lane * 4) * 4;
-          for (int sl = 0; sl < a.splits; ++sl) {
+    if (int64_t(tc) * BN + half * (BN / 2) < e.cols) {
+#pragma unroll 1
+      for (int row = nrows * slice / a.splits + (warp >> 1) * R; row < rend; row += R * (NW / 2)) {
+        // every slice's values are on their way before the first is added
+        float4 f[8][R];
+        const uint32_t mine = smem_u32(smem) + uint32_t(row * C::PSTRIDE + half * (BN / 2) + lane * 4) * 4;
+#pragma unroll
+        for (int sl = 0; sl < 8; ++sl) {
+          if (sl < a.splits) {
             const uint32_t base = peer_addr(mine, uint32_t(2 * sl) + rank);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (row + j >= rend) continue;
-              float4 f;
+            for (int j = 0; j < R; ++j)  // (a row past rend is another CTA's: read, not used)
               asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                           : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-                           : "r"(base + uint32_t(j * C::PSTRIDE * 4)));
-              v[j][0] += f.x, v[j][1] += f.y, v[j][2] += f.z, v[j][3] += f.w;
-            }
+                           : "=f"(f[sl][j].x), "=f"(f[sl][j].y), "=f"(f[sl][j].z), "=f"(f[sl][j].w)
+                           : "r"(base + uint32_t((row + j < kHalf ? j : 0) * C::PSTRIDE * 4)));
           }
-          epilogue4<PASS, 4>(e, r0 + row, last, col, bias, v);
         }
+        float v[R][4];
+#pragma unroll
+        for (int j = 0; j < R; ++j) v[j][0] = f[0][j].x, v[j][1] = f[0][j].y, v[j][2] = f[0][j].z, v[j][3] = f[0][j].w;
+#pragma unroll
+        for (int sl = 1; sl < 8; ++sl) {
+          if (sl < a.splits) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+              v[j][0] += f[sl][j].x, v[j][1] += f[sl][j].y, v[j][2] += f[sl][j].z, v[j][3] += f[sl][j].w;
+          }
+        }
+        epilogue4<PASS, R>(e, r0 + row, r0 + rend, col, bias, v);
       }
     }
   }
@@ -693,6 +703,210 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (warp == 2) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
+}
+
+// ---------------------------------------------------------------------------
+// small products: one CTA per 128 x 128 tile and slice of the inner axis, the S
+// slices of a tile in a cluster.  Six stages of 32 KiB; warp 0 issues the loads, warp
+// 1 the MMAs; then all eight warps move the accumulators to shared memory (the
+// stages are consumed), the cluster meets, and each CTA finishes its share of the
+// rows that exist: a warp takes whole rows of 128 columns, reads every slice's
+// value through distributed shared memory and adds them in the slices' order.
+// Few rows (a token or two): the weight is streamed once by tiles x S CTAs.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 128;
+constexpr int kStagesC = 6;
+constexpr int kStrideC = kTile + 4;  // floats per row of partial sums
+constexpr size_t kSmemC = 1024 + size_t(kStagesC) * 2 * kABytes + 256;
+static_assert(size_t(kTile) * kStrideC * 4 <= size_t(kStagesC) * 2 * kABytes, "partial sums fit the stages");
+
+struct __align__(8) CtaShared {
+  uint64_t full[kStagesC], empty[kStagesC];
+  uint64_t accum;
+  uint32_t tmem;
+  int32_t abort;
+};
+
+template <int PASS>
+__global__ void __launch_bounds__(256, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const PairArgs a, const Epi e) {
+  constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+  constexpr int R = 2;  // rows per warp and turn
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  CtaShared* sh = reinterpret_cast<CtaShared*>(smem + kStagesC * 2 * kABytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = int(cluster_rank());
+  const int tile = blockIdx.x / a.splits;
+  // tiles column by column: neighbours share their columns' operand
+  const int tr = tile % a.nr, tc = tile / a.nr;
+  const int64_t r0 = int64_t(tr) * kTile, c0 = int64_t(tc) * kTile;
+  const int k0 = int(int64_t(a.ksteps) * slice / a.splits);
+  const int n = int(int64_t(a.ksteps) * (slice + 1) / a.splits) - k0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < kStagesC; ++s) {
+        mbar_init(&sh->full[s], 1);
+        mbar_init(&sh->empty[s], 1);
+      }
+      mbar_init(&sh->accum, 1);
+      sh->abort = 0;
+      fence_barrier_init();
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&sh->tmem, kTile);
+  } else if (warp == 2 && lane == 0) {
+    prefetch_tmap(&ta);
+    prefetch_tmap(&tb);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  volatile int32_t* abort = &sh->abort;
+
+  if (warp == 0) {
+    int s = 0;
+    uint32_t phase = 1;  // the first round finds every stage empty
+    for (int k = 0; k < n; ++k) {
+      if (k >= kStagesC && !mbar_wait_suspend(&sh->empty[s], phase)) {
+        *abort = 1;
+        break;
+      }
+      if (elect_one()) {
+        uint8_t *da = smem + s * 2 * kABytes, *db = da + kABytes;
+        const int kk = (k0 + k) * kBK;
+        mbar_arrive_expect_tx(&sh->full[s], 2 * kABytes);
+        if constexpr (A_MN) {
+          tma_load_2d(da, &ta, &sh->full[s], int(r0), kk);
+          tma_load_2d(da + kABytes / 2, &ta, &sh->full[s], int(r0) + 64, kk);
+        } else {
+          tma_load_2d(da, &ta, &sh->full[s], kk, int(r0));
+        }
+        if constexpr (B_MN) {
+          tma_load_2d(db, &tb, &sh->full[s], int(c0), kk);
+          tma_load_2d(db + kABytes / 2, &tb, &sh->full[s], int(c0) + 64, kk);
+        } else {
+          tma_load_2d(db, &tb, &sh->full[s], kk, int(c0));
+        }
+      }
+      __syncwarp();
+      if (++s == kStagesC) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile) | (A_MN ? kIdescTransA : 0) |
+                               (B_MN ? kIdescTransB : 0);
+    const uint32_t base = smem_u32(smem);
+    const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base, 8192) : smem_desc_sw128(base);
+    const uint64_t db0 = B_MN ? smem_desc_mn_sw128(base + kABytes, 8192) : smem_desc_sw128(base + kABytes);
+    constexpr uint32_t ka = A_MN ? 2048 >> 4 : 32 >> 4, kb = B_MN ? 2048 >> 4 : 32 >> 4;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int k = 0; k < n; ++k) {
+      if (!mbar_wait_suspend(&sh->full[s], phase)) {
+        *abort = 1;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint64_t da = da0 + ((s * 2 * kABytes) >> 4), db = db0 + ((s * 2 * kABytes) >> 4);
+      if (elect_one()) {
+        tc_mma_f16(tmem, da, db, idesc, k > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 1; kk < kBK / 16; ++kk) tc_mma_f16(tmem, da + kk * ka, db + kk * kb, idesc, 1u);
+        tc_commit(&sh->empty[s]);
+      }
+      __syncwarp();
+      if (++s == kStagesC) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) tc_commit(&sh->accum);  // also after a timeout: what was issued drains
+    __syncwarp();
+  }
+  __syncwarp();
+  const int64_t col = c0 + lane * 4;
+  float bias[4] = {};
+  if (PASS == P_FWD) load_bias4(e, col, bias);
+  if (!mbar_wait_suspend(&sh->accum, 0)) *abort = 1;
+  __syncwarp();
+  tc_fence_after_sync();
+  const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
+  float* sums = reinterpret_cast<float*>(smem);
+  {
+    const int q = warp & 3, half = warp >> 2;  // 32 rows x 64 columns
+    if (q * 32 < nrows) {
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 64);
+      float* dst = sums + (q * 32 + lane) * kStrideC + half * 64;
+      uint32_t t[16];
+      float v[16];
+      tmem_issue(taddr, t);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        tmem_take(t, v);
+        if (c < 3) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  if (a.splits > 1) cluster_sync();
+  else __syncthreads();
+  const int rend = nrows * (slice + 1) / a.splits;
+#pragma unroll 1
+  for (int row = nrows * slice / a.splits + warp * R; row < rend; row += R * 8) {
+    float v[R][4];
+    if (a.splits > 1) {
+      // every slice's values are on their way before the first is added
+      float4 f[8][R];
+      const uint32_t mine = smem_u32(sums + row * kStrideC + lane * 4);
+#pragma unroll
+      for (int sl = 0; sl < 8; ++sl) {
+        if (sl < a.splits) {
+          const uint32_t base = peer_addr(mine, uint32_t(sl));
+#pragma unroll
+          for (int j = 0; j < R; ++j)  // (a row past rend is another CTA's: read, not used)
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(f[sl][j].x), "=f"(f[sl][j].y), "=f"(f[sl][j].z), "=f"(f[sl][j].w)
+                         : "r"(base + uint32_t((row + j < kTile ? j : 0) * kStrideC * 4)));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) v[j][0] = f[0][j].x, v[j][1] = f[0][j].y, v[j][2] = f[0][j].z, v[j][3] = f[0][j].w;
+#pragma unroll
+      for (int sl = 1; sl < 8; ++sl) {
+        if (sl < a.splits) {
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+            v[j][0] += f[sl][j].x, v[j][1] += f[sl][j].y, v[j][2] += f[sl][j].z, v[j][3] += f[sl][j].w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float4 f = *reinterpret_cast<const float4*>(sums + (row + j < kTile ? row + j : row) * kStrideC + lane * 4);
+        v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
+      }
+    }
+    epilogue4<PASS, R>(e, r0 + row, r0 + rend, col, bias, v);
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  if (a.splits > 1) cluster_sync();  // the others have read this CTA's sums
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTile);
   }
   if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
 }
@@ -764,30 +978,50 @@ struct Plan {
   int ksteps;
   int splits;     // slices of the inner axis
   bool cluster;   // joined in a cluster; else through scratch and finish_kernel
+  bool small;     // tile_kernel (128 x 128 tiles, one CTA each)
   int64_t cols4;
   size_t bytes;   // scratch
 };
 
 constexpr int kPairs = 76;  // SM pairs
 constexpr int kBN = 256;
+static_assert(kBN / 2 == kHalf && kTile == kHalf, "one box for every operand tile");
 
-// Fewer tiles than half the SM pairs: the inner axis is split.  Up to four slices
-// join in a cluster (8 CTAs, the portable size); a long inner axis with very few
-// tiles takes more slices through scratch.
+// Clusters of 2 S CTAs (one per SM) that run at the same time on this GPU, by S
+// (what the occupancy query reports; clusters stay within a GPC)
+constexpr int kClusters[9] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
+// the same for clusters of S CTAs
+constexpr int kClustersC[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+
+// Fewer tiles than half the SM pairs: the inner axis is split into as many slices
+// as still run together, at least two steps each, joined in a cluster.  A long
+// inner axis with very few tiles takes more slices through scratch.
 Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   Plan p;
   p.nr = int((rows + kRows - 1) / kRows);
   p.nc = int((cols + kBN - 1) / kBN);
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
-  p.cluster = false;
+  p.cluster = p.small = false;
   const int64_t tiles = int64_t(p.nr) * p.nc;
+  const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
+  if (small <= kClustersC[1] && p.ksteps > 0 && !(tiles <= 9 && p.ksteps >= 128)) {
+    p.small = true;
+    p.nr = int((rows + kTile - 1) / kTile), p.nc = int((cols + kTile - 1) / kTile);
+    int sp = 8;
+    while (sp > 1 && (small > kClustersC[sp] || sp > p.ksteps)) --sp;
+    p.splits = sp;
+    p.cluster = true;
+    p.cols4 = 0, p.bytes = 0;
+    return p;
+  }
   if (tiles <= 9 && p.ksteps >= 128) {
     p.splits = int(kPairs / tiles < p.ksteps / 16 ? kPairs / tiles : p.ksteps / 16);
   } else if (tiles <= kPairs / 2 && p.ksteps >= 4) {
-    p.splits = tiles <= 16 ? 4 : tiles <= 24 ? 3 : 2;
-    if (p.splits > p.ksteps / 2) p.splits = p.ksteps / 2;
-    p.cluster = p.splits > 1;
+    int sp = 8;
+    while (sp > 1 && (tiles > kClusters[sp] || sp > p.ksteps / 2)) --sp;
+    p.splits = sp;
+    p.cluster = sp > 1;
   }
   p.cols4 = (cols + 3) / 4 * 4;
   p.bytes = p.splits > 1 && !p.cluster ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
@@ -801,6 +1035,11 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   static const cudaError_t attr = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
   if (attr != cudaSuccess) return attr;
+  if (SPLIT) {  // more than 8 CTAs per cluster
+    static const cudaError_t wide =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (wide != cudaSuccess) return wide;
+  }
   const int64_t tiles = int64_t(a.nr) * a.nc, units = tiles * a.splits;
   cudaLaunchConfig_t cfg = {};
   const int csize = SPLIT ? 2 * a.splits : 2;
@@ -813,6 +1052,24 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   at[0].val.clusterDim.x = unsigned(csize), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, a, e);
+}
+
+template <int PASS>
+cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
+                        cudaStream_t st) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      tile_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemC));
+  if (attr != cudaSuccess) return attr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a.nr * a.nc * a.splits));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kSmemC;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(a.splits), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tile_kernel<PASS>, ta, tb, a, e);
 }
 
 // out[r, c] = epilogue(sum over k of A(r, k) B(c, k)); A, B as stored
@@ -830,11 +1087,13 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     CUtensorMap ta, tb;
     constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
     if (!encode(&ta, A, kBK, A_MN ? kBK : kHalf) ||
-        !encode(&tb, B, kBK, B_MN ? kBK : unsigned(kBN / 2)))
+        !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
       return AQFQ_ERR_CUDA;
     PairArgs a = {p.nr, p.nc, p.splits, p.ksteps, part, p.cols4, err};
     cudaError_t r;
-    if (p.cluster) {
+    if (p.small) {
+      r = launch_tile<PASS>(ta, tb, a, e, st);
+    } else if (p.cluster) {
       r = launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st);
     } else if (PASS == P_WGRAD || p.splits > 1) {  // finish_kernel has the epilogue, or it is plain
       r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
