@@ -263,6 +263,28 @@ struct ChunkIn {
   }
 };
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// The row's residual, previous output or codes for w columns on their way to L2: the
+// accumulators of this tile are still being summed.
+template <int PASS>
+__device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t col, int w, bool codes) {
+  const int n = e.cols - col < w ? int(e.cols - col) : w;
+  const uint8_t *p = nullptr, *q = nullptr;
+  if (PASS == P_WGRAD) {
+    const int es = e.out_dtype == AQFQ_F32 ? 4 : 2;
+    if (e.accumulate) p = static_cast<const uint8_t*>(e.out) + (r * e.ldo + col) * es, q = p + n * es;
+  } else if (e.res) {
+    p = reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + col), q = p + n * 2;
+  }
+  for (; p < q; p += 128) prefetch_l2(p);
+  if (codes) {
+    prefetch_l2(e.c.codes + r * e.cols + col);
+    prefetch_l2(e.c.codes + r * e.cols + col + n - 1);
+  }
+}
+
 // Columns [col, col + 16 chunks) of row r (one row per lane of the warp; chunks
 // * 16 a multiple of the checkpoint's group), sums at taddr.  `in`: the row
 // exists.  Every lane of the warp calls it.  sb: the columns' bias in shared
@@ -420,7 +442,9 @@ struct __align__(8) PairShared {
 
 struct PairArgs {
   int nr, nc;        // tiles
+  int first, count;  // the tiles of this launch
   int splits;        // slices of the inner axis
+  int a_rows;        // rows of A per box (tile_kernel: fewer when there are fewer rows)
   int ksteps;        // 64-element steps of the inner axis
   float* part;       // [splits][rows][cols4] partial sums when splits > 1
   int64_t cols4;     // cols rounded up to 4
@@ -454,7 +478,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   PairShared* sh = reinterpret_cast<PairShared*>(reinterpret_cast<uint8_t*>(sbias) + C::BIAS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
-  const int tiles = a.nr * a.nc, units = SPLIT ? tiles : tiles * a.splits;
+  const int tiles = a.count, units = SPLIT ? tiles : tiles * a.splits;
   // one unit per cluster, or a strided share of the units per pair
   const int pair = SPLIT ? blockIdx.x / (2 * a.splits) : blockIdx.x >> 1;
   const int npairs = SPLIT ? units : gridDim.x >> 1;
@@ -489,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       bool ok = true;
       for (int u = pair; u < units && ok; u += npairs) {
         int tr, tc;
-        tile_of(a, u % tiles, tr, tc);
+        tile_of(a, a.first + u % tiles, tr, tc);
         const int sp = SPLIT ? slice : u / tiles;
         const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
@@ -585,7 +609,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     int n = 0;
     for (int u = pair; u < units; u += npairs, ++n) {
       int tr, tc;
-      tile_of(a, u % tiles, tr, tc);
+      tile_of(a, a.first + u % tiles, tr, tc);
       const int buf = n & 1;
       const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
       const int64_t col = int64_t(tc) * BN + half * W;
@@ -601,7 +625,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
           __syncwarp();
         }
-        if (r < e.rows) first.load(e, r, col, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
+        if (r < e.rows) {
+          prefetch_inputs<PASS>(e, r, col, W, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
+          first.load(e, r, col, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
+        }
       }
       bool ok = true;
       if (lane == 0) {
@@ -656,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     // this CTA's rows of the tile; a warp takes half the columns of R rows per turn
     constexpr int R = 2, NW = kThreadsP / 32;
     int tr, tc;
-    tile_of(a, pair, tr, tc);
+    tile_of(a, a.first + pair, tr, tc);
     const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
     const int nrows = e.rows - r0 > kHalf ? kHalf : (e.rows > r0 ? int(e.rows - r0) : 0);
     const int half = warp & 1, rend = nrows * (slice + 1) / a.splits;
@@ -781,7 +808,7 @@ __global__ void __launch_bounds__(256, 1)
       if (elect_one()) {
         uint8_t *da = smem + s * 2 * kABytes, *db = da + kABytes;
         const int kk = (k0 + k) * kBK;
-        mbar_arrive_expect_tx(&sh->full[s], 2 * kABytes);
+        mbar_arrive_expect_tx(&sh->full[s], kABytes + (A_MN ? kABytes : uint32_t(a.a_rows * kBK * 2)));
         if constexpr (A_MN) {
           tma_load_2d(da, &ta, &sh->full[s], int(r0), kk);
           tma_load_2d(da + kABytes / 2, &ta, &sh->full[s], int(r0) + 64, kk);
@@ -979,6 +1006,8 @@ struct Plan {
   int splits;     // slices of the inner axis
   bool cluster;   // joined in a cluster; else through scratch and finish_kernel
   bool small;     // tile_kernel (128 x 128 tiles, one CTA each)
+  int a_rows;     // rows of A per box
+  int tail, tail_splits;  // last tiles that a second launch splits (0: none)
   int64_t cols4;
   size_t bytes;   // scratch
 };
@@ -1003,10 +1032,14 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
   p.cluster = p.small = false;
+  p.a_rows = kHalf, p.tail = p.tail_splits = 0;
   const int64_t tiles = int64_t(p.nr) * p.nc;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
   if (small <= kClustersC[1] && p.ksteps > 0 && !(tiles <= 9 && p.ksteps >= 128)) {
     p.small = true;
+    // zero rows that only the fill would write cost as much as loaded ones (1 row, 4096 x
+    // 4096: 12.9 us with boxes of 128 rows); rows past the box stay unread
+    if (rows < kHalf) p.a_rows = int((rows + 7) / 8 * 8);
     p.nr = int((rows + kTile - 1) / kTile), p.nc = int((cols + kTile - 1) / kTile);
     int sp = 8;
     while (sp > 1 && (small > kClustersC[sp] || sp > p.ksteps)) --sp;
@@ -1022,6 +1055,14 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
     while (sp > 1 && (tiles > kClusters[sp] || sp > p.ksteps / 2)) --sp;
     p.splits = sp;
     p.cluster = sp > 1;
+  } else if (tiles > kPairs) {
+    // The last round has `rem` tiles for 76 pairs.  Where they are few, a second launch
+    // splits them; it pays when the time it saves (0.34 us per step) exceeds its own
+    // start, joining and epilogue (about 8 us).
+    const int rem = int(tiles % kPairs);
+    int sp = 8;
+    while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
+    if (rem > 0 && sp > 1 && 0.34 * p.ksteps * (1.0 - 1.0 / sp) > 10.0) p.tail = rem, p.tail_splits = sp;
   }
   p.cols4 = (cols + 3) / 4 * 4;
   p.bytes = p.splits > 1 && !p.cluster ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
@@ -1040,7 +1081,7 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (wide != cudaSuccess) return wide;
   }
-  const int64_t tiles = int64_t(a.nr) * a.nc, units = tiles * a.splits;
+  const int64_t tiles = a.count, units = tiles * a.splits;
   cudaLaunchConfig_t cfg = {};
   const int csize = SPLIT ? 2 * a.splits : 2;
   cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < kPairs ? units : kPairs));
@@ -1086,11 +1127,12 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     if (!encode_fn()) return AQFQ_ERR_CUDA;
     CUtensorMap ta, tb;
     constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
-    if (!encode(&ta, A, kBK, A_MN ? kBK : kHalf) ||
+    if (!encode(&ta, A, kBK, A_MN ? kBK : unsigned(p.a_rows)) ||
         !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
       return AQFQ_ERR_CUDA;
-    PairArgs a = {p.nr, p.nc, p.splits, p.ksteps, part, p.cols4, err};
+    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
     cudaError_t r;
+    a.count -= p.tail;
     if (p.small) {
       r = launch_tile<PASS>(ta, tb, a, e, st);
     } else if (p.cluster) {
@@ -1110,6 +1152,10 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
       }
     }
     if (r != cudaSuccess) return AQFQ_ERR_CUDA;
+    if (p.tail > 0) {
+      a.first = a.count, a.count = p.tail, a.splits = p.tail_splits;
+      if (launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
+    }
   }
   if (p.splits != 1 && !p.cluster) {
     const int64_t gy = (e.rows + 7) / 8;
