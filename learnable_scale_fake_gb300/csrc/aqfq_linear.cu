@@ -285,10 +285,11 @@ __device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t
   }
 }
 
-// Columns [col, col + 16 chunks) of row r (one row per lane of the warp; chunks
-// * 16 a multiple of the checkpoint's group), sums at taddr.  `in`: the row
-// exists.  Every lane of the warp calls it.  sb: the columns' bias in shared
-// memory.  nx holds the first chunk's inputs (loaded before the accumulators were
+// Columns [col, col + 16 chunks) of row r (one row per lane of the warp), sums at
+// taddr.  `in`: the row exists.  Every lane of the warp calls it.  sb: the columns'
+// bias in shared memory.  A checkpoint group may be larger than the warp's columns:
+// its amax is then taken by every warp that has a part of it (the accumulators and
+// the bias of the 128 columns around are at hand).  nx holds the first chunk's inputs (loaded before the accumulators were
 // waited for); the next chunk's inputs and sums are under way while one is computed.
 template <int PASS, int ACT>
 __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col, int chunks,
@@ -299,19 +300,21 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
   const int64_t avail = (e.cols - col + 15) / 16;
   const int nch = avail < chunks ? int(avail) : chunks;
   const int gch = codes_out ? 1 << (e.c.lg - 4) : nch;  // chunks per group
+  const int lead = codes_out ? int(col >> 4) & (gch - 1) : 0;  // chunks of the group before col
   uint32_t t[16];
   float v[16];
 #pragma unroll 1
-  for (int g = 0; g < nch; g += gch) {
-    const int end = g + gch < nch ? g + gch : nch;
+  for (int g0 = -lead; g0 < nch; g0 += gch) {
+    const int g = g0 < 0 ? 0 : g0, end = g0 + gch < nch ? g0 + gch : nch;
     Divisor div = {};
     if (codes_out) {
       uint32_t m = 0;
-      tmem_issue(taddr + uint32_t(g * 16), t);
+      const int gend = g0 + gch < avail ? g0 + gch : int(avail);
+      tmem_issue(taddr + uint32_t(g0 * 16), t);
 #pragma unroll 1
-      for (int c = g; c < end; ++c) {
+      for (int c = g0; c < gend; ++c) {
         tmem_take(t, v);
-        if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
+        if (c + 1 < gend) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
         const int64_t left = e.cols - (col + c * 16);
         if (e.bias) {
 #pragma unroll
@@ -324,7 +327,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
         m = max(m, amax_bits(v));
       }
       div = ckpt_divisor(m, e.c.fmt);
-      if (in) e.c.scale[r * e.c.groups + ((col + g * 16) >> e.c.lg)] = div.s;
+      if (in && g0 >= 0) e.c.scale[r * e.c.groups + ((col + g0 * 16) >> e.c.lg)] = div.s;
     }
     tmem_issue(taddr + uint32_t(g * 16), t);
 #pragma unroll 1
@@ -409,14 +412,16 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
 // a tile runs under the next tile's MMAs.  Ragged edges and the tail of k are
 // zeros from the TMA's fill.
 //   warp 0  TMA producer    warp 1  MMA issuer (leader)    warp 2  tensor memory
-//   warps 4-11  epilogue, two per quarter of the rows, half of the columns each
+//   warps 4-19  epilogue, four per quarter of the rows, a quarter of the columns each
+//               (two per quarter left half of the issue slots idle: 4096 x 8192 over 2048 with
+//               GELU's slope from a checkpoint 115 us, EPI16 us with four)
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
 using namespace sm100;
 
 constexpr int kRows = 256, kHalf = 128, kBK = 64;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreadsP = 128 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
@@ -425,7 +430,7 @@ struct Cfg {
   static constexpr int STAGES = 6;
   static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
   static constexpr uint32_t STAGE = kABytes + B_BYTES;
-  static constexpr uint32_t BIAS = kEpiWarps * (BN / 2) * 4;  // a warp's columns
+  static constexpr uint32_t BIAS = kEpiWarps * 128 * 4;  // the 128 columns around a warp's
   static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + BIAS + 256;
   // a split tile's partial sums (one row per 16-byte odd stride) reuse the stages
   static constexpr int PSTRIDE = BN + 4;
@@ -437,7 +442,7 @@ struct __align__(8) PairShared {
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem;
-  int32_t abort;
+  int32_t abort, stop[2];
 };
 
 struct PairArgs {
@@ -603,26 +608,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    constexpr int W = BN / 2;  // columns of this warp
-    float* mybias = sbias + (warp - 4) * W;
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    constexpr int W = BN / (kEpiWarps / 4);  // columns of this warp
+    float* mybias = sbias + (warp - 4) * 128;
     int n = 0;
     for (int u = pair; u < units; u += npairs, ++n) {
       int tr, tc;
       tile_of(a, a.first + u % tiles, tr, tc);
       const int buf = n & 1;
       const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
-      const int64_t col = int64_t(tc) * BN + half * W;
+      const int64_t col = int64_t(tc) * BN + part * W;
       const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
       ChunkIn<PASS> first;
       if (live && whole) {
         if (PASS == P_FWD && e.bias) {
           float b[4];
           __syncwarp();
-          if (lane * 4 < W) {
-            load_bias4(e, col + lane * 4, b);
-            *reinterpret_cast<float4*>(mybias + lane * 4) = make_float4(b[0], b[1], b[2], b[3]);
-          }
+          load_bias4(e, (col & ~int64_t(127)) + lane * 4, b);
+          *reinterpret_cast<float4*>(mybias + lane * 4) = make_float4(b[0], b[1], b[2], b[3]);
           __syncwarp();
         }
         if (r < e.rows) {
@@ -630,19 +633,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           first.load(e, r, col, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
         }
       }
-      bool ok = true;
-      if (lane == 0) {
-        ok = mbar_wait_suspend(&sh->tfull[buf], (n >> 1) & 1) && !*abort;
+      // one thread waits for the tile, the other warps for it at a barrier: sixteen
+      // polling warps slowed the MMAs beside them by a tenth
+      if (warp == 4 && lane == 0) {
+        const bool ok = mbar_wait_long(&sh->tfull[buf], (n >> 1) & 1) && !*abort;
         if (!ok) *abort = 1;
+        sh->stop[buf] = ok ? 0 : 1;  // read by every warp after this barrier, before the next one
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
+      __syncwarp();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+      if (*reinterpret_cast<volatile int32_t*>(&sh->stop[buf])) break;
       tc_fence_after_sync();
-      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + half * W);
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + part * W);
       if (live) {
         if (SPLIT) {
           // into this CTA's shared memory (its stages are all consumed)
-          float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * C::PSTRIDE + half * W;
+          float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * C::PSTRIDE + part * W;
           uint32_t t[16];
           float v[16];
           tmem_issue(taddr, t);
@@ -671,7 +677,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
           }
         } else {
-          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr, mybias, first);
+          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr, mybias + int(col & 127), first);
         }
       }
       tc_fence_before_sync();

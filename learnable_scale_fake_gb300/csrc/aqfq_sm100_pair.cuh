@@ -23,6 +23,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// mbar_wait_suspend with a longer suspension per try (hint in ns), for waits of
+// whole tiles: the waiting warp leaves the issue slots to the others
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > (1ll << 31)) return false;
+  }
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -38,9 +56,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
-// one arrival on an mbarrier given by its cluster address
+// one arrival on an mbarrier given by its cluster address.  Relaxed: it hands over
+// tensor memory whose loads are complete, no data in memory, and a release would
+// first wait for the thread's outstanding global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // 2D tile into this CTA's shared memory, its bytes counted on the mbarrier at
