@@ -180,6 +180,10 @@ __device__ __forceinline__ void st16(bf16* p, bool a32, bool a16, int n, const u
   }
 }
 
+constexpr int kEpiWarps = 16;
+constexpr int kBN = 256;                            // columns of a pair's tile
+constexpr int kChunks = kBN / (kEpiWarps / 4) / 16;  // 16-column chunks of an epilogue warp
+
 // alignment of a row segment of 16 columns that lies in the row
 struct Seg {
   bool a32, a16;
@@ -212,14 +216,12 @@ __device__ __forceinline__ void tmem_take(uint32_t (&r)[16], float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// What 16 columns of a row read besides the sums: the residual, the previous
-// output of an accumulation, or the checkpoint's codes.
+// What 16 columns of a row read besides the sums: the residual, or the previous
+// output of an accumulation.
 template <int PASS>
 struct ChunkIn {
   uint32_t w[PASS == P_WGRAD ? 16 : 8];
-  uint32_t code[4];
-  float scale;
-  __device__ __forceinline__ void load(const Epi& e, int64_t r, int64_t cc, bool codes) {
+  __device__ __forceinline__ void load(const Epi& e, int64_t r, int64_t cc) {
     const int64_t left = e.cols - cc;
     const int n = left > 16 ? 16 : int(left);
     if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
@@ -246,19 +248,33 @@ struct ChunkIn {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = t[i];
     }
-    if (codes) {
-      const uint8_t* p = e.c.codes + r * e.cols + cc;
-      if (seg(p, n == 16).a16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        code[0] = u.x, code[1] = u.y, code[2] = u.z, code[3] = u.w;
+  }
+};
+
+// The codes of a row's 16 CH columns from col on and their scales (one per 32 columns):
+// all of them are fetched before the accumulators are waited for.
+template <int CH>
+struct RowCodes {
+  uint32_t w[CH][4];
+  float scale[CH / 2];
+  __device__ __forceinline__ void load(const Epi& e, int64_t r, int64_t col) {
+    const uint8_t* p = e.c.codes + r * e.cols + col;
+    const float* sc = e.c.scale + r * e.c.groups;
+    const int64_t left = e.cols - col;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (c * 16 >= left) break;
+      if (seg(p + c * 16, left >= c * 16 + 16).a16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + c * 16);
+        w[c][0] = u.x, w[c][1] = u.y, w[c][2] = u.z, w[c][3] = u.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = 0;
+        for (int i = 0; i < 4; ++i) w[c][i] = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (i < n) code[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+          if (c * 16 + i < left) w[c][i >> 2] |= uint32_t(p[c * 16 + i]) << (8 * (i & 3));
       }
-      scale = e.c.scale[r * e.c.groups + (cc >> e.c.lg)];
+      if (c % 2 == 0) scale[c / 2] = sc[(col + c * 16) >> e.c.lg];
     }
   }
 };
@@ -266,10 +282,10 @@ struct ChunkIn {
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-// The row's residual, previous output or codes for w columns on their way to L2: the
+// The row's residual or previous output for w columns on their way to L2: the
 // accumulators of this tile are still being summed.
 template <int PASS>
-__device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t col, int w, bool codes) {
+__device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t col, int w) {
   const int n = e.cols - col < w ? int(e.cols - col) : w;
   const uint8_t *p = nullptr, *q = nullptr;
   if (PASS == P_WGRAD) {
@@ -279,26 +295,23 @@ __device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t
     p = reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + col), q = p + n * 2;
   }
   for (; p < q; p += 128) prefetch_l2(p);
-  if (codes) {
-    prefetch_l2(e.c.codes + r * e.cols + col);
-    prefetch_l2(e.c.codes + r * e.cols + col + n - 1);
-  }
 }
 
-// Columns [col, col + 16 chunks) of row r (one row per lane of the warp), sums at
+// Columns [col, col + 16 kChunks) of row r (one row per lane of the warp), sums at
 // taddr.  `in`: the row exists.  Every lane of the warp calls it.  sb: the columns'
 // bias in shared memory.  A checkpoint group may be larger than the warp's columns:
 // its amax is then taken by every warp that has a part of it (the accumulators and
 // the bias of the 128 columns around are at hand).  nx holds the first chunk's inputs (loaded before the accumulators were
 // waited for); the next chunk's inputs and sums are under way while one is computed.
 template <int PASS, int ACT>
-__device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col, int chunks,
-                                             uint32_t taddr, const float* sb, ChunkIn<PASS>& nx) {
+__device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col,
+                                             uint32_t taddr, const float* sb, ChunkIn<PASS>& nx,
+                                             const RowCodes<kChunks>& codes) {
   constexpr bool CODES_IN = PASS == P_DGRAD && ACT != AQFQ_ACT_NONE;
   const bool codes_out = PASS == P_FWD && e.c.codes;
   const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
   const int64_t avail = (e.cols - col + 15) / 16;
-  const int nch = avail < chunks ? int(avail) : chunks;
+  const int nch = avail < kChunks ? int(avail) : kChunks;
   const int gch = codes_out ? 1 << (e.c.lg - 4) : nch;  // chunks per group
   const int lead = codes_out ? int(col >> 4) & (gch - 1) : 0;  // chunks of the group before col
   uint32_t t[16];
@@ -330,13 +343,21 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
       if (in && g0 >= 0) e.c.scale[r * e.c.groups + ((col + g0 * 16) >> e.c.lg)] = div.s;
     }
     tmem_issue(taddr + uint32_t(g * 16), t);
-#pragma unroll 1
-    for (int c = g; c < end; ++c) {
+    // (the codes are in registers: unrolled, so that their indices are constants)
+#pragma unroll(CODES_IN ? kChunks : 1)
+    for (int i0 = 0; i0 < kChunks; ++i0) {
+      const int c = CODES_IN ? i0 : g + i0;
+      if (c >= end) break;
       const int64_t cc = col + c * 16;
       const int64_t left = e.cols - cc;
       const int n = left > 16 ? 16 : int(left);
-      const ChunkIn<PASS> cur = nx;
-      if (c + 1 < nch && in) nx.load(e, r, cc + 16, CODES_IN);
+      ChunkIn<PASS> cur;
+      if constexpr (CODES_IN) {  // (the codes take the registers of a second set)
+        if (in) cur.load(e, r, cc);
+      } else {
+        cur = nx;
+        if (c + 1 < nch && in) nx.load(e, r, cc + 16);
+      }
       tmem_take(t, v);
       if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
       if (PASS == P_FWD) {
@@ -364,7 +385,8 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
       if (CODES_IN) {
         float p[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ckpt_values4(cur.code[i], cur.scale, e.c.fmt, p + 4 * i);
+        for (int i = 0; i < 4; ++i)
+          ckpt_values4(codes.w[CODES_IN ? i0 : 0][i], codes.scale[CODES_IN ? i0 / 2 : 0], e.c.fmt, p + 4 * i);
         slope_all<ACT>(p, v);
       }
       if (in) {
@@ -421,7 +443,6 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
 using namespace sm100;
 
 constexpr int kRows = 256, kHalf = 128, kBK = 64;
-constexpr int kEpiWarps = 16;
 constexpr int kThreadsP = 128 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
@@ -620,6 +641,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int64_t col = int64_t(tc) * BN + part * W;
       const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
       ChunkIn<PASS> first;
+      RowCodes<kChunks> codes;
       if (live && whole) {
         if (PASS == P_FWD && e.bias) {
           float b[4];
@@ -629,8 +651,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           __syncwarp();
         }
         if (r < e.rows) {
-          prefetch_inputs<PASS>(e, r, col, W, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
-          first.load(e, r, col, PASS == P_DGRAD && ACT != AQFQ_ACT_NONE);
+          prefetch_inputs<PASS>(e, r, col, W);
+          if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) codes.load(e, r, col);
+          else first.load(e, r, col);
         }
       }
       // one thread waits for the tile, the other warps for it at a barrier: sixteen
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
           }
         } else {
-          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, W / 16, taddr, mybias + int(col & 127), first);
+          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), first, codes);
         }
       }
       tc_fence_before_sync();
@@ -1019,7 +1042,6 @@ struct Plan {
 };
 
 constexpr int kPairs = 76;  // SM pairs
-constexpr int kBN = 256;
 static_assert(kBN / 2 == kHalf && kTile == kHalf, "one box for every operand tile");
 
 // Clusters of 2 S CTAs (one per SM) that run at the same time on this GPU, by S
