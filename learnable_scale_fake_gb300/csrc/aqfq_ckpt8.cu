@@ -105,6 +105,40 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
+// Wide rows of BF16: a lane packs 16 consecutive columns (one division and one 16-byte
+// store for them), a warp 512; 2^lr lanes share a row.
+template <int FMT, int U>
+__global__ void __launch_bounds__(kWarps * 32)
+    pack16_kernel(const bf16* x, int64_t ldx, int64_t rows, int64_t cols, int lr, bool a32, const Ckpt c) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rpw = 32 >> lr;
+  const int64_t base = (int64_t(blockIdx.y) * kWarps + warp) * rpw;
+  const int64_t step = int64_t(gridDim.y) * kWarps * rpw;
+  const int64_t col = ((int64_t(blockIdx.x) << lr) + (lane & ((1 << lr) - 1))) * 16;
+  const bool in0 = col < cols, in1 = col + 8 < cols;
+  for (int64_t b = base, r = base + (lane >> lr); b < rows; b += step * U, r += step * U) {
+    uint32_t w[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t ru = r + u * step < rows ? r + u * step : rows - 1;
+      const bf16* p = x + ru * ldx + (in0 ? col : 0);
+      if (a32 && in1) {
+        ld_stream(p, w[u]);
+      } else {
+        ld_stream_v4(p, w[u][0], w[u][1], w[u][2], w[u][3]);
+        ld_stream_v4(in1 ? p + 8 : p, w[u][4], w[u][5], w[u][6], w[u][7]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool e = r + u * step < rows;
+      f2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (i < 4 ? in0 : in1) ? bf2(w[u][i]) : 0ull;
+      ckpt_write16<FMT>(c, r + u * step, cols, int(col), in0 && e, in1 && e, v);
+    }
+  }
+}
+
 template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
     unpack_kernel(const Ckpt c, int64_t rows, int64_t cols, int lr, T* y, int64_t ldy) {
@@ -199,27 +233,32 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// 32 columns x 8 slices per block: slice j adds the parts j, j + 8, ... in
-// order, then the eight slices are added in order
-__global__ void __launch_bounds__(256)
+// 32 columns x 32 slices per block: slice j adds the parts j, j + 32, ... in
+// order, then the slices are added pairwise.  At most ten parts per slice, all of
+// them under way at once.
+__global__ void __launch_bounds__(1024)
     part_sums_kernel(const float* part, const float* part2, int parts, int64_t cols, float* out,
                      float* out2, int accumulate) {
-  __shared__ float red[8][32];
+  constexpr int MOST = (kMaxParts + 31) / 32;
+  __shared__ float red[32][33];
   const float* src = blockIdx.y ? part2 : part;
   float* dst = blockIdx.y ? out2 : out;
-  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
-  const int j = threadIdx.x / 32;
-  float t = 0.0f;
-  if (c < cols)
-    for (int p = j; p < parts; p += 8) t += src[int64_t(p) * cols + c];
-  red[j][threadIdx.x % 32] = t;
-  __syncthreads();
-  if (j == 0 && c < cols) {
-    t = 0.0f;
+  const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  float v[MOST], t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][threadIdx.x];
-    dst[c] = accumulate ? dst[c] + t : t;
-  }
+  for (int i = 0; i < MOST; ++i)
+    v[i] = c < cols && j + 32 * i < parts ? src[int64_t(j + 32 * i) * cols + c] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) t += v[i];
+  red[j][lane] = t;
+  __syncthreads();
+  // warp j adds up column j of the 32 x 32 totals
+  t = red[lane][j];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  const int64_t cj = int64_t(blockIdx.x) * 32 + j;
+  if (lane == 0 && cj < cols) dst[cj] = accumulate ? dst[cj] + t : t;
 }
 
 size_t act_bwd_ws(int64_t rows, int64_t cols) {
@@ -270,7 +309,7 @@ cudaError_t launch_part_sums(const float* part, const float* part2, int parts, i
     out = out2, part = part2;
     out2 = nullptr;
   }
-  part_sums_kernel<<<dim3(unsigned((cols + 31) / 32), out2 ? 2 : 1), 256, 0, st>>>(
+  part_sums_kernel<<<dim3(unsigned((cols + 31) / 32), out2 ? 2 : 1), 1024, 0, st>>>(
       part, part2, parts, cols, out, out2, accumulate);
   return cudaGetLastError();
 }
@@ -293,12 +332,24 @@ extern "C" aqfq_status aqfq_ckpt8_pack(const aqfq_ckpt8* ckpt, int dtype, const 
   if (!al(x, esize(dtype))) return AQFQ_ERR_ALIGN;
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
   const bool wide = cols % 8 == 0 && rows_aligned<8>(x, ldx, esize(dtype)) && al(c.codes, 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (wide && dtype == AQFQ_BF16 && cols > 256) {
+    // (half as many columns per segment below; 257 x 512 and up fill the lanes)
+    const Map m = make_map(rows, (cols + 1) / 2, c.lg, true, 65535);
+    const bf16* in = static_cast<const bf16*>(x);
+    const bool a32 = al(x, 32) && ldx % 16 == 0;
+    const dim3 grid(unsigned((cols + (16ll << m.lr) - 1) / (16ll << m.lr)), m.gy);
+    if (c.fmt == AQFQ_INT8)
+      pack16_kernel<AQFQ_INT8, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, a32, c);
+    else
+      pack16_kernel<AQFQ_FP8_E4M3, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, a32, c);
+    return done();
+  }
   const Map m = make_map(rows, cols, c.lg, wide, 65535);
   by_type(dtype, wide, [&](auto t, auto v) {
     using T = typename decltype(t)::type;
     constexpr int V = decltype(v)::value;
     const dim3 grid(m.gx, m.gy);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const T* in = static_cast<const T*>(x);
     if (c.fmt == AQFQ_INT8)
       pack_kernel<T, V, AQFQ_INT8, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, c);

@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(1024, 1)
 // A wait gives up after about a second; the rows left are then written as NaN.
 // ---------------------------------------------------------------------------
 constexpr int kMaxStages = 16;
+constexpr int kFwdBlocks = 2;           // blocks per SM of the forward ring
 constexpr int kRingBytes = 200 * 1024;  // per SM
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -592,14 +593,43 @@ struct RingArgs {
   int row_bytes;            // of a tensor's row; a multiple of 16
 };
 
-// NW warps per block, MB blocks per SM
-template <typename T, int NV, int G, int NW, int MB>
+// sums of two values over a group: half a warp carries each of them, so that five
+// exchanges serve both; the totals of every warp through red[2][G]
+template <int G>
+__device__ __forceinline__ void group_sum2(float (&s)[2], float* red, int grp) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane >= 16;
+  float t = (up ? s[1] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? s[0] : s[1], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  if constexpr (G == 1) {
+    s[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
+    s[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
+    group_sync<G>(grp);
+  } else {
+    if ((lane & 15) == 0) red[(up ? G : 0) + (threadIdx.x >> 5) % G] = t;
+    group_sync<G>(grp);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f2* p = reinterpret_cast<const f2*>(red + k * G);
+      f2 u = p[0];
+#pragma unroll
+      for (int w = 1; w < G / 2; ++w) u = add2(u, p[w]);
+      s[k] = lo2(u) + hi2(u);
+    }
+  }
+}
+
+// NW warps per block, MB blocks per SM.  A lane has 16 consecutive columns; a stage is
+// two rows, which share the waits, the barriers and the sums' exchanges.  CK: the
+// checkpoint's format, or -1 (a run-time choice kept the two rows' arithmetic apart).
+template <typename T, int G, int NW, int MB, int CK>
 __global__ void __launch_bounds__(32 * NW, MB)
     norm_fwd_ring(const T* x, T* y, const FwdArgs a, const RingArgs q) {
-  constexpr int NG = NW / G, P = NV * 4;
+  constexpr int NG = NW / G, P = 8, R = 2;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[NG][kMaxStages];
-  __shared__ __align__(8) float red[NG][2][G];
+  __shared__ __align__(8) float red[NG][2][R * G];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp / G, wr = warp % G;
   uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
@@ -609,75 +639,103 @@ __global__ void __launch_bounds__(32 * NW, MB)
     sm100::fence_barrier_init();
   }
   __syncthreads();
-  const int64_t step = int64_t(gridDim.x) * NG;
-  int64_t r = int64_t(blockIdx.x) * NG + grp;
+  const int64_t step = int64_t(gridDim.x) * NG * R;
+  int64_t r = (int64_t(blockIdx.x) * NG + grp) * R;
   const bool loader = wr == 0 && lane == 0;
   auto fetch = [&](int64_t row, int st) {
     if (row < a.rows) {
-      sm100::mbar_arrive_expect_tx(&full[grp][st], uint32_t(q.row_bytes));
-      bulk_load(sm100::smem_u32(mine + st * q.stage_bytes), x + row * a.ldx, uint32_t(q.row_bytes),
-                &full[grp][st]);
+      uint64_t* bar = &full[grp][st];
+      const uint32_t dst = sm100::smem_u32(mine + st * q.stage_bytes), n = uint32_t(q.row_bytes);
+      const bool two = row + 1 < a.rows;
+      sm100::mbar_arrive_expect_tx(bar, two ? 2 * n : n);
+      bulk_load(dst, x + row * a.ldx, n, bar);
+      if (two) bulk_load(dst + n, x + (row + 1) * a.ldx, n, bar);
     }
   };
   if (loader)
     for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
   const float inv = 1.0f / float(a.cols);
-  int col[NV];
-  int64_t col64[NV];
-  bool in[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    col64[j] = (wr * NV * 32 + j * 32 + lane) * 8;
-    in[j] = col64[j] < a.cols;
-    col[j] = in[j] ? int(col64[j]) : 0;
-  }
+  const int col = (wr * 32 + lane) * 16;
+  const bool in[2] = {col < a.cols, col + 8 < a.cols};
+  const int cl[2] = {in[0] ? col : 0, in[1] ? col + 8 : 0};
+  const int64_t col64[2] = {cl[0], cl[1]};
   f2 g[P], b[P];
-  params<8, NV>(a.gamma, a.pdtype, col64, in, 1.0f, g);
-  params<8, NV>(a.beta, a.pdtype, col64, in, 0.0f, b);
+  params<8, 2>(a.gamma, a.pdtype, col64, in, 1.0f, g);
+  params<8, 2>(a.beta, a.pdtype, col64, in, 0.0f, b);
+  T* yrow = y + r * a.ldy + col;
+  const int64_t ystep = step * a.ldy;
+  // 32-byte stores where the rows allow them
+  const bool wide = sizeof(T) == 2 && in[1] &&
+                    ((reinterpret_cast<uintptr_t>(yrow) | uintptr_t(a.ldy * sizeof(T))) & 31) == 0;
   int st = 0, prev = q.stages - 1;
   uint32_t phase = 0;
   bool ok = true;
-  for (bool first = true; r < a.rows; r += step, first = false) {
-    if (ok) {
+  for (bool first = true; r < a.rows; r += step, yrow += ystep, first = false) {
+    if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
       if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
     }
-    f2 v[P], t = 0;
-    smem_pairs<true, T, NV>(mine + st * q.stage_bytes, col, in, v);
-    if (!ok) v[0] = pair(__int_as_float(0x7FC00000));
+    const bool two = r + 1 < a.rows;
+    f2 v[R][P];
+    float s[R];
 #pragma unroll
-    for (int i = 0; i < P; ++i) t = add2(t, v[i]);
-    if (a.c.codes) {
-      if (a.c.fmt == AQFQ_INT8) ckpt_write<AQFQ_INT8, 8, NV>(a.c, r, a.cols, col64, in, v);
-      else ckpt_write<AQFQ_FP8_E4M3, 8, NV>(a.c, r, a.cols, col64, in, v);
+    for (int k = 0; k < R; ++k) {
+      smem_pairs<true, T, 2>(mine + st * q.stage_bytes + k * q.row_bytes, cl, in, v[k]);
+      if (!ok) v[k][0] = pair(__int_as_float(0x7FC00000));
+      f2 t = v[k][0];
+#pragma unroll
+      for (int i = 1; i < P; ++i) t = add2(t, v[k][i]);
+      s[k] = lo2(t) + hi2(t);
     }
-    float s[1] = {lo2(t) + hi2(t)};
-    group_sum<G, 1>(s, red[grp][0], grp);
-    // every warp has read the row before this one
-    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
-    const float mu = s[0] * inv;
-    s[0] = 0.0f;
+    if constexpr (CK >= 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      t = 0;
-#pragma unroll
-      for (int i = 4 * j; i < 4 * j + 4; ++i) {
-        v[i] = sub2(v[i], pair(mu));
-        t = fma2(v[i], v[i], t);
+      for (int k = 0; k < R; ++k) {
+        const bool e = k == 0 || two;  // uniform
+        ckpt_write16<CK>(a.c, r + k, a.cols, col, in[0] && e, in[1] && e, v[k]);
       }
-      s[0] += in[j] ? lo2(t) + hi2(t) : 0.0f;
     }
-    group_sum<G, 1>(s, red[grp][1], grp);
-    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
-    if (loader) {
-      if (a.mean) a.mean[r] = mu;
-      if (a.rstd) a.rstd[r] = rs;
+    group_sum2<G>(s, red[grp][0], grp);
+    // every warp has read the rows before these
+    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+    float mu[R], rs[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mu[k] = s[k] * inv;
+      s[k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f2 t = 0;
+#pragma unroll
+        for (int i = 4 * j; i < 4 * j + 4; ++i) {
+          v[k][i] = sub2(v[k][i], pair(mu[k]));
+          t = fma2(v[k][i], v[k][i], t);
+        }
+        s[k] += in[j] ? lo2(t) + hi2(t) : 0.0f;
+      }
+    }
+    group_sum2<G>(s, red[grp][1], grp);
+#pragma unroll
+    for (int k = 0; k < R; ++k) rs[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+    if (wr == 0 && lane < R && r + lane < a.rows) {
+      if (a.mean) a.mean[r + lane] = lane ? mu[1] : mu[0];
+      if (a.rstd) a.rstd[r + lane] = lane ? rs[1] : rs[0];
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = fma2(mul2(v[i], pair(rs)), g[i], b[i]);
+    for (int k = 0; k < R; ++k) {
+      if (k == 1 && !two) break;
+      const f2 f = pair(rs[k]);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (in[j]) put<T, 8>(y + r * a.ldy + col[j], v, j);
+      for (int i = 0; i < P; ++i) v[k][i] = fma2(mul2(v[k][i], f), g[i], b[i]);
+      T* p = yrow + (k ? a.ldy : 0);
+      if (wide) {
+        const uint32_t w[8] = {pack2(v[k][0]), pack2(v[k][1]), pack2(v[k][2]), pack2(v[k][3]),
+                               pack2(v[k][4]), pack2(v[k][5]), pack2(v[k][6]), pack2(v[k][7])};
+        st_256(p, w);
+      } else {
+        if (in[0]) put<T, 8>(p, v[k], 0);
+        if (in[1]) put<T, 8>(p + 8, v[k], 1);
+      }
+    }
     prev = st;
     if (++st == q.stages) st = 0, phase ^= 1;
   }
@@ -866,14 +924,20 @@ cudaError_t ring_smem(K kernel) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
 }
 
-template <typename T, int NV, int G, int NW, int MB>
+template <typename T, int G, int NW, int MB>
 cudaError_t run_fwd_ring(const void* x, void* y, const FwdArgs& a, const RingArgs& q, cudaStream_t st) {
   constexpr int NG = NW / G;
-  static const cudaError_t attr = ring_smem(norm_fwd_ring<T, NV, G, NW, MB>);
-  if (attr != cudaSuccess) return attr;
-  int64_t blocks = (a.rows + NG - 1) / NG;
+  static const cudaError_t attr[3] = {ring_smem(norm_fwd_ring<T, G, NW, MB, -1>),
+                                      ring_smem(norm_fwd_ring<T, G, NW, MB, AQFQ_INT8>),
+                                      ring_smem(norm_fwd_ring<T, G, NW, MB, AQFQ_FP8_E4M3>)};
+  const int k = !a.c.codes ? 0 : a.c.fmt == AQFQ_INT8 ? 1 : 2;
+  if (attr[k] != cudaSuccess) return attr[k];
+  auto kernel = k == 0   ? norm_fwd_ring<T, G, NW, MB, -1>
+                : k == 1 ? norm_fwd_ring<T, G, NW, MB, AQFQ_INT8>
+                         : norm_fwd_ring<T, G, NW, MB, AQFQ_FP8_E4M3>;
+  int64_t blocks = (a.rows + 2 * NG - 1) / (2 * NG);
   if (blocks > MB * kSms) blocks = MB * kSms;
-  norm_fwd_ring<T, NV, G, NW, MB><<<unsigned(blocks), 32 * NW, size_t(NG) * q.stages * q.stage_bytes, st>>>(
+  kernel<<<unsigned(blocks), 32 * NW, size_t(NG) * q.stages * q.stage_bytes, st>>>(
       static_cast<const T*>(x), static_cast<T*>(y), a, q);
   return cudaGetLastError();
 }
@@ -885,17 +949,16 @@ inline bool ring_rows(int64_t rows, int64_t groups) { return rows >= 4 * groups;
 template <typename T>
 cudaError_t launch_fwd(const void* x, void* y, const FwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
-  if (a.vec && a.pvec && c % 8 == 0 && a.cvec && c > 256 && c <= 8192) {
-    // 16 columns per lane; blocks of 8 warps, three per SM, or of 16 for the widest rows
-    const int G = c <= 512 ? 1 : c <= 1024 ? 2 : c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
-    const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : 3, row = int(c) * int(sizeof(T));
-    const RingArgs q = make_ring(row, row, nw / G, kRingBytes / mb);
-    if (q.stages >= 3 && ring_rows(a.rows, kSms * mb * (nw / G))) {
-      if (G == 1) return run_fwd_ring<T, 2, 1, 8, 3>(x, y, a, q, st);
-      if (G == 2) return run_fwd_ring<T, 2, 2, 8, 3>(x, y, a, q, st);
-      if (G == 4) return run_fwd_ring<T, 2, 4, 8, 3>(x, y, a, q, st);
-      if (G == 8) return run_fwd_ring<T, 2, 8, 8, 3>(x, y, a, q, st);
-      return run_fwd_ring<T, 2, 16, 16, 1>(x, y, a, q, st);
+  if (a.vec && a.pvec && c % 8 == 0 && a.cvec && c > 1024 && c <= 8192) {
+    // (narrower rows: norm_fwd_rows is faster, 16384 x 768 14.9 us against 16.4)
+    // blocks of 8 warps, or of 16 for the widest rows
+    const int G = c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
+    const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : kFwdBlocks, row = int(c) * int(sizeof(T));
+    const RingArgs q = make_ring(2 * row, row, nw / G, kRingBytes / mb);
+    if (q.stages >= 3 && ring_rows(a.rows, 2 * kSms * mb * (nw / G))) {
+      if (G == 4) return run_fwd_ring<T, 4, 8, kFwdBlocks>(x, y, a, q, st);
+      if (G == 8) return run_fwd_ring<T, 8, 8, kFwdBlocks>(x, y, a, q, st);
+      return run_fwd_ring<T, 16, 16, 1>(x, y, a, q, st);
     }
   }
   // one block per (few) rows: the grid has to hold them
