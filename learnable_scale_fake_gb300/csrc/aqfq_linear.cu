@@ -763,16 +763,32 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
 }
 
+// lines of what row r's 128 columns from c0 on read, one per lane (of 16)
+template <int PASS>
+__device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0, int lane) {
+  const int64_t n = e.cols - c0 > kHalf ? kHalf : e.cols - c0;
+  const int64_t at = lane * 128;  // byte
+  if (PASS == P_WGRAD) {
+    const int es = e.out_dtype == AQFQ_F32 ? 4 : 2;
+    if (e.accumulate && at < n * es)
+      prefetch_l2(static_cast<const uint8_t*>(e.out) + (r * e.ldo + c0) * es + at);
+  } else {
+    if (e.res && at < n * 2) prefetch_l2(reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + c0) + at);
+    if (PASS == P_DGRAD && e.c.codes && lane == 8) prefetch_l2(e.c.codes + r * e.cols + c0);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // small products: one CTA per 128 x 128 tile and slice of the inner axis, the S
 // slices of a tile in a cluster.  Six stages of 32 KiB; warp 0 issues the loads, warp
-// 1 the MMAs; then all eight warps move the accumulators to shared memory (the
+// 1 the MMAs; then all sixteen warps move the accumulators to shared memory (the
 // stages are consumed), the cluster meets, and each CTA finishes its share of the
 // rows that exist: a warp takes whole rows of 128 columns, reads every slice's
 // value through distributed shared memory and adds them in the slices' order.
 // Few rows (a token or two): the weight is streamed once by tiles x S CTAs.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
+constexpr int kWarpsC = 16;
 constexpr int kStagesC = 6;
 constexpr int kStrideC = kTile + 4;  // floats per row of partial sums
 constexpr size_t kSmemC = 1024 + size_t(kStagesC) * 2 * kABytes + 256;
@@ -786,7 +802,7 @@ struct __align__(8) CtaShared {
 };
 
 template <int PASS>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(32 * kWarpsC, 1)
     tile_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
   constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
@@ -889,26 +905,31 @@ __global__ void __launch_bounds__(256, 1)
     __syncwarp();
   }
   __syncwarp();
+  // this CTA's rows, R per warp and turn; what they read is sent to L2 meanwhile
+  const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
+  const int row0 = nrows * slice / a.splits + warp * R, rend = nrows * (slice + 1) / a.splits;
+  for (int row = row0 + (lane >> 4); row < rend; row += R * kWarpsC)
+    prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
   const int64_t col = c0 + lane * 4;
   float bias[4] = {};
   if (PASS == P_FWD) load_bias4(e, col, bias);
+  __syncwarp();
   if (!mbar_wait_suspend(&sh->accum, 0)) *abort = 1;
   __syncwarp();
   tc_fence_after_sync();
-  const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
   float* sums = reinterpret_cast<float*>(smem);
   {
-    const int q = warp & 3, half = warp >> 2;  // 32 rows x 64 columns
+    const int q = warp & 3, part = warp >> 2;  // 32 rows x 32 columns
     if (q * 32 < nrows) {
-      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 64);
-      float* dst = sums + (q * 32 + lane) * kStrideC + half * 64;
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(part * 32);
+      float* dst = sums + (q * 32 + lane) * kStrideC + part * 32;
       uint32_t t[16];
       float v[16];
       tmem_issue(taddr, t);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         tmem_take(t, v);
-        if (c < 3) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
+        if (c < 1) tmem_issue(taddr + 16, t);
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
           *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -918,9 +939,8 @@ __global__ void __launch_bounds__(256, 1)
   __syncwarp();
   if (a.splits > 1) cluster_sync();
   else __syncthreads();
-  const int rend = nrows * (slice + 1) / a.splits;
 #pragma unroll 1
-  for (int row = nrows * slice / a.splits + warp * R; row < rend; row += R * 8) {
+  for (int row = row0; row < rend; row += R * kWarpsC) {
     float v[R][4];
     if (a.splits > 1) {
       // every slice's values are on their way before the first is added
@@ -1131,7 +1151,7 @@ cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.nr * a.nc * a.splits));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kWarpsC);
   cfg.dynamicSmemBytes = kSmemC;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
