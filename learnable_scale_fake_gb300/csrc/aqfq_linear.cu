@@ -24,8 +24,10 @@ namespace {
 enum Pass { P_FWD = AQFQ_LINEAR_FWD, P_DGRAD = AQFQ_LINEAR_DGRAD, P_WGRAD = AQFQ_LINEAR_WGRAD };
 
 // ---------------------------------------------------------------------------
-// epilogue: a warp holds 128 columns of a row, a lane 4 of them, so an 8-bit
-// group of 32, 64 or 128 columns is 8, 16 or 32 neighbouring lanes
+// epilogue of sums in memory: 16 lanes hold 128 columns of a row, a lane 8 of them, a
+// warp two rows; an 8-bit group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring
+// lanes.  (4 columns per lane and 32 lanes per row: twice the address arithmetic per
+// element, 0.9 us instead of EPI8 us per turn of 16 warps with GELU and residual.)
 // ---------------------------------------------------------------------------
 struct Epi {
   int64_t rows, cols;
@@ -35,110 +37,130 @@ struct Epi {
   void* out;
   int64_t ldo;
   int bias_dtype, out_dtype, act, accumulate;
-  bool vec_out, vec_res, vec_bias, vec_codes;  // 4-element accesses are aligned
+  bool vec_out, vec_res, vec_bias, vec_codes;  // 8-element accesses are aligned
   Ckpt c;               // forward: written; input gradient: read
 };
 
-// the bias of columns [col, col + 4)
-__device__ __forceinline__ void load_bias4(const Epi& e, int64_t col, float (&b)[4]) {
-  const int n = e.cols - col > 4 ? 4 : int(e.cols - col);
+// columns of [col, col + V) that lie in the row
+template <int V>
+__device__ __forceinline__ int in_row(const Epi& e, int64_t col) {
+  const int64_t left = e.cols - col;
+  return left > V ? V : int(left);
+}
+
+// the bias of columns [col, col + V)
+template <int V>
+__device__ __forceinline__ void load_bias(const Epi& e, int64_t col, float (&b)[V]) {
+  const int n = in_row<V>(e, col);
   if (e.bias && n > 0) {
     if (e.bias_dtype == AQFQ_BF16)
-      load_row(static_cast<const bf16*>(e.bias) + col, e.vec_bias && n == 4, n, b);
+      load_row(static_cast<const bf16*>(e.bias) + col, e.vec_bias && n == V, n, b);
     else
-      load_row(static_cast<const float*>(e.bias) + col, e.vec_bias && n == 4, n, b);
+      load_row(static_cast<const float*>(e.bias) + col, e.vec_bias && n == V, n, b);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = 0.0f;
+    for (int i = 0; i < V; ++i) b[i] = 0.0f;
   }
 }
 
-// v[j]: the sums of row r + j < rend, columns [col, col + 4); every lane of the warp
-// calls it.  What the rows read is fetched for all of them first.
-template <int PASS, int R>
-__device__ __forceinline__ void epilogue4(const Epi& e, int64_t r, int64_t rend, int64_t col,
-                                          const float (&bias)[4], float (&v)[R][4]) {
-  const int n = e.cols - col > 4 ? 4 : int(e.cols - col);
-  const bool full = n == 4;
-  bool in[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) in[j] = r + j < rend && n > 0;
-  float add[R][4];
-  uint32_t code[R][1];
-  float cs[R];
+// v: the sums of row r, columns [col, col + 8); `in`: the row is this call's.  Every
+// lane of the warp calls it.
+template <int PASS>
+__device__ __forceinline__ void epilogue8(const Epi& e, int64_t r, bool in, int64_t col,
+                                          const float (&bias)[8], float (&v)[8]) {
+  const int n = in_row<8>(e, col);
+  const bool full = n == 8;
+  in = in && n > 0;
   const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
-  if (adds) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (!in[j]) continue;
-      if constexpr (PASS == P_WGRAD) {
-        if (e.out_dtype == AQFQ_BF16)
-          load_row(static_cast<const bf16*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, add[j]);
-        else
-          load_row(static_cast<const float*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, add[j]);
-      } else {
-        load_row(e.res + (r + j) * e.ldr + col, e.vec_res && full, n, add[j]);
-      }
+  float add[8];
+  if (adds && in) {
+    if constexpr (PASS == P_WGRAD) {
+      if (e.out_dtype == AQFQ_BF16)
+        load_row(static_cast<const bf16*>(e.out) + r * e.ldo + col, e.vec_out && full, n, add);
+      else
+        load_row(static_cast<const float*>(e.out) + r * e.ldo + col, e.vec_out && full, n, add);
+    } else {
+      load_row(e.res + r * e.ldr + col, e.vec_res && full, n, add);
     }
   }
   if constexpr (PASS == P_DGRAD) {
-    if (e.c.codes) {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (!in[j]) continue;
-        load_bytes<4>(e.c.codes + (r + j) * e.cols + col, e.vec_codes && full, n, code[j]);
-        cs[j] = e.c.scale[(r + j) * e.c.groups + (col >> e.c.lg)];
-      }
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (!in[j]) continue;
-        float p[4];
-        ckpt_values4(code[j][0], cs[j], e.c.fmt, p);
-        slope_apply(e.act, p, v[j]);
-      }
+    if (e.c.codes && in) {
+      uint32_t w[2];
+      load_bytes<8>(e.c.codes + r * e.cols + col, e.vec_codes && full, n, w);
+      const float s = e.c.scale[r * e.c.groups + (col >> e.c.lg)];
+      float p[8];
+      ckpt_values4(w[0], s, e.c.fmt, p);
+      ckpt_values4(w[1], s, e.c.fmt, p + 4);
+      slope_apply(e.act, p, v);
     }
   }
   if constexpr (PASS == P_FWD) {
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] += bias[i];
+    for (int i = 0; i < 8; ++i) v[i] += bias[i];
     if (e.c.codes) {
-      uint32_t m[R];
+      if (!full) {
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = i < n ? v[j][i] : 0.0f;  // no share beyond the row
-        m[j] = amax_bits(v[j]);
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] : 0.0f;  // no share beyond the row
       }
-      for (int o = 1; o < (1 << (e.c.lg - 2)); o <<= 1)
+      uint32_t m = amax_bits(v);
 #pragma unroll
-        for (int j = 0; j < R; ++j) m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (!in[j]) continue;
-        const Divisor d = ckpt_divisor(m[j], e.c.fmt);
-        const f2 x[2] = {mk2(v[j][0], v[j][1]), mk2(v[j][2], v[j][3])};
-        uint32_t w[1];
+      for (int o = 1; o < 16; o <<= 1)
+        if (o < 4 || o < (1 << (e.c.lg - 3))) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (in) {
+        const Divisor d = ckpt_divisor(m, e.c.fmt);
+        const f2 x[4] = {mk2(v[0], v[1]), mk2(v[2], v[3]), mk2(v[4], v[5]), mk2(v[6], v[7])};
+        uint32_t w[2];
         ckpt_codes(x, d, e.c.fmt, w);
-        store_bytes<4>(e.c.codes + (r + j) * e.cols + col, e.vec_codes && full, n, w);
-        if ((col & ((1 << e.c.lg) - 1)) == 0) e.c.scale[(r + j) * e.c.groups + (col >> e.c.lg)] = d.s;
+        store_bytes<8>(e.c.codes + r * e.cols + col, e.vec_codes && full, n, w);
+        if ((int(col) & ((1 << e.c.lg) - 1)) == 0) e.c.scale[r * e.c.groups + (col >> e.c.lg)] = d.s;
       }
     }
+    act_apply(e.act, v);
+  }
+  if (!in) return;
+  if (adds) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) act_apply(e.act, v[j]);
+    for (int i = 0; i < 8; ++i) v[i] += add[i];
+  }
+  if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32)
+    store_row(static_cast<float*>(e.out) + r * e.ldo + col, e.vec_out && full, n, v);
+  else
+    store_row(static_cast<bf16*>(e.out) + r * e.ldo + col, e.vec_out && full, n, v);
+}
+
+// Partial sums of 128 columns in shared memory: the 16-byte units of 4 columns with an
+// even number first, then the odd ones, so that the two units of a lane's 8 columns
+// lie at unit `lane` and unit 16 + `lane`: both reads of 16 lanes are contiguous (at a
+// stride of 32 bytes the reads from other CTAs took twice as long).
+__device__ __forceinline__ int unit_at(int unit) { return ((unit & 1) << 4) + (unit >> 1); }
+
+// The sums of 8 columns at `mine` (this CTA's address) over `slices` CTAs of the cluster,
+// `stride` ranks apart from rank `first`; all reads are on their way before the first
+// addition, which go in the slices' order.
+__device__ __forceinline__ void cluster_sum8(uint32_t mine, int slices, uint32_t first, uint32_t stride,
+                                             float (&v)[8]) {
+  float4 f[8][2];
+#pragma unroll
+  for (int sl = 0; sl < 8; ++sl) {
+    if (sl < slices) {
+      const uint32_t base = sm100::peer_addr(mine, first + stride * uint32_t(sl));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(f[sl][j].x), "=f"(f[sl][j].y), "=f"(f[sl][j].z), "=f"(f[sl][j].w)
+                     : "r"(base + uint32_t(256 * j)));
+    }
   }
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    if (!in[j]) continue;
-    if (adds) {
+  for (int j = 0; j < 2; ++j)
+    v[4 * j] = f[0][j].x, v[4 * j + 1] = f[0][j].y, v[4 * j + 2] = f[0][j].z, v[4 * j + 3] = f[0][j].w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] += add[j][i];
+  for (int sl = 1; sl < 8; ++sl) {
+    if (sl < slices) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        v[4 * j] += f[sl][j].x, v[4 * j + 1] += f[sl][j].y, v[4 * j + 2] += f[sl][j].z, v[4 * j + 3] += f[sl][j].w;
     }
-    if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32)
-      store_row(static_cast<float*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, v[j]);
-    else
-      store_row(static_cast<bf16*>(e.out) + (r + j) * e.ldo + col, e.vec_out && full, n, v[j]);
   }
 }
 
@@ -295,6 +317,21 @@ __device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t
     p = reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + col), q = p + n * 2;
   }
   for (; p < q; p += 128) prefetch_l2(p);
+}
+
+// lines of what row r's 128 columns from c0 on read, one per lane (of 16)
+template <int PASS>
+__device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0, int lane) {
+  const int64_t n = e.cols - c0 > 128 ? 128 : e.cols - c0;
+  const int64_t at = lane * 128;  // byte
+  if (PASS == P_WGRAD) {
+    const int es = e.out_dtype == AQFQ_F32 ? 4 : 2;
+    if (e.accumulate && at < n * es)
+      prefetch_l2(static_cast<const uint8_t*>(e.out) + (r * e.ldo + c0) * es + at);
+  } else {
+    if (e.res && at < n * 2) prefetch_l2(reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + c0) + at);
+    if (PASS == P_DGRAD && e.c.codes && lane == 8) prefetch_l2(e.c.codes + r * e.cols + c0);
+  }
 }
 
 // Columns [col, col + 16 kChunks) of row r (one row per lane of the warp), sums at
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (PASS == P_FWD && e.bias) {
           float b[4];
           __syncwarp();
-          load_bias4(e, (col & ~int64_t(127)) + lane * 4, b);
+          load_bias(e, (col & ~int64_t(127)) + lane * 4, b);
           *reinterpret_cast<float4*>(mybias + lane * 4) = make_float4(b[0], b[1], b[2], b[3]);
           __syncwarp();
         }
@@ -671,7 +708,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (live) {
         if (SPLIT) {
           // into this CTA's shared memory (its stages are all consumed)
-          float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * C::PSTRIDE + part * W;
+          float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * C::PSTRIDE + part * W / 128 * 128;
           uint32_t t[16];
           float v[16];
           tmem_issue(taddr, t);
@@ -681,7 +718,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (c + 1 < W / 16) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              *reinterpret_cast<float4*>(dst + unit_at((part * W % 128 + c * 16 + i) / 4) * 4) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         } else if (a.splits > 1) {
           float* dst = a.part + (int64_t(u / tiles) * e.rows + r) * a.cols4 + col;
@@ -709,47 +747,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
   }
   if constexpr (SPLIT) {
-    // this CTA's rows of the tile; a warp takes half the columns of R rows per turn
-    constexpr int R = 2, NW = kThreadsP / 32;
+    // this CTA's rows of the tile; a warp takes half the columns of two rows per turn
+    constexpr int NW = kThreadsP / 32;
     int tr, tc;
     tile_of(a, a.first + pair, tr, tc);
     const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
     const int nrows = e.rows - r0 > kHalf ? kHalf : (e.rows > r0 ? int(e.rows - r0) : 0);
-    const int half = warp & 1, rend = nrows * (slice + 1) / a.splits;
-    const int64_t col = int64_t(tc) * BN + half * (BN / 2) + lane * 4;
-    float bias[4] = {};
-    if (PASS == P_FWD) load_bias4(e, col, bias);
+    const int half = warp & 1, row0 = nrows * slice / a.splits, rend = nrows * (slice + 1) / a.splits;
+    const int64_t c0 = int64_t(tc) * BN + half * (BN / 2), col = c0 + (lane & 15) * 8;
+    float bias[8] = {};
+    if (PASS == P_FWD) load_bias(e, col, bias);
+    if (warp >= 4 && c0 < e.cols)
+      for (int row = row0 + (warp >> 1) * 2 + (lane >> 4); row < rend; row += NW)
+        prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
     __syncwarp();
     cluster_sync();  // every slice's partial sums are in shared memory
-    if (int64_t(tc) * BN + half * (BN / 2) < e.cols) {
+    if (c0 < e.cols) {
 #pragma unroll 1
-      for (int row = nrows * slice / a.splits + (warp >> 1) * R; row < rend; row += R * (NW / 2)) {
-        // every slice's values are on their way before the first is added
-        float4 f[8][R];
-        const uint32_t mine = smem_u32(smem) + uint32_t(row * C::PSTRIDE + half * (BN / 2) + lane * 4) * 4;
-#pragma unroll
-        for (int sl = 0; sl < 8; ++sl) {
-          if (sl < a.splits) {
-            const uint32_t base = peer_addr(mine, uint32_t(2 * sl) + rank);
-#pragma unroll
-            for (int j = 0; j < R; ++j)  // (a row past rend is another CTA's: read, not used)
-              asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                           : "=f"(f[sl][j].x), "=f"(f[sl][j].y), "=f"(f[sl][j].z), "=f"(f[sl][j].w)
-                           : "r"(base + uint32_t((row + j < kHalf ? j : 0) * C::PSTRIDE * 4)));
-          }
-        }
-        float v[R][4];
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j][0] = f[0][j].x, v[j][1] = f[0][j].y, v[j][2] = f[0][j].z, v[j][3] = f[0][j].w;
-#pragma unroll
-        for (int sl = 1; sl < 8; ++sl) {
-          if (sl < a.splits) {
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-              v[j][0] += f[sl][j].x, v[j][1] += f[sl][j].y, v[j][2] += f[sl][j].z, v[j][3] += f[sl][j].w;
-          }
-        }
-        epilogue4<PASS, R>(e, r0 + row, r0 + rend, col, bias, v);
+      for (int base = row0 + (warp >> 1) * 2; base < rend; base += NW) {
+        const int row = base + (lane >> 4);
+        // (a row past rend is another CTA's or the last one again: read, not used)
+        float v[8];
+        cluster_sum8(smem_u32(smem) + uint32_t((row < kHalf ? row : base) * C::PSTRIDE + half * (BN / 2) +
+                                               (lane & 15) * 4) * 4,
+                     a.splits, rank, 2, v);
+        epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
       }
     }
   }
@@ -761,21 +783,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     tmem_dealloc_pair(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
-}
-
-// lines of what row r's 128 columns from c0 on read, one per lane (of 16)
-template <int PASS>
-__device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0, int lane) {
-  const int64_t n = e.cols - c0 > kHalf ? kHalf : e.cols - c0;
-  const int64_t at = lane * 128;  // byte
-  if (PASS == P_WGRAD) {
-    const int es = e.out_dtype == AQFQ_F32 ? 4 : 2;
-    if (e.accumulate && at < n * es)
-      prefetch_l2(static_cast<const uint8_t*>(e.out) + (r * e.ldo + c0) * es + at);
-  } else {
-    if (e.res && at < n * 2) prefetch_l2(reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + c0) + at);
-    if (PASS == P_DGRAD && e.c.codes && lane == 8) prefetch_l2(e.c.codes + r * e.cols + c0);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -806,7 +813,6 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     tile_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
   constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
-  constexpr int R = 2;  // rows per warp and turn
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -905,14 +911,14 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     __syncwarp();
   }
   __syncwarp();
-  // this CTA's rows, R per warp and turn; what they read is sent to L2 meanwhile
+  // this CTA's rows, two per warp and turn; what they read is sent to L2 meanwhile
   const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
-  const int row0 = nrows * slice / a.splits + warp * R, rend = nrows * (slice + 1) / a.splits;
-  for (int row = row0 + (lane >> 4); row < rend; row += R * kWarpsC)
+  const int row0 = nrows * slice / a.splits + warp * 2, rend = nrows * (slice + 1) / a.splits;
+  for (int row = row0 + (lane >> 4); row < rend; row += 2 * kWarpsC)
     prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
-  const int64_t col = c0 + lane * 4;
-  float bias[4] = {};
-  if (PASS == P_FWD) load_bias4(e, col, bias);
+  const int64_t col = c0 + (lane & 15) * 8;
+  float bias[8] = {};
+  if (PASS == P_FWD) load_bias(e, col, bias);
   __syncwarp();
   if (!mbar_wait_suspend(&sh->accum, 0)) *abort = 1;
   __syncwarp();
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     const int q = warp & 3, part = warp >> 2;  // 32 rows x 32 columns
     if (q * 32 < nrows) {
       const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(part * 32);
-      float* dst = sums + (q * 32 + lane) * kStrideC + part * 32;
+      float* dst = sums + (q * 32 + lane) * kStrideC;
       uint32_t t[16];
       float v[16];
       tmem_issue(taddr, t);
@@ -932,7 +938,8 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         if (c < 1) tmem_issue(taddr + 16, t);
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          *reinterpret_cast<float4*>(dst + unit_at((part * 32 + c * 16 + i) / 4) * 4) =
+              make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
   }
@@ -940,41 +947,18 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   if (a.splits > 1) cluster_sync();
   else __syncthreads();
 #pragma unroll 1
-  for (int row = row0; row < rend; row += R * kWarpsC) {
-    float v[R][4];
+  for (int base = row0; base < rend; base += 2 * kWarpsC) {
+    const int row = base + (lane >> 4);
+    // (a row past rend is another CTA's or the last one again: read, not used)
+    const float* at = sums + (row < kTile ? row : base) * kStrideC + (lane & 15) * 4;
+    float v[8];
     if (a.splits > 1) {
-      // every slice's values are on their way before the first is added
-      float4 f[8][R];
-      const uint32_t mine = smem_u32(sums + row * kStrideC + lane * 4);
-#pragma unroll
-      for (int sl = 0; sl < 8; ++sl) {
-        if (sl < a.splits) {
-          const uint32_t base = peer_addr(mine, uint32_t(sl));
-#pragma unroll
-          for (int j = 0; j < R; ++j)  // (a row past rend is another CTA's: read, not used)
-            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(f[sl][j].x), "=f"(f[sl][j].y), "=f"(f[sl][j].z), "=f"(f[sl][j].w)
-                         : "r"(base + uint32_t((row + j < kTile ? j : 0) * kStrideC * 4)));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < R; ++j) v[j][0] = f[0][j].x, v[j][1] = f[0][j].y, v[j][2] = f[0][j].z, v[j][3] = f[0][j].w;
-#pragma unroll
-      for (int sl = 1; sl < 8; ++sl) {
-        if (sl < a.splits) {
-#pragma unroll
-          for (int j = 0; j < R; ++j)
-            v[j][0] += f[sl][j].x, v[j][1] += f[sl][j].y, v[j][2] += f[sl][j].z, v[j][3] += f[sl][j].w;
-        }
-      }
+      cluster_sum8(smem_u32(at), a.splits, 0, 1, v);
     } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const float4 f = *reinterpret_cast<const float4*>(sums + (row + j < kTile ? row + j : row) * kStrideC + lane * 4);
-        v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
-      }
+      const float4 f = *reinterpret_cast<const float4*>(at), g = *reinterpret_cast<const float4*>(at + 64);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
     }
-    epilogue4<PASS, R>(e, r0 + row, r0 + rend, col, bias, v);
+    epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
   }
   tc_fence_before_sync();
   __syncwarp();
@@ -988,24 +972,28 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
 }
 
 // out = epilogue(sum of the slices' partial sums, in order); also the empty
-// product (splits 0): a warp takes 128 columns of a row
+// product (splits 0): a warp takes 128 columns of two rows
 template <int PASS>
 __global__ void __launch_bounds__(256)
     finish_kernel(const float* part, int splits, int64_t cols4, const Epi e) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = int64_t(blockIdx.x) * 128 + lane * 4;
-  float bias[4];
-  if (PASS == P_FWD) load_bias4(e, col, bias);
-  for (int64_t r = int64_t(blockIdx.y) * 8 + warp; r < e.rows; r += int64_t(gridDim.y) * 8) {
-    float v[1][4] = {};
-    if (col < cols4) {
-      const float* p = part + r * cols4 + col;
-      for (int s = 0; s < splits; ++s) {
-        const float4 f = *reinterpret_cast<const float4*>(p + int64_t(s) * e.rows * cols4);
-        v[0][0] += f.x, v[0][1] += f.y, v[0][2] += f.z, v[0][3] += f.w;
+  const int64_t col = int64_t(blockIdx.x) * 128 + (lane & 15) * 8;
+  float bias[8] = {};
+  if (PASS == P_FWD) load_bias(e, col, bias);
+  for (int64_t base = int64_t(blockIdx.y) * 16 + warp * 2; base < e.rows; base += int64_t(gridDim.y) * 16) {
+    const int64_t r = base + (lane >> 4);
+    float v[8] = {};
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      if (r < e.rows && col + j < cols4) {
+        const float* p = part + r * cols4 + col + j;
+        for (int s = 0; s < splits; ++s) {
+          const float4 f = *reinterpret_cast<const float4*>(p + int64_t(s) * e.rows * cols4);
+          v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
+        }
       }
     }
-    epilogue4<PASS, 1>(e, r, e.rows, col, bias, v);
+    epilogue8<PASS>(e, r, r < e.rows, col, bias, v);
   }
 }
 
@@ -1206,7 +1194,7 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     }
   }
   if (p.splits != 1 && !p.cluster) {
-    const int64_t gy = (e.rows + 7) / 8;
+    const int64_t gy = (e.rows + 15) / 16;
     finish_kernel<PASS><<<dim3(unsigned((e.cols + 127) / 128), unsigned(gy > 65535 ? 65535 : gy)), 256,
                           0, st>>>(part, p.splits, p.cols4, e);
     if (cudaGetLastError() != cudaSuccess) return AQFQ_ERR_CUDA;
@@ -1225,10 +1213,10 @@ bool inner_ok(int64_t v, int64_t lda, int64_t ldb) {
 bool operand_ok(const void* p, int64_t ld) { return al(p, 16) && ld % 8 == 0; }
 
 void finish_epi(Epi& e, int es) {
-  e.vec_out = rows_aligned<4>(e.out, e.ldo, es);
-  e.vec_res = rows_aligned<4>(e.res, e.ldr, 2);
-  e.vec_bias = rows_aligned<4>(e.bias, 4, esize(e.bias_dtype));
-  e.vec_codes = rows_aligned<4>(e.c.codes, e.cols, 1);
+  e.vec_out = rows_aligned<8>(e.out, e.ldo, es);
+  e.vec_res = rows_aligned<8>(e.res, e.ldr, 2);
+  e.vec_bias = rows_aligned<8>(e.bias, 8, esize(e.bias_dtype));
+  e.vec_codes = rows_aligned<8>(e.c.codes, e.cols, 1);
 }
 
 }  // namespace
