@@ -371,8 +371,12 @@ _FL = (torch.float32,)
 _I32 = (torch.int32,)
 
 
+# the type codes of the tensors that the checks above let through (None: BF16)
+_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
 def _dt(t):
-    return F32 if t is not None and t.dtype == torch.float32 else BF16
+    return BF16 if t is None else _CODE.get(t.dtype, BF16)
 
 
 def _ws(workspace):
@@ -414,15 +418,17 @@ def _ck(c, rows, cols):
 def aqfq_ckpt8_pack(ckpt, x, stream=None):
     p, ld = _mat(x, "x", _ROWS)
     R, C = x.shape
-    _check("aqfq_ckpt8_pack",
-           lib().aqfq_ckpt8_pack(_ck(ckpt, R, C), _dt(x), p, ld, R, C, _stream(stream)))
+    st = (_lib or lib()).aqfq_ckpt8_pack(_ck(ckpt, R, C), _dt(x), p, ld, R, C, _stream(stream))
+    if st:
+        _check("aqfq_ckpt8_pack", st)
 
 
 def aqfq_ckpt8_unpack(ckpt, y, act=ACT_NONE, stream=None):
     p, ld = _mat(y, "y", _ROWS)
     R, C = y.shape
-    _check("aqfq_ckpt8_unpack",
-           lib().aqfq_ckpt8_unpack(_ck(ckpt, R, C), int(act), _dt(y), p, ld, R, C, _stream(stream)))
+    st = (_lib or lib()).aqfq_ckpt8_unpack(_ck(ckpt, R, C), int(act), _dt(y), p, ld, R, C, _stream(stream))
+    if st:
+        _check("aqfq_ckpt8_unpack", st)
 
 
 def aqfq_ckpt8_act_bwd_workspace_bytes(rows, cols) -> int:
@@ -437,10 +443,12 @@ def aqfq_ckpt8_act_bwd(ckpt, act, dy, dx=None, y=None, dbias=None, accumulate=Fa
     px, ldx = _mat(dx, "dx", (dy.dtype,), (R, C))
     py, ldy = _mat(y, "y", (dy.dtype,), (R, C))
     ws, wsb = _ws(workspace)
-    _check("aqfq_ckpt8_act_bwd",
-           lib().aqfq_ckpt8_act_bwd(_ck(ckpt, R, C), int(act), _dt(dy), pd, ldd, R, C, px, ldx, py,
-                                    ldy, _vec(dbias, "dbias", _FL, C), int(bool(accumulate)), ws, wsb,
-                                    _stream(stream)))
+    st = (_lib or lib()).aqfq_ckpt8_act_bwd(
+        _ck(ckpt, R, C), int(act), _dt(dy), pd, ldd, R, C, px, ldx, py,
+        ldy, _vec(dbias, "dbias", _FL, C), 1 if accumulate else 0, ws, wsb,
+        _stream(stream))
+    if st:
+        _check("aqfq_ckpt8_act_bwd", st)
 
 
 def aqfq_layernorm_fwd(x, gamma, beta, eps, y, mean=None, rstd=None, ckpt=None, stream=None):
@@ -451,11 +459,13 @@ def aqfq_layernorm_fwd(x, gamma, beta, eps, y, mean=None, rstd=None, ckpt=None, 
     par = gamma if gamma is not None else beta
     if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
         raise TypeError("gamma and beta must have one type")
-    _check("aqfq_layernorm_fwd",
-           lib().aqfq_layernorm_fwd(_dt(x), px, ldx, R, C, _dt(par), _vec(gamma, "gamma", _ROWS, C),
-                                    _vec(beta, "beta", _ROWS, C), float(eps), py, ldy,
-                                    _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
-                                    _ck(ckpt, R, C), _stream(stream)))
+    st = (_lib or lib()).aqfq_layernorm_fwd(
+        _dt(x), px, ldx, R, C, _dt(par), _vec(gamma, "gamma", _ROWS, C),
+        _vec(beta, "beta", _ROWS, C), float(eps), py, ldy,
+        _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
+        _ck(ckpt, R, C), _stream(stream))
+    if st:
+        _check("aqfq_layernorm_fwd", st)
 
 
 def aqfq_layernorm_bwd_workspace_bytes(rows, cols) -> int:
@@ -472,12 +482,14 @@ def aqfq_layernorm_bwd(dy, x, mean, rstd, gamma, dx=None, dgamma=None, dbeta=Non
     pr, ldr = _mat(dres, "dres", dt, (R, C))
     po, ldo = _mat(dx, "dx", dt, (R, C))
     ws, wsb = _ws(workspace)
-    _check("aqfq_layernorm_bwd",
-           lib().aqfq_layernorm_bwd(_dt(dy), pd, ldd, px, ldx, _ck(ckpt, R, C), R, C,
-                                    _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
-                                    _dt(gamma), _vec(gamma, "gamma", _ROWS, C), pr, ldr, po, ldo,
-                                    _vec(dgamma, "dgamma", _FL, C), _vec(dbeta, "dbeta", _FL, C),
-                                    int(bool(accumulate)), ws, wsb, _stream(stream)))
+    st = (_lib or lib()).aqfq_layernorm_bwd(
+        _dt(dy), pd, ldd, px, ldx, _ck(ckpt, R, C), R, C,
+        _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
+        _dt(gamma), _vec(gamma, "gamma", _ROWS, C), pr, ldr, po, ldo,
+        _vec(dgamma, "dgamma", _FL, C), _vec(dbeta, "dbeta", _FL, C),
+        1 if accumulate else 0, ws, wsb, _stream(stream))
+    if st:
+        _check("aqfq_layernorm_bwd", st)
 
 
 def aqfq_linear_workspace_bytes(kind, M, N, K) -> int:
@@ -494,10 +506,12 @@ def aqfq_linear_fwd(x, w, y, bias=None, act=ACT_NONE, residual=None, ckpt=None, 
     pr, ldr = _mat(residual, "residual", _BF, (M, N))
     py, ldy = _mat(y, "y", _BF, (M, N))
     ws, wsb = _ws(workspace)
-    _check("aqfq_linear_fwd",
-           lib().aqfq_linear_fwd(px, ldx, pw, ldw, M, N, K, _dt(bias), _vec(bias, "bias", _ROWS, N),
-                                 int(act), pr, ldr, py, ldy, _ck(ckpt, M, N), ws, wsb,
-                                 _flag(error_flag), _stream(stream)))
+    st = (_lib or lib()).aqfq_linear_fwd(
+        px, ldx, pw, ldw, M, N, K, _dt(bias), _vec(bias, "bias", _ROWS, N),
+        int(act), pr, ldr, py, ldy, _ck(ckpt, M, N), ws, wsb,
+        _flag(error_flag), _stream(stream))
+    if st:
+        _check("aqfq_linear_fwd", st)
 
 
 def aqfq_linear_dgrad(dy, w, dx, act=ACT_NONE, ckpt=None, residual=None, workspace=None,
@@ -510,9 +524,11 @@ def aqfq_linear_dgrad(dy, w, dx, act=ACT_NONE, ckpt=None, residual=None, workspa
     pr, ldr = _mat(residual, "residual", _BF, (M, K))
     po, ldo = _mat(dx, "dx", _BF, (M, K))
     ws, wsb = _ws(workspace)
-    _check("aqfq_linear_dgrad",
-           lib().aqfq_linear_dgrad(pd, ldd, pw, ldw, M, N, K, int(act), _ck(ckpt, M, K), pr, ldr, po,
-                                   ldo, ws, wsb, _flag(error_flag), _stream(stream)))
+    st = (_lib or lib()).aqfq_linear_dgrad(
+        pd, ldd, pw, ldw, M, N, K, int(act), _ck(ckpt, M, K), pr, ldr, po,
+        ldo, ws, wsb, _flag(error_flag), _stream(stream))
+    if st:
+        _check("aqfq_linear_dgrad", st)
 
 
 def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=None, stream=None):
@@ -523,10 +539,12 @@ def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=No
     px, ldx = _mat(x, "x", _BF, (M, K))
     po, ldo = _mat(dw, "dw", _ROWS, (N, K))
     ws, wsb = _ws(workspace)
-    _check("aqfq_linear_wgrad",
-           lib().aqfq_linear_wgrad(pd, ldd, px, ldx, M, N, K, _dt(dw), po, ldo,
-                                   int(bool(accumulate)), ws, wsb, _flag(error_flag),
-                                   _stream(stream)))
+    st = (_lib or lib()).aqfq_linear_wgrad(
+        pd, ldd, px, ldx, M, N, K, _dt(dw), po, ldo,
+        1 if accumulate else 0, ws, wsb, _flag(error_flag),
+        _stream(stream))
+    if st:
+        _check("aqfq_linear_wgrad", st)
 
 
 def aqfq_status_string(status: int) -> str:
