@@ -506,6 +506,7 @@ struct __align__(8) PairShared {
 struct PairArgs {
   int nr, nc;        // tiles
   int first, count;  // the tiles of this launch
+  int quad;          // tile order for clusters of two pairs
   int splits;        // slices of the inner axis
   int a_rows;        // rows of A per box (tile_kernel: fewer when there are fewer rows)
   int ksteps;        // 64-element steps of the inner axis
@@ -514,20 +515,28 @@ struct PairArgs {
   int32_t* err;
 };
 
-// tile t of nr x nc: groups of 8 tile rows, column by column, so that the tiles in
-// flight share their operands in L2
+// tile t: groups of 8 tile rows, column by column, so that the tiles in flight share
+// their operands in L2.  quad: t counts pairs of rows (2 t' + 0, 2 t' + 1 are two rows of
+// one column, the two pairs of a cluster of four CTAs).
 __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& tc) {
-  const int width = 8 * a.nc, g = t / width, first = g * 8;
-  const int gm = a.nr - first < 8 ? a.nr - first : 8;
-  const int in = t - g * width;
+  const int u = a.quad ? t >> 1 : t, nr = a.quad ? a.nr >> 1 : a.nr, high = a.quad ? 4 : 8;
+  const int width = high * a.nc, g = u / width, first = g * high;
+  const int gm = nr - first < high ? nr - first : high;
+  const int in = u - g * width;
   tr = first + in % gm;
   tc = in / gm;
+  if (a.quad) tr = 2 * tr + (t & 1);
 }
 
 // SPLIT: a cluster of S pairs takes one tile, pair i the i-th slice of the inner
 // axis; the partial sums meet through distributed shared memory, each CTA finishing
 // its share of the rows (one launch, no scratch; the sums in the slices' order).
-template <int PASS, int ACT, int BN, bool SPLIT>
+// MC: a cluster of two pairs takes two tiles of one column; each pair loads half of
+// their common columns' operand and multicasts it to the other.  The sum of what the
+// SMs read from L2 bounds the main loop (about 14.7 TB/s in sum, 0.34 us per step with
+// every pair loading all of its operands); a stage is then free when both pairs have
+// read it.
+template <int PASS, int ACT, int BN, bool SPLIT, bool MC>
 __global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
@@ -541,16 +550,18 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   PairShared* sh = reinterpret_cast<PairShared*>(reinterpret_cast<uint8_t*>(sbias) + C::BIAS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
+  static_assert(!(SPLIT && MC), "one use of the cluster");
   const int tiles = a.count, units = SPLIT ? tiles : tiles * a.splits;
   // one unit per cluster, or a strided share of the units per pair
   const int pair = SPLIT ? blockIdx.x / (2 * a.splits) : blockIdx.x >> 1;
   const int npairs = SPLIT ? units : gridDim.x >> 1;
   const int slice = int(crank >> 1);
+  const uint32_t mask = 3u << lead;  // the pair's CTAs
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->empty[s], MC ? 2 : 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->tfull[b], 1);
@@ -598,7 +609,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           } else {
             tma_load_2d_pair(da, &ta, bar, k * kBK, r0);
           }
-          if constexpr (B_MN) {
+          if constexpr (MC) {
+            // 64 of this CTA's 128 columns, for both pairs' CTAs of this rank
+            const uint16_t to = uint16_t(5u << rank);
+            const int off = 64 * slice;
+            if constexpr (B_MN)
+              tma_load_2d_pair_mc(db + slice * 8192, &tb, bar, c0 + off, k * kBK, to);
+            else
+              tma_load_2d_pair_mc(db + slice * 8192, &tb, bar, k * kBK, c0 + off, to);
+          } else if constexpr (B_MN) {
 #pragma unroll
             for (int j = 0; j < BN / 128; ++j)
               tma_load_2d_pair(db + j * 8192, &tb, bar, c0 + 64 * j, k * kBK);
@@ -648,8 +667,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc_mma_f16_pair(d, da, db, idesc, k > k0 ? 1u : 0u);
 #pragma unroll
             for (int kk = 1; kk < kBK / 16; ++kk) tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, 1u);
-            tc_commit_pair(&sh->empty[s], lead);
-            if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf], lead);
+            tc_commit_pair(&sh->empty[s], MC ? 15u : mask);
+            if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf], mask);
           }
           __syncwarp();
           if (++s == C::STAGES) {
@@ -660,7 +679,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       if (!ok) {  // a wait timed out: drain the MMAs already issued
         *abort = 1;
-        if (elect_one()) tc_commit_pair(&sh->drain, lead);
+        if (elect_one()) tc_commit_pair(&sh->drain, mask);
         __syncwarp();
         mbar_wait_suspend(&sh->drain, 0);
       }
@@ -1045,11 +1064,13 @@ struct Plan {
   bool small;     // tile_kernel (128 x 128 tiles, one CTA each)
   int a_rows;     // rows of A per box
   int tail, tail_splits;  // last tiles that a second launch splits (0: none)
+  int quad;       // clusters of two pairs with multicast
   int64_t cols4;
   size_t bytes;   // scratch
 };
 
 constexpr int kPairs = 76;  // SM pairs
+constexpr double kStepPair = 0.34, kStepQuad = 0.30;  // us per 64 of the inner axis, every SM busy
 static_assert(kBN / 2 == kHalf && kTile == kHalf, "one box for every operand tile");
 
 // Clusters of 2 S CTAs (one per SM) that run at the same time on this GPU, by S
@@ -1068,7 +1089,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
   p.cluster = p.small = false;
-  p.a_rows = kHalf, p.tail = p.tail_splits = 0;
+  p.a_rows = kHalf, p.tail = p.tail_splits = p.quad = 0;
   const int64_t tiles = int64_t(p.nr) * p.nc;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
   if (small <= kClustersC[1] && p.ksteps > 0 && !(tiles <= 9 && p.ksteps >= 128)) {
@@ -1092,23 +1113,32 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
     p.splits = sp;
     p.cluster = sp > 1;
   } else if (tiles > kPairs) {
-    // The last round has `rem` tiles for 76 pairs.  Where they are few, a second launch
-    // splits them; it pays when the time it saves (0.34 us per step) exceeds its own
-    // start, joining and epilogue (about 8 us).
-    const int rem = int(tiles % kPairs);
-    int sp = 8;
-    while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
-    if (rem > 0 && sp > 1 && 0.34 * p.ksteps * (1.0 - 1.0 / sp) > 10.0) p.tail = rem, p.tail_splits = sp;
+    // Clusters of two pairs (72 pairs run together, a step takes kStepQuad us) against
+    // single pairs (76, kStepPair us); the tiles of the last round, where they are few,
+    // are split by a second launch, at about 9 us of its own (start, joining, epilogue).
+    double best = 1e30;
+    for (int quad = p.nr % 2 == 0 ? 1 : 0; quad >= 0; --quad) {
+      const int64_t at_once = quad ? 2 * kClusters[2] : kPairs;
+      const double step = p.ksteps * (quad ? kStepQuad : kStepPair);
+      const int64_t rounds = tiles / at_once;
+      const int rem = int(tiles % at_once);
+      const double plain = step * double(rounds + (rem > 0));
+      if (plain < best) best = plain, p.quad = quad, p.tail = p.tail_splits = 0;
+      int sp = 8;
+      while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
+      const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 9.0;
+      if (rem > 0 && sp > 1 && split < best) best = split, p.quad = quad, p.tail = rem, p.tail_splits = sp;
+    }
   }
   p.cols4 = (cols + 3) / 4 * 4;
   p.bytes = p.splits > 1 && !p.cluster ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
   return p;
 }
 
-template <int PASS, int ACT, bool SPLIT>
+template <int PASS, int ACT, bool SPLIT, bool MC>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
-  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
+  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT, MC>;
   static const cudaError_t attr = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
   if (attr != cudaSuccess) return attr;
@@ -1119,8 +1149,9 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   }
   const int64_t tiles = a.count, units = tiles * a.splits;
   cudaLaunchConfig_t cfg = {};
-  const int csize = SPLIT ? 2 * a.splits : 2;
-  cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < kPairs ? units : kPairs));
+  const int csize = SPLIT ? 2 * a.splits : MC ? 4 : 2;
+  const int64_t most = MC ? 2 * kClusters[2] : kPairs;  // pairs that run together
+  cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < most ? units : most));
   cfg.blockDim = dim3(kThreadsP);
   cfg.dynamicSmemBytes = Cfg<kBN>::SMEM;
   cfg.stream = st;
@@ -1129,6 +1160,22 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   at[0].val.clusterDim.x = unsigned(csize), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, a, e);
+}
+
+template <int PASS, bool MC>
+cudaError_t launch_act(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
+                       cudaStream_t st) {
+  if constexpr (PASS == P_WGRAD) {
+    return launch_pair<PASS, AQFQ_ACT_NONE, false, MC>(ta, tb, a, e, st);
+  } else {
+    switch (e.act) {
+      case AQFQ_ACT_RELU: return launch_pair<PASS, AQFQ_ACT_RELU, false, MC>(ta, tb, a, e, st);
+      case AQFQ_ACT_GELU: return launch_pair<PASS, AQFQ_ACT_GELU, false, MC>(ta, tb, a, e, st);
+      case AQFQ_ACT_GELU_TANH: return launch_pair<PASS, AQFQ_ACT_GELU_TANH, false, MC>(ta, tb, a, e, st);
+      case AQFQ_ACT_SILU: return launch_pair<PASS, AQFQ_ACT_SILU, false, MC>(ta, tb, a, e, st);
+      default: return launch_pair<PASS, AQFQ_ACT_NONE, false, MC>(ta, tb, a, e, st);
+    }
+  }
 }
 
 template <int PASS>
@@ -1166,31 +1213,26 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     if (!encode(&ta, A, kBK, A_MN ? kBK : unsigned(p.a_rows)) ||
         !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
       return AQFQ_ERR_CUDA;
-    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
+    CUtensorMap tb64;
+    if (p.quad && !encode(&tb64, B, kBK, kBK)) return AQFQ_ERR_CUDA;
+    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.quad, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
     cudaError_t r;
     a.count -= p.tail;
     if (p.small) {
       r = launch_tile<PASS>(ta, tb, a, e, st);
     } else if (p.cluster) {
-      r = launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st);
-    } else if (PASS == P_WGRAD || p.splits > 1) {  // finish_kernel has the epilogue, or it is plain
-      r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
+      r = launch_pair<PASS, AQFQ_ACT_NONE, true, false>(ta, tb, a, e, st);
+    } else if (p.splits > 1) {  // finish_kernel has the epilogue
+      r = launch_pair<PASS, AQFQ_ACT_NONE, false, false>(ta, tb, a, e, st);
+    } else if (p.quad) {
+      r = launch_act<PASS, true>(ta, tb64, a, e, st);
     } else {
-      constexpr bool W = PASS == P_WGRAD;  // (instantiated once)
-      switch (e.act) {
-        case AQFQ_ACT_RELU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_RELU, false>(ta, tb, a, e, st); break;
-        case AQFQ_ACT_GELU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_GELU, false>(ta, tb, a, e, st); break;
-        case AQFQ_ACT_GELU_TANH:
-          r = launch_pair<PASS, W ? 0 : AQFQ_ACT_GELU_TANH, false>(ta, tb, a, e, st);
-          break;
-        case AQFQ_ACT_SILU: r = launch_pair<PASS, W ? 0 : AQFQ_ACT_SILU, false>(ta, tb, a, e, st); break;
-        default: r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st); break;
-      }
+      r = launch_act<PASS, false>(ta, tb, a, e, st);
     }
     if (r != cudaSuccess) return AQFQ_ERR_CUDA;
     if (p.tail > 0) {
       a.first = a.count, a.count = p.tail, a.splits = p.tail_splits;
-      if (launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
+      if (launch_pair<PASS, AQFQ_ACT_NONE, true, false>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
     }
   }
   if (p.splits != 1 && !p.cluster) {

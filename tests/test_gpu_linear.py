@@ -320,3 +320,36 @@ def test_many_tiles_exact():
     x2, dy2 = ints((72, 2056), 4), ints((72, 2100), 5)
     dw = run_wgrad(dy2, x2, torch.float32)
     assert torch.equal(dw.cpu(), dy2.float().T @ x2.float())
+
+
+@pytest.mark.parametrize("M,N", [(2560, 2056), (2550, 2300), (4608, 1290)])
+def test_many_tiles_in_clusters_of_two_pairs_exact(M, N):
+    """An even number of tile rows: two pairs share their columns' operand; full
+    rounds, a ragged last round, ragged edges in both axes."""
+    K = 328
+    x, w, dy = ints((M, K), 1), ints((N, K), 2), ints((M, N), 3, 1)
+    for seed in (0, 1):
+        y, codes, scale = run_fwd(x, w, None, "none", None, "int8", 128, seed=seed)
+        p = x.float() @ w.float().T
+        assert torch.equal(y.cpu(), p.bfloat16())
+        q, s = pack_ref(p, "int8", 128)
+        np.testing.assert_array_equal(grid_values(codes, "int8"), q)
+        dy2, w2 = ints((M, K), 4), ints((K, N), 5)
+        dx = run_dgrad(dy2, w2, seed=seed)
+        assert torch.equal(dx.cpu(), (dy2.float() @ w2.float()).bfloat16())
+        dy3, x3 = ints((K, M), 6), ints((K, N), 7)
+        dw = run_wgrad(dy3, x3, torch.float32, seed=seed)
+        assert torch.equal(dw.cpu(), dy3.float().T @ x3.float())
+
+
+def test_last_tiles_split_by_a_second_launch_exact():
+    """A long inner axis whose last round has few tiles: those are split along it."""
+    M, N, K = 2560, 2304, 4104  # 90 tiles
+    x, w = ints((M, K), 1, 1), ints((N, K), 2, 1)
+    bias, res = ints((N,), 3), ints((M, N), 4)
+    y, codes, scale = run_fwd(x, w, bias, "relu", res, "e4m3", 64)
+    p = (x.float().cuda() @ w.float().cuda().T).cpu() + bias.float()
+    assert torch.equal(y.cpu(), (torch.clamp(p, min=0) + res.float()).bfloat16())
+    q, s = pack_ref(p, "e4m3", 64)
+    np.testing.assert_array_equal(scale.cpu().numpy(), s)
+    np.testing.assert_array_equal(grid_values(codes, "e4m3"), q)
