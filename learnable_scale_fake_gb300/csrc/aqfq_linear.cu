@@ -582,27 +582,28 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   volatile int32_t* abort = &sh->abort;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int u = pair; u < units && ok; u += npairs) {
-        int tr, tc;
-        tile_of(a, a.first + u % tiles, tr, tc);
-        const int sp = SPLIT ? slice : u / tiles;
-        const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
-        const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
-        const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int s = it % C::STAGES;
-          if (*abort || (it >= C::STAGES &&
-                         !mbar_wait_suspend(&sh->empty[s], ((it / C::STAGES) & 1) ^ 1))) {
-            *abort = 1;
-            ok = false;
-            break;
-          }
-          const uint32_t bar = peer_addr(smem_u32(&sh->full[s]), lead);
+    // a warp-uniform loop; one elected lane issues (see elect_one)
+    int s = 0, it = 0;
+    uint32_t phase = 1;  // the first round finds every stage empty
+    bool ok = true;
+    const uint32_t full0 = peer_addr(smem_u32(&sh->full[0]), lead);
+    const uint32_t da0 = smem_u32(smem), db0 = smem_u32(sb);
+    for (int u = pair; u < units && ok; u += npairs) {
+      int tr, tc;
+      tile_of(a, a.first + u % tiles, tr, tc);
+      const int sp = SPLIT ? slice : u / tiles;
+      const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
+      const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
+      const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
+      for (int k = k0; k < k1; ++k, ++it) {
+        if (it >= C::STAGES && !mbar_wait_long(&sh->empty[s], phase)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t bar = full0 + uint32_t(s * 8);
           if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * C::STAGE);
-          const uint32_t da = smem_u32(smem + s * kABytes), db = smem_u32(sb + s * C::B_BYTES);
+          const uint32_t da = da0 + s * kABytes, db = db0 + s * C::B_BYTES;
           if constexpr (A_MN) {
             tma_load_2d_pair(da, &ta, bar, r0, k * kBK);
             tma_load_2d_pair(da + kABytes / 2, &ta, bar, r0 + 64, k * kBK);
@@ -625,12 +626,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tma_load_2d_pair(db, &tb, bar, k * kBK, c0);
           }
         }
+        __syncwarp();
+        if (++s == C::STAGES) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      if (!ok && rank == 0) {
-        // let the copies already issued (the peer's among them) land
+    }
+    if (!ok) {
+      *abort = 1;
+      // let the copies already issued (the peer's among them) land
+      if (rank == 0)
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-          mbar_wait_suspend(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
-      }
+          mbar_wait_long(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -650,14 +658,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
         const int buf = n & 1;
-        if (n >= 2 && !mbar_wait_suspend(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
+        if (n >= 2 && !mbar_wait_long(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + uint32_t(buf * 256);
         for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait_suspend(&sh->full[s], phase)) {
+          if (!mbar_wait_long(&sh->full[s], phase)) {
             ok = false;
             break;
           }
@@ -681,7 +689,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         *abort = 1;
         if (elect_one()) tc_commit_pair(&sh->drain, mask);
         __syncwarp();
-        mbar_wait_suspend(&sh->drain, 0);
+        mbar_wait_long(&sh->drain, 0);
       }
     }
   } else if (warp >= 4) {
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     int s = 0;
     uint32_t phase = 1;  // the first round finds every stage empty
     for (int k = 0; k < n; ++k) {
-      if (k >= kStagesC && !mbar_wait_suspend(&sh->empty[s], phase)) {
+      if (k >= kStagesC && !mbar_wait_long(&sh->empty[s], phase)) {
         *abort = 1;
         break;
       }
@@ -908,7 +916,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     int s = 0;
     uint32_t phase = 0;
     for (int k = 0; k < n; ++k) {
-      if (!mbar_wait_suspend(&sh->full[s], phase)) {
+      if (!mbar_wait_long(&sh->full[s], phase)) {
         *abort = 1;
         break;
       }
@@ -939,7 +947,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   float bias[8] = {};
   if (PASS == P_FWD) load_bias(e, col, bias);
   __syncwarp();
-  if (!mbar_wait_suspend(&sh->accum, 0)) *abort = 1;
+  if (!mbar_wait_long(&sh->accum, 0)) *abort = 1;
   __syncwarp();
   tc_fence_after_sync();
   float* sums = reinterpret_cast<float*>(smem);

@@ -23,22 +23,26 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait_suspend with a longer suspension per try (hint in ns), for waits of
-// whole tiles: the waiting warp leaves the issue slots to the others
+// Waits for a phase: one try first, for a phase that is complete already or soon;
+// then tries that may suspend the warp for long (hint in ns), which leaves the issue
+// slots to the others.  Gives up after about 2^31 cycles (~1 s) and returns false.
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity, uint32_t hint) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity) {
+  if (mbar_try(bar, parity, 1000000u)) return true;
   const long long t0 = clock64();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (ok) return true;
-    if (clock64() - t0 > (1ll << 31)) return false;
-  }
+  while (clock64() - t0 <= (1ll << 31))
+    if (mbar_try(bar, parity, 1000000u)) return true;
+  return false;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
