@@ -38,6 +38,7 @@ struct Epi {
   int64_t ldo;
   int bias_dtype, out_dtype, act, accumulate;
   bool vec_out, vec_res, vec_bias, vec_codes;  // 8-element accesses are aligned
+  bool wide;            // 16-element accesses (32 bytes) of out and res, 16 of codes
   Ckpt c;               // forward: written; input gradient: read
 };
 
@@ -319,6 +320,15 @@ __device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t
   for (; p < q; p += 128) prefetch_l2(p);
 }
 
+// 16 bias values in shared memory (16-byte aligned, the same for every lane)
+__device__ __forceinline__ void add_bias16(const float* sb, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(sb + i);
+    v[i] += b.x, v[i + 1] += b.y, v[i + 2] += b.z, v[i + 3] += b.w;
+  }
+}
+
 // lines of what row r's 128 columns from c0 on read, one per lane (of 16)
 template <int PASS>
 __device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0, int lane) {
@@ -366,10 +376,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
         tmem_take(t, v);
         if (c + 1 < gend) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
         const int64_t left = e.cols - (col + c * 16);
-        if (e.bias) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += sb[c * 16 + i];
-        }
+        if (e.bias) add_bias16(sb + c * 16, v);
         if (left < 16) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = i < left ? v[i] : 0.0f;
@@ -398,10 +405,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
       tmem_take(t, v);
       if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
       if (PASS == P_FWD) {
-        if (e.bias) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += sb[c * 16 + i];
-        }
+        if (e.bias) add_bias16(sb + c * 16, v);
         if (codes_out && in) {
           uint32_t w[4];
           f2 x[8];
@@ -459,6 +463,104 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
           st16(p, q.a32, q.a16, n, w);
         }
       }
+    }
+  }
+}
+
+// Whether epilogue_whole serves a warp's 32 rows and 16 kChunks columns: all of them
+// exist and every access is aligned (uniform).
+template <int PASS>
+__device__ __forceinline__ bool whole_block(const Epi& e, int64_t r0, int64_t col) {
+  if (r0 + 32 > e.rows || col + 16 * kChunks > e.cols || !e.wide) return false;
+  return PASS != P_WGRAD || !e.accumulate;
+}
+
+// epilogue_row for such a block: no bounds, the chunks unrolled, one base address per
+// tensor (the general form spends about 240 instructions per chunk without an
+// activation, this one a third of that).
+template <int PASS, int ACT>
+__device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t col, uint32_t taddr,
+                                               const float* sb, const RowCodes<kChunks>& codes) {
+  constexpr bool CODES_IN = PASS == P_DGRAD && ACT != AQFQ_ACT_NONE;
+  const bool codes_out = PASS == P_FWD && e.c.codes;
+  const bool adds = PASS != P_WGRAD && e.res;
+  uint32_t t[16], add[8];
+  float v[16];
+  Divisor div[kChunks / 2];  // per 32 columns
+  if (codes_out) {
+    const int gch = 1 << (e.c.lg - 4), lead = int(col >> 4) & (gch - 1);
+#pragma unroll
+    for (int h = 0; h < kChunks / 2; ++h) {
+      if (h > 0 && gch > 2) {  // the same group
+        div[h] = div[0];
+        continue;
+      }
+      const int g0 = 2 * h - (gch > 2 ? lead : 0);
+      const int64_t left = (e.cols - (col + g0 * 16) + 15) / 16;
+      const int n = left < gch ? int(left) : gch;
+      uint32_t m = 0;
+      tmem_issue(taddr + uint32_t(g0 * 16), t);
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) {
+        tmem_take(t, v);
+        if (c + 1 < n) tmem_issue(taddr + uint32_t((g0 + c + 1) * 16), t);
+        if (e.bias) add_bias16(sb + (g0 + c) * 16, v);
+        const int64_t in = e.cols - (col + (g0 + c) * 16);
+        if (in < 16) {  // (a group that reaches past this block)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = i < in ? v[i] : 0.0f;
+        }
+        m = max(m, amax_bits(v));
+      }
+      div[h] = ckpt_divisor(m, e.c.fmt);
+      if (g0 >= 0) e.c.scale[r * e.c.groups + ((col + g0 * 16) >> e.c.lg)] = div[h].s;
+    }
+  }
+  const bf16* res = adds ? e.res + r * e.ldr + col : nullptr;
+  uint8_t* code = codes_out ? e.c.codes + r * e.cols + col : nullptr;
+  const bool f32 = PASS == P_WGRAD && e.out_dtype == AQFQ_F32;
+  uint8_t* out = static_cast<uint8_t*>(e.out) + (r * e.ldo + col) * (f32 ? 4 : 2);
+  if (adds) ld16(res, true, true, 16, add);
+  tmem_issue(taddr, t);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    tmem_take(t, v);
+    if (c + 1 < kChunks) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
+    if (PASS == P_FWD) {
+      if (e.bias) add_bias16(sb + c * 16, v);
+      if (codes_out) {
+        uint32_t w[4];
+        f2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mk2(v[2 * i], v[2 * i + 1]);
+        ckpt_codes(x, div[c / 2], e.c.fmt, w);
+        st_128(code + c * 16, w[0], w[1], w[2], w[3]);
+      }
+      act_all<ACT>(v);
+    }
+    if (CODES_IN) {
+      float p[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ckpt_values4(codes.w[c][i], codes.scale[c / 2], e.c.fmt, p + 4 * i);
+      slope_all<ACT>(p, v);
+    }
+    if (adds) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(add[i]), v[2 * i + 1] += bf_hi(add[i]);
+      if (c + 1 < kChunks) ld16(res + (c + 1) * 16, true, true, 16, add);
+    }
+    uint32_t w[8];
+    if (f32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+        st_256(out + c * 64 + h * 32, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+      st_256(out + c * 32, w);
     }
   }
 }
@@ -704,6 +806,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
       const int64_t col = int64_t(tc) * BN + part * W;
       const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
+      const bool fast = whole_block<PASS>(e, r0, col);
       ChunkIn<PASS> first;
       RowCodes<kChunks> codes;
       if (live && whole) {
@@ -717,7 +820,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (r < e.rows) {
           prefetch_inputs<PASS>(e, r, col, W);
           if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) codes.load(e, r, col);
-          else first.load(e, r, col);
+          else if (!fast) first.load(e, r, col);
         }
       }
       // one thread waits for the tile, the other warps for it at a barrier: sixteen
@@ -765,7 +868,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
           }
         } else {
-          epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), first, codes);
+          if (fast) epilogue_whole<PASS, ACT>(e, r, col, taddr, mybias + int(col & 127), codes);
+          else epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), first, codes);
         }
       }
       tc_fence_before_sync();
@@ -1078,7 +1182,7 @@ struct Plan {
 };
 
 constexpr int kPairs = 76;  // SM pairs
-constexpr double kStepPair = 0.34, kStepQuad = 0.30;  // us per 64 of the inner axis, every SM busy
+constexpr double kStepPair = 0.336, kStepQuad = 0.297;  // us per 64 of the inner axis, every SM busy
 static_assert(kBN / 2 == kHalf && kTile == kHalf, "one box for every operand tile");
 
 // Clusters of 2 S CTAs (one per SM) that run at the same time on this GPU, by S
@@ -1123,7 +1227,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   } else if (tiles > kPairs) {
     // Clusters of two pairs (72 pairs run together, a step takes kStepQuad us) against
     // single pairs (76, kStepPair us); the tiles of the last round, where they are few,
-    // are split by a second launch, at about 9 us of its own (start, joining, epilogue).
+    // are split by a second launch, at about 17 us of its own (start, joining, epilogue).
     double best = 1e30;
     for (int quad = p.nr % 2 == 0 ? 1 : 0; quad >= 0; --quad) {
       const int64_t at_once = quad ? 2 * kClusters[2] : kPairs;
@@ -1134,7 +1238,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
       if (plain < best) best = plain, p.quad = quad, p.tail = p.tail_splits = 0;
       int sp = 8;
       while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
-      const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 9.0;
+      const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 17.0;
       if (rem > 0 && sp > 1 && split < best) best = split, p.quad = quad, p.tail = rem, p.tail_splits = sp;
     }
   }
@@ -1267,6 +1371,8 @@ void finish_epi(Epi& e, int es) {
   e.vec_res = rows_aligned<8>(e.res, e.ldr, 2);
   e.vec_bias = rows_aligned<8>(e.bias, 8, esize(e.bias_dtype));
   e.vec_codes = rows_aligned<8>(e.c.codes, e.cols, 1);
+  e.wide = al(e.out, 32) && (e.ldo * es) % 32 == 0 && (!e.res || (al(e.res, 32) && e.ldr % 16 == 0)) &&
+           (!e.c.codes || (al(e.c.codes, 16) && e.cols % 16 == 0));
 }
 
 }  // namespace
