@@ -27,7 +27,7 @@ enum Pass { P_FWD = AQFQ_LINEAR_FWD, P_DGRAD = AQFQ_LINEAR_DGRAD, P_WGRAD = AQFQ
 // epilogue of sums in memory: 16 lanes hold 128 columns of a row, a lane 8 of them, a
 // warp two rows; an 8-bit group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring
 // lanes.  (4 columns per lane and 32 lanes per row: twice the address arithmetic per
-// element, 0.9 us instead of EPI8 us per turn of 16 warps with GELU and residual.)
+// element, 0.9 us instead of 0.55 us per turn of 16 warps with GELU and residual.)
 // ---------------------------------------------------------------------------
 struct Epi {
   int64_t rows, cols;
@@ -574,8 +574,8 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 // zeros from the TMA's fill.
 //   warp 0  TMA producer    warp 1  MMA issuer (leader)    warp 2  tensor memory
 //   warps 4-19  epilogue, four per quarter of the rows, a quarter of the columns each
-//               (two per quarter left half of the issue slots idle: 4096 x 8192 over 2048 with
-//               GELU's slope from a checkpoint 115 us, EPI16 us with four)
+//               (with two per quarter the forward with GELU and checkpoint took 192 us at
+//               8192 x 4096 x 4096, with four 167 us)
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
@@ -1171,8 +1171,7 @@ bool encode(CUtensorMap* tm, const Operand& o, unsigned box0, unsigned box1) {
 struct Plan {
   int nr, nc;     // tiles
   int ksteps;
-  int splits;     // slices of the inner axis
-  bool cluster;   // joined in a cluster; else through scratch and finish_kernel
+  int splits;     // slices of the inner axis: of tile_kernel's clusters, or through scratch
   bool small;     // tile_kernel (128 x 128 tiles, one CTA each)
   int a_rows;     // rows of A per box
   int tail, tail_splits;  // last tiles that a second launch splits (0: none)
@@ -1191,59 +1190,65 @@ constexpr int kClusters[9] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
 // the same for clusters of S CTAs
 constexpr int kClustersC[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 
-// Fewer tiles than half the SM pairs: the inner axis is split into as many slices
-// as still run together, at least two steps each, joined in a cluster.  A long
-// inner axis with very few tiles takes more slices through scratch.
+constexpr int64_t kMostScratch = int64_t(64) << 20;
+
+// The plan by an estimate of its time in us (steps of 64 of the inner axis with every
+// SM busy as measured above):
+//   - at most one 128 x 128 tile per SM and no long inner axis: tile_kernel, with as
+//     many slices as still run together (its steps are short, 0.2 us, and it has one
+//     launch; 24 x 2048 x 768 5 us, 515 x 776 x 1032 9 us where pairs took 13 and 15);
+//   - else rounds of 256 x 256 tiles on pairs (76 at once) or clusters of two pairs (72
+//     at once, shorter steps);
+//   - the tiles of the last round, where they are few, may be split by a second launch, at
+//     about 17 us of its own (start, joining, epilogue);
+//   - or every tile's inner axis in slices through scratch, at 6 us for the second
+//     kernel and the partial sums' way to memory and back (weight gradients of many
+//     tokens: few tiles, a long sum).
 Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   Plan p;
   p.nr = int((rows + kRows - 1) / kRows);
   p.nc = int((cols + kBN - 1) / kBN);
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
-  p.cluster = p.small = false;
+  p.small = false;
   p.a_rows = kHalf, p.tail = p.tail_splits = p.quad = 0;
-  const int64_t tiles = int64_t(p.nr) * p.nc;
+  p.cols4 = (cols + 3) / 4 * 4;
+  p.bytes = 0;
+  if (p.ksteps == 0) return p;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
-  if (small <= kClustersC[1] && p.ksteps > 0 && !(tiles <= 9 && p.ksteps >= 128)) {
+  if (small <= kClustersC[1] && p.ksteps < 512) {
     p.small = true;
     // zero rows that only the fill would write cost as much as loaded ones (1 row, 4096 x
-    // 4096: 12.9 us with boxes of 128 rows); rows past the box stay unread
+    // 4096: 12.9 us with boxes of 128 rows, 9.4 us with 8); rows past the box stay unread
     if (rows < kHalf) p.a_rows = int((rows + 7) / 8 * 8);
     p.nr = int((rows + kTile - 1) / kTile), p.nc = int((cols + kTile - 1) / kTile);
     int sp = 8;
     while (sp > 1 && (small > kClustersC[sp] || sp > p.ksteps)) --sp;
     p.splits = sp;
-    p.cluster = true;
-    p.cols4 = 0, p.bytes = 0;
     return p;
   }
-  if (tiles <= 9 && p.ksteps >= 128) {
-    p.splits = int(kPairs / tiles < p.ksteps / 16 ? kPairs / tiles : p.ksteps / 16);
-  } else if (tiles <= kPairs / 2 && p.ksteps >= 4) {
+  const int64_t tiles = int64_t(p.nr) * p.nc;
+  double best = 1e30;
+  for (int quad = p.nr % 2 == 0 ? 1 : 0; quad >= 0; --quad) {
+    const int64_t at_once = quad ? 2 * kClusters[2] : kPairs;
+    const double step = p.ksteps * (quad ? kStepQuad : kStepPair);
+    const int64_t rounds = tiles / at_once;
+    const int rem = int(tiles % at_once);
+    const double plain = step * double(rounds + (rem > 0));
+    if (plain < best) best = plain, p.quad = quad, p.tail = p.tail_splits = 0;
     int sp = 8;
-    while (sp > 1 && (tiles > kClusters[sp] || sp > p.ksteps / 2)) --sp;
-    p.splits = sp;
-    p.cluster = sp > 1;
-  } else if (tiles > kPairs) {
-    // Clusters of two pairs (72 pairs run together, a step takes kStepQuad us) against
-    // single pairs (76, kStepPair us); the tiles of the last round, where they are few,
-    // are split by a second launch, at about 17 us of its own (start, joining, epilogue).
-    double best = 1e30;
-    for (int quad = p.nr % 2 == 0 ? 1 : 0; quad >= 0; --quad) {
-      const int64_t at_once = quad ? 2 * kClusters[2] : kPairs;
-      const double step = p.ksteps * (quad ? kStepQuad : kStepPair);
-      const int64_t rounds = tiles / at_once;
-      const int rem = int(tiles % at_once);
-      const double plain = step * double(rounds + (rem > 0));
-      if (plain < best) best = plain, p.quad = quad, p.tail = p.tail_splits = 0;
-      int sp = 8;
-      while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
-      const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 17.0;
-      if (rem > 0 && sp > 1 && split < best) best = split, p.quad = quad, p.tail = rem, p.tail_splits = sp;
-    }
+    while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
+    const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 17.0;
+    if (rounds > 0 && rem > 0 && sp > 1 && split < best)
+      best = split, p.quad = quad, p.tail = rem, p.tail_splits = sp;
   }
-  p.cols4 = (cols + 3) / 4 * 4;
-  p.bytes = p.splits > 1 && !p.cluster ? size_t(p.splits) * size_t(rows) * size_t(p.cols4) * 4 : 0;
+  for (int sp = 2; sp <= 64 && p.ksteps / sp >= 16; ++sp) {
+    const int64_t bytes = int64_t(sp) * rows * p.cols4 * 4;
+    if (bytes > kMostScratch) break;
+    const int64_t rounds = (tiles * sp + kPairs - 1) / kPairs;
+    const double t = double(rounds) * double((p.ksteps + sp - 1) / sp) * kStepPair + 6.0 + double(bytes) * 2 / 5e6;
+    if (t < best) best = t, p.splits = sp, p.quad = p.tail = p.tail_splits = 0, p.bytes = size_t(bytes);
+  }
   return p;
 }
 
@@ -1332,8 +1337,6 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     a.count -= p.tail;
     if (p.small) {
       r = launch_tile<PASS>(ta, tb, a, e, st);
-    } else if (p.cluster) {
-      r = launch_pair<PASS, AQFQ_ACT_NONE, true, false>(ta, tb, a, e, st);
     } else if (p.splits > 1) {  // finish_kernel has the epilogue
       r = launch_pair<PASS, AQFQ_ACT_NONE, false, false>(ta, tb, a, e, st);
     } else if (p.quad) {
@@ -1347,7 +1350,7 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
       if (launch_pair<PASS, AQFQ_ACT_NONE, true, false>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
     }
   }
-  if (p.splits != 1 && !p.cluster) {
+  if (!p.small && p.splits != 1) {
     const int64_t gy = (e.rows + 15) / 16;
     finish_kernel<PASS><<<dim3(unsigned((e.cols + 127) / 128), unsigned(gy > 65535 ? 65535 : gy)), 256,
                           0, st>>>(part, p.splits, p.cols4, e);

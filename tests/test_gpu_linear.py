@@ -353,3 +353,52 @@ def test_last_tiles_split_by_a_second_launch_exact():
     q, s = pack_ref(p, "e4m3", 64)
     np.testing.assert_array_equal(scale.cpu().numpy(), s)
     np.testing.assert_array_equal(grid_values(codes, "e4m3"), q)
+
+
+@pytest.mark.parametrize("size", [(33000, 136, 264), (32800, 8, 520), (40000, 1536, 2056)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_inner_axis_through_scratch(size, accumulate):
+    """Weight gradients of many tokens: the sum is cut into slices whose partial sums
+    meet in scratch.  Entries -1, 0, 1 keep every sum exact in binary32."""
+    M, N, K = size
+    assert aqfq.aqfq_linear_workspace_bytes(aqfq.LINEAR_WGRAD, M, N, K) > 0
+    dy, x = ints((M, N), 1, 1), ints((M, K), 2, 1)
+    base = ints((N, K), 3).float() if accumulate else None
+    dw = run_wgrad(dy, x, torch.float32, base, seed=M % 3)
+    ref = dy.float().to(DEV).T @ x.float().to(DEV)
+    if accumulate:
+        ref = ref + base.to(DEV)
+    assert torch.equal(dw, ref)
+
+
+def test_forward_with_a_long_inner_axis_through_scratch():
+    """The finishing kernel's forward epilogue: bias, checkpoint, activation, residual."""
+    M, N, K = 70, 300, 33000
+    x, w = ints((M, K), 1, 1), ints((N, K), 2, 1)
+    assert aqfq.aqfq_linear_workspace_bytes(aqfq.LINEAR_FWD, M, N, K) > 0
+    bias, res = ints((N,), 3), ints((M, N), 4)
+    y, codes, scale = run_fwd(x, w, bias, "relu", res, "int8", 128)
+    p = (x.float().to(DEV) @ w.float().to(DEV).T).cpu() + bias.float()
+    assert torch.equal(y.cpu(), (torch.clamp(p, min=0) + res.float()).bfloat16())
+    q, s = pack_ref(p, "int8", 128)
+    np.testing.assert_array_equal(scale.cpu().numpy(), s)
+    np.testing.assert_array_equal(grid_values(codes, "int8"), q)
+    ck, codes, scale = new_ckpt(M, N, "e4m3", 32)
+    aqfq.aqfq_ckpt8_pack(ck, randn((M, N), 5).to(DEV))
+    dy, w2 = ints((M, K), 6, 1), ints((K, N), 7, 1)
+    dx = run_dgrad(dy, w2, "relu", ck)
+    keep = (kept(codes, scale, "e4m3", 32) > 0).float()
+    ref = (dy.float().to(DEV) @ w2.float().to(DEV)).cpu() * keep
+    assert torch.equal(dx.cpu(), ref.bfloat16())
+
+
+def test_workspace_is_checked_and_bounded():
+    need = aqfq.aqfq_linear_workspace_bytes(aqfq.LINEAR_WGRAD, 33000, 136, 264)
+    dy, x = torch.zeros(33000, 136, device=DEV).bfloat16(), torch.zeros(33000, 264, device=DEV).bfloat16()
+    dw = torch.empty(136, 264, device=DEV)
+    for w in (None, ws(need - 16)):
+        with pytest.raises(aqfq.AqfqError) as e:
+            aqfq.aqfq_linear_wgrad(dy, x, dw, workspace=w)
+        assert e.value.status == 5
+    for M, N, K in ((1 << 20, 4096, 4096), (1 << 20, 264, 264), (1 << 22, 1536, 2048)):
+        assert aqfq.aqfq_linear_workspace_bytes(aqfq.LINEAR_WGRAD, M, N, K) <= 64 << 20
