@@ -397,12 +397,14 @@ def ckpt8(fmt, group, codes, scale) -> Ckpt8:
     _u8(codes, "codes"), _f32(scale, "scale")
     if codes.dim() != 2 or group <= 0:
         raise ValueError("codes must be [rows, cols] and group positive")
-    rows, cols = codes.shape
+    size = rows, cols = tuple(codes.shape)
     if scale.shape != (rows, -(-cols // group)):
         raise ValueError("scale must be [rows, ceil(cols / group)]")
-    c = Ckpt8(fmt, group, _ptr(codes), _ptr(scale))
+    if not (codes.is_cuda and scale.is_cuda and codes.is_contiguous() and scale.is_contiguous()):
+        _ptr(codes), _ptr(scale)  # one of them refuses
+    c = Ckpt8(fmt, group, codes.data_ptr(), scale.data_ptr())
     c.tensors = (codes, scale)
-    c.size = (rows, cols)
+    c.size = size
     return c
 
 

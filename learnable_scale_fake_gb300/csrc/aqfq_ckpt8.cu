@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 template <typename T, int V, int ACT, int U>
 __global__ void __launch_bounds__(kWarps * 32)
     act_bwd_kernel(const Ckpt c, const T* dy, int64_t lddy, int64_t rows, int64_t cols, int lr, T* dx,
-                   int64_t lddx, T* y, int64_t ldy, float* part) {
+                   int64_t lddx, T* y, int64_t ldy, float* part, const Join jn) {
   constexpr int NV = Lane<V>::NV, E = NV * V, P = E / 2;
   const Lane<V> l = lane_of<V>(lr, cols);
   f2 sum2[P] = {};
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int i = 0; i < P; ++i) sum2[i] = add2(sum2[i], v[i]);
     }
   }
-  if (part) {
+  if (part || jn.on) {
     // the lanes of a column, then the eight warps, in a fixed order
-    __shared__ float red[kWarps][32 * E];
+    __shared__ float red[kWarps + 1][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float sum[E];
 #pragma unroll
@@ -224,11 +224,17 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     __syncthreads();
     const int64_t col = l.col0 + threadIdx.x;
-    if (int(threadIdx.x) < (V == 8 ? 8 << lr : 128) && col < cols) {
+    const int seg = V == 8 ? 8 << lr : 128;
+    if (int(threadIdx.x) < seg && col < cols) {
       float t = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) t += red[w][threadIdx.x];
-      part[int64_t(blockIdx.y) * cols + col] = t;
+      if (jn.on) red[kWarps][threadIdx.x] = t;
+      else part[int64_t(blockIdx.y) * cols + col] = t;
+    }
+    if (jn.on) {  // the segment's row slices are one cluster
+      const int64_t left = cols - l.col0;
+      join_columns(Join{jn.out + l.col0, nullptr, jn.accumulate, true}, red[kWarps], 0, left < seg ? left : seg);
     }
   }
 }
@@ -426,20 +432,31 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
   const bool wide = cols % 8 == 0 && rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dx, lddx, es) &&
                     rows_aligned<8>(y, ldy, es) && al(c.codes, 8);
-  const Map m = make_map(rows, cols, c.lg, wide, dbias ? kMaxParts : 65535);
-  float* part = dbias ? static_cast<float*>(workspace) : nullptr;
+  Map m = make_map(rows, cols, c.lg, wide, dbias ? kMaxParts : 65535);
+  // few rows (eight per warp in eight slices): the slices of a column segment form a
+  // cluster and add up their sums there, in place of a second launch
+  const Join jn = {dbias, nullptr, accumulate, dbias && rows <= (int64_t(8 * 8 * kWarps) << (5 - m.lr))};
+  if (jn.on && m.gy > 8) m.gy = 8;
+  cudaError_t launched = cudaSuccess;
+  float* part = dbias && !jn.on ? static_cast<float*>(workspace) : nullptr;
   by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
     by_type(dtype, wide, [&](auto t, auto v) {
       using T = typename decltype(t)::type;
       constexpr int V = decltype(v)::value;
-      act_bwd_kernel<T, V, ACT, kUB><<<dim3(m.gx, m.gy), kWarps * 32, 0, st>>>(
-          c, static_cast<const T*>(dy), lddy, rows, cols, m.lr, static_cast<T*>(dx), lddx,
-          static_cast<T*>(y), ldy, part);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(m.gx, m.gy), cfg.blockDim = dim3(kWarps * 32), cfg.stream = st;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = at[0].val.clusterDim.z = 1, at[0].val.clusterDim.y = jn.on ? m.gy : 1;
+      cfg.attrs = at, cfg.numAttrs = 1;
+      launched = cudaLaunchKernelEx(&cfg, act_bwd_kernel<T, V, ACT, kUB>, c, static_cast<const T*>(dy), lddy,
+                                    rows, cols, m.lr, static_cast<T*>(dx), lddx, static_cast<T*>(y), ldy,
+                                    part, jn);
     });
   });
-  if (cudaGetLastError() != cudaSuccess) return AQFQ_ERR_CUDA;
-  if (dbias &&
+  if (launched != cudaSuccess) return AQFQ_ERR_CUDA;
+  if (part &&
       launch_part_sums(part, nullptr, int(m.gy), cols, dbias, nullptr, accumulate, st) != cudaSuccess)
     return AQFQ_ERR_CUDA;
   return AQFQ_OK;

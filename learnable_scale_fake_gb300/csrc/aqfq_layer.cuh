@@ -581,6 +581,58 @@ __device__ __forceinline__ void ckpt_write16(const Ckpt& c, int64_t r, int64_t c
 }
 
 // ---------------------------------------------------------------------------
+// Column sums of a few blocks that form one cluster: each block has its sums in
+// shared memory (out at [0, cols), out2 at [second, second + cols)), block i finishes
+// the i-th share of the columns, adding the blocks' values in order.  Every thread
+// of every block calls it.
+// ---------------------------------------------------------------------------
+struct Join {
+  float *out, *out2;  // either may be NULL
+  int accumulate;
+  bool on;
+};
+__device__ __forceinline__ void join_columns(const Join& j, const float* sums, int second, int64_t cols) {
+  uint32_t rank, n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  if (n == 1) {  // a single block
+    __syncthreads();
+    for (int c = int(threadIdx.x); c < int(cols); c += int(blockDim.x)) {
+      if (j.out) j.out[c] = j.accumulate ? j.out[c] + sums[c] : sums[c];
+      if (j.out2) j.out2[c] = j.accumulate ? j.out2[c] + sums[second + c] : sums[second + c];
+    }
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  const int c0 = int(cols * rank / n), c1 = int(cols * (rank + 1) / n);
+  for (int k = 0; k < 2; ++k) {
+    float* out = k ? j.out2 : j.out;
+    if (!out) continue;
+    for (int c = c0 + int(threadIdx.x); c < c1; c += int(blockDim.x)) {
+      const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(sums + (k ? second : 0) + c));
+      float v[8], t = 0.0f;
+#pragma unroll
+      for (uint32_t b = 0; b < 8; ++b) {
+        v[b] = 0.0f;
+        if (b < n)
+          asm volatile(
+              "{ .reg .b32 a;\n\t"
+              "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+              "ld.shared::cluster.f32 %0, [a]; }"
+              : "=f"(v[b])
+              : "r"(at), "r"(b)
+              : "memory");
+      }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) t += v[b];
+      out[c] = j.accumulate ? out[c] + t : t;
+    }
+  }
+  // the others have read this block's sums
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // host side: argument checks shared by the entry points
 // ---------------------------------------------------------------------------
 inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

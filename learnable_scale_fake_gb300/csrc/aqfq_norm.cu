@@ -398,7 +398,7 @@ struct RowRegs {
 template <typename T, int V, int NV, int G, bool CK, bool PF>
 __global__ void __launch_bounds__(1024, 1)
     norm_bwd_rows(const T* dy, const T* x, const T* dres, T* dx, float* pg, float* pb,
-                  const BwdArgs a) {
+                  const BwdArgs a, const Join jn) {
   constexpr int C = 32 * G * NV * V, P = NV * V / 2;  // columns a row may have
   extern __shared__ float sums[];     // [2][C] when several rows share the block
   __shared__ float2 red[32][2];       // [warp][parity]
@@ -471,9 +471,9 @@ __global__ void __launch_bounds__(1024, 1)
     if constexpr (PF) cur = nxt;
     else if (r + step < a.rows) cur.load(dy, x, dres, a, r + step, col, in);
   }
-  if (!pg) return;
+  if (!pg && !jn.on) return;  // uniform over the grid
   // the block's column sums: group after group into shared memory, in order
-  if (ng > 1) {
+  if (ng > 1 || jn.on) {
     for (int k = 0; k < ng; ++k) {
       if (k == grp) {
 #pragma unroll
@@ -487,6 +487,10 @@ __global__ void __launch_bounds__(1024, 1)
         }
       }
       __syncthreads();
+    }
+    if (jn.on) {
+      join_columns(jn, sums, C, a.cols);
+      return;
     }
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       pg[int64_t(blockIdx.x) * a.cols + c] = sums[c];
@@ -995,21 +999,35 @@ template <typename T, int V, int NV, int G, bool PF>
 cudaError_t run_bwd(const void* dy, const void* x, const void* dres, const BwdOut& o, const BwdArgs& a,
                     cudaStream_t st) {
   // rows per block: up to 32 warps (and 15 named barriers), fewer when there are few rows
-  constexpr int most = G == 1 ? 32 : (32 / G < 15 ? 32 / G : 15);
+  constexpr int most = G == 1 ? 32 : (32 / G < 15 ? 32 / G : 15), C = 32 * G * NV * V;
+  const bool cols = o.dgamma || o.dbeta;
   int64_t ng = (a.rows + kSms - 1) / kSms;
+  Join jn = {o.dgamma, o.dbeta, o.accumulate, false};
+  // at most four rows per group of a cluster's eight blocks: one launch, the blocks'
+  // column sums meet in the cluster
+  if (cols && C <= 4096 && a.rows <= 8 * 4 * most) {
+    jn.on = true;
+    ng = a.rows < most ? a.rows : most;
+  }
   if (ng > most) ng = most;
   int64_t parts = (a.rows + ng - 1) / ng;
   if (parts > kSms) parts = kSms;
-  const bool cols = o.dgamma || o.dbeta;
-  float* pb = cols ? o.ws + size_t(parts) * size_t(a.cols) : nullptr;
-  const size_t smem = ng > 1 && cols ? size_t(2) * 32 * G * NV * V * 4 : 0;  // 32 KiB at most
+  if (jn.on && parts > 8) parts = 8;
+  float* pg = cols && !jn.on ? o.ws : nullptr;
+  float* pb = pg ? o.ws + size_t(parts) * size_t(a.cols) : nullptr;
+  const size_t smem = (ng > 1 && cols) || jn.on ? size_t(2) * C * 4 : 0;  // 32 KiB at most
   auto kernel = x ? norm_bwd_rows<T, V, NV, G, false, PF> : norm_bwd_rows<T, V, NV, G, true, PF>;
-  kernel<<<unsigned(parts), unsigned(32 * G * ng), smem, st>>>(
-      static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const T*>(dres),
-      static_cast<T*>(o.dx), cols ? o.ws : nullptr, pb, a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !cols) return e;
-  return launch_part_sums(o.ws, pb, int(parts), a.cols, o.dgamma, o.dbeta, o.accumulate, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(parts)), cfg.blockDim = dim3(unsigned(32 * G * ng));
+  cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(jn.on ? parts : 1), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(dy), static_cast<const T*>(x),
+                                           static_cast<const T*>(dres), static_cast<T*>(o.dx), pg, pb, a, jn);
+  if (e != cudaSuccess || !pg) return e;
+  return launch_part_sums(pg, pb, int(parts), a.cols, o.dgamma, o.dbeta, o.accumulate, st);
 }
 
 template <typename T, int NV, int G, bool CK>
