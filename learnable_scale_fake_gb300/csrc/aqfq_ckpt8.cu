@@ -2,12 +2,16 @@
 // activation recomputed) and the activation gradient read from a checkpoint.
 //
 // A row is cut into groups of 32, 64 or 128 columns (the last one may be
-// shorter).  One lane holds 8 consecutive columns, so a group is 4, 8 or 16
-// neighbouring lanes and its amax a butterfly over them.  A warp covers 256
+// shorter).  One lane holds 8 or 16 consecutive columns, so a group is 2 to 16
+// neighbouring lanes and its amax a butterfly over them.  A warp covers 256 or 512
 // columns of one row (narrow rows: several rows per warp) and walks down the
 // rows of its slice; the bias gradient's column sums stay in its registers.
-// All three are bound by memory: pack moves 2 + 1 bytes per BF16 element,
-// unpack 1 + 2, the gradient 1 + 2 + 2 (+ 2 with the recomputed activation).
+// Memory is the floor: pack moves 2 + 1 bytes per BF16 element, unpack 1 + 2, the
+// gradient 1 + 2 + 2 (+ 2 with the recomputed activation).  At 8192 x 8192 in E4M3, a
+// plain copy moving 6.78 TB/s: pack 36 us (5.6 TB/s), unpack 33 us (6.1), the gradient
+// with SiLU 60 us (5.6), with GELU 70 us (4.8: two transcendental instructions and about
+// twelve packed ones per pair keep the issue slots 62 % busy), with GELU, the recomputed
+// activation and the bias gradient 83 us (5.6).
 #include <type_traits>
 
 #include "aqfq_internal.h"
@@ -21,8 +25,9 @@ constexpr int kWarps = 8;
 // rows in flight per lane
 constexpr int kU = 2, kUB = 2;
 
-// How a [rows, cols] matrix is covered.  V = 8 (rows allow 16-byte accesses): a
-// lane holds 8 columns, 2^lr lanes share a row (narrow rows: several per warp).
+// How a [rows, cols] matrix is covered.  V = 8 (rows allow 16-byte accesses) or 16
+// (BF16 rows that allow 32-byte ones): a lane holds V columns, 2^lr lanes share a row
+// (narrow rows: several per warp).
 // V = 1: a warp holds 128 columns of one row as four vectors of 32.
 struct Map {
   int lr;          // log2 of the lanes that share a row
@@ -31,11 +36,11 @@ struct Map {
 };
 
 // Enough blocks for eight per SM; the bias gradient's partial sums bound the slices.
-inline Map make_map(int64_t rows, int64_t cols, int lg, bool wide, int64_t max_parts) {
+inline Map make_map(int64_t rows, int64_t cols, int lg, int v, int64_t max_parts) {
   Map m;
-  m.lr = wide ? lg - 3 : 5;
-  while (m.lr < 5 && (int64_t(8) << m.lr) < cols) ++m.lr;
-  const int64_t seg = wide ? int64_t(8) << m.lr : 128;
+  m.lr = v == 16 ? lg - 4 : v == 8 ? lg - 3 : 5;
+  while (m.lr < 5 && (int64_t(v) << m.lr) < cols) ++m.lr;
+  const int64_t seg = v > 1 ? int64_t(v) << m.lr : 128;
   m.gx = unsigned((cols + seg - 1) / seg);
   const int64_t per = int64_t(kWarps) << (5 - m.lr);  // rows of one block step
   int64_t gy = (rows + per - 1) / per;
@@ -48,7 +53,7 @@ inline Map make_map(int64_t rows, int64_t cols, int lg, bool wide, int64_t max_p
 
 template <int V>
 struct Lane {
-  static constexpr int NV = V == 8 ? 1 : 4;
+  static constexpr int NV = V > 1 ? 1 : 4;
   int64_t row, step;  // first row, rows between two of this lane's rows
   int64_t base;       // first row of the warp (the same trip count in every lane)
   int64_t col0;       // first column of the warp
@@ -63,10 +68,10 @@ __device__ __forceinline__ Lane<V> lane_of(int lr, int64_t cols) {
   l.base = (int64_t(blockIdx.y) * kWarps + warp) * rpw;
   l.row = l.base + (lane >> lr);
   l.step = int64_t(gridDim.y) * kWarps * rpw;
-  l.col0 = V == 8 ? (int64_t(blockIdx.x) << lr) * 8 : int64_t(blockIdx.x) * 128;
+  l.col0 = V > 1 ? (int64_t(blockIdx.x) << lr) * V : int64_t(blockIdx.x) * 128;
 #pragma unroll
   for (int j = 0; j < Lane<V>::NV; ++j) {
-    const int64_t c = l.col0 + (V == 8 ? (lane & ((1 << lr) - 1)) * 8 : j * 32 + lane);
+    const int64_t c = l.col0 + (V > 1 ? (lane & ((1 << lr) - 1)) * V : j * 32 + lane);
     l.in[j] = c < cols;
     l.col[j] = l.in[j] ? c : 0;
   }
@@ -280,14 +285,14 @@ struct Type {
 
 // f(tag of the element type, columns per vector)
 template <typename F>
-void by_type(int dtype, bool wide, F f) {
+void by_type(int dtype, int v, F f) {
   using V8 = std::integral_constant<int, 8>;
   using V1 = std::integral_constant<int, 1>;
   if (dtype == AQFQ_BF16) {
-    if (wide) f(Type<bf16>(), V8());
+    if (v == 8) f(Type<bf16>(), V8());
     else f(Type<bf16>(), V1());
   } else {
-    if (wide) f(Type<float>(), V8());
+    if (v == 8) f(Type<float>(), V8());
     else f(Type<float>(), V1());
   }
 }
@@ -340,19 +345,18 @@ extern "C" aqfq_status aqfq_ckpt8_pack(const aqfq_ckpt8* ckpt, int dtype, const 
   const bool wide = cols % 8 == 0 && rows_aligned<8>(x, ldx, esize(dtype)) && al(c.codes, 8);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (wide && dtype == AQFQ_BF16 && cols > 256) {
-    // (half as many columns per segment below; 257 x 512 and up fill the lanes)
-    const Map m = make_map(rows, (cols + 1) / 2, c.lg, true, 65535);
+    const Map m = make_map(rows, cols, c.lg, 16, 65535);
     const bf16* in = static_cast<const bf16*>(x);
     const bool a32 = al(x, 32) && ldx % 16 == 0;
-    const dim3 grid(unsigned((cols + (16ll << m.lr) - 1) / (16ll << m.lr)), m.gy);
+    const dim3 grid(m.gx, m.gy);
     if (c.fmt == AQFQ_INT8)
       pack16_kernel<AQFQ_INT8, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, a32, c);
     else
       pack16_kernel<AQFQ_FP8_E4M3, kU><<<grid, kWarps * 32, 0, st>>>(in, ldx, rows, cols, m.lr, a32, c);
     return done();
   }
-  const Map m = make_map(rows, cols, c.lg, wide, 65535);
-  by_type(dtype, wide, [&](auto t, auto v) {
+  const Map m = make_map(rows, cols, c.lg, wide ? 8 : 1, 65535);
+  by_type(dtype, wide ? 8 : 1, [&](auto t, auto v) {
     using T = typename decltype(t)::type;
     constexpr int V = decltype(v)::value;
     const dim3 grid(m.gx, m.gy);
@@ -376,11 +380,21 @@ extern "C" aqfq_status aqfq_ckpt8_unpack(const aqfq_ckpt8* ckpt, int act, int dt
   if (!y) return AQFQ_ERR_NULL;
   if (!al(y, esize(dtype))) return AQFQ_ERR_ALIGN;
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
-  const bool wide = cols % 8 == 0 && rows_aligned<8>(y, ldy, esize(dtype)) && al(c.codes, 8);
-  const Map m = make_map(rows, cols, c.lg, wide, 65535);
+  const int vec = cols % 8 == 0 && rows_aligned<8>(y, ldy, esize(dtype)) && al(c.codes, 8) ? 8 : 1;
+  // 16 columns per lane for many elements (8192 x 8192 with GELU 52 -> 44 us, 8192 x 4096
+  // 28 -> 25; 2048 x 2048 would go from 5.2 to 6.8, 16384 x 768 from 13.5 to 14.0)
+  const bool v16 = dtype == AQFQ_BF16 && cols > 256 && cols % 16 == 0 && ldy % 16 == 0 && al(y, 32) &&
+                   al(c.codes, 16) && rows * cols >= (int64_t(1) << 24);
+  const Map m = make_map(rows, cols, c.lg, v16 ? 16 : vec, 65535);
   by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    by_type(dtype, wide, [&](auto t, auto v) {
+    if (v16) {
+      unpack_kernel<bf16, 16, ACT, kU>
+          <<<dim3(m.gx, m.gy), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+              c, rows, cols, m.lr, static_cast<bf16*>(y), ldy);
+      return;
+    }
+    by_type(dtype, vec, [&](auto t, auto v) {
       using T = typename decltype(t)::type;
       constexpr int V = decltype(v)::value;
       unpack_kernel<T, V, ACT, kU>
@@ -430,9 +444,11 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
     return AQFQ_OK;
   }
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
-  const bool wide = cols % 8 == 0 && rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dx, lddx, es) &&
-                    rows_aligned<8>(y, ldy, es) && al(c.codes, 8);
-  Map m = make_map(rows, cols, c.lg, wide, dbias ? kMaxParts : 65535);
+  const int vec = cols % 8 == 0 && rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dx, lddx, es) &&
+                          rows_aligned<8>(y, ldy, es) && al(c.codes, 8)
+                      ? 8
+                      : 1;
+  Map m = make_map(rows, cols, c.lg, vec, dbias ? kMaxParts : 65535);
   // few rows (eight per warp in eight slices): the slices of a column segment form a
   // cluster and add up their sums there, in place of a second launch
   const Join jn = {dbias, nullptr, accumulate, dbias && rows <= (int64_t(8 * 8 * kWarps) << (5 - m.lr))};
@@ -441,7 +457,7 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
   float* part = dbias && !jn.on ? static_cast<float*>(workspace) : nullptr;
   by_act(act, [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    by_type(dtype, wide, [&](auto t, auto v) {
+    by_type(dtype, vec, [&](auto t, auto v) {
       using T = typename decltype(t)::type;
       constexpr int V = decltype(v)::value;
       cudaLaunchConfig_t cfg = {};

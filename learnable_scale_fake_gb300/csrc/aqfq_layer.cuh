@@ -407,9 +407,9 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, bool vec, int n, ui
 // ---------------------------------------------------------------------------
 // A lane's share of a row: NV vectors of V consecutive elements, kept as they are
 // in memory until all loads are under way.  V = 8 where rows allow 16-byte
-// accesses; V = 1 (neighbouring lanes on neighbouring columns) where they do not.
-// In arithmetic the E = NV V elements are E / 2 pairs: neighbours within a vector
-// (V = 8), or the same lane's elements of vectors 2k and 2k + 1 (V = 1).
+// accesses (16 BF16 where they allow 32-byte ones); V = 1 (neighbouring lanes on
+// neighbouring columns) where they do not.  In arithmetic the E = NV V elements are E / 2 pairs: neighbours within a vector
+// (V = 8, 16), or the same lane's elements of vectors 2k and 2k + 1 (V = 1).
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NV>
 struct Row {
@@ -419,6 +419,9 @@ struct Row {
     if constexpr (V == 1) {
       if constexpr (sizeof(T) == 2) w[j][0] = __ldg(reinterpret_cast<const uint16_t*>(p));
       else w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (V == 16) {
+      static_assert(sizeof(T) == 2, "32 bytes");
+      ld_stream(p, w[j]);
     } else {
 #pragma unroll
       for (int i = 0; i < W; i += 4)
@@ -435,7 +438,7 @@ struct Row {
       return sizeof(T) == 2 ? mk2(__uint_as_float(a << 16), __uint_as_float(b << 16))
                             : mk2(__uint_as_float(a), __uint_as_float(b));
     } else if constexpr (sizeof(T) == 2) {
-      return bf2(w[i / 4][i % 4]);
+      return bf2(w[i / W][i % W]);
     } else {
       return mk2(__uint_as_float(w[i / 4][2 * (i % 4)]), __uint_as_float(w[i / 4][2 * (i % 4) + 1]));
     }
@@ -446,6 +449,11 @@ template <typename T, int V>
 __device__ __forceinline__ void put(T* p, const f2* v, int j) {
   if constexpr (V == 1) {
     from_f(j & 1 ? hi2(v[j / 2]) : lo2(v[j / 2]), *p);
+  } else if constexpr (V == 16) {
+    const f2* q = v + 8 * j;
+    const uint32_t w[8] = {pack2(q[0]), pack2(q[1]), pack2(q[2]), pack2(q[3]),
+                           pack2(q[4]), pack2(q[5]), pack2(q[6]), pack2(q[7])};
+    st_256(p, w);
   } else if constexpr (sizeof(T) == 2) {
     const f2* q = v + 4 * j;
     st_128(p, pack2(q[0]), pack2(q[1]), pack2(q[2]), pack2(q[3]));
@@ -460,11 +468,14 @@ __device__ __forceinline__ void put(T* p, const f2* v, int j) {
 // the codes of a lane's vectors
 template <int V, int NV>
 struct CodeRow {
-  uint32_t w[NV][V == 8 ? 2 : 1];
+  static constexpr int W = V == 1 ? 1 : V / 4;
+  uint32_t w[NV][W];
   float s[NV];
   __device__ __forceinline__ void load(int j, const Ckpt& c, int64_t r, int64_t cols, int64_t col) {
     const uint8_t* p = c.codes + r * cols + col;
-    if constexpr (V == 8)
+    if constexpr (V == 16)
+      ld_stream_v4(p, w[j][0], w[j][1], w[j][2], w[j][3]);
+    else if constexpr (V == 8)
       asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[j][0]), "=r"(w[j][1]) : "l"(p));
     else
       w[j][0] = __ldg(p);
@@ -472,16 +483,15 @@ struct CodeRow {
   }
   __device__ __forceinline__ void zero(int j) {
 #pragma unroll
-    for (int i = 0; i < (V == 8 ? 2 : 1); ++i) w[j][i] = 0;
+    for (int i = 0; i < W; ++i) w[j][i] = 0;
     s[j] = 0.0f;
   }
   __device__ __forceinline__ void values(int fmt, f2 (&v)[NV * V / 2]) const {
-    if constexpr (V == 8) {
+    if constexpr (V > 1) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        ckpt_values4(w[j][0], s[j], fmt, v + 4 * j);
-        ckpt_values4(w[j][1], s[j], fmt, v + 4 * j + 2);
-      }
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < W; ++i) ckpt_values4(w[j][i], s[j], fmt, v + (j * W + i) * 2);
     } else {
 #pragma unroll
       for (int j = 0; j < NV; j += 2) {

@@ -224,3 +224,23 @@ def test_same_bits_again_and_on_another_stream():
         out.append((codes, scale, dx, db))
     for o in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out[0], o))
+
+
+@pytest.mark.parametrize("fmt", [aqfq.INT8, aqfq.FP8_E4M3])
+def test_unpack_of_many_rows_equals_its_slices(fmt):
+    # 17 million elements take 16 columns per lane, the slices 8: the same arithmetic
+    R, C, group = 16401, 1040, 64
+    x = torch.randn(R, C, device="cuda").bfloat16()
+    codes = torch.empty(R, C, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(R, -(-C // group), device="cuda")
+    ck = aqfq.ckpt8(fmt, group, codes, scale)
+    aqfq.aqfq_ckpt8_pack(ck, x)
+    for act in (aqfq.ACT_NONE, aqfq.ACT_SILU):
+        whole = torch.full_like(x, float("nan"))
+        parts = torch.full_like(x, float("nan"))
+        aqfq.aqfq_ckpt8_unpack(ck, whole, act=act)
+        for lo in range(0, R, 6000):
+            hi = min(R, lo + 6000)
+            aqfq.aqfq_ckpt8_unpack(aqfq.ckpt8(fmt, group, codes[lo:hi], scale[lo:hi]),
+                                   parts[lo:hi], act=act)
+        assert torch.equal(whole.view(torch.int16), parts.view(torch.int16))
