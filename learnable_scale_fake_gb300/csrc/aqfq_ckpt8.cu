@@ -39,12 +39,16 @@ struct Map {
 inline Map make_map(int64_t rows, int64_t cols, int lg, int v, int64_t max_parts) {
   Map m;
   m.lr = v == 16 ? lg - 4 : v == 8 ? lg - 3 : 5;
+  const int least = m.lr;  // a group's lanes
   while (m.lr < 5 && (int64_t(v) << m.lr) < cols) ++m.lr;
+  // fewer lanes per row where more than an eighth of them would have no columns
+  auto idle = [&] { return (cols + (int64_t(v) << m.lr) - 1) / (int64_t(v) << m.lr) * (int64_t(v) << m.lr) - cols; };
+  while (v > 1 && m.lr > least && idle() * 8 > cols) --m.lr;
   const int64_t seg = v > 1 ? int64_t(v) << m.lr : 128;
   m.gx = unsigned((cols + seg - 1) / seg);
   const int64_t per = int64_t(kWarps) << (5 - m.lr);  // rows of one block step
   int64_t gy = (rows + per - 1) / per;
-  const int64_t fill = (int64_t(sm_count()) * 8 + m.gx - 1) / m.gx;
+  const int64_t fill = int64_t(sm_count()) * 8 / m.gx;  // (not one block more: it would run alone)
   if (gy > fill) gy = fill;
   if (gy > max_parts) gy = max_parts;
   m.gy = unsigned(gy < 1 ? 1 : gy);
@@ -119,13 +123,17 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t base = (int64_t(blockIdx.y) * kWarps + warp) * rpw;
   const int64_t step = int64_t(gridDim.y) * kWarps * rpw;
   const int64_t col = ((int64_t(blockIdx.x) << lr) + (lane & ((1 << lr) - 1))) * 16;
-  const bool in0 = col < cols, in1 = col + 8 < cols;
-  for (int64_t b = base, r = base + (lane >> lr); b < rows; b += step * U, r += step * U) {
+  const bool in0 = col < cols, in1 = col + 8 < cols, first = (int(col) & ((1 << c.lg) - 1)) == 0;
+  const bool a16 = cols % 16 == 0 && (reinterpret_cast<uintptr_t>(c.codes) & 15) == 0;
+  int64_t r = base + (lane >> lr);
+  const bf16* from = x + (in0 ? col : 0);
+  uint8_t* code = c.codes + r * cols + col;
+  float* scale = c.scale + r * c.groups + (col >> c.lg);
+  for (int64_t b = base; b < rows; b += step * U, r += step * U) {
     uint32_t w[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t ru = r + u * step < rows ? r + u * step : rows - 1;
-      const bf16* p = x + ru * ldx + (in0 ? col : 0);
+      const bf16* p = from + (r + u * step < rows ? r + u * step : rows - 1) * ldx;
       if (a32 && in1) {
         ld_stream(p, w[u]);
       } else {
@@ -139,7 +147,8 @@ __global__ void __launch_bounds__(kWarps * 32)
       f2 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = (i < 4 ? in0 : in1) ? bf2(w[u][i]) : 0ull;
-      ckpt_write16<FMT>(c, r + u * step, cols, int(col), in0 && e, in1 && e, v);
+      ckpt_write16<FMT>(c.lg, code, a16, scale, first, in0 && e, in1 && e, v);
+      code += step * cols, scale += step * c.groups;
     }
   }
 }

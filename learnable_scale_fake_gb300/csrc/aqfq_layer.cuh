@@ -569,25 +569,25 @@ __device__ __forceinline__ void ckpt_write(const Ckpt& c, int64_t r, int64_t col
 }
 
 // The checkpoint of a lane's 16 consecutive columns (in two halves of 8, zero beyond
-// the row): a group is 2, 4 or 8 neighbouring lanes.
+// the row): a group is 2, 4 or 8 neighbouring lanes.  p: its codes (a16: 16-byte
+// aligned), scale: its group's, written by the lane with the group's first column.
 template <int FMT>
-__device__ __forceinline__ void ckpt_write16(const Ckpt& c, int64_t r, int64_t cols, int col, bool in0,
-                                             bool in1, const f2 (&v)[8]) {
+__device__ __forceinline__ void ckpt_write16(int lg, uint8_t* p, bool a16, float* scale, bool first,
+                                             bool in0, bool in1, const f2 (&v)[8]) {
   uint32_t m = amax_bits(v);
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  if (c.lg > 5) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  if (c.lg > 6) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+  if (lg > 5) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  if (lg > 6) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
   const Divisor d = ckpt_divisor<FMT>(m);
   uint32_t w[4];
   ckpt_codes<FMT>(v, d, w);
-  uint8_t* p = c.codes + r * cols + col;
-  if (in1 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+  if (a16 && in1) {
     st_128(p, w[0], w[1], w[2], w[3]);
   } else {
     if (in0) st_64(p, w[0], w[1]);
     if (in1) st_64(p + 8, w[2], w[3]);
   }
-  if (in0 && (col & ((1 << c.lg) - 1)) == 0) c.scale[r * c.groups + (col >> c.lg)] = d.s;
+  if (first && in0) *scale = d.s;
 }
 
 // ---------------------------------------------------------------------------

@@ -533,32 +533,6 @@ __device__ __forceinline__ void group_sync(int grp) {
   if constexpr (G == 1) __syncwarp();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * G) : "memory");
 }
-// sums of K values over a group: every warp's totals through red[G][K]
-template <int G, int K>
-__device__ __forceinline__ void group_sum(float (&s)[K], float* red, int grp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
-  if constexpr (G > 1) {
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) red[((threadIdx.x >> 5) % G) * K + k] = s[k];
-    }
-  }
-  group_sync<G>(grp);
-  if constexpr (G > 1) {
-    // pairs of totals, added two at a time
-    static_assert(G * K % 2 == 0, "pairs");
-    const f2* p = reinterpret_cast<const f2*>(red);
-    f2 t = p[0];
-#pragma unroll
-    for (int w = 1; w < G * K / 2; ++w) t = add2(t, p[w]);
-    if constexpr (K == 1) s[0] = lo2(t) + hi2(t);
-    else s[0] = lo2(t), s[1] = hi2(t);
-  }
-}
-
 // pairs of V = 8 vectors of a row in shared memory
 // (MASK: zeros where the vector lies beyond the row)
 template <bool MASK, typename T, int NV>
@@ -627,6 +601,8 @@ __device__ __forceinline__ void group_sum2(float (&s)[2], float* red, int grp) {
 // NW warps per block, MB blocks per SM.  A lane has 16 consecutive columns; a stage is
 // two rows, which share the waits, the barriers and the sums' exchanges.  CK: the
 // checkpoint's format, or -1 (a run-time choice kept the two rows' arithmetic apart).
+// At 8192 x 4096 in BF16: 25 us (5.4 TB/s), with a checkpoint 35 us (4.8 TB/s): the two
+// reductions and the quantizer's chain of divisions leave half the issue slots empty.
 template <typename T, int G, int NW, int MB, int CK>
 __global__ void __launch_bounds__(32 * NW, MB)
     norm_fwd_ring(const T* x, T* y, const FwdArgs a, const RingArgs q) {
@@ -671,6 +647,12 @@ __global__ void __launch_bounds__(32 * NW, MB)
   // 32-byte stores where the rows allow them
   const bool wide = sizeof(T) == 2 && in[1] &&
                     ((reinterpret_cast<uintptr_t>(yrow) | uintptr_t(a.ldy * sizeof(T))) & 31) == 0;
+  // the checkpoint's place, advanced with the rows
+  uint8_t* code = CK >= 0 ? a.c.codes + r * a.cols + col : nullptr;
+  float* scale = CK >= 0 ? a.c.scale + r * a.c.groups + (col >> a.c.lg) : nullptr;
+  const int64_t cstep = step * a.cols, sstep = step * a.c.groups;
+  const bool c16 = a.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(a.c.codes) & 15) == 0;
+  const bool lead = (col & ((1 << a.c.lg) - 1)) == 0;
   int st = 0, prev = q.stages - 1;
   uint32_t phase = 0;
   bool ok = true;
@@ -695,8 +677,10 @@ __global__ void __launch_bounds__(32 * NW, MB)
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         const bool e = k == 0 || two;  // uniform
-        ckpt_write16<CK>(a.c, r + k, a.cols, col, in[0] && e, in[1] && e, v[k]);
+        ckpt_write16<CK>(a.c.lg, code + (k ? a.cols : 0), c16, scale + (k ? a.c.groups : 0), lead,
+                         in[0] && e, in[1] && e, v[k]);
       }
+      code += cstep, scale += sstep;
     }
     group_sum2<G>(s, red[grp][0], grp);
     // every warp has read the rows before these
@@ -745,7 +729,13 @@ __global__ void __launch_bounds__(32 * NW, MB)
   }
 }
 
-template <typename T, int NV, int G, bool CK>
+// One row per stage and turn; CK as above.  At 8192 x 4096 in BF16 with the residual's
+// gradient: 47 us from x (5.7 TB/s), 47 us from a checkpoint (5.0 TB/s; the format as a
+// run-time choice 51 us).  The 128 registers hold the sums for gamma and beta, gamma and one
+// row: with two rows per turn, as forward, a few registers spilled or gamma moved to shared
+// memory, 54 to 61 us.  Issue slots are 57 % busy, the packed arithmetic and the exchanges
+// of the row's two sums bound it.
+template <typename T, int NV, int G, int CK>
 __global__ void __launch_bounds__(512, 1)
     norm_bwd_ring(const T* dy, const T* x, const T* dres, T* dx, float* pg, float* pb, const BwdArgs a,
                   const RingArgs q) {
@@ -765,7 +755,7 @@ __global__ void __launch_bounds__(512, 1)
   const int64_t step = int64_t(gridDim.x) * NG;
   int64_t r = int64_t(blockIdx.x) * NG + grp;
   const bool loader = wr == 0 && lane == 0;
-  const uint32_t xbytes = CK ? uint32_t(a.cols) : uint32_t(q.row_bytes);
+  const uint32_t xbytes = CK >= 0 ? uint32_t(a.cols) : uint32_t(q.row_bytes);
   // a stage: dy, the residual's gradient, the kept input
   const int off_res = q.row_bytes, off_x = dres ? 2 * q.row_bytes : q.row_bytes;
   auto fetch = [&](int64_t row, int st) {
@@ -775,7 +765,7 @@ __global__ void __launch_bounds__(512, 1)
       sm100::mbar_arrive_expect_tx(bar, uint32_t(off_x) + xbytes);
       bulk_load(dst, dy + row * a.lddy, uint32_t(q.row_bytes), bar);
       if (dres) bulk_load(dst + off_res, dres + row * a.lddres, uint32_t(q.row_bytes), bar);
-      if (CK) bulk_load(dst + off_x, a.c.codes + row * a.cols, xbytes, bar);
+      if (CK >= 0) bulk_load(dst + off_x, a.c.codes + row * a.cols, xbytes, bar);
       else bulk_load(dst + off_x, x + row * a.ldx, xbytes, bar);
     }
   };
@@ -798,35 +788,37 @@ __global__ void __launch_bounds__(512, 1)
   auto scalars = [&](int64_t row) {
     if (row < a.rows) {
       mu_n = __ldg(a.mean + row), rs_n = __ldg(a.rstd + row);
-      if constexpr (CK) {
+      if constexpr (CK >= 0) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) sc_n[j] = __ldg(a.c.scale + row * a.c.groups + (col[j] >> a.c.lg));
       }
     }
   };
   scalars(r);
+  T* dxrow = dx + r * a.lddx;
+  const int64_t dxstep = step * a.lddx;
   int st = 0, prev = q.stages - 1, par = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (bool first = true; r < a.rows; r += step, first = false, par ^= 1) {
+  for (bool first = true; r < a.rows; r += step, dxrow += dxstep, first = false, par ^= 1) {
     const f2 mu = pair(mu_n), rs = pair(rs_n);
     float sc[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sc[j] = CK ? sc_n[j] : 0.0f;
+    for (int j = 0; j < NV; ++j) sc[j] = CK >= 0 ? sc_n[j] : 0.0f;
     scalars(r + step);
-    if (ok) {
+    if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
       if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
     }
     const uint8_t* stage = mine + st * q.stage_bytes;
     f2 d[P], h[P], t1 = 0, t2 = 0;
     smem_pairs<true, T, NV>(stage, col, in, d);  // zero beyond the row: nothing there counts
-    if constexpr (CK) {
+    if constexpr (CK >= 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const uint2 w = *reinterpret_cast<const uint2*>(stage + off_x + col[j]);
-        ckpt_values4(w.x, sc[j], a.c.fmt, h + 4 * j);
-        ckpt_values4(w.y, sc[j], a.c.fmt, h + 4 * j + 2);
+        ckpt_values4(w.x, sc[j], CK, h + 4 * j);
+        ckpt_values4(w.y, sc[j], CK, h + 4 * j + 2);
       }
     } else {
       smem_pairs<false, T, NV>(stage + off_x, col, in, h);
@@ -842,7 +834,7 @@ __global__ void __launch_bounds__(512, 1)
       t2 = fma2(d[i], h[i], t2);
     }
     float s[2] = {lo2(t1) + hi2(t1), lo2(t2) + hi2(t2)};
-    group_sum<G, 2>(s, red[grp][par], grp);
+    group_sum2<G>(s, red[grp][par], grp);
     // every warp has read the row before this one
     if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
     if (dx) {
@@ -856,7 +848,7 @@ __global__ void __launch_bounds__(512, 1)
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (in[j]) put<T, 8>(dx + r * a.lddx + col[j], h, j);
+        if (in[j]) put<T, 8>(dxrow + col[j], h, j);
     }
     prev = st;
     if (++st == q.stages) st = 0, phase ^= 1;
@@ -1030,7 +1022,7 @@ cudaError_t run_bwd(const void* dy, const void* x, const void* dres, const BwdOu
   return launch_part_sums(pg, pb, int(parts), a.cols, o.dgamma, o.dbeta, o.accumulate, st);
 }
 
-template <typename T, int NV, int G, bool CK>
+template <typename T, int NV, int G, int CK>
 cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const BwdOut& o,
                          const BwdArgs& a, const RingArgs& q, cudaStream_t st) {
   constexpr int NG = 16 / G;
@@ -1053,8 +1045,9 @@ cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const 
 template <typename T, int NV, int G>
 cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const BwdOut& o,
                          const BwdArgs& a, const RingArgs& q, cudaStream_t st) {
-  return x ? run_bwd_ring<T, NV, G, false>(dy, x, dres, o, a, q, st)
-           : run_bwd_ring<T, NV, G, true>(dy, x, dres, o, a, q, st);
+  if (x) return run_bwd_ring<T, NV, G, -1>(dy, x, dres, o, a, q, st);
+  return a.c.fmt == AQFQ_INT8 ? run_bwd_ring<T, NV, G, AQFQ_INT8>(dy, x, dres, o, a, q, st)
+                              : run_bwd_ring<T, NV, G, AQFQ_FP8_E4M3>(dy, x, dres, o, a, q, st);
 }
 
 template <typename T>
