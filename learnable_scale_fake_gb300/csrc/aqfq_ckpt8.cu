@@ -459,7 +459,8 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
                       : 1;
   Map m = make_map(rows, cols, c.lg, vec, dbias ? kMaxParts : 65535);
   // few rows (eight per warp in eight slices): the slices of a column segment form a
-  // cluster and add up their sums there, in place of a second launch
+  // cluster and add up their sums there (512 x 1024 6.7 us on the GPU against 4.9 with a
+  // second launch, which costs the host 3.3 us; 64 x 4096 3.8 both ways)
   const Join jn = {dbias, nullptr, accumulate, dbias && rows <= (int64_t(8 * 8 * kWarps) << (5 - m.lr))};
   if (jn.on && m.gy > 8) m.gy = 8;
   cudaError_t launched = cudaSuccess;

@@ -348,8 +348,9 @@ __device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0
 // taddr.  `in`: the row exists.  Every lane of the warp calls it.  sb: the columns'
 // bias in shared memory.  A checkpoint group may be larger than the warp's columns:
 // its amax is then taken by every warp that has a part of it (the accumulators and
-// the bias of the 128 columns around are at hand).  nx holds the first chunk's inputs (loaded before the accumulators were
-// waited for); the next chunk's inputs and sums are under way while one is computed.
+// the bias of the 128 columns around are at hand).  nx holds the first chunk's inputs
+// (loaded before the accumulators were waited for); the next chunk's inputs and sums are
+// under way while one is computed.
 template <int PASS, int ACT>
 __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col,
                                              uint32_t taddr, const float* sb, ChunkIn<PASS>& nx,
@@ -572,17 +573,23 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 // x BN columns per CTA) are double-buffered in tensor memory, so the epilogue of
 // a tile runs under the next tile's MMAs.  Ragged edges and the tail of k are
 // zeros from the TMA's fill.
-//   warp 0  TMA producer    warp 1  MMA issuer (leader)    warp 2  tensor memory
-//   warps 4-19  epilogue, four per quarter of the rows, a quarter of the columns each
+//   warp 0  TMA producer    warp 1  MMA issuer (leader), tensor memory
+//   warps 2-17  epilogue, four per quarter of the rows, a quarter of the columns each
 //               (with two per quarter the forward with GELU and checkpoint took 192 us at
-//               8192 x 4096 x 4096, with four 167 us)
+//               8192 x 4096 x 4096, with four 167 us).  Eighteen warps leave 112
+//               registers a thread; with twenty and 96 the input gradient's epilogue spilled
+//               (4096 x 2048 x 8192 with GELU's slope 96 us, now 88).
+// At 8192 x 4096 x 4096 (1884 TFLOP/s in a plain library product of that precision): forward
+// with GELU 145-155 us, with a checkpoint too 160 us, input gradient 140-147 us (1.9
+// PFLOP/s), weight gradient 155-165 us.  The MMAs run 82 % of the time; the rest is the
+// first loads, the last tile's epilogue and tiles that do not divide evenly among 76 pairs.
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
 using namespace sm100;
 
 constexpr int kRows = 256, kHalf = 128, kBK = 64;
-constexpr int kThreadsP = 128 + 32 * kEpiWarps;
+constexpr int kThreadsP = 64 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
 template <int BN>
@@ -634,10 +641,9 @@ __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& 
 // axis; the partial sums meet through distributed shared memory, each CTA finishing
 // its share of the rows (one launch, no scratch; the sums in the slices' order).
 // MC: a cluster of two pairs takes two tiles of one column; each pair loads half of
-// their common columns' operand and multicasts it to the other.  The sum of what the
-// SMs read from L2 bounds the main loop (about 14.7 TB/s in sum, 0.34 us per step with
-// every pair loading all of its operands); a stage is then free when both pairs have
-// read it.
+// their common columns' operand and multicasts it to the other, a quarter less to read
+// from L2 (0.297 us per step of every SM against 0.336); a stage is then free when both
+// pairs have read it.
 template <int PASS, int ACT, int BN, bool SPLIT, bool MC>
 __global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     prefetch_tmap(&ta);
     prefetch_tmap(&tb);
   }
-  if (warp == 2) tmem_alloc_pair(&sh->tmem, 512);
+  if (warp == 1) tmem_alloc_pair(&sh->tmem, 512);
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -794,10 +800,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         mbar_wait_long(&sh->drain, 0);
       }
     }
-  } else if (warp >= 4) {
-    const int q = warp & 3, part = (warp - 4) >> 2;
+  } else {
+    const int q = warp & 3, part = (warp - 2) >> 2;
     constexpr int W = BN / (kEpiWarps / 4);  // columns of this warp
-    float* mybias = sbias + (warp - 4) * 128;
+    float* mybias = sbias + (warp - 2) * 128;
     int n = 0;
     for (int u = pair; u < units; u += npairs, ++n) {
       int tr, tc;
@@ -825,7 +831,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       // one thread waits for the tile, the other warps for it at a barrier: sixteen
       // polling warps slowed the MMAs beside them by a tenth
-      if (warp == 4 && lane == 0) {
+      if (warp == 2 && lane == 0) {
         const bool ok = mbar_wait_long(&sh->tfull[buf], (n >> 1) & 1) && !*abort;
         if (!ok) *abort = 1;
         sh->stop[buf] = ok ? 0 : 1;  // read by every warp after this barrier, before the next one
@@ -888,7 +894,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int64_t c0 = int64_t(tc) * BN + half * (BN / 2), col = c0 + (lane & 15) * 8;
     float bias[8] = {};
     if (PASS == P_FWD) load_bias(e, col, bias);
-    if (warp >= 4 && c0 < e.cols)
+    if (warp >= 2 && c0 < e.cols)
       for (int row = row0 + (warp >> 1) * 2 + (lane >> 4); row < rend; row += NW)
         prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
     __syncwarp();
@@ -909,7 +915,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();  // the peer's MMAs and arrivals into this CTA are done
-  if (warp == 2) {
+  if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, 512);
   }

@@ -395,8 +395,11 @@ struct RowRegs {
   }
 };
 
+// (with 1024 threads, 64 registers each, 30 to 60 of them spilled: 64 x 1024 11 us instead
+// of 6.8, 2000 x 4001 from a checkpoint 53 instead of 31)
+constexpr int kBwdThreads = 512;
 template <typename T, int V, int NV, int G, bool CK, bool PF>
-__global__ void __launch_bounds__(1024, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     norm_bwd_rows(const T* dy, const T* x, const T* dres, T* dx, float* pg, float* pb,
                   const BwdArgs a, const Join jn) {
   constexpr int C = 32 * G * NV * V, P = NV * V / 2;  // columns a row may have
@@ -991,13 +994,14 @@ template <typename T, int V, int NV, int G, bool PF>
 cudaError_t run_bwd(const void* dy, const void* x, const void* dres, const BwdOut& o, const BwdArgs& a,
                     cudaStream_t st) {
   // rows per block: up to 32 warps (and 15 named barriers), fewer when there are few rows
-  constexpr int most = G == 1 ? 32 : (32 / G < 15 ? 32 / G : 15), C = 32 * G * NV * V;
+  constexpr int most = G == 1 ? 16 : kBwdThreads / 32 / G, C = 32 * G * NV * V;
   const bool cols = o.dgamma || o.dbeta;
   int64_t ng = (a.rows + kSms - 1) / kSms;
   Join jn = {o.dgamma, o.dbeta, o.accumulate, false};
-  // at most four rows per group of a cluster's eight blocks: one launch, the blocks'
-  // column sums meet in the cluster
-  if (cols && C <= 4096 && a.rows <= 8 * 4 * most) {
+  // at most one row per group of a cluster's eight blocks: one launch, the blocks' column
+  // sums meet in the cluster (32 x 1024 6.1 us on the GPU against 4.2 for two launches, the
+  // second of which costs the host 3.3 us; at four rows per group 7.9 against 4.6)
+  if (cols && C <= 4096 && a.rows <= 8 * most) {
     jn.on = true;
     ng = a.rows < most ? a.rows : most;
   }
@@ -1068,20 +1072,19 @@ cudaError_t launch_bwd(const void* dy, const void* x, const void* dres, const Bw
     }
   }
   if (a.vec && a.pvec && c % 8 == 0 && a.cvec) {
-    constexpr bool PF = sizeof(T) == 2;  // two binary32 rows do not fit the registers
-    if (c <= 256) return run_bwd<T, 8, 1, 1, PF>(dy, x, dres, o, a, st);
-    if (c <= 512) return run_bwd<T, 8, 1, 2, PF>(dy, x, dres, o, a, st);
-    if (c <= 1024) return run_bwd<T, 8, 1, 4, PF>(dy, x, dres, o, a, st);
-    if (c <= 2048) return run_bwd<T, 8, 1, 8, PF>(dy, x, dres, o, a, st);
-    if (c <= 4096) return run_bwd<T, 8, 1, 16, PF>(dy, x, dres, o, a, st);
-    if (c <= 8192) return run_bwd<T, 8, 1, 32, PF>(dy, x, dres, o, a, st);
+    if (c <= 256) return run_bwd<T, 8, 1, 1, true>(dy, x, dres, o, a, st);
+    if (c <= 512) return run_bwd<T, 8, 1, 2, true>(dy, x, dres, o, a, st);
+    if (c <= 1024) return run_bwd<T, 8, 1, 4, true>(dy, x, dres, o, a, st);
+    if (c <= 2048) return run_bwd<T, 8, 1, 8, true>(dy, x, dres, o, a, st);
+    if (c <= 4096) return run_bwd<T, 8, 1, 16, true>(dy, x, dres, o, a, st);
+    if (c <= 8192) return run_bwd<T, 8, 2, 16, sizeof(T) == 2>(dy, x, dres, o, a, st);
   } else {
     if (c <= 128) return run_bwd<T, 1, 4, 1, true>(dy, x, dres, o, a, st);
     if (c <= 512) return run_bwd<T, 1, 4, 4, true>(dy, x, dres, o, a, st);
     if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(dy, x, dres, o, a, st);
     if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(dy, x, dres, o, a, st);
-    if (c <= 4096) return run_bwd<T, 1, 4, 32, true>(dy, x, dres, o, a, st);
-    if (c <= 8192) return run_bwd<T, 1, 8, 32, false>(dy, x, dres, o, a, st);
+    if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(dy, x, dres, o, a, st);
+    if (c <= 8192) return run_bwd<T, 1, 16, 16, false>(dy, x, dres, o, a, st);
   }
   const T *tdy = static_cast<const T*>(dy), *tx = static_cast<const T*>(x);
   if (o.dx) {
