@@ -274,6 +274,44 @@ struct ChunkIn {
   }
 };
 
+// 16 columns of row r from cc on (n of them in the row): adds what `cur` holds and stores
+template <int PASS>
+__device__ __forceinline__ void finish_chunk(const Epi& e, int64_t r, int64_t cc, int n,
+                                             const ChunkIn<PASS>& cur, float (&v)[16]) {
+  const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
+  if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
+    float* p = static_cast<float*>(e.out) + r * e.ldo + cc;
+    const bool a16 = seg(p, n == 16).a16;
+    if constexpr (PASS == P_WGRAD) {
+      if (adds) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(cur.w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      if (a16) {
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < n) p[i + j] = v[i + j];
+      }
+    }
+  } else {
+    if (adds) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(cur.w[i]), v[2 * i + 1] += bf_hi(cur.w[i]);
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+    bf16* p = static_cast<bf16*>(e.out) + r * e.ldo + cc;
+    const Seg q = seg(p, n == 16);
+    st16(p, q.a32, q.a16, n, w);
+  }
+}
+
 // The codes of a row's 16 CH columns from col on and their scales (one per 32 columns):
 // all of them are fetched before the accumulators are waited for.
 template <int CH>
@@ -357,7 +395,6 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
                                              const RowCodes<kChunks>& codes) {
   constexpr bool CODES_IN = PASS == P_DGRAD && ACT != AQFQ_ACT_NONE;
   const bool codes_out = PASS == P_FWD && e.c.codes;
-  const bool adds = PASS == P_WGRAD ? e.accumulate != 0 : e.res != nullptr;
   const int64_t avail = (e.cols - col + 15) / 16;
   const int nch = avail < kChunks ? int(avail) : kChunks;
   const int gch = codes_out ? 1 << (e.c.lg - 4) : nch;  // chunks per group
@@ -431,39 +468,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
           ckpt_values4(codes.w[CODES_IN ? i0 : 0][i], codes.scale[CODES_IN ? i0 / 2 : 0], e.c.fmt, p + 4 * i);
         slope_all<ACT>(p, v);
       }
-      if (in) {
-        if (PASS == P_WGRAD && e.out_dtype == AQFQ_F32) {
-          float* p = static_cast<float*>(e.out) + r * e.ldo + cc;
-          const bool a16 = seg(p, n == 16).a16;
-          if constexpr (PASS == P_WGRAD) {
-            if (adds) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(cur.w[i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            if (a16) {
-              *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (i + j < n) p[i + j] = v[i + j];
-            }
-          }
-        } else {
-          if (adds) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[2 * i] += bf_lo(cur.w[i]), v[2 * i + 1] += bf_hi(cur.w[i]);
-          }
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
-          bf16* p = static_cast<bf16*>(e.out) + r * e.ldo + cc;
-          const Seg q = seg(p, n == 16);
-          st16(p, q.a32, q.a16, n, w);
-        }
-      }
+      if (in) finish_chunk<PASS>(e, r, cc, n, cur, v);
     }
   }
 }
@@ -924,12 +929,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
 // ---------------------------------------------------------------------------
 // small products: one CTA per 128 x 128 tile and slice of the inner axis, the S
-// slices of a tile in a cluster.  Six stages of 32 KiB; warp 0 issues the loads, warp
-// 1 the MMAs; then all sixteen warps move the accumulators to shared memory (the
-// stages are consumed), the cluster meets, and each CTA finishes its share of the
-// rows that exist: a warp takes whole rows of 128 columns, reads every slice's
-// value through distributed shared memory and adds them in the slices' order.
+// slices of a tile in a cluster.  Six stages of 32 KiB; warp 0 issues the loads (the
+// first six before the block has set up), warp 1 the MMAs.  A whole sum (one slice, no
+// checkpoint to write) goes from tensor memory through the epilogue, a row per lane;
+// else all sixteen warps move the accumulators to shared memory (the stages are
+// consumed), the cluster meets, and each CTA finishes its share of the rows that exist: a
+// warp takes whole rows of 128 columns, reads every slice's value through distributed
+// shared memory and adds them in the slices' order.
 // Few rows (a token or two): the weight is streamed once by tiles x S CTAs.
+// 24 x 2048 x 768 5 us, 1 x 4096 x 4096 8.6 us (the weight at 3.9 TB/s), 1000 x 1536 x
+// 2048 10.5 us: about 4.5 us are launch, first loads and epilogue, a step of 64 takes 0.2
+// us (a whole SM's MMAs: 0.17).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
 constexpr int kWarpsC = 16;
@@ -963,6 +973,26 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   const int k0 = int(int64_t(a.ksteps) * slice / a.splits);
   const int n = int(int64_t(a.ksteps) * (slice + 1) / a.splits) - k0;
 
+  auto load = [&](int k, int s) {
+    if (elect_one()) {
+      uint8_t *da = smem + s * 2 * kABytes, *db = da + kABytes;
+      const int kk = (k0 + k) * kBK;
+      mbar_arrive_expect_tx(&sh->full[s], kABytes + (A_MN ? kABytes : uint32_t(a.a_rows * kBK * 2)));
+      if constexpr (A_MN) {
+        tma_load_2d(da, &ta, &sh->full[s], int(r0), kk);
+        tma_load_2d(da + kABytes / 2, &ta, &sh->full[s], int(r0) + 64, kk);
+      } else {
+        tma_load_2d(da, &ta, &sh->full[s], kk, int(r0));
+      }
+      if constexpr (B_MN) {
+        tma_load_2d(db, &tb, &sh->full[s], int(c0), kk);
+        tma_load_2d(db + kABytes / 2, &tb, &sh->full[s], int(c0) + 64, kk);
+      } else {
+        tma_load_2d(db, &tb, &sh->full[s], kk, int(c0));
+      }
+    }
+    __syncwarp();
+  };
   if (warp == 0) {
     if (lane == 0) {
       for (int s = 0; s < kStagesC; ++s) {
@@ -973,11 +1003,11 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
       sh->abort = 0;
       fence_barrier_init();
     }
+    __syncwarp();
+    // the first stages are on their way before the others have set up
+    for (int k = 0; k < n && k < kStagesC; ++k) load(k, k);
   } else if (warp == 1) {
     tmem_alloc(&sh->tmem, kTile);
-  } else if (warp == 2 && lane == 0) {
-    prefetch_tmap(&ta);
-    prefetch_tmap(&tb);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -987,30 +1017,13 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
 
   if (warp == 0) {
     int s = 0;
-    uint32_t phase = 1;  // the first round finds every stage empty
-    for (int k = 0; k < n; ++k) {
-      if (k >= kStagesC && !mbar_wait_long(&sh->empty[s], phase)) {
+    uint32_t phase = 0;
+    for (int k = kStagesC; k < n; ++k) {
+      if (!mbar_wait_long(&sh->empty[s], phase)) {
         *abort = 1;
         break;
       }
-      if (elect_one()) {
-        uint8_t *da = smem + s * 2 * kABytes, *db = da + kABytes;
-        const int kk = (k0 + k) * kBK;
-        mbar_arrive_expect_tx(&sh->full[s], kABytes + (A_MN ? kABytes : uint32_t(a.a_rows * kBK * 2)));
-        if constexpr (A_MN) {
-          tma_load_2d(da, &ta, &sh->full[s], int(r0), kk);
-          tma_load_2d(da + kABytes / 2, &ta, &sh->full[s], int(r0) + 64, kk);
-        } else {
-          tma_load_2d(da, &ta, &sh->full[s], kk, int(r0));
-        }
-        if constexpr (B_MN) {
-          tma_load_2d(db, &tb, &sh->full[s], int(c0), kk);
-          tma_load_2d(db + kABytes / 2, &tb, &sh->full[s], int(c0) + 64, kk);
-        } else {
-          tma_load_2d(db, &tb, &sh->full[s], kk, int(c0));
-        }
-      }
-      __syncwarp();
+      load(k, s);
       if (++s == kStagesC) {
         s = 0;
         phase ^= 1;
@@ -1048,8 +1061,65 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     __syncwarp();
   }
   __syncwarp();
-  // this CTA's rows, two per warp and turn; what they read is sent to L2 meanwhile
   const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
+  if (a.splits == 1 && !(PASS == P_FWD && e.c.codes)) {
+    // a whole sum: from tensor memory, a row per lane and 32 columns per warp (through shared
+    // memory below, 1000 x 1536 x 2048 took 12.1 us instead of 10.5)
+    const int q = warp & 3;
+    const int64_t r = r0 + q * 32 + lane, col = c0 + (warp >> 2) * 32;
+    const bool live = q * 32 < nrows && col < e.cols, in = live && r < e.rows;  // live: uniform
+    ChunkIn<PASS> add[2];
+    RowCodes<2> codes;
+    float bias[4][8];
+    if (in) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (col + c * 16 < e.cols) add[c].load(e, r, col + c * 16);
+      if (PASS == P_DGRAD && e.c.codes) codes.load(e, r, col);
+      if (PASS == P_FWD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_bias(e, col + i * 8, bias[i]);
+      }
+    }
+    __syncwarp();
+    if (!mbar_wait_long(&sh->accum, 0)) *abort = 1;
+    __syncwarp();
+    tc_fence_after_sync();
+    if (live) {
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
+      uint32_t t[16];
+      float v[16];
+      tmem_issue(taddr, t);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t left = e.cols - (col + c * 16);
+        tmem_take(t, v);
+        if (c == 0) tmem_issue(taddr + 16, t);
+        if (!in || left <= 0) continue;
+        if (PASS == P_FWD) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += bias[2 * c + i / 8][i % 8];
+          act_apply(e.act, v);
+        }
+        if (PASS == P_DGRAD && e.c.codes) {
+          float p[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ckpt_values4(codes.w[c][i], codes.scale[0], e.c.fmt, p + 4 * i);
+          slope_apply(e.act, p, v);
+        }
+        finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v);
+      }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after_sync();
+      tmem_dealloc(tmem, kTile);
+    }
+    if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
+    return;
+  }
+  // this CTA's rows, two per warp and turn; what they read is sent to L2 meanwhile
   const int row0 = nrows * slice / a.splits + warp * 2, rend = nrows * (slice + 1) / a.splits;
   for (int row = row0 + (lane >> 4); row < rend; row += 2 * kWarpsC)
     prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
