@@ -402,3 +402,41 @@ def test_workspace_is_checked_and_bounded():
         assert e.value.status == 5
     for M, N, K in ((1 << 20, 4096, 4096), (1 << 20, 264, 264), (1 << 22, 1536, 2048)):
         assert aqfq.aqfq_linear_workspace_bytes(aqfq.LINEAR_WGRAD, M, N, K) <= 64 << 20
+
+
+# 77 to 152 tiles of 128 x 128: one slice each, the sums go straight through the epilogue
+@pytest.mark.parametrize("size", [(1000, 264, 1544), (1100, 136, 1290)])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("fmt,group", [("int8", 32), ("e4m3", 128)])
+def test_input_gradient_of_whole_sums(size, act, fmt, group):
+    M, N, K = size
+    i = group % 3
+    dy, w = randn((M, N), 400 + i), randn((N, K), 410 + i, 0.05)
+    ck, codes, scale = new_ckpt(M, K, fmt, group)
+    aqfq.aqfq_ckpt8_pack(ck, randn((M, K), 420 + i, 1.5).to(DEV))
+    res = randn((M, K), 430 + i) if i else None
+    dx = run_dgrad(dy, w, act, ck, res, seed=i)
+    a, d = dy.double() @ w.double(), dact64(kept(codes, scale, fmt, group), act)
+    e = 2 * N * U * (dy.double().abs() @ w.double().abs())
+    ref = a * d
+    tol = 1.2 * e + (0 if act in ("none", "relu") else ACT_ERR * a.abs()) + 4 * U * ref.abs()
+    if res is not None:
+        ref = ref + res.double()
+    close(dx, ref, tol + BF * ref.abs(), act)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_of_whole_sums(dtype, accumulate):
+    M, N, K = 200, 1000, 1290
+    dy, x = randn((M, N), 440), randn((M, K), 441)
+    base = randn((N, K), 442, 3.0, dtype) if accumulate else None
+    for seed in (0, 1, 2):
+        dw = run_wgrad(dy, x, dtype, base, seed=seed)
+        ref = dy.double().T @ x.double()
+        tol = 2 * M * U * (dy.double().abs().T @ x.double().abs())
+        if base is not None:
+            ref = ref + base.double()
+        tol = tol + 2 * U * ref.abs() + (BF * ref.abs() if dtype == torch.bfloat16 else 0)
+        close(dw, ref, tol)
+
