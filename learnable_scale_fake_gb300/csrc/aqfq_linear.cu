@@ -386,12 +386,13 @@ __device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0
 // taddr.  `in`: the row exists.  Every lane of the warp calls it.  sb: the columns'
 // bias in shared memory.  A checkpoint group may be larger than the warp's columns:
 // its amax is then taken by every warp that has a part of it (the accumulators and
-// the bias of the 128 columns around are at hand).  nx holds the first chunk's inputs
-// (loaded before the accumulators were waited for); the next chunk's inputs and sums are
-// under way while one is computed.
+// the bias of the 128 columns around are at hand).  The next chunk's sums are under way
+// while one is computed; its other inputs, sent to L2 before, are read when it begins (held
+// a chunk ahead, they cost every warp of the kernel 30 spilled registers: 8191 x 4104 x 768
+// with GELU and residual 86 us instead of 78).
 template <int PASS, int ACT>
 __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col,
-                                             uint32_t taddr, const float* sb, ChunkIn<PASS>& nx,
+                                             uint32_t taddr, const float* sb,
                                              const RowCodes<kChunks>& codes) {
   constexpr bool CODES_IN = PASS == P_DGRAD && ACT != AQFQ_ACT_NONE;
   const bool codes_out = PASS == P_FWD && e.c.codes;
@@ -434,12 +435,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
       const int64_t left = e.cols - cc;
       const int n = left > 16 ? 16 : int(left);
       ChunkIn<PASS> cur;
-      if constexpr (CODES_IN) {  // (the codes take the registers of a second set)
-        if (in) cur.load(e, r, cc);
-      } else {
-        cur = nx;
-        if (c + 1 < nch && in) nx.load(e, r, cc + 16);
-      }
+      if (in) cur.load(e, r, cc);
       tmem_take(t, v);
       if (c + 1 < end) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
       if (PASS == P_FWD) {
@@ -818,7 +814,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int64_t col = int64_t(tc) * BN + part * W;
       const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
       const bool fast = whole_block<PASS>(e, r0, col);
-      ChunkIn<PASS> first;
       RowCodes<kChunks> codes;
       if (live && whole) {
         if (PASS == P_FWD && e.bias) {
@@ -831,7 +826,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (r < e.rows) {
           prefetch_inputs<PASS>(e, r, col, W);
           if (PASS == P_DGRAD && ACT != AQFQ_ACT_NONE) codes.load(e, r, col);
-          else if (!fast) first.load(e, r, col);
         }
       }
       // one thread waits for the tile, the other warps for it at a barrier: sixteen
@@ -880,7 +874,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
         } else {
           if (fast) epilogue_whole<PASS, ACT>(e, r, col, taddr, mybias + int(col & 127), codes);
-          else epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), first, codes);
+          else epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), codes);
         }
       }
       tc_fence_before_sync();
