@@ -577,13 +577,15 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 //   warp 0  TMA producer    warp 1  MMA issuer (leader), tensor memory
 //   warps 2-17  epilogue, four per quarter of the rows, a quarter of the columns each
 //               (with two per quarter the forward with GELU and checkpoint took 192 us at
-//               8192 x 4096 x 4096, with four 167 us).  Eighteen warps leave 112
-//               registers a thread; with twenty and 96 the input gradient's epilogue spilled
-//               (4096 x 2048 x 8192 with GELU's slope 96 us, now 88).
-// At 8192 x 4096 x 4096 (1884 TFLOP/s in a plain library product of that precision): forward
-// with GELU 145-155 us, with a checkpoint too 160 us, input gradient 140-147 us (1.9
-// PFLOP/s), weight gradient 155-165 us.  The MMAs run 82 % of the time; the rest is the
-// first loads, the last tile's epilogue and tiles that do not divide evenly among 76 pairs.
+//               8192 x 4096 x 4096, with four 167 us).  Five of the eighteen warps share a
+//               quarter of the SM, which leaves 96 registers a thread: what the epilogues
+//               keep across a tile is counted, spilled registers go to L2 beside 200 KB of
+//               shared memory.
+// At 8192 x 4096 x 4096 (a plain library product: 137-150 us): forward with GELU 145-151
+// us, with a checkpoint too 159-169 us, input gradient 140-153 us, weight gradient 153-165
+// us; two runs differ by so much with the clock under the power limit.  The MMAs run 77 to
+// 83 % of the time; the rest is the first loads, the last tile's epilogue and tiles that do
+// not divide evenly among 76 pairs.
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
