@@ -239,6 +239,22 @@ __device__ __forceinline__ void tmem_take(uint32_t (&r)[16], float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// n <= 16 codes at p: whole, in halves where rows start at odd multiples of 8 (300 x 1000 x
+// 576 with a checkpoint: single bytes 15 us instead of 8), or one by one
+__device__ __forceinline__ void store_codes16(uint8_t* p, int n, const uint32_t (&w)[4]) {
+  const uint32_t a = uint32_t(reinterpret_cast<uintptr_t>(p));
+  if (n == 16 && (a & 15) == 0) {
+    st_128(p, w[0], w[1], w[2], w[3]);
+  } else if ((n & 7) == 0 && (a & 7) == 0) {
+    st_64(p, w[0], w[1]);
+    if (n > 8) st_64(p + 8, w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
 // What 16 columns of a row read besides the sums: the residual, or the previous
 // output of an accumulation.
 template <int PASS>
@@ -328,6 +344,10 @@ struct RowCodes {
       if (seg(p + c * 16, left >= c * 16 + 16).a16) {
         const uint4 u = *reinterpret_cast<const uint4*>(p + c * 16);
         w[c][0] = u.x, w[c][1] = u.y, w[c][2] = u.z, w[c][3] = u.w;
+      } else if (e.vec_codes) {  // rows start at multiples of 8
+        const uint2 u = *reinterpret_cast<const uint2*>(p + c * 16);
+        const uint2 z = left > c * 16 + 8 ? *reinterpret_cast<const uint2*>(p + c * 16 + 8) : make_uint2(0, 0);
+        w[c][0] = u.x, w[c][1] = u.y, w[c][2] = z.x, w[c][3] = z.y;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[c][i] = 0;
@@ -446,14 +466,7 @@ __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, i
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = mk2(v[2 * i], v[2 * i + 1]);
           ckpt_codes(x, div, e.c.fmt, w);
-          uint8_t* p = e.c.codes + r * e.cols + cc;
-          if (seg(p, n == 16).a16) {
-            st_128(p, w[0], w[1], w[2], w[3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i < n) p[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
-          }
+          store_codes16(e.c.codes + r * e.cols + cc, n, w);
         }
         act_all<ACT>(v);
       }
@@ -926,8 +939,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 // ---------------------------------------------------------------------------
 // small products: one CTA per 128 x 128 tile and slice of the inner axis, the S
 // slices of a tile in a cluster.  Six stages of 32 KiB; warp 0 issues the loads (the
-// first six before the block has set up), warp 1 the MMAs.  A whole sum (one slice, no
-// checkpoint to write) goes from tensor memory through the epilogue, a row per lane;
+// first six before the block has set up), warp 1 the MMAs.  A whole sum (one slice) goes
+// from tensor memory through the epilogue, a row per lane;
 // else all sixteen warps move the accumulators to shared memory (the stages are
 // consumed), the cluster meets, and each CTA finishes its share of the rows that exist: a
 // warp takes whole rows of 128 columns, reads every slice's value through distributed
@@ -1058,7 +1071,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   }
   __syncwarp();
   const int nrows = e.rows - r0 > kTile ? kTile : int(e.rows - r0);
-  if (a.splits == 1 && !(PASS == P_FWD && e.c.codes)) {
+  if (a.splits == 1) {
     // a whole sum: from tensor memory, a row per lane and 32 columns per warp (through shared
     // memory below, 1000 x 1536 x 2048 took 12.1 us instead of 10.5)
     const int q = warp & 3;
@@ -1081,29 +1094,63 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     if (!mbar_wait_long(&sh->accum, 0)) *abort = 1;
     __syncwarp();
     tc_fence_after_sync();
+    float v[2][16];
     if (live) {
       const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
       uint32_t t[16];
-      float v[16];
       tmem_issue(taddr, t);
+      tmem_take(t, v[0]);
+      tmem_issue(taddr + 16, t);
+      tmem_take(t, v[1]);
+    }
+    if (PASS == P_FWD && in) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i / 16][i % 16] += bias[i / 8][i % 8];
+    }
+    if (PASS == P_FWD && e.c.codes) {  // uniform over the grid
+      // a group is this warp's 32 columns, or those of two or four neighbouring warps too
+      float* most = reinterpret_cast<float*>(smem);  // [4][128]; the stages are consumed
+      uint32_t m = 0;
+      if (in) {
+        const int64_t left = e.cols - col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = i < left ? v[i / 16][i % 16] : 0.0f;
+        m = max(amax_bits(v[0]), amax_bits(v[1]));
+      }
+      const int part = warp >> 2, at = q * 32 + lane;
+      most[part * 128 + at] = __uint_as_float(m);
+      __syncthreads();
+      if (in) {
+        const int first = part & ~((1 << (e.c.lg - 5)) - 1);
+        for (int i = 0; i < (1 << (e.c.lg - 5)); ++i)
+          m = max(m, __float_as_uint(most[(first + i) * 128 + at]));
+        const Divisor d = ckpt_divisor(m, e.c.fmt);
+        if (part == first) e.c.scale[r * e.c.groups + (col >> e.c.lg)] = d.s;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int64_t left = e.cols - (col + c * 16);
+          uint32_t w[4];
+          f2 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mk2(v[c][2 * i], v[c][2 * i + 1]);
+          ckpt_codes(x, d, e.c.fmt, w);
+          if (left > 0) store_codes16(e.c.codes + r * e.cols + col + c * 16, left > 16 ? 16 : int(left), w);
+        }
+      }
+    }
+    if (in) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int64_t left = e.cols - (col + c * 16);
-        tmem_take(t, v);
-        if (c == 0) tmem_issue(taddr + 16, t);
-        if (!in || left <= 0) continue;
-        if (PASS == P_FWD) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += bias[2 * c + i / 8][i % 8];
-          act_apply(e.act, v);
-        }
+        if (left <= 0) continue;
+        if (PASS == P_FWD) act_apply(e.act, v[c]);
         if (PASS == P_DGRAD && e.c.codes) {
           float p[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) ckpt_values4(codes.w[c][i], codes.scale[0], e.c.fmt, p + 4 * i);
-          slope_apply(e.act, p, v);
+          slope_apply(e.act, p, v[c]);
         }
-        finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v);
+        finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v[c]);
       }
     }
     tc_fence_before_sync();
@@ -1147,26 +1194,19 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     }
   }
   __syncwarp();
-  if (a.splits > 1) cluster_sync();
-  else __syncthreads();
+  cluster_sync();
 #pragma unroll 1
   for (int base = row0; base < rend; base += 2 * kWarpsC) {
     const int row = base + (lane >> 4);
     // (a row past rend is another CTA's or the last one again: read, not used)
     const float* at = sums + (row < kTile ? row : base) * kStrideC + (lane & 15) * 4;
     float v[8];
-    if (a.splits > 1) {
-      cluster_sum8(smem_u32(at), a.splits, 0, 1, v);
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(at), g = *reinterpret_cast<const float4*>(at + 64);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
-    }
+    cluster_sum8(smem_u32(at), a.splits, 0, 1, v);
     epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
   }
   tc_fence_before_sync();
   __syncwarp();
-  if (a.splits > 1) cluster_sync();  // the others have read this CTA's sums
-  else __syncthreads();
+  cluster_sync();  // the others have read this CTA's sums
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTile);
@@ -1276,6 +1316,7 @@ constexpr int64_t kMostScratch = int64_t(64) << 20;
 //   - or every tile's inner axis in slices through scratch, at 6 us for the second
 //     kernel and the partial sums' way to memory and back (weight gradients of many
 //     tokens: few tiles, a long sum).
+// (The same with and without a checkpoint, so that keeping one changes no sum.)
 Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   Plan p;
   p.nr = int((rows + kRows - 1) / kRows);
@@ -1296,6 +1337,10 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
     p.nr = int((rows + kTile - 1) / kTile), p.nc = int((cols + kTile - 1) / kTile);
     int sp = 8;
     while (sp > 1 && (small > kClustersC[sp] || sp > p.ksteps)) --sp;
+    // a short sum over whole tiles is not worth the joining (weight gradient 300 x 520 x
+    // 1032, five steps: 5.5 us in one slice, 7.3 in five; nine steps 6.9 and 7.8; sixteen
+    // steps, 300 x 1000 x 1000, 10.9 and 8.0); few rows are joined quickly
+    if (rows > 64 && p.ksteps <= 10) sp = 1;
     p.splits = sp;
     return p;
   }
