@@ -594,11 +594,11 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 //               quarter of the SM, which leaves 96 registers a thread: what the epilogues
 //               keep across a tile is counted, spilled registers go to L2 beside 200 KB of
 //               shared memory.
-// At 8192 x 4096 x 4096 (a plain library product: 137-150 us): forward with GELU 145-151
-// us, with a checkpoint too 159-169 us, input gradient 140-153 us, weight gradient 153-165
-// us; two runs differ by so much with the clock under the power limit.  The MMAs run 77 to
-// 83 % of the time; the rest is the first loads, the last tile's epilogue and tiles that do
-// not divide evenly among 76 pairs.
+// At 8192 x 4096 x 4096 (plain library products beside: 139-149, 148-153 and 168 us):
+// forward with GELU 148-153 us, with a checkpoint too 160 us, input gradient 154-167 us,
+// weight gradient 162-168 us; two runs differ by so much with the clock under the power
+// limit.  The rest is the first loads, the last tile's epilogue and tiles that do not
+// divide evenly among 76 pairs.
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
@@ -631,7 +631,6 @@ struct __align__(8) PairShared {
 struct PairArgs {
   int nr, nc;        // tiles
   int first, count;  // the tiles of this launch
-  int quad;          // tile order for clusters of two pairs
   int splits;        // slices of the inner axis
   int a_rows;        // rows of A per box (tile_kernel: fewer when there are fewer rows)
   int ksteps;        // 64-element steps of the inner axis
@@ -641,26 +640,19 @@ struct PairArgs {
 };
 
 // tile t: groups of 8 tile rows, column by column, so that the tiles in flight share
-// their operands in L2.  quad: t counts pairs of rows (2 t' + 0, 2 t' + 1 are two rows of
-// one column, the two pairs of a cluster of four CTAs).
+// their operands in L2
 __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& tc) {
-  const int u = a.quad ? t >> 1 : t, nr = a.quad ? a.nr >> 1 : a.nr, high = a.quad ? 4 : 8;
-  const int width = high * a.nc, g = u / width, first = g * high;
-  const int gm = nr - first < high ? nr - first : high;
-  const int in = u - g * width;
+  const int width = 8 * a.nc, g = t / width, first = g * 8;
+  const int gm = a.nr - first < 8 ? a.nr - first : 8;
+  const int in = t - g * width;
   tr = first + in % gm;
   tc = in / gm;
-  if (a.quad) tr = 2 * tr + (t & 1);
 }
 
 // SPLIT: a cluster of S pairs takes one tile, pair i the i-th slice of the inner
 // axis; the partial sums meet through distributed shared memory, each CTA finishing
 // its share of the rows (one launch, no scratch; the sums in the slices' order).
-// MC: a cluster of two pairs takes two tiles of one column; each pair loads half of
-// their common columns' operand and multicasts it to the other, a quarter less to read
-// from L2 (0.297 us per step of every SM against 0.336); a stage is then free when both
-// pairs have read it.
-template <int PASS, int ACT, int BN, bool SPLIT, bool MC>
+template <int PASS, int ACT, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
@@ -674,7 +666,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   PairShared* sh = reinterpret_cast<PairShared*>(reinterpret_cast<uint8_t*>(sbias) + C::BIAS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;
-  static_assert(!(SPLIT && MC), "one use of the cluster");
   const int tiles = a.count, units = SPLIT ? tiles : tiles * a.splits;
   // one unit per cluster, or a strided share of the units per pair
   const int pair = SPLIT ? blockIdx.x / (2 * a.splits) : blockIdx.x >> 1;
@@ -685,7 +676,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], MC ? 2 : 1);
+      mbar_init(&sh->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->tfull[b], 1);
@@ -734,15 +725,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           } else {
             tma_load_2d_pair(da, &ta, bar, k * kBK, r0);
           }
-          if constexpr (MC) {
-            // 64 of this CTA's 128 columns, for both pairs' CTAs of this rank
-            const uint16_t to = uint16_t(5u << rank);
-            const int off = 64 * slice;
-            if constexpr (B_MN)
-              tma_load_2d_pair_mc(db + slice * 8192, &tb, bar, c0 + off, k * kBK, to);
-            else
-              tma_load_2d_pair_mc(db + slice * 8192, &tb, bar, k * kBK, c0 + off, to);
-          } else if constexpr (B_MN) {
+          if constexpr (B_MN) {
 #pragma unroll
             for (int j = 0; j < BN / 128; ++j)
               tma_load_2d_pair(db + j * 8192, &tb, bar, c0 + 64 * j, k * kBK);
@@ -799,7 +782,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc_mma_f16_pair(d, da, db, idesc, k > k0 ? 1u : 0u);
 #pragma unroll
             for (int kk = 1; kk < kBK / 16; ++kk) tc_mma_f16_pair(d, da + kk * ka, db + kk * kb, idesc, 1u);
-            tc_commit_pair(&sh->empty[s], MC ? 15u : mask);
+            tc_commit_pair(&sh->empty[s], mask);
             if (k + 1 == k1) tc_commit_pair(&sh->tfull[buf], mask);
           }
           __syncwarp();
@@ -1287,13 +1270,12 @@ struct Plan {
   bool small;     // tile_kernel (128 x 128 tiles, one CTA each)
   int a_rows;     // rows of A per box
   int tail, tail_splits;  // last tiles that a second launch splits (0: none)
-  int quad;       // clusters of two pairs with multicast
   int64_t cols4;
   size_t bytes;   // scratch
 };
 
 constexpr int kPairs = 76;  // SM pairs
-constexpr double kStepPair = 0.336, kStepQuad = 0.297;  // us per 64 of the inner axis, every SM busy
+constexpr double kStepPair = 0.336;  // us per 64 of the inner axis, every SM busy
 static_assert(kBN / 2 == kHalf && kTile == kHalf, "one box for every operand tile");
 
 // Clusters of 2 S CTAs (one per SM) that run at the same time on this GPU, by S
@@ -1309,8 +1291,7 @@ constexpr int64_t kMostScratch = int64_t(64) << 20;
 //   - at most one 128 x 128 tile per SM and no long inner axis: tile_kernel, with as
 //     many slices as still run together (its steps are short, 0.2 us, and it has one
 //     launch; 24 x 2048 x 768 5 us, 515 x 776 x 1032 9 us where pairs took 13 and 15);
-//   - else rounds of 256 x 256 tiles on pairs (76 at once) or clusters of two pairs (72
-//     at once, shorter steps);
+//   - else rounds of 256 x 256 tiles on pairs, 76 at once;
 //   - the tiles of the last round, where they are few, may be split by a second launch, at
 //     about 17 us of its own (start, joining, epilogue);
 //   - or every tile's inner axis in slices through scratch, at 6 us for the second
@@ -1324,7 +1305,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
   p.small = false;
-  p.a_rows = kHalf, p.tail = p.tail_splits = p.quad = 0;
+  p.a_rows = kHalf, p.tail = p.tail_splits = 0;
   p.cols4 = (cols + 3) / 4 * 4;
   p.bytes = 0;
   if (p.ksteps == 0) return p;
@@ -1345,34 +1326,28 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
     return p;
   }
   const int64_t tiles = int64_t(p.nr) * p.nc;
-  double best = 1e30;
-  for (int quad = p.nr % 2 == 0 ? 1 : 0; quad >= 0; --quad) {
-    const int64_t at_once = quad ? 2 * kClusters[2] : kPairs;
-    const double step = p.ksteps * (quad ? kStepQuad : kStepPair);
-    const int64_t rounds = tiles / at_once;
-    const int rem = int(tiles % at_once);
-    const double plain = step * double(rounds + (rem > 0));
-    if (plain < best) best = plain, p.quad = quad, p.tail = p.tail_splits = 0;
-    int sp = 8;
-    while (sp > 1 && (rem > kClusters[sp] || sp > p.ksteps / 2)) --sp;
-    const double split = step * double(rounds) + p.ksteps * kStepPair / sp + 17.0;
-    if (rounds > 0 && rem > 0 && sp > 1 && split < best)
-      best = split, p.quad = quad, p.tail = rem, p.tail_splits = sp;
-  }
+  const double step = p.ksteps * kStepPair;
+  const int64_t rounds = tiles / kPairs;
+  const int rem = int(tiles % kPairs);
+  double best = step * double(rounds + (rem > 0));
+  int cut = 8;
+  while (cut > 1 && (rem > kClusters[cut] || cut > p.ksteps / 2)) --cut;
+  const double split = step * double(rounds) + step / cut + 17.0;
+  if (rounds > 0 && rem > 0 && cut > 1 && split < best) best = split, p.tail = rem, p.tail_splits = cut;
   for (int sp = 2; sp <= 64 && p.ksteps / sp >= 16; ++sp) {
     const int64_t bytes = int64_t(sp) * rows * p.cols4 * 4;
     if (bytes > kMostScratch) break;
-    const int64_t rounds = (tiles * sp + kPairs - 1) / kPairs;
-    const double t = double(rounds) * double((p.ksteps + sp - 1) / sp) * kStepPair + 6.0 + double(bytes) * 2 / 5e6;
-    if (t < best) best = t, p.splits = sp, p.quad = p.tail = p.tail_splits = 0, p.bytes = size_t(bytes);
+    const int64_t all = (tiles * sp + kPairs - 1) / kPairs;
+    const double t = double(all) * double((p.ksteps + sp - 1) / sp) * kStepPair + 6.0 + double(bytes) * 2 / 5e6;
+    if (t < best) best = t, p.splits = sp, p.tail = p.tail_splits = 0, p.bytes = size_t(bytes);
   }
   return p;
 }
 
-template <int PASS, int ACT, bool SPLIT, bool MC>
+template <int PASS, int ACT, bool SPLIT>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
-  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT, MC>;
+  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
   static const cudaError_t attr = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
   if (attr != cudaSuccess) return attr;
@@ -1383,9 +1358,8 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   }
   const int64_t tiles = a.count, units = tiles * a.splits;
   cudaLaunchConfig_t cfg = {};
-  const int csize = SPLIT ? 2 * a.splits : MC ? 4 : 2;
-  const int64_t most = MC ? 2 * kClusters[2] : kPairs;  // pairs that run together
-  cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < most ? units : most));
+  const int csize = SPLIT ? 2 * a.splits : 2;
+  cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < kPairs ? units : kPairs));
   cfg.blockDim = dim3(kThreadsP);
   cfg.dynamicSmemBytes = Cfg<kBN>::SMEM;
   cfg.stream = st;
@@ -1396,18 +1370,18 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, a, e);
 }
 
-template <int PASS, bool MC>
+template <int PASS>
 cudaError_t launch_act(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                        cudaStream_t st) {
   if constexpr (PASS == P_WGRAD) {
-    return launch_pair<PASS, AQFQ_ACT_NONE, false, MC>(ta, tb, a, e, st);
+    return launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
   } else {
     switch (e.act) {
-      case AQFQ_ACT_RELU: return launch_pair<PASS, AQFQ_ACT_RELU, false, MC>(ta, tb, a, e, st);
-      case AQFQ_ACT_GELU: return launch_pair<PASS, AQFQ_ACT_GELU, false, MC>(ta, tb, a, e, st);
-      case AQFQ_ACT_GELU_TANH: return launch_pair<PASS, AQFQ_ACT_GELU_TANH, false, MC>(ta, tb, a, e, st);
-      case AQFQ_ACT_SILU: return launch_pair<PASS, AQFQ_ACT_SILU, false, MC>(ta, tb, a, e, st);
-      default: return launch_pair<PASS, AQFQ_ACT_NONE, false, MC>(ta, tb, a, e, st);
+      case AQFQ_ACT_RELU: return launch_pair<PASS, AQFQ_ACT_RELU, false>(ta, tb, a, e, st);
+      case AQFQ_ACT_GELU: return launch_pair<PASS, AQFQ_ACT_GELU, false>(ta, tb, a, e, st);
+      case AQFQ_ACT_GELU_TANH: return launch_pair<PASS, AQFQ_ACT_GELU_TANH, false>(ta, tb, a, e, st);
+      case AQFQ_ACT_SILU: return launch_pair<PASS, AQFQ_ACT_SILU, false>(ta, tb, a, e, st);
+      default: return launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
     }
   }
 }
@@ -1447,24 +1421,20 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     if (!encode(&ta, A, kBK, A_MN ? kBK : unsigned(p.a_rows)) ||
         !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
       return AQFQ_ERR_CUDA;
-    CUtensorMap tb64;
-    if (p.quad && !encode(&tb64, B, kBK, kBK)) return AQFQ_ERR_CUDA;
-    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.quad, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
+    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
     cudaError_t r;
     a.count -= p.tail;
     if (p.small) {
       r = launch_tile<PASS>(ta, tb, a, e, st);
     } else if (p.splits > 1) {  // finish_kernel has the epilogue
-      r = launch_pair<PASS, AQFQ_ACT_NONE, false, false>(ta, tb, a, e, st);
-    } else if (p.quad) {
-      r = launch_act<PASS, true>(ta, tb64, a, e, st);
+      r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
     } else {
-      r = launch_act<PASS, false>(ta, tb, a, e, st);
+      r = launch_act<PASS>(ta, tb, a, e, st);
     }
     if (r != cudaSuccess) return AQFQ_ERR_CUDA;
     if (p.tail > 0) {
       a.first = a.count, a.count = p.tail, a.splits = p.tail_splits;
-      if (launch_pair<PASS, AQFQ_ACT_NONE, true, false>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
+      if (launch_pair<PASS, AQFQ_ACT_NONE, true>(ta, tb, a, e, st) != cudaSuccess) return AQFQ_ERR_CUDA;
     }
   }
   if (!p.small && p.splits != 1) {
