@@ -161,6 +161,17 @@ __device__ __forceinline__ f2 masked(f2 v, int i, const bool (&in)[NV]) {
   else return mk2(in[2 * i] ? lo2(v) : 0.0f, in[2 * i + 1] ? hi2(v) : 0.0f);
 }
 
+// a lane's vector j of column sums to scratch, which the caller aligns to 8 bytes only
+template <int V>
+__device__ __forceinline__ void put_sums(float* p, const f2* v, int j) {
+  if constexpr (V == 1) {
+    put<float, 1>(p, v, j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) *reinterpret_cast<f2*>(p + 2 * i) = v[j * (V / 2) + i];
+  }
+}
+
 template <typename T, int V, int NV, int G, int R>
 __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
     norm_fwd_rows(const T* x, T* y, const FwdArgs a) {
@@ -503,8 +514,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (in[j]) {
-        put<float, V>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
-        put<float, V>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
+        put_sums<V>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
+        put_sums<V>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
       }
     }
   }
@@ -884,8 +895,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (in[j]) {
-        put<float, 8>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
-        put<float, 8>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
+        put_sums<8>(pg + int64_t(blockIdx.x) * a.cols + col[j], ag, j);
+        put_sums<8>(pb + int64_t(blockIdx.x) * a.cols + col[j], ab, j);
       }
     }
   }
