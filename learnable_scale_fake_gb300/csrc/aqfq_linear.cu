@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
       const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
       for (int k = k0; k < k1; ++k, ++it) {
-        if (it >= C::STAGES && !mbar_wait_long(&sh->empty[s], phase)) {
+        if (it >= C::STAGES && !mbar_wait_warp(&sh->empty[s], phase)) {
           ok = false;
           break;
         }
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       // let the copies already issued (the peer's among them) land
       if (rank == 0)
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-          mbar_wait_long(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
+          mbar_wait_warp(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -765,14 +765,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
         const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
         const int buf = n & 1;
-        if (n >= 2 && !mbar_wait_long(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
+        if (n >= 2 && !mbar_wait_warp(&sh->tempty[buf], ((n >> 1) & 1) ^ 1)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + uint32_t(buf * 256);
         for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait_long(&sh->full[s], phase)) {
+          if (!mbar_wait_warp(&sh->full[s], phase)) {
             ok = false;
             break;
           }
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         *abort = 1;
         if (elect_one()) tc_commit_pair(&sh->drain, mask);
         __syncwarp();
-        mbar_wait_long(&sh->drain, 0);
+        mbar_wait_warp(&sh->drain, 0);
       }
     }
   } else {
@@ -1011,7 +1011,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     int s = 0;
     uint32_t phase = 0;
     for (int k = kStagesC; k < n; ++k) {
-      if (!mbar_wait_long(&sh->empty[s], phase)) {
+      if (!mbar_wait_warp(&sh->empty[s], phase)) {
         *abort = 1;
         break;
       }
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     int s = 0;
     uint32_t phase = 0;
     for (int k = 0; k < n; ++k) {
-      if (!mbar_wait_long(&sh->full[s], phase)) {
+      if (!mbar_wait_warp(&sh->full[s], phase)) {
         *abort = 1;
         break;
       }
@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
       }
     }
     __syncwarp();
-    if (!mbar_wait_long(&sh->accum, 0)) *abort = 1;
+    if (!mbar_wait_warp(&sh->accum, 0)) *abort = 1;
     __syncwarp();
     tc_fence_after_sync();
     float v[2][16];
@@ -1153,7 +1153,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   float bias[8] = {};
   if (PASS == P_FWD) load_bias(e, col, bias);
   __syncwarp();
-  if (!mbar_wait_long(&sh->accum, 0)) *abort = 1;
+  if (!mbar_wait_warp(&sh->accum, 0)) *abort = 1;
   __syncwarp();
   tc_fence_after_sync();
   float* sums = reinterpret_cast<float*>(smem);

@@ -25,7 +25,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // Waits for a phase: one try first, for a phase that is complete already or soon;
 // then tries that may suspend the warp for long (hint in ns), which leaves the issue
-// slots to the others.  Gives up after about 2^31 cycles (~1 s) and returns false.
+// slots to the others.  Gives up after `limit` cycles (2^31: ~1 s) and returns false.
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity, uint32_t hint) {
   uint32_t ok;
   asm volatile(
@@ -37,12 +37,20 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity, uint32_
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity) {
+constexpr long long kWaitCycles = 1ll << 31;
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity,
+                                               long long limit = kWaitCycles) {
   if (mbar_try(bar, parity, 1000000u)) return true;
   const long long t0 = clock64();
-  while (clock64() - t0 <= (1ll << 31))
+  while (clock64() - t0 <= limit)
     if (mbar_try(bar, parity, 1000000u)) return true;
   return false;
+}
+// The same for a converged warp, with one answer for all of it: every lane has its own
+// clock, and at the limit some could give up while others go on to a warp-wide instruction.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               long long limit = kWaitCycles) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_long(bar, parity, limit));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -1,0 +1,33 @@
+"""The bounded waits of the product kernels, from a small program around the same header."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from learnable_scale_fake_gb300 import _build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def waits(tmp_path_factory):
+    lib = str(tmp_path_factory.mktemp("waits") / "waits.so")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "device_waits.cu")
+    subprocess.run([_build.nvcc(), *_build.ARCH, *_build.FLAGS, "-I", _build.CSRC, "-I", _build.INCLUDE,
+                    "-shared", "-cudart", "shared", "-o", lib, src], check=True)
+    return ctypes.CDLL(lib)
+
+
+def test_a_warp_gives_up_as_one(waits):
+    """Lanes with limits below and above the time the phase completes: alone some give up and
+    some do not; the warp's answer is the same in every lane."""
+    own, every = torch.full((2, 32), -1, dtype=torch.int32, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    torch.cuda.synchronize()
+    # limits of 1 to 32 units of 4 ms: well above the time a suspended try may take
+    assert waits.run_uneven_limits(ctypes.c_longlong(1 << 23), p(own), p(every)) == 0
+    own, every = own.cpu().tolist(), every.cpu().tolist()
+    assert own[0] == 0 and own[31] == 1
+    assert every == [0] * 32

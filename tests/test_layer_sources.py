@@ -27,3 +27,14 @@ def test_no_load_is_multicast_to_a_cluster():
     assert not found
     # the rule sees the copies that are there
     assert any("cp.async.bulk.tensor" in s for s in sources().values())
+
+
+def test_waits_of_the_products_are_uniform_in_a_warp():
+    """The product kernels' loops issue warp-wide instructions after a bounded wait: the answer
+    has to be the warp's, or one thread's that hands it on."""
+    s = sources()["aqfq_linear.cu"]
+    alone = [m.start() for m in re.finditer(r"\bmbar_(?:wait|wait_long|wait_suspend)\(", s)]
+    for at in alone:
+        block = s[:at].rsplit("if (", 1)[1]
+        assert re.match(r"warp == \d+ && lane == 0\)", block), s[at - 200:at + 80]
+    assert len(re.findall(r"\bmbar_wait_warp\(", s)) >= 7
