@@ -626,6 +626,7 @@ struct __align__(8) PairShared {
   uint64_t drain;
   uint32_t tmem;
   int32_t abort, stop[2];
+  int32_t issued;  // steps whose loads were issued
 };
 
 struct PairArgs {
@@ -740,13 +741,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
       }
     }
-    if (!ok) {
-      *abort = 1;
-      // let the copies already issued (the peer's among them) land
-      if (rank == 0)
-        for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-          mbar_wait_warp(&sh->full[i % C::STAGES], (i / C::STAGES) & 1);
-    }
+    if (!ok) *abort = 1;
+    if (lane == 0) sh->issued = it;
   } else if (warp == 1) {
     if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kRows, BN) | (A_MN ? kIdescTransA : 0) |
@@ -911,6 +907,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
+  // whichever wait gave up: the pair's copies, which all count on the leader's barriers
+  if (warp == 0 && rank == 0 && *abort) drain_loads(sh->full, C::STAGES, sh->issued);
+  __syncwarp();
   cluster_sync();  // the peer's MMAs and arrivals into this CTA are done
   if (warp == 1) {
     tc_fence_after_sync();
@@ -945,6 +944,7 @@ struct __align__(8) CtaShared {
   uint64_t accum;
   uint32_t tmem;
   int32_t abort;
+  int32_t issued;  // steps whose loads were issued
 };
 
 template <int PASS>
@@ -1010,7 +1010,8 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   if (warp == 0) {
     int s = 0;
     uint32_t phase = 0;
-    for (int k = kStagesC; k < n; ++k) {
+    int k = n < kStagesC ? n : kStagesC;
+    for (; k < n; ++k) {
       if (!mbar_wait_warp(&sh->empty[s], phase)) {
         *abort = 1;
         break;
@@ -1021,6 +1022,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         phase ^= 1;
       }
     }
+    if (lane == 0) sh->issued = k;
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile) | (A_MN ? kIdescTransA : 0) |
                                (B_MN ? kIdescTransB : 0);
@@ -1142,6 +1144,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
       tc_fence_after_sync();
       tmem_dealloc(tmem, kTile);
     }
+    if (warp == 0 && *abort) drain_loads(sh->full, kStagesC, sh->issued);
     if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
     return;
   }
@@ -1194,6 +1197,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTile);
   }
+  if (warp == 0 && *abort) drain_loads(sh->full, kStagesC, sh->issued);
   if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
 }
 

@@ -53,6 +53,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
   return __all_sync(0xFFFFFFFFu, mbar_wait_long(bar, parity, limit));
 }
 
+// After a wait that gave up: waits, bounded, for the loads still on their way, at most one
+// per stage.  issued: loads so far, number i on the barrier of stage i % stages.  A warp
+// calls it before its block ends, so that no copy lands in the next block's memory.
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int issued,
+                                            long long limit = kWaitCycles) {
+  for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+    mbar_wait_warp(&full[i % stages], (i / stages) & 1, limit);
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

@@ -1,5 +1,6 @@
 // device_waits.cu -- the bounded waits of aqfq_sm100_pair.cuh on their own: a warp whose lanes
-// reach their limits at different times.  Nothing here faults or waits without a limit.
+// reach their limits at different times, and the drain of loads after a wait that gave up.
+// Nothing here faults or waits without a limit.
 #include "aqfq_sm100_pair.cuh"
 
 using namespace aqfq::sm100;
@@ -31,5 +32,48 @@ __global__ void uneven_limits(long long unit, int* own, int* all) {
 
 extern "C" int run_uneven_limits(long long unit, int* own, int* all) {
   uneven_limits<<<1, 96>>>(unit, own, all);
+  return int(cudaDeviceSynchronize());
+}
+
+// One warp issues 5 loads of 1 KiB on 3 stages (reusing a stage only after its load landed),
+// optionally announces a sixth whose bytes never come, drains, and copies the stages out.
+__global__ void drain(const uint8_t* src, int missing, long long limit, uint8_t* out, int* done) {
+  constexpr int N = 1024, STAGES = 3, LOADS = 5;
+  __shared__ __align__(128) uint8_t stage[STAGES][N];
+  __shared__ uint64_t full[STAGES];
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  bool ok = true;
+  for (int i = 0; i < LOADS && ok; ++i) {
+    const int s = i % STAGES;
+    if (i >= STAGES) ok = mbar_wait_warp(&full[s], (i / STAGES - 1) & 1);
+    if (ok && lane == 0) {
+      mbar_arrive_expect_tx(&full[s], N);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              smem_u32(stage[s])),
+          "l"(src + i * N), "r"(N), "r"(smem_u32(&full[s]))
+          : "memory");
+    }
+    __syncwarp();
+  }
+  int issued = LOADS;
+  if (missing && ok) {
+    const int s = issued % STAGES;
+    ok = mbar_wait_warp(&full[s], (issued / STAGES - 1) & 1);
+    if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], N);
+    ++issued;
+  }
+  drain_loads(full, STAGES, issued, limit);
+  for (int i = lane; i < STAGES * N; i += 32) out[i] = (&stage[0][0])[i];
+  if (lane == 0) *done = ok ? 1 : 2;
+}
+
+extern "C" int run_drain(const uint8_t* src, int missing, long long limit, uint8_t* out, int* done) {
+  drain<<<1, 32>>>(src, missing, limit, out, done);
   return int(cudaDeviceSynchronize());
 }

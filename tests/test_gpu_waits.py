@@ -31,3 +31,15 @@ def test_a_warp_gives_up_as_one(waits):
     own, every = own.cpu().tolist(), every.cpu().tolist()
     assert own[0] == 0 and own[31] == 1
     assert every == [0] * 32
+
+
+@pytest.mark.parametrize("missing", [0, 1])
+def test_drain_waits_for_the_loads_in_flight_and_no_longer_than_its_limit(waits, missing):
+    src = torch.randint(0, 256, (5, 1024), dtype=torch.uint8, device="cuda")
+    out, done = torch.zeros(3, 1024, dtype=torch.uint8, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    torch.cuda.synchronize()
+    assert waits.run_drain(p(src), missing, ctypes.c_longlong(1 << 22), p(out), p(done)) == 0
+    assert int(done.item()) == 1
+    # stages 0 and 1 hold loads 3 and 4, stage 2 load 2 (the announced sixth never arrives)
+    assert torch.equal(out, src[[3, 4, 2]])

@@ -38,3 +38,12 @@ def test_waits_of_the_products_are_uniform_in_a_warp():
         block = s[:at].rsplit("if (", 1)[1]
         assert re.match(r"warp == \d+ && lane == 0\)", block), s[at - 200:at + 80]
     assert len(re.findall(r"\bmbar_wait_warp\(", s)) >= 7
+
+
+def test_products_drain_their_loads_before_a_block_ends():
+    """After a wait that gave up, whichever it was: both kernels wait (bounded) for the loads in
+    flight past their last barrier, before the block's memory goes to another one."""
+    s = sources()["aqfq_linear.cu"]
+    drain = r"if \(warp == 0 && (?:rank == 0 && )?\*abort\) drain_loads\(sh->full, \S+ sh->issued\);"
+    assert len(re.findall(drain, s)) == 3
+    assert len(re.findall(r"sh->issued = \w+;", s)) == 2
