@@ -527,13 +527,12 @@ extern "C" aqfq_status aqfq_grouped_qdq_gemm(const void* x, const int32_t* m_off
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return AQFQ_ERR_CUDA;
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(grouped_qdq_gemm_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
-  });
-  if (attr_err != cudaSuccess) return AQFQ_ERR_CUDA;
+  static DeviceOnce once;
+  if (once_per_device(once, [] {
+        return cudaFuncSetAttribute(grouped_qdq_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(kGemmSmem));
+      }) != cudaSuccess)
+    return AQFQ_ERR_CUDA;
   GemmArgs a;
   a.w = static_cast<const uint8_t*>(w);
   a.scale = scale;

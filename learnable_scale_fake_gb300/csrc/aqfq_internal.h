@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "aqfq_device.cuh"
+#include "aqfq_once.h"
 
 namespace aqfq {
 
@@ -26,6 +27,14 @@ struct Problem {
 };
 
 int sm_count();
+
+// set(), which gives the current kernel its attributes, once per device
+template <typename F>
+cudaError_t once_per_device(DeviceOnce& once, F set) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaError_t(once.run(dev, set));
+}
 
 // forward (kernels.cu)
 cudaError_t launch_qdq_fwd(const Problem& p, const void* x, const float* scale,

@@ -1352,14 +1352,15 @@ template <int PASS, int ACT, bool SPLIT>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
   auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
+  static DeviceOnce once;
+  const cudaError_t attr = once_per_device(once, [&] {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
+    if (e != cudaSuccess || !SPLIT) return e;
+    // more than 8 CTAs per cluster
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
   if (attr != cudaSuccess) return attr;
-  if (SPLIT) {  // more than 8 CTAs per cluster
-    static const cudaError_t wide =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (wide != cudaSuccess) return wide;
-  }
   const int64_t tiles = a.count, units = tiles * a.splits;
   cudaLaunchConfig_t cfg = {};
   const int csize = SPLIT ? 2 * a.splits : 2;
@@ -1393,8 +1394,10 @@ cudaError_t launch_act(const CUtensorMap& ta, const CUtensorMap& tb, const PairA
 template <int PASS>
 cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
                         cudaStream_t st) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      tile_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemC));
+  static DeviceOnce once;
+  const cudaError_t attr = once_per_device(once, [] {
+    return cudaFuncSetAttribute(tile_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemC));
+  });
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.nr * a.nc * a.splits));

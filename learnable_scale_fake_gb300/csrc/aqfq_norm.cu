@@ -930,21 +930,22 @@ inline RingArgs make_ring(int stage_bytes, int row_bytes, int groups, int bytes)
 }
 
 template <typename K>
-cudaError_t ring_smem(K kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+cudaError_t ring_smem(DeviceOnce& once, K kernel) {
+  return once_per_device(once, [=] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  });
 }
 
 template <typename T, int G, int NW, int MB>
 cudaError_t run_fwd_ring(const void* x, void* y, const FwdArgs& a, const RingArgs& q, cudaStream_t st) {
   constexpr int NG = NW / G;
-  static const cudaError_t attr[3] = {ring_smem(norm_fwd_ring<T, G, NW, MB, -1>),
-                                      ring_smem(norm_fwd_ring<T, G, NW, MB, AQFQ_INT8>),
-                                      ring_smem(norm_fwd_ring<T, G, NW, MB, AQFQ_FP8_E4M3>)};
+  static DeviceOnce once[3];
   const int k = !a.c.codes ? 0 : a.c.fmt == AQFQ_INT8 ? 1 : 2;
-  if (attr[k] != cudaSuccess) return attr[k];
   auto kernel = k == 0   ? norm_fwd_ring<T, G, NW, MB, -1>
                 : k == 1 ? norm_fwd_ring<T, G, NW, MB, AQFQ_INT8>
                          : norm_fwd_ring<T, G, NW, MB, AQFQ_FP8_E4M3>;
+  const cudaError_t attr = ring_smem(once[k], kernel);
+  if (attr != cudaSuccess) return attr;
   int64_t blocks = (a.rows + 2 * NG - 1) / (2 * NG);
   if (blocks > MB * kSms) blocks = MB * kSms;
   kernel<<<unsigned(blocks), 32 * NW, size_t(NG) * q.stages * q.stage_bytes, st>>>(
@@ -1041,7 +1042,8 @@ template <typename T, int NV, int G, int CK>
 cudaError_t run_bwd_ring(const void* dy, const void* x, const void* dres, const BwdOut& o,
                          const BwdArgs& a, const RingArgs& q, cudaStream_t st) {
   constexpr int NG = 16 / G;
-  static const cudaError_t attr = ring_smem(norm_bwd_ring<T, NV, G, CK>);
+  static DeviceOnce once;
+  const cudaError_t attr = ring_smem(once, norm_bwd_ring<T, NV, G, CK>);
   if (attr != cudaSuccess) return attr;
   const bool cols = o.dgamma || o.dbeta;
   int64_t parts = (a.rows + NG - 1) / NG;
