@@ -365,7 +365,8 @@ aqfq_status aqfq_kd_loss(int kd_type, const void* student, const void* teacher,
  * Sums are held in binary32; stored values are rounded to their type once.
  * Results do not depend on the launch's timing: no floating-point atomics.
  * Non-finite values follow the formulas' arithmetic and stay in the rows (or
- * column sums) they belong to.  Outputs must not overlap inputs or each other. */
+ * column sums) they belong to.  Outputs must not overlap inputs or each other.
+ * All memory of a call is the current device's, as is the stream. */
 typedef enum aqfq_dtype { AQFQ_BF16 = 0, AQFQ_F32 = 1 } aqfq_dtype;
 
 /* act(p): p | max(p, 0) | p Phi(p) | p (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))) / 2

@@ -327,24 +327,33 @@ def aqfq_scale_init(spec, x, scale, tensor_scale, stream=None):
 
 
 # ---- the layer around the fake-quantized weight ---------------------------------------
-# Matrices are 2D tensors with contiguous columns; the row stride is passed on.
+# Matrices are 2D tensors with contiguous columns; the row stride is passed on.  All tensors
+# of a call are on one device, the current one.
 
-def _mat(t, name, dtypes, shape=None):
-    """(address, leading dimension) of a matrix; None gives (None, 0)."""
+def _mat(t, name, dtypes, shape=None, dev=None):
+    """(address, leading dimension) of a matrix; None gives (None, 0).  dev: the index of the
+    call's device, None for the tensor that sets it."""
     if t is None:
         return None, 0
     size = t.shape
-    if t.dtype in dtypes and t.is_cuda and len(size) == 2 and (shape is None or size == shape):
+    if (t.dtype in dtypes and (t.is_cuda if dev is None else t.get_device() == dev) and len(size) == 2
+            and (shape is None or size == shape)):
         ld, inner = t.stride()
         if inner == 1 or size[1] <= 1:
             # a single row has no second one: a leading dimension that every check accepts
             return t.data_ptr(), ld if size[0] > 1 else (size[1] + 7) // 8 * 8
-    _refuse_mat(t, name, dtypes, shape)
+    _refuse_mat(t, name, dtypes, shape, dev)
 
 
-def _refuse_mat(t, name, dtypes, shape):
+def _refuse_device(t, name, dev):
     if not t.is_cuda:
         raise ValueError("aqfq works on CUDA tensors only")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's other tensors on cuda:{dev}")
+
+
+def _refuse_mat(t, name, dtypes, shape, dev):
+    _refuse_device(t, name, dev)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
     if shape is not None and tuple(t.shape) != shape:
@@ -352,14 +361,13 @@ def _refuse_mat(t, name, dtypes, shape):
     raise ValueError(f"{name} must be a matrix with contiguous columns")
 
 
-def _vec(t, name, dtypes, n):
+def _vec(t, name, dtypes, n, dev):
     """Address of a contiguous vector of n elements, or None."""
     if t is None:
         return None
-    if t.dtype in dtypes and t.is_cuda and t.numel() == n and t.is_contiguous():
+    if t.dtype in dtypes and t.get_device() == dev and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
-    if not t.is_cuda:
-        raise ValueError("aqfq works on CUDA tensors only")
+    _refuse_device(t, name, dev)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}")
     raise ValueError(f"{name} must have {n} contiguous elements")
@@ -379,16 +387,27 @@ def _dt(t):
     return BF16 if t is None else _CODE.get(t.dtype, BF16)
 
 
-def _ws(workspace):
+def _ws(workspace, dev):
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse_device(workspace, "workspace", dev)
         _ptr(workspace)  # refuses
     return workspace.data_ptr(), workspace.nbytes
 
 
-def _flag(t):
-    return _vec(t, "error_flag", _I32, 1)
+def _flag(t, dev):
+    return _vec(t, "error_flag", _I32, 1, dev)
+
+
+def _stream_on(stream, dev):
+    """The stream's handle; dev, the device of the call's tensors, has to be the current one."""
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{cur}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(cur)
+    return _stream(stream)
 
 
 def ckpt8(fmt, group, codes, scale) -> Ckpt8:
@@ -402,33 +421,40 @@ def ckpt8(fmt, group, codes, scale) -> Ckpt8:
         raise ValueError("scale must be [rows, ceil(cols / group)]")
     if not (codes.is_cuda and scale.is_cuda and codes.is_contiguous() and scale.is_contiguous()):
         _ptr(codes), _ptr(scale)  # one of them refuses
+    if scale.get_device() != codes.get_device():
+        _refuse_device(scale, "scale", codes.get_device())
     c = Ckpt8(fmt, group, codes.data_ptr(), scale.data_ptr())
     c.tensors = (codes, scale)
     c.size = size
+    c.device = codes.get_device()
     return c
 
 
-def _ck(c, rows, cols):
+def _ck(c, rows, cols, dev):
     """Pointer to the checkpoint of a [rows, cols] matrix, or None."""
     if c is None:
         return None
     if c.size != (rows, cols):
         raise ValueError(f"the checkpoint must be of a [{rows}, {cols}] matrix")
+    if c.device != dev:
+        raise ValueError(f"the checkpoint is on cuda:{c.device}, the call's other tensors on cuda:{dev}")
     return ctypes.byref(c)
 
 
 def aqfq_ckpt8_pack(ckpt, x, stream=None):
     p, ld = _mat(x, "x", _ROWS)
+    dev = x.get_device()
     R, C = x.shape
-    st = (_lib or lib()).aqfq_ckpt8_pack(_ck(ckpt, R, C), _dt(x), p, ld, R, C, _stream(stream))
+    st = (_lib or lib()).aqfq_ckpt8_pack(_ck(ckpt, R, C, dev), _dt(x), p, ld, R, C, _stream_on(stream, dev))
     if st:
         _check("aqfq_ckpt8_pack", st)
 
 
 def aqfq_ckpt8_unpack(ckpt, y, act=ACT_NONE, stream=None):
     p, ld = _mat(y, "y", _ROWS)
+    dev = y.get_device()
     R, C = y.shape
-    st = (_lib or lib()).aqfq_ckpt8_unpack(_ck(ckpt, R, C), int(act), _dt(y), p, ld, R, C, _stream(stream))
+    st = (_lib or lib()).aqfq_ckpt8_unpack(_ck(ckpt, R, C, dev), int(act), _dt(y), p, ld, R, C, _stream_on(stream, dev))
     if st:
         _check("aqfq_ckpt8_unpack", st)
 
@@ -441,14 +467,15 @@ def aqfq_ckpt8_act_bwd(ckpt, act, dy, dx=None, y=None, dbias=None, accumulate=Fa
                        stream=None):
     """dx = dy act'(p), y = act(p) and dbias = column sums of dx for the p kept in ckpt."""
     pd, ldd = _mat(dy, "dy", _ROWS)
+    dev = dy.get_device()
     R, C = dy.shape
-    px, ldx = _mat(dx, "dx", (dy.dtype,), (R, C))
-    py, ldy = _mat(y, "y", (dy.dtype,), (R, C))
-    ws, wsb = _ws(workspace)
+    px, ldx = _mat(dx, "dx", (dy.dtype,), (R, C), dev)
+    py, ldy = _mat(y, "y", (dy.dtype,), (R, C), dev)
+    ws, wsb = _ws(workspace, dev)
     st = (_lib or lib()).aqfq_ckpt8_act_bwd(
-        _ck(ckpt, R, C), int(act), _dt(dy), pd, ldd, R, C, px, ldx, py,
-        ldy, _vec(dbias, "dbias", _FL, C), 1 if accumulate else 0, ws, wsb,
-        _stream(stream))
+        _ck(ckpt, R, C, dev), int(act), _dt(dy), pd, ldd, R, C, px, ldx, py,
+        ldy, _vec(dbias, "dbias", _FL, C, dev), 1 if accumulate else 0, ws, wsb,
+        _stream_on(stream, dev))
     if st:
         _check("aqfq_ckpt8_act_bwd", st)
 
@@ -456,16 +483,17 @@ def aqfq_ckpt8_act_bwd(ckpt, act, dy, dx=None, y=None, dbias=None, accumulate=Fa
 def aqfq_layernorm_fwd(x, gamma, beta, eps, y, mean=None, rstd=None, ckpt=None, stream=None):
     """y = (x - mean) rstd gamma + beta per row of x [rows, cols]."""
     px, ldx = _mat(x, "x", _ROWS)
+    dev = x.get_device()
     R, C = x.shape
-    py, ldy = _mat(y, "y", (x.dtype,), (R, C))
+    py, ldy = _mat(y, "y", (x.dtype,), (R, C), dev)
     par = gamma if gamma is not None else beta
     if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
         raise TypeError("gamma and beta must have one type")
     st = (_lib or lib()).aqfq_layernorm_fwd(
-        _dt(x), px, ldx, R, C, _dt(par), _vec(gamma, "gamma", _ROWS, C),
-        _vec(beta, "beta", _ROWS, C), float(eps), py, ldy,
-        _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
-        _ck(ckpt, R, C), _stream(stream))
+        _dt(x), px, ldx, R, C, _dt(par), _vec(gamma, "gamma", _ROWS, C, dev),
+        _vec(beta, "beta", _ROWS, C, dev), float(eps), py, ldy,
+        _vec(mean, "mean", _FL, R, dev), _vec(rstd, "rstd", _FL, R, dev),
+        _ck(ckpt, R, C, dev), _stream_on(stream, dev))
     if st:
         _check("aqfq_layernorm_fwd", st)
 
@@ -478,18 +506,19 @@ def aqfq_layernorm_bwd(dy, x, mean, rstd, gamma, dx=None, dgamma=None, dbeta=Non
                        ckpt=None, accumulate=False, workspace=None, stream=None):
     """Gradient of aqfq_layernorm_fwd from its input x, or (x None) from ckpt."""
     pd, ldd = _mat(dy, "dy", _ROWS)
+    dev = dy.get_device()
     R, C = dy.shape
     dt = (dy.dtype,)
-    px, ldx = _mat(x, "x", dt, (R, C))
-    pr, ldr = _mat(dres, "dres", dt, (R, C))
-    po, ldo = _mat(dx, "dx", dt, (R, C))
-    ws, wsb = _ws(workspace)
+    px, ldx = _mat(x, "x", dt, (R, C), dev)
+    pr, ldr = _mat(dres, "dres", dt, (R, C), dev)
+    po, ldo = _mat(dx, "dx", dt, (R, C), dev)
+    ws, wsb = _ws(workspace, dev)
     st = (_lib or lib()).aqfq_layernorm_bwd(
-        _dt(dy), pd, ldd, px, ldx, _ck(ckpt, R, C), R, C,
-        _vec(mean, "mean", _FL, R), _vec(rstd, "rstd", _FL, R),
-        _dt(gamma), _vec(gamma, "gamma", _ROWS, C), pr, ldr, po, ldo,
-        _vec(dgamma, "dgamma", _FL, C), _vec(dbeta, "dbeta", _FL, C),
-        1 if accumulate else 0, ws, wsb, _stream(stream))
+        _dt(dy), pd, ldd, px, ldx, _ck(ckpt, R, C, dev), R, C,
+        _vec(mean, "mean", _FL, R, dev), _vec(rstd, "rstd", _FL, R, dev),
+        _dt(gamma), _vec(gamma, "gamma", _ROWS, C, dev), pr, ldr, po, ldo,
+        _vec(dgamma, "dgamma", _FL, C, dev), _vec(dbeta, "dbeta", _FL, C, dev),
+        1 if accumulate else 0, ws, wsb, _stream_on(stream, dev))
     if st:
         _check("aqfq_layernorm_bwd", st)
 
@@ -502,16 +531,17 @@ def aqfq_linear_fwd(x, w, y, bias=None, act=ACT_NONE, residual=None, ckpt=None, 
                     error_flag=None, stream=None):
     """y = act(x @ w.T + bias) + residual; ckpt keeps x @ w.T + bias in 8 bits."""
     px, ldx = _mat(x, "x", _BF)
+    dev = x.get_device()
     M, K = x.shape
     N = w.shape[0]
-    pw, ldw = _mat(w, "w", _BF, (N, K))
-    pr, ldr = _mat(residual, "residual", _BF, (M, N))
-    py, ldy = _mat(y, "y", _BF, (M, N))
-    ws, wsb = _ws(workspace)
+    pw, ldw = _mat(w, "w", _BF, (N, K), dev)
+    pr, ldr = _mat(residual, "residual", _BF, (M, N), dev)
+    py, ldy = _mat(y, "y", _BF, (M, N), dev)
+    ws, wsb = _ws(workspace, dev)
     st = (_lib or lib()).aqfq_linear_fwd(
-        px, ldx, pw, ldw, M, N, K, _dt(bias), _vec(bias, "bias", _ROWS, N),
-        int(act), pr, ldr, py, ldy, _ck(ckpt, M, N), ws, wsb,
-        _flag(error_flag), _stream(stream))
+        px, ldx, pw, ldw, M, N, K, _dt(bias), _vec(bias, "bias", _ROWS, N, dev),
+        int(act), pr, ldr, py, ldy, _ck(ckpt, M, N, dev), ws, wsb,
+        _flag(error_flag, dev), _stream_on(stream, dev))
     if st:
         _check("aqfq_linear_fwd", st)
 
@@ -520,15 +550,16 @@ def aqfq_linear_dgrad(dy, w, dx, act=ACT_NONE, ckpt=None, residual=None, workspa
                       error_flag=None, stream=None):
     """dx = (dy @ w) act'(p) + residual, p [M, K] kept in ckpt."""
     pd, ldd = _mat(dy, "dy", _BF)
+    dev = dy.get_device()
     M, N = dy.shape
     K = w.shape[1]
-    pw, ldw = _mat(w, "w", _BF, (N, K))
-    pr, ldr = _mat(residual, "residual", _BF, (M, K))
-    po, ldo = _mat(dx, "dx", _BF, (M, K))
-    ws, wsb = _ws(workspace)
+    pw, ldw = _mat(w, "w", _BF, (N, K), dev)
+    pr, ldr = _mat(residual, "residual", _BF, (M, K), dev)
+    po, ldo = _mat(dx, "dx", _BF, (M, K), dev)
+    ws, wsb = _ws(workspace, dev)
     st = (_lib or lib()).aqfq_linear_dgrad(
-        pd, ldd, pw, ldw, M, N, K, int(act), _ck(ckpt, M, K), pr, ldr, po,
-        ldo, ws, wsb, _flag(error_flag), _stream(stream))
+        pd, ldd, pw, ldw, M, N, K, int(act), _ck(ckpt, M, K, dev), pr, ldr, po,
+        ldo, ws, wsb, _flag(error_flag, dev), _stream_on(stream, dev))
     if st:
         _check("aqfq_linear_dgrad", st)
 
@@ -536,15 +567,16 @@ def aqfq_linear_dgrad(dy, w, dx, act=ACT_NONE, ckpt=None, residual=None, workspa
 def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=None, stream=None):
     """dw (+)= dy.T @ x."""
     pd, ldd = _mat(dy, "dy", _BF)
+    dev = dy.get_device()
     M, N = dy.shape
     K = x.shape[1]
-    px, ldx = _mat(x, "x", _BF, (M, K))
-    po, ldo = _mat(dw, "dw", _ROWS, (N, K))
-    ws, wsb = _ws(workspace)
+    px, ldx = _mat(x, "x", _BF, (M, K), dev)
+    po, ldo = _mat(dw, "dw", _ROWS, (N, K), dev)
+    ws, wsb = _ws(workspace, dev)
     st = (_lib or lib()).aqfq_linear_wgrad(
         pd, ldd, px, ldx, M, N, K, _dt(dw), po, ldo,
-        1 if accumulate else 0, ws, wsb, _flag(error_flag),
-        _stream(stream))
+        1 if accumulate else 0, ws, wsb, _flag(error_flag, dev),
+        _stream_on(stream, dev))
     if st:
         _check("aqfq_linear_wgrad", st)
 
