@@ -460,7 +460,8 @@ aqfq_status aqfq_layernorm_bwd(int dtype, const void* dy, int64_t lddy, const vo
  *   weight grad  dw = dy^T x (dtype BF16 or F32 [N, K]), added to with
  *                accumulate
  *   x, w, dy     16-byte aligned, leading dimension a multiple of 8 elements
- *                (M, N and K themselves are free, also 0: an empty sum is 0)
+ *                (M, N and K themselves are free, also 0: an empty sum is 0, and
+ *                an operand without elements may have any address and dimension)
  *   bias         optional [N] of bias_dtype;  residual  optional BF16
  *   workspace    device, aqfq_linear_workspace_bytes(pass, M, N, K) bytes,
  *                16-byte aligned (0 bytes for many sizes: partial sums of a

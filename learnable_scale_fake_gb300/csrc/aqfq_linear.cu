@@ -1460,8 +1460,10 @@ bool inner_ok(int64_t v, int64_t lda, int64_t ldb) {
   return v <= (1 << 26) && lda < (int64_t(1) << 38) && ldb < (int64_t(1) << 38);
 }
 // operands that the tensor memory accelerator can read: 16-byte base, rows a
-// multiple of 16 bytes (and less than 2^40 bytes) apart
-bool operand_ok(const void* p, int64_t ld) { return al(p, 16) && ld % 8 == 0; }
+// multiple of 16 bytes (and less than 2^40 bytes) apart; an empty one is not read
+bool operand_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  return rows == 0 || cols == 0 || (al(p, 16) && ld % 8 == 0);
+}
 
 void finish_epi(Epi& e, int es) {
   e.vec_out = rows_aligned<8>(e.out, e.ldo, es);
@@ -1505,7 +1507,7 @@ extern "C" aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w
     if (s != AQFQ_OK) return s;
   }
   if (M > 0 && N > 0 && (!y || (K > 0 && (!x || !w)))) return AQFQ_ERR_NULL;
-  if (!operand_ok(x, ldx) || !operand_ok(w, ldw) || !al(bias, esize(bias_dtype)) ||
+  if (!operand_ok(x, ldx, M, K) || !operand_ok(w, ldw, N, K) || !al(bias, esize(bias_dtype)) ||
       !al(residual, 2) || !al(y, 2) || !al(error_flag, 4))
     return AQFQ_ERR_ALIGN;
   if (M == 0 || N == 0) return AQFQ_OK;
@@ -1536,7 +1538,7 @@ extern "C" aqfq_status aqfq_linear_dgrad(const void* dy, int64_t lddy, const voi
     return AQFQ_ERR_NULL;  // an activation's derivative needs its input
   }
   if (M > 0 && K > 0 && (!dx || (N > 0 && (!dy || !w)))) return AQFQ_ERR_NULL;
-  if (!operand_ok(dy, lddy) || !operand_ok(w, ldw) || !al(residual, 2) || !al(dx, 2) ||
+  if (!operand_ok(dy, lddy, M, N) || !operand_ok(w, ldw, N, K) || !al(residual, 2) || !al(dx, 2) ||
       !al(error_flag, 4))
     return AQFQ_ERR_ALIGN;
   if (M == 0 || K == 0) return AQFQ_OK;
@@ -1558,7 +1560,7 @@ extern "C" aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const voi
     return AQFQ_ERR_SHAPE;
   if (!dtype_ok(dtype)) return AQFQ_ERR_UNSUPPORTED;
   if (N > 0 && K > 0 && (!dw || (M > 0 && (!dy || !x)))) return AQFQ_ERR_NULL;
-  if (!operand_ok(dy, lddy) || !operand_ok(x, ldx) || !al(dw, esize(dtype)) || !al(error_flag, 4))
+  if (!operand_ok(dy, lddy, M, N) || !operand_ok(x, ldx, M, K) || !al(dw, esize(dtype)) || !al(error_flag, 4))
     return AQFQ_ERR_ALIGN;
   if (N == 0 || K == 0) return AQFQ_OK;
   Epi e = {};

@@ -5,7 +5,7 @@ import subprocess
 
 import pytest
 
-from learnable_scale_fake_gb300 import _build
+from learnable_scale_fake_gb300 import _build, aqfq
 from test_layer_sources import sources
 
 ONCE = r"""
@@ -51,3 +51,14 @@ def test_no_kernel_sets_its_attributes_once_per_process():
             at = s.find("cudaFuncSetAttribute", at + 1)
         assert not ("call_once" in s and "cudaFuncSetAttribute" in s.split("call_once", 1)[1][:300]), f
     assert os.path.exists(os.path.join(_build.CSRC, "aqfq_once.h"))
+
+
+def test_operands_without_elements_need_no_alignment():
+    """A contiguous [rows, 0] tensor has rows one element apart; nothing is launched here."""
+    _build.build()
+    L, A = aqfq.lib(), 0x10000
+    assert L.aqfq_linear_fwd(None, 1, None, 1, 0, 5, 0, 0, None, 0, None, 0, None, 8, None, None, 0, None, None) == 0
+    assert L.aqfq_linear_dgrad(A, 8, A + 2, 1, 4, 5, 0, 0, None, None, 0, None, 1, None, 0, None, None) == 0
+    assert L.aqfq_linear_wgrad(A, 8, A + 2, 1, 4, 5, 0, 0, None, 1, 0, None, 0, None, None) == 0
+    # with elements the rule stands
+    assert L.aqfq_linear_fwd(A, 9, A, 16, 4, 5, 9, 0, None, 0, None, 0, A, 8, None, None, 0, None, None) == 3
