@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int64_t ru = r + u * l.step;
       f2 v[P];
       w[u].values(c.fmt, v);
-      act_all<ACT>(v);
+      act_all<ACT, sizeof(T) == 4>(v);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (ru < rows && l.in[j]) put<T, V>(y + ru * ldy + l.col[j], v, j);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (c.codes) {
         f2 p[P];
         w[u].values(c.fmt, p);
-        slope_all<ACT>(p, v);
+        slope_all<ACT, sizeof(T) == 4>(p, v);
         if (y) {
 #pragma unroll
           for (int j = 0; j < NV; ++j)

@@ -127,7 +127,7 @@ __device__ __forceinline__ f2 logistic2(f2 z) { return rcp_pair(add2(ex2_pair(z)
 // it falls like 1 / z).  Its coefficients and c minimise the largest relative error over
 // 0 <= z <= 14 (a linear program over 1600 points), as evaluated in binary32:
 //   degree 8  4e-7   derivatives, whose column sums are stored in binary32
-//   degree 6  4e-6   values, which are stored in BF16 (2^-8): 8192 x 8192 recomputed
+//   degree 6  4e-6   values that are stored in BF16 (2^-8): 8192 x 8192 recomputed
 //                    46 us, with degree 8 51
 // A bound on the absolute error would not do: gelu(x) for x < -4 is this tail alone.
 // (The exponential adds its argument's rounding, 2^-23 of x^2 / 2.)
@@ -213,6 +213,53 @@ __device__ __forceinline__ f2 act_fd2(f2 x, f2& d) {
   }
 }
 
+// value and derivative where they are stored in binary32: as above, but
+//   gelu       within |x| <= 1.5 from Phi = 1/2 + x C(x^2), C of degree 6 (absolute error of Phi
+//              7e-10), outside from a tail of degree 6 fitted to |z| >= 1.45 (2.4e-7 of itself)
+//   tanh gelu  the gate's complement as 2^z times the gate: 1 - s cancels for large x
+// On normal inputs the 2-norm of the error is 4e-8 for gelu and its derivative, as of a
+// plain binary32 evaluation with erf; the tail alone, as for BF16, leaves 6.6e-8 in the
+// derivative.  Recomputed at 8192 x 8192: 71 us (without an activation 70),
+// with that tail 62, with CUDA's normcdff 143.
+template <int ACT>
+__device__ __forceinline__ f2 act_fd2_f32(f2 x, f2& d) {
+  if constexpr (ACT == AQFQ_ACT_GELU) {
+    const f2 a = x & 0x7FFFFFFF7FFFFFFFull, s = mul2(x, x);
+    const f2 g = ex2_pair(mul2(s, pair(-0.5f * kLog2e)));
+    const f2 t = rcp_pair(fma2(pair(0.335f), a, pair(1.0f)));
+    f2 p = fma2(pair(-0.0726788342f), t, pair(0.124253586f));
+    p = fma2(p, t, pair(0.0547424667f));
+    p = fma2(p, t, pair(0.126858488f));
+    p = fma2(p, t, pair(0.132618517f));
+    p = fma2(p, t, pair(0.133697599f));
+    const f2 q = mul2(mul2(p, t), g);  // Phi(-|x|)
+    const f2 r = sub2(pair(1.0f), q);
+    f2 m = fma2(pair(3.99588544e-07f), s, pair(-8.62985507e-06f));
+    m = fma2(m, s, pair(0.000114104412f));
+    m = fma2(m, s, pair(-0.00118614291f));
+    m = fma2(m, s, pair(0.00997301005f));
+    m = fma2(m, s, pair(-0.0664902702f));
+    m = fma2(m, s, pair(0.398942262f));
+    const bool mid0 = lo2(a) <= 1.5f, mid1 = hi2(a) <= 1.5f;
+    const f2 tail = mk2(lo2(x) < 0.0f ? lo2(q) : lo2(r), hi2(x) < 0.0f ? hi2(q) : hi2(r));
+    const f2 cm = fma2(m, x, pair(0.5f)), ym = fma2(m, s, mul2(x, pair(0.5f))), yt = mul2(x, tail);
+    const f2 c = mk2(mid0 ? lo2(cm) : lo2(tail), mid1 ? hi2(cm) : hi2(tail));
+    d = fma2(mul2(x, pair(0.3989422804f)), g, c);
+    return mk2(mid0 ? lo2(ym) : lo2(yt), mid1 ? hi2(ym) : hi2(yt));
+  } else if constexpr (ACT == AQFQ_ACT_GELU_TANH) {
+    const f2 k = fma2(mul2(x, x), pair(-2.0f * kTanhC * kLog2e * kTanhA), pair(-2.0f * kTanhC * kLog2e));
+    const f2 z = ex2_pair(mul2(x, k));
+    const f2 e = mk2(fminf(lo2(z), 1e38f), fminf(hi2(z), 1e38f));  // (times a gate of zero)
+    const f2 s = rcp_pair(add2(z, pair(1.0f)));
+    const f2 c = mk2(fminf(fmaxf(lo2(x), -16.0f), 16.0f), fminf(fmaxf(hi2(x), -16.0f), 16.0f));
+    const f2 u = fma2(mul2(c, c), pair(6.0f * kTanhC * kTanhA), pair(2.0f * kTanhC));
+    d = fma2(mul2(mul2(c, s), mul2(e, s)), u, s);
+    return mul2(x, s);
+  } else {
+    return act_fd2<ACT>(x, d);
+  }
+}
+
 // the same for V values (even)
 template <int ACT, int V>
 __device__ __forceinline__ void act_all(float (&v)[V]) {
@@ -239,19 +286,30 @@ __device__ __forceinline__ void slope_all(float (&p)[V], float (&v)[V]) {
   }
 }
 
-// the same for pairs
-template <int ACT, int P>
+// the same for pairs; F32: stored in binary32
+template <int ACT, bool F32, int P>
 __device__ __forceinline__ void act_all(f2 (&v)[P]) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) v[i] = act2<ACT>(v[i]);
+  for (int i = 0; i < P; ++i) {
+    if constexpr (F32) {
+      f2 d;
+      v[i] = act_fd2_f32<ACT>(v[i], d);
+    } else {
+      v[i] = act2<ACT>(v[i]);
+    }
+  }
 }
-template <int ACT, int P>
+template <int ACT, bool F32, int P>
 __device__ __forceinline__ void slope_all(f2 (&p)[P], f2 (&v)[P]) {
   if constexpr (ACT != AQFQ_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       f2 d;
-      p[i] = act_fd2<ACT>(p[i], d);
+      if constexpr (F32) {
+        p[i] = act_fd2_f32<ACT>(p[i], d);
+      } else {
+        p[i] = act_fd2<ACT>(p[i], d);
+      }
       v[i] = mul2(v[i], d);
     }
   }

@@ -12,7 +12,7 @@ import math
 import pytest
 import torch
 
-from layerlib import ACTS, DEV, act64, kept, new_ckpt, ws
+from layerlib import ACTS, DEV, U, act64, close, kept, new_ckpt, ws
 from learnable_scale_fake_gb300 import aqfq
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +125,67 @@ def test_input_gradient_epilogue(M, K, act):
     a, b, amp = terms(p, act)
     between(dx[:rows], a + b, E * (a.abs() + b.abs()) + LEAST * amp, act)
     assert torch.equal(dx[rows:], dx[:M - rows] if M % rows == 0 else dx[:rows].repeat(-(-M // rows), 1)[rows:M])
+
+
+# FP32 outputs, U the unit roundoff of binary32.  An exponential 2^z of a z that is r times
+# rounded is (4 + r |z| ln 2) U of itself off (the hardware's 2^-22 is 4 U), its reciprocal 2 U.
+#   gelu       |p| <= 1.5: Phi = 1/2 + p C, 3 U and the fit's 7e-10; beyond, the tail: the fit's
+#              2.4e-7 (4 U), reciprocal and eight roundings (12 U), exponential (z = p^2 / 2 log2 e,
+#              3 times rounded); its complement one rounding more
+#   tanh gelu  z four times rounded; the gate and its complement (with 2^z) from it
+#   silu       z twice rounded; 1 - s as it is
+def bounds_f32(p, act):
+    p = p.double()
+    a, b, amp = terms(p, act)
+    y, d = p * a, a + b
+    if act == "gelu":
+        tail = (16 + 1.5 * p * p) * torch.minimum(a, 1 - a)
+        phi = torch.where(p.abs() <= 1.5, torch.full_like(p, 3 + 7e-10 / U), tail + (p > 0))
+        ev, ed = p.abs() * phi + y.abs(), phi + (6 + 1.5 * p * p) * b.abs() + d.abs()
+    elif act == "gelu_tanh":
+        z = (2 * math.sqrt(2 / math.pi) * (p + 0.044715 * p ** 3)).abs()
+        ev, ed = (4 * z + 9) * y.abs(), (4 * z + 8) * a + (8 * z + 26) * b.abs() + d.abs()
+    else:
+        t, n = 1 - a, p.abs()
+        inner = 1 + p * t
+        ev = (2 * n + 9) * y.abs()
+        ed = a * (n * (t * a * (2 * n + 4) + 3 * a + 1) + inner.abs() + n * t) + (2 * n + 9) * d.abs()
+    return U * ev + LEAST * (1 + p.abs()), U * ed + LEAST * amp
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 288), (33, 992), (600, 1024)])
+@pytest.mark.parametrize("act", SMOOTH)
+def test_fp32_outputs(rows, cols, act):
+    for pad in (0, 1):
+        ck, p = checkpoint(rows, cols)
+        new = lambda: torch.empty(rows, cols + pad, device=DEV)[:, :cols]
+        one, y, y2, dx = new().fill_(1.0), new(), new(), new()
+        aqfq.aqfq_ckpt8_unpack(ck, y, act=ACTS[act])
+        aqfq.aqfq_ckpt8_act_bwd(ck, ACTS[act], one, dx=dx, y=y2)
+        torch.cuda.synchronize()
+        a, b, _ = terms(p, act)
+        ev, ed = bounds_f32(p, act)
+        close(y, value64(p, act), ev, "value")
+        close(y2, value64(p, act), ev, "value")
+        close(dx, a + b, ed, "derivative")
+
+
+@pytest.mark.parametrize("act", SMOOTH)
+def test_fp32_outputs_of_large_arguments(act):
+    """Far beyond the range where the formulas change: p or 0, 1 or 0."""
+    x = torch.zeros(4, 32)
+    x[0, :2] = torch.tensor([3e38, -3e38])
+    x[1, :2] = torch.tensor([1e20, -1e20])
+    x[2, :2] = torch.tensor([200.0, -200.0])
+    x[3, :2] = torch.tensor([20.0, -20.0])
+    ck, codes, scale = new_ckpt(4, 32, "int8", 32)
+    aqfq.aqfq_ckpt8_pack(ck, x.to(DEV))
+    torch.cuda.synchronize()
+    p = kept(codes, scale, "int8", 32)
+    one, y, dx = torch.ones(4, 32, device=DEV), torch.empty(4, 32, device=DEV), torch.empty(4, 32, device=DEV)
+    aqfq.aqfq_ckpt8_act_bwd(ck, ACTS[act], one, dx=dx, y=y)
+    torch.cuda.synchronize()
+    close(y[:, 0], p[:, 0], 2 * U * p[:, 0].abs())
+    close(dx[:, 0], torch.ones(4), torch.full((4,), 1e-7))
+    close(y[:, 1], torch.zeros(4), torch.full((4,), 1e-7))
+    close(dx[:, 1], torch.zeros(4), torch.full((4,), 1e-7))
