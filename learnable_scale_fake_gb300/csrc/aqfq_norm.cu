@@ -444,10 +444,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int i = 0; i < P; ++i) h[i] = cur.x.pair_at(i);
     }
     const f2 mu = pair(cur.mu), rs = pair(cur.rs);
+    // dy is zero beyond the row, and h has to be finite there: (0 - mu) rstd may overflow where
+    // the row's own h do not
+    f2 rv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) rv[j] = V == 8 && !in[j] ? 0ull : rs;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const f2 d = cur.dy.pair_at(i);  // zero beyond the row, so h there does not count
-      h[i] = mul2(sub2(h[i], mu), rs);
+      const f2 d = cur.dy.pair_at(i);
+      h[i] = mul2(sub2(h[i], mu), V == 8 ? rv[i / 4] : rs);
       if constexpr (V == 1) h[i] = masked<V, NV>(h[i], i, in);
       ag[i] = fma2(d, h[i], ag[i]);
       ab[i] = add2(ab[i], d);

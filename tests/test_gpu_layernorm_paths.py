@@ -1,5 +1,5 @@
 """Layer norm where the kernel is chosen by the size: workspaces at every alignment that the
-header allows.  Bounds as in test_gpu_layernorm.py."""
+header allows, rows whose mean times 1 / deviation overflows.  Bounds as in test_gpu_layernorm.py."""
 import pytest
 import torch
 
@@ -41,3 +41,23 @@ def test_backward_workspace_at_any_multiple_of_8_bytes(R, C, dtype, fmt):
             first = (dx, dg, db)
             _check_bwd(kx, dy, m, r, g, None, dx, dg, db)
         assert all(torch.equal(a, b) for a, b in zip(first, (dx, dg, db)))
+
+
+# widths that fill their lanes and ones that leave some beyond the row, aligned and odd
+@pytest.mark.parametrize("C", [8, 32, 64, 256, 512, 1024, 2048])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_constant_rows_of_a_large_value(C, pad, dtype):
+    """x - mean is zero all over the row: dx = rstd (dy gamma - mean(dy gamma)) and dgamma = 0
+    though mean rstd is beyond binary32 (the widths are powers of two, so the mean is exact)."""
+    R, big = 5, 1.5 * 2.0 ** 121
+    rows = lambda t: torch.cat([t, torch.zeros(R, pad, dtype=t.dtype)], 1).to(DEV)[:, :C]
+    x, dy = torch.full((R, C), big, dtype=dtype), randn((R, C), C, dtype=dtype)
+    _, g, _ = _case(R, C, 5, dtype)
+    m, r = torch.full((R,), big, device=DEV), torch.full((R,), 316.0, device=DEV)
+    dx, dg, db = torch.empty(R, C, dtype=dtype, device=DEV), *torch.empty(2, C, device=DEV)
+    w = torch.empty(aqfq.aqfq_layernorm_bwd_workspace_bytes(R, C), dtype=torch.uint8, device=DEV)
+    aqfq.aqfq_layernorm_bwd(rows(dy), rows(x), m, r, g.to(DEV), dx, dgamma=dg, dbeta=db, workspace=w)
+    torch.cuda.synchronize()
+    _check_bwd(x, dy, m, r, g, None, dx, dg, db)
+    assert bool((dg == 0).all())
