@@ -39,7 +39,8 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_ckpt8_act_bwd_workspace_bytes", "aqfq_layernorm_fwd", "aqfq_layernorm_bwd",
            "aqfq_layernorm_bwd_workspace_bytes", "aqfq_linear_fwd", "aqfq_linear_dgrad",
            "aqfq_linear_wgrad", "aqfq_linear_workspace_bytes",
-           "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_status_string",
+           "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_selftest_linear_plan",
+           "aqfq_selftest_layernorm_ring", "aqfq_status_string",
            "aqfq_version")
 
 
@@ -113,6 +114,8 @@ def lib():
                 "aqfq_linear_workspace_bytes": (sz, [i32, i64, i64, i64]),
                 "aqfq_selftest_wait_timeout": (i32, [P, ctypes.c_uint32, P]),
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
+                "aqfq_selftest_linear_plan": (i32, [i32, i64, i64, i64, P]),
+                "aqfq_selftest_layernorm_ring": (i32, [i32, i32, i64, i64, i32, i32]),
                 "aqfq_status_string": (ctypes.c_char_p, [i32]),
                 "aqfq_version": (i32, []),
             }
@@ -579,6 +582,21 @@ def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=No
         _stream_on(stream, dev))
     if st:
         _check("aqfq_linear_wgrad", st)
+
+
+def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:
+    """How the product is cut: kernel ("empty", "tile" or "pair"), slices of the inner axis, tiles
+    of the last round that a second launch splits, and into how many slices."""
+    plan = (ctypes.c_int32 * 4)()
+    _check("aqfq_selftest_linear_plan", lib().aqfq_selftest_linear_plan(int(kind), M, N, K, plan))
+    return {"kernel": ("empty", "tile", "pair")[plan[0]], "splits": plan[1], "tail": plan[2],
+            "tail_splits": plan[3]}
+
+
+def aqfq_selftest_layernorm_ring(backward, dtype, rows, cols, ckpt=False, dres=False) -> int:
+    """Warps per row of the ring kernel that serves aligned tensors of this size; 0: no ring."""
+    return int(lib().aqfq_selftest_layernorm_ring(int(backward), _CODE[dtype], rows, cols, int(ckpt),
+                                                  int(dres)))
 
 
 def aqfq_status_string(status: int) -> str:

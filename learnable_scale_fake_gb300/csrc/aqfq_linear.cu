@@ -1491,6 +1491,21 @@ extern "C" size_t aqfq_linear_workspace_bytes(int pass, int64_t M, int64_t N, in
   }
 }
 
+extern "C" aqfq_status aqfq_selftest_linear_plan(int pass, int64_t M, int64_t N, int64_t K, int32_t* plan) {
+  if (!plan) return AQFQ_ERR_NULL;
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return AQFQ_ERR_SHAPE;
+  Plan p;
+  switch (pass) {
+    case AQFQ_LINEAR_FWD: p = make_plan(M, N, K); break;
+    case AQFQ_LINEAR_DGRAD: p = make_plan(M, K, N); break;
+    case AQFQ_LINEAR_WGRAD: p = make_plan(N, K, M); break;
+    default: return AQFQ_ERR_UNSUPPORTED;
+  }
+  plan[0] = p.ksteps == 0 ? 0 : p.small ? 1 : 2;
+  plan[1] = p.splits, plan[2] = p.tail, plan[3] = p.tail_splits;
+  return AQFQ_OK;
+}
+
 extern "C" aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw,
                                        int64_t M, int64_t N, int64_t K, int bias_dtype,
                                        const void* bias, int act, const void* residual,

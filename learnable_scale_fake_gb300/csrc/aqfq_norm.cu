@@ -962,20 +962,36 @@ cudaError_t run_fwd_ring(const void* x, void* y, const FwdArgs& a, const RingArg
 // fwd: groups on the GPU; the ring's set-up costs about a microsecond
 inline bool ring_rows(int64_t rows, int64_t groups) { return rows >= 4 * groups; }
 
+// Warps per row of the ring that serves the forward pass of aligned tensors; 0: none.
+// (1024 columns and fewer: norm_fwd_rows is faster, 16384 x 768 14.9 us against 16.4)
+int fwd_ring(int64_t rows, int64_t c, int esize, RingArgs& q) {
+  if (c % 8 != 0 || c <= 1024 || c > 8192) return 0;
+  // blocks of 8 warps, or of 16 for the widest rows
+  const int G = c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
+  const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : kFwdBlocks, row = int(c) * esize;
+  q = make_ring(2 * row, row, nw / G, kRingBytes / mb);
+  return q.stages >= 3 && ring_rows(rows, 2 * kSms * mb * (nw / G)) ? G : 0;
+}
+
+// The same of the backward pass.  Bulk copies: every row's bytes and its start a multiple
+// of 16 (kept codes: columns); 16 columns per lane.
+int bwd_ring(int64_t rows, int64_t c, int esize, bool ckpt, bool dres, RingArgs& q) {
+  if (c % (ckpt ? 16 : 8) != 0 || c <= 256 || c > 8192) return 0;
+  const int G = c <= 512 ? 1 : c <= 1024 ? 2 : c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
+  const int row = int(c) * esize;
+  q = make_ring(row * (dres ? 2 : 1) + (ckpt ? int(c) : row), row, 16 / G, kRingBytes);
+  return q.stages >= 3 && ring_rows(rows, kSms * (16 / G)) ? G : 0;
+}
+
 template <typename T>
 cudaError_t launch_fwd(const void* x, void* y, const FwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
-  if (a.vec && a.pvec && c % 8 == 0 && a.cvec && c > 1024 && c <= 8192) {
-    // (narrower rows: norm_fwd_rows is faster, 16384 x 768 14.9 us against 16.4)
-    // blocks of 8 warps, or of 16 for the widest rows
-    const int G = c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
-    const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : kFwdBlocks, row = int(c) * int(sizeof(T));
-    const RingArgs q = make_ring(2 * row, row, nw / G, kRingBytes / mb);
-    if (q.stages >= 3 && ring_rows(a.rows, 2 * kSms * mb * (nw / G))) {
-      if (G == 4) return run_fwd_ring<T, 4, 8, kFwdBlocks>(x, y, a, q, st);
-      if (G == 8) return run_fwd_ring<T, 8, 8, kFwdBlocks>(x, y, a, q, st);
-      return run_fwd_ring<T, 16, 16, 1>(x, y, a, q, st);
-    }
+  if (a.vec && a.pvec && a.cvec) {
+    RingArgs q;
+    const int G = fwd_ring(a.rows, c, sizeof(T), q);
+    if (G == 4) return run_fwd_ring<T, 4, 8, kFwdBlocks>(x, y, a, q, st);
+    if (G == 8) return run_fwd_ring<T, 8, 8, kFwdBlocks>(x, y, a, q, st);
+    if (G == 16) return run_fwd_ring<T, 16, 16, 1>(x, y, a, q, st);
   }
   // one block per (few) rows: the grid has to hold them
   const bool regs = a.rows <= 0x7FFFFFFF;
@@ -1076,18 +1092,14 @@ template <typename T>
 cudaError_t launch_bwd(const void* dy, const void* x, const void* dres, const BwdOut& o,
                        const BwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
-  // bulk copies: every row's bytes and its start a multiple of 16 (codes: columns)
-  if (a.vec && a.pvec && c % (x ? 8 : 16) == 0 && (x || al(a.c.codes, 16)) && c > 256 && c <= 8192) {
-    const int G = c <= 512 ? 1 : c <= 1024 ? 2 : c <= 2048 ? 4 : c <= 4096 ? 8 : 16;  // 16 columns per lane
-    const int row = int(c) * int(sizeof(T));
-    const RingArgs q = make_ring(row * (dres ? 2 : 1) + (x ? row : int(c)), row, 16 / G, kRingBytes);
-    if (q.stages >= 3 && ring_rows(a.rows, kSms * (16 / G))) {
-      if (G == 1) return run_bwd_ring<T, 2, 1>(dy, x, dres, o, a, q, st);
-      if (G == 2) return run_bwd_ring<T, 2, 2>(dy, x, dres, o, a, q, st);
-      if (G == 4) return run_bwd_ring<T, 2, 4>(dy, x, dres, o, a, q, st);
-      if (G == 8) return run_bwd_ring<T, 2, 8>(dy, x, dres, o, a, q, st);
-      return run_bwd_ring<T, 2, 16>(dy, x, dres, o, a, q, st);
-    }
+  if (a.vec && a.pvec && (x || al(a.c.codes, 16))) {
+    RingArgs q;
+    const int G = bwd_ring(a.rows, c, sizeof(T), !x, dres != nullptr, q);
+    if (G == 1) return run_bwd_ring<T, 2, 1>(dy, x, dres, o, a, q, st);
+    if (G == 2) return run_bwd_ring<T, 2, 2>(dy, x, dres, o, a, q, st);
+    if (G == 4) return run_bwd_ring<T, 2, 4>(dy, x, dres, o, a, q, st);
+    if (G == 8) return run_bwd_ring<T, 2, 8>(dy, x, dres, o, a, q, st);
+    if (G == 16) return run_bwd_ring<T, 2, 16>(dy, x, dres, o, a, q, st);
   }
   if (a.vec && a.pvec && c % 8 == 0 && a.cvec) {
     if (c <= 256) return run_bwd<T, 8, 1, 1, true>(dy, x, dres, o, a, st);
@@ -1128,6 +1140,14 @@ cudaError_t launch_bwd(const void* dy, const void* x, const void* dres, const Bw
 
 using namespace aqfq;
 using namespace aqfq::layer;
+
+extern "C" int32_t aqfq_selftest_layernorm_ring(int backward, int dtype, int64_t rows, int64_t cols,
+                                                int ckpt, int dres) {
+  if (!view_ok(rows, cols, cols) || !dtype_ok(dtype)) return 0;
+  RingArgs q;
+  return backward ? bwd_ring(rows, cols, esize(dtype), ckpt != 0, dres != 0, q)
+                  : fwd_ring(rows, cols, esize(dtype), q);
+}
 
 extern "C" aqfq_status aqfq_layernorm_fwd(int dtype, const void* x, int64_t ldx, int64_t rows,
                                           int64_t cols, int param_dtype, const void* gamma,
