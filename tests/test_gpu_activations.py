@@ -74,6 +74,17 @@ def test_recomputed_in_bf16(rows, cols, act):
         between(y, ref, E * ref.abs() + LEAST * (1 + p.abs()), act)
 
 
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_many_elements_recomputed_exactly(act, fmt):
+    """16 columns per lane (2^24 elements and more)."""
+    ck, p = checkpoint(4100, 4096, fmt)
+    y = torch.empty(4100, 4096, dtype=torch.bfloat16, device=DEV)
+    aqfq.aqfq_ckpt8_unpack(ck, y, act=ACTS[act])
+    torch.cuda.synchronize()
+    assert torch.equal(y.cpu(), act64(p, act).bfloat16())
+
+
 @pytest.mark.parametrize("rows,cols", [(40, 288), (600, 1024)])
 @pytest.mark.parametrize("act", SMOOTH)
 def test_gradient_in_bf16(rows, cols, act):

@@ -1,6 +1,7 @@
-"""Layer norm where the kernel is chosen by the size: workspaces at every alignment that the
-header allows, rows whose mean times 1 / deviation overflows, and the rings that serve many
-rows, at the least rows that take them and with every stage reused.  Bounds as in test_gpu_layernorm.py."""
+"""Layer norm where the kernel is chosen by the size: every class of widths, aligned and not, for
+one row, a cluster's and many; workspaces at every alignment that the
+header allows; rows whose mean times 1 / deviation overflows; the rings that serve many rows, at
+the least rows that take them and with every stage reused.  Bounds as in test_gpu_layernorm.py."""
 import pytest
 import torch
 
@@ -193,3 +194,35 @@ def test_rings_give_the_same_bits_again_and_on_another_stream():
         out.append((y, m, r, dx, dg, db))
     for o in out[1:]:
         assert all(torch.equal(p, q) for p, q in zip(out[0], o))
+
+
+# both ends of the classes of columns that have kernels of their own, up to the widths that a
+# block walks; pad 1: rows that allow no wide access
+@pytest.mark.parametrize("C", [120, 128, 256, 264, 384, 512, 520, 1024, 1032, 1536, 2048, 3000, 4096, 4104, 6000,
+                               8192, 8200, 12288, 16384, 16392])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_every_class_of_widths(C, pad, dtype):
+    for k, R in enumerate((1, 7, 61, 400)):
+        x, g, b = _case(R, C, 3 * C + R, dtype)
+        fmt, group = (("int8", 32), ("e4m3", 128))[k % 2]
+        fx, fy = Framed(R, C, dtype, pad, pad, x), Framed(R, C, dtype, pad, pad)
+        m, r = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+        ck, codes, scale = new_ckpt(R, C, fmt, group)
+        aqfq.aqfq_layernorm_fwd(fx.view, g.to(DEV), b.to(DEV), EPS, fy.view, mean=m, rstd=r, ckpt=ck)
+        torch.cuda.synchronize()
+        _check_fwd(x, g, b, fy.view, m, r)
+        q, s = pack_ref(x, fmt, group)
+        assert fy.intact() and (scale.cpu().numpy() == s).all() and (grid_values(codes, fmt) == q).all()
+        dy, dres = randn((R, C), C + R, dtype=dtype), randn((R, C), C + R + 1, dtype=dtype)
+        fd, fo = Framed(R, C, dtype, pad, pad, dy), Framed(R, C, dtype, pad, pad)
+        w = ws(aqfq.aqfq_layernorm_bwd_workspace_bytes(R, C))
+        for from_ck in (False, True):
+            dg, db = torch.full((2, C), float("nan"), device=DEV)
+            aqfq.aqfq_layernorm_bwd(fd.view, None if from_ck else fx.view, m, r, g.to(DEV), fo.view, dgamma=dg,
+                                    dbeta=db, dres=dres.to(DEV) if k % 2 else None,
+                                    ckpt=ck if from_ck else None, workspace=w)
+            torch.cuda.synchronize()
+            kx = kept(codes, scale, fmt, group) if from_ck else x
+            _check_bwd(kx, dy, m, r, g, dres if k % 2 else None, fo.view, dg, db)
+            assert fo.intact()
