@@ -8,10 +8,11 @@
 // rows of its slice; the bias gradient's column sums stay in its registers.
 // Memory is the floor: pack moves 2 + 1 bytes per BF16 element, unpack 1 + 2, the
 // gradient 1 + 2 + 2 (+ 2 with the recomputed activation).  At 8192 x 8192 in E4M3, a
-// plain copy moving 6.78 TB/s: pack 36 us (5.6 TB/s), unpack 33 us (6.1), the gradient
-// with SiLU 60 us (5.6), with GELU 70 us (4.8: two transcendental instructions and about
-// twelve packed ones per pair keep the issue slots 62 % busy), with GELU, the recomputed
-// activation and the bias gradient 83 us (5.6).
+// plain copy moving 6.78 TB/s: pack 35 us (5.7 TB/s), unpack 33 us (6.0), the gradient
+// with SiLU 59 us (5.7), with GELU 75 us (4.5: two transcendental instructions and about
+// fifteen packed ones per pair keep the issue slots 60 % busy), with GELU, the recomputed
+// activation and the bias gradient 86 us (5.4).  FP32 from INT8: pack 55 us (6.2), unpack 70
+// (4.8), with GELU 71, the gradient with GELU, activation and bias gradient 143 (6.1).
 #include <type_traits>
 
 #include "aqfq_internal.h"
@@ -390,8 +391,8 @@ extern "C" aqfq_status aqfq_ckpt8_unpack(const aqfq_ckpt8* ckpt, int act, int dt
   if (!al(y, esize(dtype))) return AQFQ_ERR_ALIGN;
   if (sm_count() <= 0) return AQFQ_ERR_CUDA;
   const int vec = cols % 8 == 0 && rows_aligned<8>(y, ldy, esize(dtype)) && al(c.codes, 8) ? 8 : 1;
-  // 16 columns per lane for many elements (8192 x 8192 with GELU 52 -> 44 us, 8192 x 4096
-  // 28 -> 25; 2048 x 2048 would go from 5.2 to 6.8, 16384 x 768 from 13.5 to 14.0)
+  // 16 columns per lane for many elements (8192 x 8192 with GELU 52 -> 46 us, 8192 x 4096
+  // 28 -> 26; 2048 x 2048 would go from 5.1 to 7.0, 16384 x 768 from 13.2 to 12.1)
   const bool v16 = dtype == AQFQ_BF16 && cols > 256 && cols % 16 == 0 && ldy % 16 == 0 && al(y, 32) &&
                    al(c.codes, 16) && rows * cols >= (int64_t(1) << 24);
   const Map m = make_map(rows, cols, c.lg, v16 ? 16 : vec, 65535);

@@ -409,7 +409,7 @@ __device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0
 // the bias of the 128 columns around are at hand).  The next chunk's sums are under way
 // while one is computed; its other inputs, sent to L2 before, are read when it begins (held
 // a chunk ahead, they cost every warp of the kernel 30 spilled registers: 8191 x 4104 x 768
-// with GELU and residual 86 us instead of 78).
+// with GELU and residual 86 us instead of 75).
 template <int PASS, int ACT>
 __device__ __forceinline__ void epilogue_row(const Epi& e, int64_t r, bool in, int64_t col,
                                              uint32_t taddr, const float* sb,
@@ -591,14 +591,16 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 //   warps 2-17  epilogue, four per quarter of the rows, a quarter of the columns each
 //               (with two per quarter the forward with GELU and checkpoint took 192 us at
 //               8192 x 4096 x 4096, with four 167 us).  Five of the eighteen warps share a
-//               quarter of the SM, which leaves 96 registers a thread: what the epilogues
-//               keep across a tile is counted, spilled registers go to L2 beside 200 KB of
-//               shared memory.
-// At 8192 x 4096 x 4096 (plain library products beside: 139-149, 148-153 and 168 us):
-// forward with GELU 148-153 us, with a checkpoint too 160 us, input gradient 154-167 us,
-// weight gradient 162-168 us; two runs differ by so much with the clock under the power
-// limit.  The rest is the first loads, the last tile's epilogue and tiles that do not
-// divide evenly among 76 pairs.
+//               quarter of the SM, which leaves 96 registers a thread, and spilled ones go to
+//               L2 beside 200 KB of shared memory: 8 to 28 bytes in the forward kernels and
+//               in the input gradient with GELU or tanh GELU, 248 and 116 in the forward's
+//               and the input gradient's split tail, none in the other kernels but 16 in the
+//               weight gradient's split tail.
+// At 8192 x 4096 x 4096 (plain library products beside: 137-152, 147-156 and 155-168 us):
+// forward with GELU 146-153 us, with a checkpoint too 160-167 us, input gradient 142-167 us,
+// weight gradient 152-175 us; two runs differ by so much with the clock under the power
+// limit.  The MMAs run 81 to 89 % of the time; the rest is the first loads, the last tile's
+// epilogue and tiles that do not divide evenly among 76 pairs.
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
 // ---------------------------------------------------------------------------
@@ -928,9 +930,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 // warp takes whole rows of 128 columns, reads every slice's value through distributed
 // shared memory and adds them in the slices' order.
 // Few rows (a token or two): the weight is streamed once by tiles x S CTAs.
-// 24 x 2048 x 768 5 us, 1 x 4096 x 4096 8.6 us (the weight at 3.9 TB/s), 1000 x 1536 x
-// 2048 10.5 us: about 4.5 us are launch, first loads and epilogue, a step of 64 takes 0.2
-// us (a whole SM's MMAs: 0.17).
+// 24 x 2048 x 768 5 us, 1 x 4096 x 4096 8.4-8.7 us (the weight at 3.9 TB/s; up to 10 after
+// a hot kernel), 1000 x 1536 x 2048 11.1 us: about 4.5 us are launch, first loads and
+// epilogue, a step of 64 takes 0.2 us (a whole SM's MMAs: 0.17).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
 constexpr int kWarpsC = 16;

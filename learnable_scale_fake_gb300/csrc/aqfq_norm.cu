@@ -18,7 +18,7 @@ namespace layer {
 namespace {
 
 constexpr int kT = 256;
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // of a GB300: grids and the workspace's size; the results do not need it
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -407,7 +407,8 @@ struct RowRegs {
 };
 
 // (with 1024 threads, 64 registers each, 30 to 60 of them spilled: 64 x 1024 11 us instead
-// of 6.8, 2000 x 4001 from a checkpoint 53 instead of 31)
+// of 4.7, 2000 x 4001 from a checkpoint 53 instead of 31.  The kernel of 4097 to 8192 columns
+// that allow no wide access still spills: 88 to 144 bytes, from a checkpoint 468 to 592.)
 constexpr int kBwdThreads = 512;
 template <typename T, int V, int NV, int G, bool CK, bool PF>
 __global__ void __launch_bounds__(kBwdThreads, 1)

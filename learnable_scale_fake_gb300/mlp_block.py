@@ -4,9 +4,15 @@
 
 W1_hat and W2_hat are the NVFP4 fake-quant of frozen BF16 weights; only their
 block scales train.  Between the forward and the backward pass the block keeps
-x and the hidden pre-activation in 8 bits (one byte and 1/32 of a float per
-element in place of two to eight bytes) and two floats per token; the norm's
+x and the hidden pre-activation in 8 bits (one byte per element and one float
+per `group` of them, 128 by default) and two floats per token; the norm's
 output and the hidden activation are recomputed.
+
+The backward pass sees x as its checkpoint gives it back, x~, in two places, and
+not in the same way: the norm's output, an operand of the first weight's
+gradient, is recomputed from x~ with the mean and deviation of x~; the norm's
+own gradient forms h = (x~ - mean) rstd with those of the exact x, which the
+forward kept.
 
 ``python -m learnable_scale_fake_gb300.mlp_block`` trains the scales of a small
 block against its unquantized self and prints the loss.
