@@ -11,7 +11,7 @@
 
 #include "aqfq_internal.h"
 #include "aqfq_layer.cuh"
-#include "aqfq_sm100.cuh"
+#include "aqfq_sm100_pair.cuh"
 
 namespace aqfq {
 namespace layer {
@@ -576,14 +576,11 @@ __device__ __forceinline__ void smem_pairs(const uint8_t* row, const int (&col)[
   }
 }
 
-// after a timeout at row r (stage st): waits, bounded, for the copies that may still be
-// on their way into the block's memory
-__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int st, uint32_t phase, int64_t r,
-                                           int64_t step, int64_t rows) {
-  for (int i = 0; i < stages && r < rows; ++i, r += step) {
-    sm100::mbar_wait_suspend(&full[st], phase);
-    if (++st == stages) st = 0, phase ^= 1;
-  }
+// Loads on their way when a wait for row r gives up: the rows left, at most one per stage, and
+// after the first turn the stage of the row before r has not been refilled yet.
+__device__ __forceinline__ int64_t in_flight(int stages, bool first, int64_t r, int64_t step, int64_t rows) {
+  const int64_t left = (rows - r + step - 1) / step, most = first ? stages : stages - 1;
+  return left < most ? left : most;
 }
 
 struct RingArgs {
@@ -679,7 +676,7 @@ __global__ void __launch_bounds__(32 * NW, MB)
   for (bool first = true; r < a.rows; r += step, yrow += ystep, first = false) {
     if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
-      if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
     }
     const bool two = r + 1 < a.rows;
     f2 v[R][P];
@@ -828,7 +825,7 @@ __global__ void __launch_bounds__(512, 1)
     scalars(r + step);
     if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
-      if (!ok && loader) ring_drain(full[grp], q.stages, st, phase, r, step, a.rows);
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
     }
     const uint8_t* stage = mine + st * q.stage_bytes;
     f2 d[P], h[P], t1 = 0, t2 = 0;

@@ -62,6 +62,16 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int issu
     mbar_wait_warp(&full[i % stages], (i / stages) & 1, limit);
 }
 
+// The same for one thread that refills a ring itself: `left` loads are on their way, the
+// oldest on the barrier of stage st with this phase.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int st, uint32_t phase, int64_t left,
+                                           long long limit = kWaitCycles) {
+  for (int64_t i = 0; i < left; ++i) {
+    mbar_wait_long(&full[st], phase, limit);
+    if (++st == stages) st = 0, phase ^= 1;
+  }
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

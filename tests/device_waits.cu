@@ -77,3 +77,44 @@ extern "C" int run_drain(const uint8_t* src, int missing, long long limit, uint8
   drain<<<1, 32>>>(src, missing, limit, out, done);
   return int(cudaDeviceSynchronize());
 }
+
+// One thread runs a ring of 3 stages over `turns` loads of 1 KiB, refilling a stage after its
+// turn; the loads from turn `lost` on are announced but never issued.  At the wait that gives up
+// it drains what is on its way and stops; *done: the turn, out: the stages.
+__global__ void ring(const uint8_t* src, int turns, int lost, long long limit, uint8_t* out, int* done) {
+  constexpr int N = 1024, STAGES = 3;
+  __shared__ __align__(128) uint8_t stage[STAGES][N];
+  __shared__ uint64_t full[STAGES];
+  for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+  fence_barrier_init();
+  auto fetch = [&](int i) {
+    if (i >= turns) return;
+    const int s = i % STAGES;
+    mbar_arrive_expect_tx(&full[s], N);
+    if (i < lost)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              smem_u32(stage[s])),
+          "l"(src + i * N), "r"(N), "r"(smem_u32(&full[s]))
+          : "memory");
+  };
+  for (int i = 0; i < STAGES; ++i) fetch(i);
+  int st = 0, i = 0;
+  uint32_t phase = 0;
+  for (; i < turns; ++i) {
+    if (!mbar_wait_long(&full[st], phase, limit)) {
+      const int left = turns - i, most = i == 0 ? STAGES : STAGES - 1;
+      drain_ring(full, STAGES, st, phase, left < most ? left : most, limit);
+      break;
+    }
+    if (i > 0) fetch(i + STAGES - 1);
+    if (++st == STAGES) st = 0, phase ^= 1;
+  }
+  for (int k = 0; k < STAGES * N; ++k) out[k] = (&stage[0][0])[k];
+  *done = i;
+}
+
+extern "C" int run_ring(const uint8_t* src, int turns, int lost, long long limit, uint8_t* out, int* done) {
+  ring<<<1, 1>>>(src, turns, lost, limit, out, done);
+  return int(cudaDeviceSynchronize());
+}

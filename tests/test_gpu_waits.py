@@ -43,3 +43,17 @@ def test_drain_waits_for_the_loads_in_flight_and_no_longer_than_its_limit(waits,
     assert int(done.item()) == 1
     # stages 0 and 1 hold loads 3 and 4, stage 2 load 2 (the announced sixth never arrives)
     assert torch.equal(out, src[[3, 4, 2]])
+
+
+@pytest.mark.parametrize("turns,lost", [(7, 7), (7, 6), (7, 4), (2, 1), (7, 0)])
+def test_ring_drains_what_is_on_its_way(waits, turns, lost):
+    """A ring whose loads stop coming at turn `lost`: it gives up there, drains within its limits
+    and returns; what was loaded before is in place."""
+    src = torch.randint(0, 256, (7, 1024), dtype=torch.uint8, device="cuda")
+    out, done = torch.zeros(3, 1024, dtype=torch.uint8, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    torch.cuda.synchronize()
+    assert waits.run_ring(p(src), turns, lost, ctypes.c_longlong(1 << 22), p(out), p(done)) == 0
+    assert int(done.item()) == lost
+    for i in range(max(0, lost - 3), lost):
+        assert torch.equal(out[i % 3], src[i])
