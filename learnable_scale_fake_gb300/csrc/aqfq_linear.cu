@@ -9,6 +9,10 @@
 //   forward       r = m, c = n, k = k:  A = x (k contiguous), B = W (k contiguous)
 //   input grad    r = m, c = k, k = n:  A = dy (n contiguous), B = W (c contiguous)
 //   weight grad   r = n, c = k, k = m:  A = dy (r contiguous), B = x (c contiguous)
+//
+// Products of BF16 are exact in binary32 and their sums are held in it.  Over 3680 terms the
+// tensor cores' sums measured 4e-6 off (2-norm, relative), a blocked sum of FMAs 6e-7: far
+// below a BF16 output's rounding of 4e-3, but an FP32 weight gradient shows it.
 #include <cuda.h>
 
 #include <mutex>
