@@ -487,6 +487,60 @@ aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const void* x, int64
                               int accumulate, void* workspace, size_t workspace_bytes,
                               int32_t* error_flag, void* stream);
 
+/* ---- between a layer's quantized products ------------------------------------
+ * Rotary positions, the norms and the join of two blocks, and the gated
+ * feed-forward product: what a layer runs between the products whose weights and
+ * heads the calls above quantize (msModelSlim guide, "FA3Quant": per-head
+ * quantization of queries and keys, which are rotated before; AngelSlim mcore_qad
+ * article, section 2.4: stacked gate and up projections of an expert).  Rules as
+ * for the layer calls above: views with any stride, sums in binary32, stored
+ * values rounded once, no allocation, outputs apart from the inputs. */
+
+/* Rotary positions of query and key heads [T, heads, D].  Pair i of the first rot
+ * elements of each head is (x[i], x[i + rot / 2]) (AQFQ_ROTARY_HALF) or
+ * (x[2 i], x[2 i + 1]) (AQFQ_ROTARY_INTERLEAVED); with the angle t = pos freqs[i]
+ *   (a, b) -> mscale (a cos t - b sin t, a sin t + b cos t)
+ * and with transposed != 0 the transposed matrix (-sin t), which takes the
+ * outputs' gradient to the inputs'.  Elements from rot on pass through unscaled.
+ *   q, k        heads; k may be NULL.  x [T, heads, D] with elements of a head
+ *               contiguous, tokens ldx and heads hsx elements apart (also 0 or
+ *               overlapping); y likewise, each element a place of its own; y = x
+ *               with the same strides rotates in place
+ *   pos         device int64 [T], any sign and size
+ *   freqs       device double [rot / 2], angle per position in radians, finite
+ * The angle's fraction of a turn is formed in 64-bit integers: off by at most
+ * (|pos| + 2^33) 2^-65 turns and the binary64 rounding of pos times freqs[i] / 2 pi.
+ * Limits: 1 <= D <= 8192, rot even, heads <= 2^20; T, heads and rot may be 0. */
+typedef enum aqfq_rotary_layout { AQFQ_ROTARY_HALF = 0, AQFQ_ROTARY_INTERLEAVED = 1 } aqfq_rotary_layout;
+typedef struct aqfq_heads {
+  const void* x;
+  void* y;
+  int64_t heads;
+  int64_t ldx, hsx, ldy, hsy;
+} aqfq_heads;
+aqfq_status aqfq_rotary(int dtype, const aqfq_heads* q, const aqfq_heads* k, int64_t T, int64_t D,
+                        int64_t rot, int layout, const int64_t* pos, const double* freqs,
+                        float mscale, int transposed, void* stream);
+
+/* The angles per position of pairs 0 .. rot / 2 - 1 (host only; freqs is host
+ * memory that the caller copies to the device once):
+ *   PLAIN   base^(-2 i / rot)
+ *   LINEAR  the same / factor (positions interpolated)
+ *   NTK     with base factor^(rot / (rot - 2)) in base's place
+ *   PARTS   f k + (f / factor) (1 - k), f the plain angle, k = (turns - low) /
+ *           (high - low) clamped to [0, 1], turns = length f / 2 pi the full turns of
+ *           the pair over the trained length
+ * mscale (optional): the factor for aqfq_rotary, 1 or (PARTS) 0.1 ln(factor) + 1.
+ * base > 0; factor >= 1 (not PLAIN); length > 0 and low < high (PARTS). */
+typedef enum aqfq_rotary_scaling {
+  AQFQ_ROTARY_PLAIN = 0,
+  AQFQ_ROTARY_LINEAR = 1,
+  AQFQ_ROTARY_NTK = 2,
+  AQFQ_ROTARY_PARTS = 3
+} aqfq_rotary_scaling;
+aqfq_status aqfq_rotary_freqs(int64_t rot, double base, int scaling, double factor, double length,
+                              double low, double high, double* freqs, float* mscale);
+
 /* Diagnostic (the pages have no counterpart): checks the bounded-wait path
  * that the GEMM's pipeline uses when a stage never arrives.  One thread waits
  * on an mbarrier phase that nothing completes, polling at most `polls` times

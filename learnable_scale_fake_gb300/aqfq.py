@@ -26,6 +26,8 @@ KD_KL, KD_RKL, KD_CAKLD, KD_MSE = 0, 1, 2, 3
 BF16, F32 = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 LINEAR_FWD, LINEAR_DGRAD, LINEAR_WGRAD = 0, 1, 2
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_PARTS = 0, 1, 2, 3
 
 STATUS = {0: "AQFQ_OK", 1: "AQFQ_ERR_NULL", 2: "AQFQ_ERR_SHAPE", 3: "AQFQ_ERR_ALIGN",
           4: "AQFQ_ERR_UNSUPPORTED", 5: "AQFQ_ERR_WORKSPACE", 6: "AQFQ_ERR_CUDA"}
@@ -39,6 +41,7 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_ckpt8_act_bwd_workspace_bytes", "aqfq_layernorm_fwd", "aqfq_layernorm_bwd",
            "aqfq_layernorm_bwd_workspace_bytes", "aqfq_linear_fwd", "aqfq_linear_dgrad",
            "aqfq_linear_wgrad", "aqfq_linear_workspace_bytes",
+           "aqfq_rotary", "aqfq_rotary_freqs",
            "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_selftest_linear_plan",
            "aqfq_selftest_layernorm_ring", "aqfq_status_string",
            "aqfq_version")
@@ -56,6 +59,12 @@ class Ckpt8(ctypes.Structure):
     """An activation checkpoint in 8 bits (keeps its tensors alive)."""
     _fields_ = [("fmt", ctypes.c_int32), ("group", ctypes.c_int32), ("codes", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    """One tensor of aqfq_rotary."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("heads", "ldx", "hsx", "ldy", "hsy")]
 
 
 class AqfqError(RuntimeError):
@@ -79,7 +88,7 @@ def lib():
                 raise RuntimeError(f"libaqfq.so is not built ({LIB_PATH}); run __graft_entry__.build()")
             L = ctypes.CDLL(LIB_PATH)
             P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-            S = ctypes.POINTER(QSpec)
+            f64, S = ctypes.c_double, ctypes.POINTER(QSpec)
             sig = {
                 "aqfq_qdq_fwd": (i32, [S, P, i64, i64, i64, P, P, P, P, P, P]),
                 "aqfq_grouped_qdq": (i32, [S, P, i64, i64, i64, P, P, P, P, P, P]),
@@ -112,6 +121,8 @@ def lib():
                 "aqfq_linear_wgrad": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, i64, i32, P, sz, P,
                                             P]),
                 "aqfq_linear_workspace_bytes": (sz, [i32, i64, i64, i64]),
+                "aqfq_rotary": (i32, [i32, P, P, i64, i64, i64, i32, P, P, ctypes.c_float, i32, P]),
+                "aqfq_rotary_freqs": (i32, [i64, f64, i32, f64, f64, f64, f64, P, P]),
                 "aqfq_selftest_wait_timeout": (i32, [P, ctypes.c_uint32, P]),
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
                 "aqfq_selftest_linear_plan": (i32, [i32, i64, i64, i64, P]),
@@ -380,6 +391,8 @@ _ROWS = (torch.bfloat16, torch.float32)
 _BF = (torch.bfloat16,)
 _FL = (torch.float32,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_F64 = (torch.float64,)
 
 
 # the type codes of the tensors that the checks above let through (None: BF16)
@@ -582,6 +595,63 @@ def aqfq_linear_wgrad(dy, x, dw, accumulate=False, workspace=None, error_flag=No
         _stream_on(stream, dev))
     if st:
         _check("aqfq_linear_wgrad", st)
+
+
+# ---- between a layer's quantized products ----------------------------------------------
+
+def _heads(x, y, name, T, D, dtypes, dev):
+    """The heads x [T, heads, D] and where their rotation goes."""
+    if x is not None and y is not None:
+        size, on = x.shape, x.get_device()
+        if (x.dtype in dtypes and y.dtype == x.dtype and size == y.shape and len(size) == 3 and size[0] == T
+                and size[2] == D and y.get_device() == on and (x.is_cuda if dev is None else on == dev)):
+            (ldx, hsx, ex), (ldy, hsy, ey) = x.stride(), y.stride()
+            if ex == ey == 1 or D <= 1:
+                return ctypes.byref(Heads(x.data_ptr(), y.data_ptr(), size[1], ldx, hsx, ldy, hsy))
+    _refuse_heads(x, y, name, T, D, dtypes, dev)
+
+
+def _refuse_heads(x, y, name, T, D, dtypes, dev):
+    if x is None or y is None:
+        raise ValueError(f"{name} and y{name} come together")
+    for t, what in ((x, name), (y, "y" + name)):
+        _refuse_device(t, what, dev)
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what} must be one of {[str(d) for d in dtypes]}")
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.shape[1] != x.shape[1]:
+            raise ValueError(f"{what} must be [{T}, heads, {D}], as many heads as {name}")
+        dtypes, dev = (x.dtype,), t.get_device()
+    raise ValueError(f"{name} and y{name} must have contiguous elements in each head")
+
+
+def aqfq_rotary(q, pos, freqs, yq, k=None, yk=None, layout=ROTARY_HALF, mscale=1.0, transposed=False,
+                stream=None):
+    """yq, yk: heads q, k [T, heads, D] turned by pos (int64 [T]) times freqs (float64 [rot / 2]) and
+    multiplied by mscale; transposed: the gradient.  yq may be q, and yk may be k."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, D]")
+    T, _, D = q.shape
+    hq = _heads(q, yq, "q", T, D, _ROWS, None)
+    dev = q.get_device()
+    hk = None if k is None and yk is None else _heads(k, yk, "k", T, D, (q.dtype,), dev)
+    half = freqs.numel()
+    st = (_lib or lib()).aqfq_rotary(
+        _dt(q), hq, hk, T, D, 2 * half, int(layout), _vec(pos, "pos", _I64, T, dev),
+        _vec(freqs, "freqs", _F64, half, dev), float(mscale), 1 if transposed else 0,
+        _stream_on(stream, dev))
+    if st:
+        _check("aqfq_rotary", st)
+
+
+def aqfq_rotary_freqs(rot, base=10000.0, scaling=ROTARY_PLAIN, factor=1.0, length=0.0, low=1.0, high=32.0):
+    """(freqs, mscale): the angles per position of a head's pairs as a float64 tensor on the CPU, and
+    the factor on the rotated values."""
+    freqs = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float()
+    _check("aqfq_rotary_freqs", lib().aqfq_rotary_freqs(
+        int(rot), float(base), int(scaling), float(factor), float(length), float(low), float(high),
+        freqs.data_ptr(), ctypes.byref(m)))
+    return freqs, m.value
 
 
 def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:

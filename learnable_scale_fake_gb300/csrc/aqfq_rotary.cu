@@ -1,0 +1,310 @@
+// aqfq_rotary.cu -- rotary positions of query and key heads.
+//
+// Pair i of a head's first `rot` elements (elements i and i + rot / 2, or 2 i and 2 i + 1) is
+// turned by the angle pos freqs[i] and multiplied by mscale:
+//   (a, b) -> mscale (a cos - b sin, a sin + b cos),
+// transposed (the gradient): with -sin.  The other elements pass through.
+//
+// The angle in turns is a product of integers modulo 2^64: freqs[i] / 2 pi modulo 1 as a
+// 64-bit fraction F, the position as a 64-bit integer, and the product's low 64 bits are
+// the fraction of a turn, however far the position: off by at most |pos| 2^-65 and F's own
+// rounding of freqs[i] / 2 pi in binary64.  Its upper 32 bits, as binary32 in
+// [-1/2, 1/2], go to sincospif: the angle is off by 2^-25 of itself and 2^-32 turns.
+//
+// Bound by memory: each element is read and written once.  A thread owns P pairs of one
+// token, computes their sines once and walks over heads of a chunk; four heads' loads are
+// under way before the first is turned (the first four before the sines).  65536 tokens of 32
+// and 8 heads of 128 in BF16: 198 us, 6.8 TB/s, what a plain copy of as many bytes takes.
+#include <cmath>
+
+#include "aqfq_internal.h"
+#include "aqfq_layer.cuh"
+
+namespace aqfq {
+namespace layer {
+namespace {
+
+constexpr int kT = 256;
+constexpr int kSms = 152;  // of a GB300; the results do not need it
+
+struct Part {  // one tensor's heads
+  const void* x;
+  void* y;
+  int64_t ldx, hsx, ldy, hsy;
+  int heads, per, chunks;  // heads of a chunk
+};
+struct RotArgs {
+  Part part[2];
+  int64_t T, units;
+  const int64_t* pos;
+  const double* freqs;
+  int D, rot, items;  // items per head: rot / 2 / P that turn, then those that pass through
+  float mscale;
+  bool transposed, copy;  // copy: the elements that pass through are written
+};
+
+// P consecutive elements, aligned to their size
+template <typename T, int P>
+struct Vec {
+  static constexpr int BYTES = P * int(sizeof(T)), W = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else {
+      static_assert(BYTES == 16, "at most 16 bytes");
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES == 2) *reinterpret_cast<uint16_t*>(p) = uint16_t(w[0]);
+    else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else if constexpr (BYTES == 8) st_64(p, w[0], w[1]);
+    else st_128(p, w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return i & 1 ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[P]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (P == 1) {
+      w[0] = pack_bf16x2(0.0f, v[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+    }
+  }
+};
+
+// A unit is an item (two vectors of P elements) of a token and a chunk of heads.
+template <typename T, int P, bool HALF>
+__global__ void __launch_bounds__(kT) rotary_kernel(const RotArgs a) {
+  constexpr int U = 4;  // heads in flight
+  extern __shared__ int64_t turn[];  // [rot / 2] turns per position
+  for (int i = threadIdx.x; i < a.rot / 2; i += kT) {
+    const double t = a.freqs[i] * 0.15915494309189533577;  // 1 / 2 pi
+    turn[i] = __double2ll_rn((t - rint(t)) * 0x1p64);
+  }
+  __syncthreads();
+  const int chunks = a.part[0].chunks + a.part[1].chunks, turning = a.rot / 2 / P;
+  for (int64_t u = int64_t(blockIdx.x) * kT + threadIdx.x; u < a.units; u += int64_t(gridDim.x) * kT) {
+    int item, c;
+    int64_t t;
+    if (a.units <= 0x7FFFFFFF) {
+      const uint32_t r = uint32_t(u) / uint32_t(a.items), s = r / uint32_t(chunks);
+      item = int(uint32_t(u) - r * uint32_t(a.items)), c = int(r - s * uint32_t(chunks)), t = s;
+    } else {
+      const int64_t r = u / a.items;
+      t = r / chunks, item = int(u - r * a.items), c = int(r - t * chunks);
+    }
+    const bool turns = item < turning;
+    if (!turns && !a.copy) continue;
+    const bool second = c >= a.part[0].chunks;
+    const Part& p = a.part[second ? 1 : 0];
+    const int h0 = (second ? c - a.part[0].chunks : c) * p.per;
+    const int n = p.heads - h0 < p.per ? p.heads - h0 : p.per;
+    // the item's two vectors
+    const int e0 = turns ? (HALF ? item * P : item * 2 * P) : a.rot + (item - turning) * 2 * P;
+    const int e1 = HALF && turns ? e0 + a.rot / 2 : e0 + P;
+    const bool two = P > 1 || e1 < a.D;  // the last element of an odd rest stands alone
+    const T* x = static_cast<const T*>(p.x) + t * p.ldx + h0 * p.hsx;
+    T* y = static_cast<T*>(p.y) + t * p.ldy + h0 * p.hsy;
+    Vec<T, P> v[U], w[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (j < n) {
+        v[j].load(x + j * p.hsx + e0);
+        if (two) w[j].load(x + j * p.hsx + e1);
+      }
+    }
+    float cs[P], sn[P];
+    if (turns) {
+      const int64_t pos = a.pos[t];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int64_t f = int64_t(uint64_t(pos) * uint64_t(turn[item * P + i]));
+        sincospif(float(int32_t(f >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+        cs[i] *= a.mscale;
+        sn[i] *= a.transposed ? -a.mscale : a.mscale;
+      }
+    }
+    for (int h = 0; h < n; h += U) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (h + j >= n) break;
+        if (turns) {
+          float f[2 * P], o[P], q[P];
+#pragma unroll
+          for (int i = 0; i < P; ++i) f[i] = v[j].get(i), f[P + i] = w[j].get(i);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int k = HALF ? i : 2 * i, l = HALF ? P + i : 2 * i + 1;
+            const float s = f[k], r = f[l];
+            f[k] = fmaf(s, cs[i], -(r * sn[i]));
+            f[l] = fmaf(r, cs[i], s * sn[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < P; ++i) o[i] = f[i], q[i] = f[P + i];
+          v[j].set(o), w[j].set(q);
+        }
+        T* at = y + (h + j) * p.hsy;
+        v[j].store(at + e0);
+        if (two) w[j].store(at + e1);
+        if (h + j + U < n) {
+          const T* nx = x + (h + j + U) * p.hsx;
+          v[j].load(nx + e0);
+          if (two) w[j].load(nx + e1);
+        }
+      }
+    }
+  }
+}
+
+// Heads per chunk: as many as leave every SM about 1024 threads, at most 16 (the sines of a
+// chunk are then an eighth of its instructions).
+int chunk_heads(int64_t T, int heads, int items) {
+  if (heads == 0) return 1;
+  int64_t per = T * heads * items / (int64_t(kSms) * 1024);
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  const int64_t chunks = (heads + per - 1) / per;
+  return int((heads + chunks - 1) / chunks);
+}
+
+template <typename T, int P>
+cudaError_t launch(RotArgs a, bool half, cudaStream_t st) {
+  const int turning = a.rot / 2 / P, rest = (a.D - a.rot + 2 * P - 1) / (2 * P);
+  a.items = turning + rest;
+  int64_t chunks = 0;
+  for (Part& p : a.part) {
+    p.per = chunk_heads(a.T, p.heads, a.items);
+    p.chunks = (p.heads + p.per - 1) / p.per;
+    chunks += p.chunks;
+  }
+  a.units = a.T * chunks * a.items;
+  int64_t blocks = (a.units + kT - 1) / kT;
+  if (blocks > kSms * 64) blocks = kSms * 64;
+  const size_t smem = size_t(a.rot / 2) * 8;
+  if (half) rotary_kernel<T, P, true><<<unsigned(blocks), kT, smem, st>>>(a);
+  else rotary_kernel<T, P, false><<<unsigned(blocks), kT, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Whether vectors of P elements fit: every vector of a head starts at a multiple of its size.
+bool fits(const RotArgs& a, bool half, int es, int P) {
+  const int64_t b = int64_t(P) * es;
+  if (a.rot % (2 * P) != 0 || (a.D - a.rot) % (2 * P) != 0) return false;
+  for (const Part& p : a.part) {
+    if (p.heads == 0) continue;
+    if (!al(p.x, uintptr_t(b)) || !al(p.y, uintptr_t(b))) return false;
+    if ((p.ldx * es) % b || (p.hsx * es) % b || (p.ldy * es) % b || (p.hsy * es) % b) return false;
+  }
+  return true;
+}
+
+// the widest accesses that fit: 16 bytes, 8, or single elements
+template <typename T>
+cudaError_t dispatch(const RotArgs& a, bool half, cudaStream_t st) {
+  constexpr int P = 16 / int(sizeof(T));
+  if (fits(a, half, sizeof(T), P)) return launch<T, P>(a, half, st);
+  if (fits(a, half, sizeof(T), P / 2)) return launch<T, P / 2>(a, half, st);
+  return launch<T, 1>(a, half, st);
+}
+
+// strides of [T, heads, D] elements that do not overlap; `once`: each is a place of its own
+bool strides_ok(int64_t T, int64_t heads, int64_t D, int64_t ld, int64_t hs, bool once) {
+  if (ld < 0 || hs < 0) return false;
+  if (T > 0 && ld > (int64_t(1) << 59) / T) return false;
+  if (heads > 0 && hs > (int64_t(1) << 59) / heads) return false;
+  if (!once || T == 0 || heads == 0) return true;  // (nothing is written)
+  // the axis with the smaller stride lies within a step of the other one
+  const bool heads_in = T <= 1 || (heads > 1 && hs <= ld);
+  const int64_t n = heads_in ? heads : T, s = heads_in ? hs : ld;
+  if (n > 1 && s < D) return false;
+  const int64_t extent = n > 1 ? (n - 1) * s + D : D;
+  return (heads_in ? T : heads) <= 1 || (heads_in ? ld : hs) >= extent;
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace aqfq
+
+using namespace aqfq;
+using namespace aqfq::layer;
+
+extern "C" aqfq_status aqfq_rotary_freqs(int64_t rot, double base, int scaling, double factor,
+                                         double length, double low, double high, double* freqs,
+                                         float* mscale) {
+  if (rot < 0 || rot % 2 != 0 || rot > 8192) return AQFQ_ERR_SHAPE;
+  if (rot > 0 && !freqs) return AQFQ_ERR_NULL;
+  if (scaling < AQFQ_ROTARY_PLAIN || scaling > AQFQ_ROTARY_PARTS) return AQFQ_ERR_UNSUPPORTED;
+  if (!(base > 0.0) || !std::isfinite(base)) return AQFQ_ERR_SHAPE;
+  if (scaling != AQFQ_ROTARY_PLAIN && !(factor >= 1.0 && std::isfinite(factor))) return AQFQ_ERR_SHAPE;
+  if (scaling == AQFQ_ROTARY_PARTS &&
+      !(length > 0.0 && std::isfinite(length) && low < high && std::isfinite(low) && std::isfinite(high)))
+    return AQFQ_ERR_SHAPE;
+  if (scaling == AQFQ_ROTARY_NTK && rot > 2) base *= std::pow(factor, double(rot) / double(rot - 2));
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * double(i) / double(rot));
+    if (scaling == AQFQ_ROTARY_LINEAR) f /= factor;
+    if (scaling == AQFQ_ROTARY_PARTS) {
+      // full turns of this pair over the trained length: above `high` kept, below `low` divided
+      double keep = (length * f / 6.283185307179586477 - low) / (high - low);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    freqs[i] = f;
+  }
+  if (mscale) *mscale = scaling == AQFQ_ROTARY_PARTS ? float(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return AQFQ_OK;
+}
+
+extern "C" aqfq_status aqfq_rotary(int dtype, const aqfq_heads* q, const aqfq_heads* k, int64_t T,
+                                   int64_t D, int64_t rot, int layout, const int64_t* pos,
+                                   const double* freqs, float mscale, int transposed, void* stream) {
+  if (!q) return AQFQ_ERR_NULL;
+  if (T < 0 || T > (int64_t(1) << 40) || D < 1 || D > 8192 || rot < 0 || rot > D || rot % 2 != 0)
+    return AQFQ_ERR_SHAPE;
+  if (!dtype_ok(dtype) || (layout != AQFQ_ROTARY_HALF && layout != AQFQ_ROTARY_INTERLEAVED))
+    return AQFQ_ERR_UNSUPPORTED;
+  const int es = esize(dtype);
+  RotArgs a = {};
+  a.T = T, a.D = int(D), a.rot = int(rot), a.mscale = mscale, a.transposed = transposed != 0;
+  a.pos = pos, a.freqs = freqs;
+  const aqfq_heads* in[2] = {q, k};
+  bool any = false;
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    const aqfq_heads& h = *in[i];
+    if (h.heads < 0 || h.heads > (1 << 20)) return AQFQ_ERR_SHAPE;
+    if (!strides_ok(T, h.heads, D, h.ldx, h.hsx, false) || !strides_ok(T, h.heads, D, h.ldy, h.hsy, true))
+      return AQFQ_ERR_SHAPE;
+    if (T == 0 || h.heads == 0) continue;
+    if (!h.x || !h.y) return AQFQ_ERR_NULL;
+    if (!al(h.x, es) || !al(h.y, es)) return AQFQ_ERR_ALIGN;
+    const bool place = h.x == h.y;
+    // in place every element is read where it is written
+    if (place && ((T > 1 && h.ldx != h.ldy) || (h.heads > 1 && h.hsx != h.hsy))) return AQFQ_ERR_UNSUPPORTED;
+    a.copy |= !place;
+    // a single token or head has no stride
+    const bool tokens = T > 1, heads = h.heads > 1;
+    a.part[i] = {h.x, h.y, tokens ? h.ldx : 0, heads ? h.hsx : 0, tokens ? h.ldy : 0, heads ? h.hsy : 0,
+                 int(h.heads), 1, 0};
+    any = true;
+  }
+  if (any && rot > 0 && (!pos || !freqs)) return AQFQ_ERR_NULL;
+  if (!al(pos, 8) || !al(freqs, 8)) return AQFQ_ERR_ALIGN;
+  if (!any || (rot == 0 && !a.copy)) return AQFQ_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool half = layout == AQFQ_ROTARY_HALF;
+  const cudaError_t e = dtype == AQFQ_BF16 ? dispatch<bf16>(a, half, st) : dispatch<float>(a, half, st);
+  return e == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
+}

@@ -1,0 +1,97 @@
+"""Refusals of the calls between a layer's quantized products, before any launch (fake
+pointer values are safe), the binding's own checks on the CPU, and the host-only calls."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from learnable_scale_fake_gb300 import _build, aqfq
+
+OK, NULL, SHAPE, ALIGN, UNSUP, WS = 0, 1, 2, 3, 4, 5
+A = 0x10000
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return aqfq.lib()
+
+
+# ---- rotary positions ----------------------------------------------------------------
+
+def hd(x=A, y=2 * A, heads=4, ldx=256, hsx=64, ldy=256, hsy=64):
+    return ctypes.byref(aqfq.Heads(x, y, heads, ldx, hsx, ldy, hsy))
+
+
+def rotary(L, dtype=0, q=None, k=None, T=4, D=64, rot=64, layout=0, pos=3 * A, freqs=4 * A, m=1.0):
+    return L.aqfq_rotary(dtype, hd() if q is None else q, k, T, D, rot, layout, pos, freqs, ctypes.c_float(m),
+                         0, None)
+
+
+def test_rotary_checks(L):
+    none = ctypes.c_void_p(None)
+    assert rotary(L, q=none) == NULL
+    assert rotary(L, dtype=2) == UNSUP and rotary(L, layout=2) == UNSUP and rotary(L, layout=-1) == UNSUP
+    assert rotary(L, T=-1) == SHAPE
+    assert rotary(L, D=0, rot=0) == SHAPE and rotary(L, D=8193) == SHAPE
+    assert rotary(L, rot=63) == SHAPE and rotary(L, rot=66) == SHAPE and rotary(L, rot=-2) == SHAPE
+    assert rotary(L, pos=None) == NULL and rotary(L, freqs=None) == NULL
+    assert rotary(L, pos=A + 4) == ALIGN and rotary(L, freqs=A + 4) == ALIGN
+    for part in ("q", "k"):
+        def f(dtype=0, **kw):
+            return rotary(L, dtype, **{part: hd(**kw)})
+        assert f(x=None) == NULL and f(y=None) == NULL
+        assert f(x=A + 1) == ALIGN and f(y=A + 1) == ALIGN and f(dtype=1, x=A + 2) == ALIGN
+        assert f(heads=-1) == SHAPE and f(heads=(1 << 20) + 1) == SHAPE
+        assert f(ldx=-1) == SHAPE and f(hsx=-64) == SHAPE
+        assert f(ldx=1 << 58) == SHAPE
+        # outputs that share elements: heads, tokens, or both axes with one stride
+        assert f(hsy=63) == SHAPE and f(ldy=255) == SHAPE and f(ldy=64) == SHAPE
+        assert f(ldy=0) == SHAPE and f(hsy=0) == SHAPE
+        # in place with other strides
+        assert f(y=A, ldy=512) == UNSUP and f(y=A, ldx=64, hsx=256, ldy=256, hsy=64) == UNSUP
+    # nothing to do needs no buffers
+    assert rotary(L, T=0, q=hd(None, None), pos=None, freqs=None) == OK
+    assert rotary(L, q=hd(None, None, 0), pos=None, freqs=None) == OK
+    assert rotary(L, q=hd(y=A), rot=0, pos=None, freqs=None) == OK
+
+
+def test_rotary_frequencies(L):
+    f, m = aqfq.aqfq_rotary_freqs(8, base=100.0)
+    want = torch.tensor([100.0 ** (-i / 4) for i in range(4)], dtype=torch.float64)
+    assert m == 1.0 and float((f / want - 1).abs().max()) < 1e-14
+    g, m = aqfq.aqfq_rotary_freqs(8, base=100.0, scaling=aqfq.ROTARY_LINEAR, factor=4.0)
+    assert m == 1.0 and float((g * 4 / want - 1).abs().max()) < 1e-14
+    # the last pair is interpolated in full, the first one kept
+    g, m = aqfq.aqfq_rotary_freqs(8, base=100.0, scaling=aqfq.ROTARY_NTK, factor=4.0)
+    assert m == 1.0 and abs(float(g[0]) - 1) < 1e-14 and abs(float(g[3] * 4 / want[3]) - 1) < 1e-13
+    # turns over the length: 1000 / 2 pi = 159, 50, 15.9, 5.03; kept above 40, divided below 10
+    g, m = aqfq.aqfq_rotary_freqs(8, base=100.0, scaling=aqfq.ROTARY_PARTS, factor=4.0, length=1000.0,
+                                  low=10.0, high=40.0)
+    k = (1000 * float(want[2]) / (2 * math.pi) - 10) / 30
+    assert 0 < k < 1
+    parts = torch.tensor([1, 1, k + (1 - k) / 4, 0.25], dtype=torch.float64) * want
+    assert float((g / parts - 1).abs().max()) < 1e-13 and abs(m - (0.1 * math.log(4) + 1)) < 1e-7
+    f, m = aqfq.aqfq_rotary_freqs(0)
+    assert len(f) == 0
+    buf = (ctypes.c_double * 64)()
+    p = ctypes.addressof(buf)
+    g = lambda rot=8, base=1e4, s=0, factor=4.0, length=1e3, low=1.0, high=32.0, out=p: L.aqfq_rotary_freqs(
+        rot, base, s, factor, length, low, high, out, None)
+    assert g() == OK and g(rot=7) == SHAPE and g(rot=-2) == SHAPE and g(out=None) == NULL
+    assert g(rot=8194) == SHAPE
+    assert g(base=0.0) == SHAPE and g(base=float("nan")) == SHAPE and g(base=float("inf")) == SHAPE
+    assert g(s=4) == UNSUP and g(s=-1) == UNSUP
+    for s in (1, 2, 3):
+        assert g(s=s, factor=0.5) == SHAPE and g(s=s, factor=float("nan")) == SHAPE and g(s=s) == OK
+    assert g(s=3, length=0.0) == SHAPE and g(s=3, low=32.0) == SHAPE and g(s=3, high=float("nan")) == SHAPE
+
+
+def test_rotary_binding_checks():
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    pos, freqs = torch.zeros(4, dtype=torch.int64), torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="CUDA"):
+        aqfq.aqfq_rotary(q, pos, freqs, torch.empty_like(q))
+    with pytest.raises(ValueError, match="heads"):
+        aqfq.aqfq_rotary(q[0], pos, freqs, q)
