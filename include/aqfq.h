@@ -541,6 +541,47 @@ typedef enum aqfq_rotary_scaling {
 aqfq_status aqfq_rotary_freqs(int64_t rot, double base, int scaling, double factor, double length,
                               double low, double high, double* freqs, float* mscale);
 
+/* What lies between two blocks of a layer, root-mean-square norms of rows:
+ *   n = post ? f rstd_post gamma_post : f      rstd_post = 1 / sqrt(mean(f^2) + eps)
+ *   h = x + alpha gate n                       the residual stream
+ *   y = h rstd_pre gamma_pre                   rstd_pre = 1 / sqrt(mean(h^2) + eps)
+ *   x           [rows, cols] of dtype, the residual stream before; NULL = zeros
+ *   f           [rows, cols], the block's output; NULL: h = x (a plain norm of x)
+ *   gamma_post, gate, gamma_pre  [cols] of param_dtype; NULL = ones.  gamma_post
+ *               goes with post, gate and post with f, gamma_pre with y
+ *   h, y        [rows, cols], each optional, not both NULL; y is the norm of the
+ *               unrounded h
+ *   rstd_post, rstd_pre  float [rows], optional (the backward needs them)
+ *   eps         finite, >= 0;  cols >= 1 */
+aqfq_status aqfq_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* f, int64_t ldf,
+                                int64_t rows, int64_t cols, int post, int param_dtype,
+                                const void* gamma_post, const void* gate, float alpha,
+                                const void* gamma_pre, float eps, void* h, int64_t ldh, void* y,
+                                int64_t ldy, float* rstd_post, float* rstd_pre, void* stream);
+
+/* Its gradient from h as it was stored, with c = alpha gate gamma_post, hh = h
+ * rstd_pre, fh = f rstd_post (f without post), u = dy gamma_pre:
+ *   dx = rstd_pre (u - hh mean(u hh)) + dh
+ *   df = rstd_post (c dx - fh mean(c dx fh))   (c dx without post)
+ *   dgamma_pre = sum over rows of dy hh;  with S = sum over rows of dx fh
+ *   dgate = alpha gamma_post S;  dgamma_post = alpha gate S   (dx unrounded)
+ *   dy, dh      gradients of y and of h [rows, cols]; one may be NULL (zeros)
+ *   h           the forward's h (its x where f was NULL); needed with dy
+ *   f           the forward's; NULL: a plain norm
+ *   rstd_post   the forward's; NULL: f was not normalised.  rstd_pre goes with dy
+ *   dx, df      optional [rows, cols]
+ *   dgamma_post, dgate, dgamma_pre  optional float [cols], added to with accumulate
+ *   workspace   device, aqfq_block_norm_bwd_workspace_bytes(rows, cols) bytes, 8-byte
+ *               aligned; needed with one of the three vectors only */
+size_t aqfq_block_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+aqfq_status aqfq_block_norm_bwd(int dtype, const void* dy, int64_t lddy, const void* dh, int64_t lddh,
+                                const void* h, int64_t ldh, const void* f, int64_t ldf, int64_t rows,
+                                int64_t cols, const float* rstd_post, const float* rstd_pre,
+                                int param_dtype, const void* gamma_post, const void* gate, float alpha,
+                                const void* gamma_pre, void* dx, int64_t lddx, void* df, int64_t lddf,
+                                float* dgamma_post, float* dgate, float* dgamma_pre, int accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Diagnostic (the pages have no counterpart): checks the bounded-wait path
  * that the GEMM's pipeline uses when a stage never arrives.  One thread waits
  * on an mbarrier phase that nothing completes, polling at most `polls` times

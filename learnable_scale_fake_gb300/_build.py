@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libaqfq.so")
 
 SOURCES = ["aqfq_api.cu", "aqfq_kernels.cu", "aqfq_fused.cu", "aqfq_stats.cu", "aqfq_noalloc.cu",
            "aqfq_gemm.cu", "aqfq_kd.cu", "aqfq_diag.cu", "aqfq_ckpt8.cu", "aqfq_norm.cu",
-           "aqfq_linear.cu", "aqfq_rotary.cu"]
+           "aqfq_linear.cu", "aqfq_rotary.cu", "aqfq_block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE division and denormals are part of the numerics contract: never fast math
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-prec-div=true",

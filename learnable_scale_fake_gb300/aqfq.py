@@ -41,7 +41,8 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_ckpt8_act_bwd_workspace_bytes", "aqfq_layernorm_fwd", "aqfq_layernorm_bwd",
            "aqfq_layernorm_bwd_workspace_bytes", "aqfq_linear_fwd", "aqfq_linear_dgrad",
            "aqfq_linear_wgrad", "aqfq_linear_workspace_bytes",
-           "aqfq_rotary", "aqfq_rotary_freqs",
+           "aqfq_rotary", "aqfq_rotary_freqs", "aqfq_block_norm_fwd", "aqfq_block_norm_bwd",
+           "aqfq_block_norm_bwd_workspace_bytes",
            "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_selftest_linear_plan",
            "aqfq_selftest_layernorm_ring", "aqfq_status_string",
            "aqfq_version")
@@ -88,7 +89,7 @@ def lib():
                 raise RuntimeError(f"libaqfq.so is not built ({LIB_PATH}); run __graft_entry__.build()")
             L = ctypes.CDLL(LIB_PATH)
             P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-            f64, S = ctypes.c_double, ctypes.POINTER(QSpec)
+            f32, f64, S = ctypes.c_float, ctypes.c_double, ctypes.POINTER(QSpec)
             sig = {
                 "aqfq_qdq_fwd": (i32, [S, P, i64, i64, i64, P, P, P, P, P, P]),
                 "aqfq_grouped_qdq": (i32, [S, P, i64, i64, i64, P, P, P, P, P, P]),
@@ -123,6 +124,11 @@ def lib():
                 "aqfq_linear_workspace_bytes": (sz, [i32, i64, i64, i64]),
                 "aqfq_rotary": (i32, [i32, P, P, i64, i64, i64, i32, P, P, ctypes.c_float, i32, P]),
                 "aqfq_rotary_freqs": (i32, [i64, f64, i32, f64, f64, f64, f64, P, P]),
+                "aqfq_block_norm_fwd": (i32, [i32, P, i64, P, i64, i64, i64, i32, i32, P, P, f32, P, f32, P,
+                                              i64, P, i64, P, P, P]),
+                "aqfq_block_norm_bwd": (i32, [i32, P, i64, P, i64, P, i64, P, i64, i64, i64, P, P, i32, P, P,
+                                              f32, P, P, i64, P, i64, P, P, P, i32, P, sz, P]),
+                "aqfq_block_norm_bwd_workspace_bytes": (sz, [i64, i64]),
                 "aqfq_selftest_wait_timeout": (i32, [P, ctypes.c_uint32, P]),
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
                 "aqfq_selftest_linear_plan": (i32, [i32, i64, i64, i64, P]),
@@ -652,6 +658,75 @@ def aqfq_rotary_freqs(rot, base=10000.0, scaling=ROTARY_PLAIN, factor=1.0, lengt
         int(rot), float(base), int(scaling), float(factor), float(length), float(low), float(high),
         freqs.data_ptr(), ctypes.byref(m)))
     return freqs, m.value
+
+
+def _one_type(*vectors):
+    """The type of the vectors that are there."""
+    found = None
+    for v in vectors:
+        if v is not None:
+            if found is not None and v.dtype != found.dtype:
+                raise TypeError("gamma_post, gate and gamma_pre must have one type")
+            found = v
+    return _dt(found)
+
+
+def aqfq_block_norm_fwd(x, f, eps, h=None, y=None, post=False, gamma_post=None, gate=None, alpha=1.0,
+                        gamma_pre=None, rstd_post=None, rstd_pre=None, stream=None):
+    """h = x + alpha gate n, n = norm(f) gamma_post with post, else f; y = norm(h) gamma_pre.  x, f
+    [rows, cols], one of them may be None."""
+    a = x if x is not None else f
+    if a is None:
+        raise ValueError("x and f are both missing")
+    px, ldx = _mat(x, "x", _ROWS)
+    dev = a.get_device()
+    R, C = a.shape
+    dt = (a.dtype,)
+    pf, ldf = _mat(f, "f", dt if x is not None else _ROWS, (R, C), None if x is None else dev)
+    ph, ldh = _mat(h, "h", dt, (R, C), dev)
+    py, ldy = _mat(y, "y", dt, (R, C), dev)
+    st = (_lib or lib()).aqfq_block_norm_fwd(
+        _dt(a), px, ldx, pf, ldf, R, C, 1 if post else 0, _one_type(gamma_post, gate, gamma_pre),
+        _vec(gamma_post, "gamma_post", _ROWS, C, dev), _vec(gate, "gate", _ROWS, C, dev), float(alpha),
+        _vec(gamma_pre, "gamma_pre", _ROWS, C, dev), float(eps), ph, ldh, py, ldy,
+        _vec(rstd_post, "rstd_post", _FL, R, dev), _vec(rstd_pre, "rstd_pre", _FL, R, dev),
+        _stream_on(stream, dev))
+    if st:
+        _check("aqfq_block_norm_fwd", st)
+
+
+def aqfq_block_norm_bwd_workspace_bytes(rows, cols) -> int:
+    return int(lib().aqfq_block_norm_bwd_workspace_bytes(int(rows), int(cols)))
+
+
+def aqfq_block_norm_bwd(dy, dh, h, f, rstd_post=None, rstd_pre=None, gamma_post=None, gate=None, alpha=1.0,
+                        gamma_pre=None, dx=None, df=None, dgamma_post=None, dgate=None, dgamma_pre=None,
+                        accumulate=False, workspace=None, stream=None):
+    """Gradient of aqfq_block_norm_fwd from those of y and h (one may be None); rstd_post None: f was
+    not normalised."""
+    a = dy if dy is not None else dh
+    if a is None:
+        raise ValueError("dy and dh are both missing")
+    pd, ldd = _mat(dy, "dy", _ROWS)
+    dev = a.get_device()
+    R, C = a.shape
+    dt = (a.dtype,)
+    pdh, lddh = _mat(dh, "dh", dt if dy is not None else _ROWS, (R, C), None if dy is None else dev)
+    ph, ldh = _mat(h, "h", dt, (R, C), dev)
+    pf, ldf = _mat(f, "f", dt, (R, C), dev)
+    px, ldx = _mat(dx, "dx", dt, (R, C), dev)
+    po, ldo = _mat(df, "df", dt, (R, C), dev)
+    ws, wsb = _ws(workspace, dev)
+    st = (_lib or lib()).aqfq_block_norm_bwd(
+        _dt(a), pd, ldd, pdh, lddh, ph, ldh, pf, ldf, R, C, _vec(rstd_post, "rstd_post", _FL, R, dev),
+        _vec(rstd_pre, "rstd_pre", _FL, R, dev), _one_type(gamma_post, gate, gamma_pre),
+        _vec(gamma_post, "gamma_post", _ROWS, C, dev), _vec(gate, "gate", _ROWS, C, dev), float(alpha),
+        _vec(gamma_pre, "gamma_pre", _ROWS, C, dev), px, ldx, po, ldo,
+        _vec(dgamma_post, "dgamma_post", _FL, C, dev), _vec(dgate, "dgate", _FL, C, dev),
+        _vec(dgamma_pre, "dgamma_pre", _FL, C, dev), 1 if accumulate else 0, ws, wsb,
+        _stream_on(stream, dev))
+    if st:
+        _check("aqfq_block_norm_bwd", st)
 
 
 def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:

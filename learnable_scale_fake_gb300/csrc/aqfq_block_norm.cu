@@ -1,0 +1,687 @@
+// aqfq_block_norm.cu -- what lies between two blocks of a layer: the norm after the first,
+// its gate and residual scale, the residual's addition and the norm before the next one.
+//
+// Rows of C columns, root-mean-square norms, r_t = (sum t^2 / C + eps)^-1/2:
+//   n = f r_f gamma_post  (or f),   h = x + alpha gate n,   y = h r_h gamma_pre
+// Backward, with c = alpha gate gamma_post, hh = h r_h, fh = f r_f, u = dy gamma_pre:
+//   D  = r_h (u - hh mean(u hh)) + dh                       (dx)
+//   df = r_f (c D - fh mean(c D fh))
+//   S  = sum over rows of D fh:  dgate = alpha gamma_post S,  dgamma_post = alpha gate S
+//   dgamma_pre = sum over rows of dy hh
+// The two means of the backward pass take one reduction: with q = r_h u + dh,
+//   mean(c D fh) = mean(c fh q) - r_h mean(u hh) mean(c fh hh),
+// terms of the size of those that D itself is the difference of.  The forward's two sums
+// depend on each other and stay two: h is often much smaller than its terms' products.
+#include "aqfq_internal.h"
+#include "aqfq_layer.cuh"
+#include "aqfq_rows.cuh"
+
+namespace aqfq {
+namespace layer {
+namespace {
+
+// c = alpha gate gamma_post of a lane's pairs
+struct Coef {
+  const void *gate, *gamma_post;
+  float alpha;
+};
+
+struct FwdArgs {
+  int64_t ldx, ldf, ldh, ldy, rows, cols;
+  Coef c;
+  const void* gamma_pre;
+  float *rstd_post, *rstd_pre;
+  float eps;
+  int pdtype;
+  bool post;
+  bool vec, pvec;
+};
+
+template <int V, int NV>
+__device__ __forceinline__ void coefs(const Coef& c, int pdtype, const int64_t (&col)[NV],
+                                      const bool (&in)[NV], f2 (&v)[NV * V / 2]) {
+  params<V, NV>(c.gate, pdtype, col, in, 1.0f, v);
+#pragma unroll
+  for (int i = 0; i < NV * V / 2; ++i) v[i] = mul2(v[i], pair(c.alpha));
+  if (c.gamma_post) {
+    f2 g[NV * V / 2];
+    params<V, NV>(c.gamma_post, pdtype, col, in, 1.0f, g);
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = mul2(v[i], g[i]);
+  }
+}
+__device__ __forceinline__ void coefs8(const Coef& c, int pdtype, bool vec, int64_t col, int n, float (&v)[8]) {
+  float g[8];
+  load_param(c.gate, pdtype, vec, col, n, 1.0f, v);
+  load_param(c.gamma_post, pdtype, vec, col, n, 1.0f, g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * c.alpha * g[i];
+}
+
+// ---------------------------------------------------------------------------
+// wide rows: a block walks each row, which it reads once per sum and once more
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kT) join_fwd_walk(const T* x, const T* f, T* h, T* y, const FwdArgs a) {
+  __shared__ float red[kT / 32];
+  const float inv = 1.0f / float(a.cols);
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    float rf = 1.0f, rh = 0.0f;
+    // h of 8 columns, rf known
+    auto joined = [&](int64_t col, int n, float (&v)[8]) {
+      float b[8] = {}, c[8];
+      if (x) load_row(x + r * a.ldx + col, a.vec && n == 8, n, b);
+      if (f) {
+        load_row(f + r * a.ldf + col, a.vec && n == 8, n, v);
+        coefs8(a.c, a.pdtype, a.pvec, col, n, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? fmaf(v[i] * rf, c[i], b[i]) : 0.0f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = b[i];
+      }
+    };
+    if (a.post) {
+      float s = 0.0f;
+      for (int64_t col = threadIdx.x * 8; col < a.cols; col += kT * 8) {
+        const int n = a.cols - col > 8 ? 8 : int(a.cols - col);
+        float v[8];
+        load_row(f + r * a.ldf + col, a.vec && n == 8, n, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+      }
+      rf = rsqrtf(fmaf(block_sum(s, red), inv, a.eps));
+      if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[r] = rf;
+    }
+    float s = 0.0f;
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kT * 8) {
+      const int n = a.cols - col > 8 ? 8 : int(a.cols - col);
+      float v[8];
+      joined(col, n, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+      if (h) store_row(h + r * a.ldh + col, a.vec && n == 8, n, v);
+    }
+    if (!y) continue;
+    rh = rsqrtf(fmaf(block_sum(s, red), inv, a.eps));
+    if (threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[r] = rh;
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kT * 8) {
+      const int n = a.cols - col > 8 ? 8 : int(a.cols - col);
+      float v[8], g[8];
+      joined(col, n, v);
+      load_param(a.gamma_pre, a.pdtype, a.pvec, col, n, 1.0f, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * rh * g[i];
+      store_row(y + r * a.ldy + col, a.vec && n == 8, n, v);
+    }
+  }
+}
+
+// sums of R values over the G warps of a block's row (G = 1: of a warp)
+template <int R, int G>
+__device__ __forceinline__ void row_sums(float (&s)[R], float (&red)[R][G]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+  if constexpr (G > 1) {
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) red[k][threadIdx.x >> 5] = s[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      s[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < G; ++w) s[k] += red[k][w];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows held in registers (columns as in the layer norm): a row belongs to G warps, a block
+// takes R rows (G = 1: each of its four warps does), whose loads are all under way first.
+// ---------------------------------------------------------------------------
+template <typename T, int V, int NV, int G, int R>
+__global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
+    join_fwd_rows(const T* x, const T* f, T* h, T* y, const FwdArgs a) {
+  constexpr int RB = G == 1 ? 4 : 1, P = NV * V / 2;
+  __shared__ float red[2][R][G];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float inv = 1.0f / float(a.cols);
+  const int64_t r0 = (int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0)) * R;
+  if (G == 1 && r0 >= a.rows) return;
+  int64_t col[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col[j] = ((G == 1 ? 0 : int64_t(warp) * (NV * 32)) + j * 32 + lane) * V;
+    in[j] = col[j] < a.cols;
+  }
+  Row<T, V, NV> rx[R], rf[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int64_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rx[k].zero(j), rf[k].zero(j);
+      if (in[j] && f) rf[k].load(j, f + r * a.ldf + col[j]);
+      if (in[j] && x) rx[k].load(j, x + r * a.ldx + col[j]);
+    }
+  }
+  f2 v[R][P];
+  float s[R], scale[R];
+  if (f) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      f2 t = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        v[k][i] = rf[k].pair_at(i);
+        t = fma2(v[k][i], v[k][i], t);
+      }
+      s[k] = lo2(t) + hi2(t);
+      scale[k] = 1.0f;
+    }
+    if (a.post) {
+      row_sums<R, G>(s, red[0]);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+        if (a.rstd_post && lane == 0 && (G == 1 || warp == 0) && r0 + k < a.rows) a.rstd_post[r0 + k] = scale[k];
+      }
+    }
+    f2 c[P];
+    coefs<V, NV>(a.c, a.pdtype, col, in, c);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        v[k][i] = masked<V, NV>(fma2(mul2(v[k][i], pair(scale[k])), c[i], rx[k].pair_at(i)), i, in);
+  } else {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[k][i] = rx[k].pair_at(i);
+  }
+  if (h) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (r0 + k >= a.rows) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (in[j]) put<T, V>(h + (r0 + k) * a.ldh + col[j], v[k], j);
+    }
+  }
+  if (!y) return;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    f2 t = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) t = fma2(v[k][i], v[k][i], t);
+    s[k] = lo2(t) + hi2(t);
+  }
+  row_sums<R, G>(s, red[1]);
+  f2 g[P];
+  params<V, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (r0 + k >= a.rows) break;
+    scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+    if (a.rstd_pre && lane == 0 && (G == 1 || warp == 0)) a.rstd_pre[r0 + k] = scale[k];
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[k][i] = mul2(mul2(v[k][i], pair(scale[k])), g[i]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in[j]) put<T, V>(y + (r0 + k) * a.ldy + col[j], v[k], j);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+struct BwdArgs {
+  int64_t lddy, lddh, ldh, ldf, lddx, lddf, rows, cols;
+  const float *rstd_post, *rstd_pre;
+  Coef c;
+  const void* gamma_pre;
+  float *pg, *ps;  // the blocks' column sums [blocks][cols] of dy hh and D fh; NULL: not wanted
+  int pdtype;
+  bool post;
+  bool vec, pvec;
+};
+template <typename T>
+struct BwdIn {
+  const T *dy, *dh, *h, *f;
+  T *dx, *df;
+};
+
+// Wide rows: a block walks each row twice; it keeps its column sums in its own part of the
+// scratch, each of whose elements one thread updates.
+template <typename T>
+__global__ void __launch_bounds__(kT) join_bwd_walk(const BwdIn<T> p, const BwdArgs a) {
+  __shared__ float red[kT / 32];
+  const float inv = 1.0f / float(a.cols);
+  float* pg = a.pg ? a.pg + int64_t(blockIdx.x) * a.cols : nullptr;
+  float* ps = a.ps ? a.ps + int64_t(blockIdx.x) * a.cols : nullptr;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const float rh = p.dy ? a.rstd_pre[r] : 0.0f, rf = a.post ? a.rstd_post[r] : 1.0f;
+    float d[8], hh[8], fh[8], q[8], c[8];
+    auto load = [&](int64_t col, int n) {
+      const bool vec = a.vec && n == 8;
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = hh[i] = fh[i] = q[i] = 0.0f;
+      if (p.dy) {
+        load_row(p.dy + r * a.lddy + col, vec, n, d);
+        load_row(p.h + r * a.ldh + col, vec, n, hh);
+      }
+      if (p.dh) load_row(p.dh + r * a.lddh + col, vec, n, q);
+      if (p.f) load_row(p.f + r * a.ldf + col, vec, n, fh);
+      load_param(a.gamma_pre, a.pdtype, a.pvec, col, n, 1.0f, g);
+      coefs8(a.c, a.pdtype, a.pvec, col, n, c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        hh[i] = i < n ? hh[i] * rh : 0.0f;
+        fh[i] = i < n ? fh[i] * rf : 0.0f;
+        q[i] = i < n ? fmaf(rh, d[i] * g[i], q[i]) : 0.0f;
+        g[i] = d[i] * g[i];
+      }
+      float t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t = fmaf(g[i], hh[i], t);
+      return t;
+    };
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kT * 8) {
+      const int n = a.cols - col > 8 ? 8 : int(a.cols - col);
+      s0 += load(col, n);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float cf = i < n ? c[i] * fh[i] : 0.0f;
+        s1 = fmaf(cf, q[i], s1);
+        s2 = fmaf(cf, hh[i], s2);
+      }
+    }
+    const float m2 = rh * (block_sum(s0, red) * inv);
+    s1 = block_sum(s1, red) * inv, s2 = block_sum(s2, red) * inv;
+    const float m3 = a.post ? fmaf(-m2, s2, s1) : 0.0f;
+    const bool first = r == blockIdx.x;
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += kT * 8) {
+      const int n = a.cols - col > 8 ? 8 : int(a.cols - col);
+      load(col, n);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < n) {
+          q[i] = fmaf(-m2, hh[i], q[i]);
+          if (pg) pg[col + i] = first ? d[i] * hh[i] : fmaf(d[i], hh[i], pg[col + i]);
+          if (ps) ps[col + i] = first ? q[i] * fh[i] : fmaf(q[i], fh[i], ps[col + i]);
+          fh[i] = rf * fmaf(c[i], q[i], -fh[i] * m3);
+        }
+      }
+      if (p.dx) store_row(p.dx + r * a.lddx + col, a.vec && n == 8, n, q);
+      if (p.df) store_row(p.df + r * a.lddf + col, a.vec && n == 8, n, fh);
+    }
+  }
+}
+
+// One row's share of a lane, as in memory.
+template <typename T, int V, int NV>
+struct JoinRow {
+  Row<T, V, NV> dy, dh, h, f;
+  float rh, rf;
+  // r: a row that exists
+  __device__ __forceinline__ void load(const BwdIn<T>& p, const BwdArgs& a, int64_t r,
+                                       const int64_t (&col)[NV], const bool (&in)[NV]) {
+    rh = p.dy ? __ldg(a.rstd_pre + r) : 0.0f, rf = a.post ? __ldg(a.rstd_post + r) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      dy.zero(j), dh.zero(j), h.zero(j), f.zero(j);
+      if (in[j]) {
+        if (p.dy) dy.load(j, p.dy + r * a.lddy + col[j]), h.load(j, p.h + r * a.ldh + col[j]);
+        if (p.dh) dh.load(j, p.dh + r * a.lddh + col[j]);
+        if (p.f) f.load(j, p.f + r * a.ldf + col[j]);
+      }
+    }
+  }
+};
+
+// Rows in registers: a block is NG rows' worth of warps that walk down the rows; a lane
+// keeps its columns' sums, and with PF the next row's loads are in flight while this one is
+// reduced (one barrier per row).
+constexpr int kBwdThreads = 512;
+template <typename T, int V, int NV, int G, bool PF>
+__global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p, const BwdArgs a) {
+  constexpr int C = 32 * G * NV * V, P = NV * V / 2;
+  extern __shared__ float sums[];  // [2][C] when several rows share the block
+  __shared__ float4 red[kBwdThreads / 32][2];  // [warp][parity]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ng = int(blockDim.x) / (32 * G), grp = warp / G, wr = warp % G;
+  const float inv = 1.0f / float(a.cols);
+  int64_t col[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col[j] = (int64_t(wr) * (NV * 32) + j * 32 + lane) * V;
+    in[j] = col[j] < a.cols;
+  }
+  f2 g[P], c[P], ag[P] = {}, as[P] = {};
+  params<V, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  coefs<V, NV>(a.c, a.pdtype, col, in, c);
+  const int64_t step = int64_t(gridDim.x) * ng;
+  int64_t r = int64_t(blockIdx.x) * ng + grp;
+  JoinRow<T, V, NV> cur;
+  if (r < a.rows) cur.load(p, a, r, col, in);
+  int par = 0;
+  for (; r < a.rows; r += step, par ^= 1) {
+    JoinRow<T, V, NV> nxt;
+    if constexpr (PF) nxt.load(p, a, r + step < a.rows ? r + step : r, col, in);
+    const f2 rh = pair(cur.rh), rf = pair(cur.rf);
+    f2 hh[P], fh[P], q[P], t0 = 0, t1 = 0, t2 = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      // zero beyond the row, also where a factor is infinite
+      hh[i] = masked<V, NV>(mul2(cur.h.pair_at(i), rh), i, in);
+      fh[i] = masked<V, NV>(mul2(cur.f.pair_at(i), rf), i, in);
+      const f2 d = cur.dy.pair_at(i), u = mul2(d, g[i]), cf = mul2(c[i], fh[i]);
+      ag[i] = fma2(d, hh[i], ag[i]);
+      q[i] = masked<V, NV>(fma2(rh, u, cur.dh.pair_at(i)), i, in);
+      t0 = fma2(u, hh[i], t0);
+      t1 = fma2(cf, q[i], t1);
+      t2 = fma2(cf, hh[i], t2);
+    }
+    float s0 = lo2(t0) + hi2(t0), s1 = lo2(t1) + hi2(t1), s2 = lo2(t2) + hi2(t2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+      s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+    }
+    if constexpr (G > 1) {
+      if (lane == 0) red[warp][par] = make_float4(s0, s1, s2, 0.0f);
+      group_sync<G>(grp);
+      s0 = s1 = s2 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < G; ++w) {
+        const float4 t = red[grp * G + w][par];
+        s0 += t.x, s1 += t.y, s2 += t.z;
+      }
+    }
+    const float m2 = cur.rh * (s0 * inv);
+    const f2 n2 = pair(-m2), n3 = pair(a.post ? -fmaf(-m2, s2 * inv, s1 * inv) : 0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      q[i] = fma2(n2, hh[i], q[i]);
+      as[i] = fma2(q[i], fh[i], as[i]);
+      fh[i] = mul2(rf, fma2(fh[i], n3, mul2(c[i], q[i])));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j] && p.dx) put<T, V>(p.dx + r * a.lddx + col[j], q, j);
+      if (in[j] && p.df) put<T, V>(p.df + r * a.lddf + col[j], fh, j);
+    }
+    if constexpr (PF) cur = nxt;
+    else if (r + step < a.rows) cur.load(p, a, r + step, col, in);
+  }
+  if (!a.pg && !a.ps) return;  // uniform over the grid
+  float* pg = a.pg ? a.pg + int64_t(blockIdx.x) * a.cols : nullptr;
+  float* ps = a.ps ? a.ps + int64_t(blockIdx.x) * a.cols : nullptr;
+  if (ng > 1) {
+    // group after group into shared memory, in order
+    for (int k = 0; k < ng; ++k) {
+      if (k == grp) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c0 = V == 8 ? int(col[i / 4]) + 2 * (i % 4) : int(col[2 * i % NV]);
+          const int c1 = V == 8 ? c0 + 1 : int(col[(2 * i + 1) % NV]);
+          sums[c0] = (k ? sums[c0] : 0.0f) + lo2(ag[i]);
+          sums[c1] = (k ? sums[c1] : 0.0f) + hi2(ag[i]);
+          sums[C + c0] = (k ? sums[C + c0] : 0.0f) + lo2(as[i]);
+          sums[C + c1] = (k ? sums[C + c1] : 0.0f) + hi2(as[i]);
+        }
+      }
+      __syncthreads();
+    }
+    for (int k = threadIdx.x; k < a.cols; k += blockDim.x) {
+      if (pg) pg[k] = sums[k];
+      if (ps) ps[k] = sums[C + k];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j] && pg) put_sums<V>(pg + col[j], ag, j);
+      if (in[j] && ps) put_sums<V>(ps + col[j], as, j);
+    }
+  }
+}
+
+// The vectors' gradients from the parts of their column sums, in the parts' order: slices of
+// parts j, j + 32, ... by warp, then the slices in pairs.
+struct VecOut {
+  float *dgamma_pre, *dgamma_post, *dgate;
+  Coef c;
+  int pdtype, accumulate;
+};
+__device__ __forceinline__ float param_at(const void* p, int pdtype, int64_t c) {
+  if (!p) return 1.0f;
+  return pdtype == AQFQ_BF16 ? to_f(static_cast<const bf16*>(p)[c]) : static_cast<const float*>(p)[c];
+}
+__device__ __forceinline__ void vector_grads(const VecOut& o, bool pre, int64_t c, float t) {
+  auto put1 = [&](float* out, float v) { out[c] = o.accumulate ? out[c] + v : v; };
+  if (pre) {
+    put1(o.dgamma_pre, t);
+  } else {
+    if (o.dgate) put1(o.dgate, o.c.alpha * (param_at(o.c.gamma_post, o.pdtype, c) * t));
+    if (o.dgamma_post) put1(o.dgamma_post, o.c.alpha * (param_at(o.c.gate, o.pdtype, c) * t));
+  }
+}
+__global__ void __launch_bounds__(1024)
+    join_cols(const float* pg, const float* ps, int parts, int64_t cols, const VecOut o) {
+  constexpr int MOST = (kSms + 31) / 32;
+  __shared__ float red[32][33];
+  const bool pre = o.dgamma_pre && blockIdx.y == 0;
+  const float* src = pre ? pg : ps;
+  const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  float v[MOST], t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    v[i] = c < cols && j + 32 * i < parts ? src[int64_t(j + 32 * i) * cols + c] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) t += v[i];
+  red[j][lane] = t;
+  __syncthreads();
+  t = warp_sum(red[lane][j]);
+  const int64_t cj = int64_t(blockIdx.x) * 32 + j;
+  if (lane == 0 && cj < cols) vector_grads(o, pre, cj, t);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <typename T, int V, int NV, int G, int R>
+cudaError_t run_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaStream_t st) {
+  constexpr int RB = G == 1 ? 4 * R : R;
+  join_fwd_rows<T, V, NV, G, R><<<unsigned((a.rows + RB - 1) / RB), G == 1 ? 128 : 32 * G, 0, st>>>(x, f, h, y, a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaStream_t st) {
+  const int64_t c = a.cols;
+  const bool regs = a.rows <= 0x7FFFFFFF;  // the grid holds a block per (few) rows
+  if (regs && a.vec && a.pvec && c % 8 == 0) {
+    if (c <= 256) return run_fwd<T, 8, 1, 1, 2>(x, f, h, y, a, st);
+    if (c <= 512) return run_fwd<T, 8, 2, 1, 1>(x, f, h, y, a, st);
+    if (c <= 1024) return run_fwd<T, 8, 2, 2, 2>(x, f, h, y, a, st);
+    if (c <= 2048) return run_fwd<T, 8, 2, 4, 2>(x, f, h, y, a, st);
+    if (c <= 4096) return run_fwd<T, 8, 2, 8, 2>(x, f, h, y, a, st);
+    if (c <= 8192) return run_fwd<T, 8, 2, 16, 2>(x, f, h, y, a, st);
+  } else if (regs) {
+    if (c <= 256) return run_fwd<T, 1, 8, 1, 2>(x, f, h, y, a, st);
+    if (c <= 512) return run_fwd<T, 1, 8, 2, 2>(x, f, h, y, a, st);
+    if (c <= 1024) return run_fwd<T, 1, 8, 4, 2>(x, f, h, y, a, st);
+    if (c <= 2048) return run_fwd<T, 1, 8, 8, 2>(x, f, h, y, a, st);
+    if (c <= 4096) return run_fwd<T, 1, 8, 16, 2>(x, f, h, y, a, st);
+    if (c <= 8192) return run_fwd<T, 1, 16, 16, 1>(x, f, h, y, a, st);
+  }
+  const unsigned grid = unsigned(a.rows > 0x7FFFFFFF ? 0x7FFFFFFF : a.rows);
+  join_fwd_walk<T><<<grid, kT, 0, st>>>(x, f, h, y, a);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int NV, int G, bool PF>
+cudaError_t run_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStream_t st) {
+  constexpr int most = kBwdThreads / 32 / G, C = 32 * G * NV * V;
+  int64_t ng = (a.rows + kSms - 1) / kSms;
+  if (ng > most) ng = most;
+  int64_t blocks = (a.rows + ng - 1) / ng;
+  if (blocks > kSms) blocks = kSms;
+  *parts = int(blocks);
+  const size_t smem = ng > 1 && (a.pg || a.ps) ? size_t(2) * C * 4 : 0;  // 32 KiB at most
+  join_bwd_rows<T, V, NV, G, PF><<<unsigned(blocks), unsigned(32 * G * ng), smem, st>>>(p, a);
+  return cudaGetLastError();
+}
+
+// parts: the blocks that wrote column sums
+template <typename T>
+cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStream_t st) {
+  const int64_t c = a.cols;
+  if (a.vec && a.pvec && c % 8 == 0) {
+    if (c <= 256) return run_bwd<T, 8, 1, 1, true>(p, a, parts, st);
+    if (c <= 512) return run_bwd<T, 8, 1, 2, true>(p, a, parts, st);
+    if (c <= 1024) return run_bwd<T, 8, 1, 4, true>(p, a, parts, st);
+    if (c <= 2048) return run_bwd<T, 8, 1, 8, true>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 8, 1, 16, true>(p, a, parts, st);
+    if (c <= 8192) return run_bwd<T, 8, 2, 16, false>(p, a, parts, st);
+  } else {
+    if (c <= 128) return run_bwd<T, 1, 4, 1, true>(p, a, parts, st);
+    if (c <= 512) return run_bwd<T, 1, 4, 4, true>(p, a, parts, st);
+    if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(p, a, parts, st);
+    if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(p, a, parts, st);
+  }
+  const int64_t blocks = a.rows < kSms ? a.rows : kSms;
+  *parts = int(blocks);
+  join_bwd_walk<T><<<unsigned(blocks), kT, 0, st>>>(p, a);
+  return cudaGetLastError();
+}
+
+int64_t most_parts(int64_t rows) { return rows < kSms ? rows : kSms; }
+
+template <typename T>
+cudaError_t forward(const void* x, const void* f, void* h, void* y, const FwdArgs& a, cudaStream_t st) {
+  return launch_fwd(static_cast<const T*>(x), static_cast<const T*>(f), static_cast<T*>(h), static_cast<T*>(y), a, st);
+}
+template <typename T>
+cudaError_t backward(const void* dy, const void* dh, const void* h, const void* f, void* dx, void* df,
+                     const BwdArgs& a, int* parts, cudaStream_t st) {
+  const BwdIn<T> p = {static_cast<const T*>(dy), static_cast<const T*>(dh), static_cast<const T*>(h),
+                      static_cast<const T*>(f), static_cast<T*>(dx), static_cast<T*>(df)};
+  return launch_bwd(p, a, parts, st);
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace aqfq
+
+using namespace aqfq;
+using namespace aqfq::layer;
+
+extern "C" aqfq_status aqfq_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* f,
+                                           int64_t ldf, int64_t rows, int64_t cols, int post,
+                                           int param_dtype, const void* gamma_post, const void* gate,
+                                           float alpha, const void* gamma_pre, float eps, void* h,
+                                           int64_t ldh, void* y, int64_t ldy, float* rstd_post,
+                                           float* rstd_pre, void* stream) {
+  if (cols == 0 || !view_ok(rows, cols, cols) || (x && !view_ok(rows, cols, ldx)) ||
+      (f && !view_ok(rows, cols, ldf)) || (h && !view_ok(rows, cols, ldh)) || (y && !view_ok(rows, cols, ldy)))
+    return AQFQ_ERR_SHAPE;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return AQFQ_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return AQFQ_ERR_UNSUPPORTED;
+  if (rows > 0 && ((!x && !f) || (!h && !y))) return AQFQ_ERR_NULL;
+  // what belongs to a norm that is not taken
+  if (!post && (gamma_post || rstd_post)) return AQFQ_ERR_UNSUPPORTED;
+  if (rows > 0 && !f && (post || gate)) return AQFQ_ERR_NULL;
+  if (rows > 0 && !y && (gamma_pre || rstd_pre)) return AQFQ_ERR_NULL;
+  const int es = esize(dtype), ps = esize(param_dtype);
+  if (!al(x, es) || !al(f, es) || !al(h, es) || !al(y, es) || !al(gamma_post, ps) || !al(gate, ps) ||
+      !al(gamma_pre, ps) || !al(rstd_post, 4) || !al(rstd_pre, 4))
+    return AQFQ_ERR_ALIGN;
+  if (rows == 0) return AQFQ_OK;
+  FwdArgs a = {};
+  a.ldx = ldx, a.ldf = ldf, a.ldh = ldh, a.ldy = ldy, a.rows = rows, a.cols = cols;
+  a.c = {gate, gamma_post, alpha}, a.gamma_pre = gamma_pre, a.pdtype = param_dtype;
+  a.rstd_post = rstd_post, a.rstd_pre = rstd_pre, a.eps = eps, a.post = post != 0;
+  a.vec = rows_aligned<8>(x, ldx, es) && rows_aligned<8>(f, ldf, es) && rows_aligned<8>(h, ldh, es) &&
+          rows_aligned<8>(y, ldy, es);
+  a.pvec = rows_aligned<8>(gamma_post, 8, ps) && rows_aligned<8>(gate, 8, ps) && rows_aligned<8>(gamma_pre, 8, ps);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == AQFQ_BF16 ? forward<bf16>(x, f, h, y, a, st) : forward<float>(x, f, h, y, a, st);
+  return e == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
+}
+
+extern "C" size_t aqfq_block_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!view_ok(rows, cols, cols)) return 0;
+  return size_t(most_parts(rows)) * size_t(cols) * 8;
+}
+
+extern "C" aqfq_status aqfq_block_norm_bwd(int dtype, const void* dy, int64_t lddy, const void* dh,
+                                           int64_t lddh, const void* h, int64_t ldh, const void* f,
+                                           int64_t ldf, int64_t rows, int64_t cols,
+                                           const float* rstd_post, const float* rstd_pre,
+                                           int param_dtype, const void* gamma_post, const void* gate,
+                                           float alpha, const void* gamma_pre, void* dx, int64_t lddx,
+                                           void* df, int64_t lddf, float* dgamma_post, float* dgate,
+                                           float* dgamma_pre, int accumulate, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (cols == 0 || !view_ok(rows, cols, cols) || (dy && (!view_ok(rows, cols, lddy) || !view_ok(rows, cols, ldh))) ||
+      (dh && !view_ok(rows, cols, lddh)) || (f && !view_ok(rows, cols, ldf)) ||
+      (dx && !view_ok(rows, cols, lddx)) || (df && !view_ok(rows, cols, lddf)))
+    return AQFQ_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return AQFQ_ERR_UNSUPPORTED;
+  const bool outs = dgamma_post || dgate || dgamma_pre;
+  if (rows > 0 && !dx && !df && !outs) return AQFQ_ERR_NULL;
+  if (rows > 0 && ((!dy && !dh) || (dy && (!h || !rstd_pre)))) return AQFQ_ERR_NULL;
+  if (rows > 0 && !dy && (dgamma_pre || gamma_pre)) return AQFQ_ERR_NULL;
+  if (rows > 0 && !f && (df || dgate || dgamma_post || rstd_post || gate)) return AQFQ_ERR_NULL;
+  if (rows > 0 && !rstd_post && (gamma_post || dgamma_post)) return AQFQ_ERR_UNSUPPORTED;
+  const int es = esize(dtype), ps = esize(param_dtype);
+  if (!al(dy, es) || !al(dh, es) || !al(h, es) || !al(f, es) || !al(dx, es) || !al(df, es) ||
+      !al(gamma_post, ps) || !al(gate, ps) || !al(gamma_pre, ps) || !al(rstd_post, 4) || !al(rstd_pre, 4) ||
+      !al(dgamma_post, 4) || !al(dgate, 4) || !al(dgamma_pre, 4))
+    return AQFQ_ERR_ALIGN;
+  const size_t need = aqfq_block_norm_bwd_workspace_bytes(rows, cols);
+  if (outs && need > 0) {
+    if (!workspace || workspace_bytes < need) return AQFQ_ERR_WORKSPACE;
+    if (!al(workspace, 8)) return AQFQ_ERR_ALIGN;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  BwdArgs a = {};
+  const bool wants_s = dgamma_post || dgate;
+  int parts = 0;
+  const VecOut o = {dgamma_pre, dgamma_post, dgate, {gate, gamma_post, alpha}, param_dtype, accumulate};
+  if (rows > 0) {
+    a.lddy = lddy, a.lddh = lddh, a.ldh = ldh, a.ldf = ldf, a.lddx = lddx, a.lddf = lddf;
+    a.rows = rows, a.cols = cols, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre, a.post = rstd_post != nullptr;
+    a.c = o.c, a.gamma_pre = gamma_pre, a.pdtype = param_dtype;
+    float* part = static_cast<float*>(workspace);
+    a.pg = dgamma_pre ? part : nullptr;
+    a.ps = wants_s ? part + size_t(most_parts(rows)) * size_t(cols) : nullptr;
+    a.vec = rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dh, lddh, es) && (!dy || rows_aligned<8>(h, ldh, es)) &&
+            rows_aligned<8>(f, ldf, es) && rows_aligned<8>(dx, lddx, es) && rows_aligned<8>(df, lddf, es);
+    a.pvec = rows_aligned<8>(gamma_post, 8, ps) && rows_aligned<8>(gate, 8, ps) && rows_aligned<8>(gamma_pre, 8, ps);
+    const cudaError_t e = dtype == AQFQ_BF16 ? backward<bf16>(dy, dh, h, f, dx, df, a, &parts, st)
+                                             : backward<float>(dy, dh, h, f, dx, df, a, &parts, st);
+    if (e != cudaSuccess) return AQFQ_ERR_CUDA;
+  }
+  if (outs && (rows > 0 || !accumulate)) {
+    const float* pg = dgamma_pre ? static_cast<const float*>(workspace) : nullptr;
+    const float* ps2 = wants_s ? static_cast<const float*>(workspace) + size_t(most_parts(rows)) * size_t(cols) : nullptr;
+    join_cols<<<dim3(unsigned((cols + 31) / 32), (dgamma_pre ? 1 : 0) + (wants_s ? 1 : 0)), 1024, 0, st>>>(
+        pg, ps2, parts, cols, o);
+    if (cudaGetLastError() != cudaSuccess) return AQFQ_ERR_CUDA;
+  }
+  return AQFQ_OK;
+}

@@ -1,0 +1,187 @@
+// aqfq_rows.cuh -- pieces shared by the kernels that normalise rows (layer norm, the norms
+// between two blocks): sums over warps, groups and blocks, a lane's parameters, and the
+// ring of shared-memory stages that bulk asynchronous copies fill.
+#pragma once
+
+#include "aqfq_internal.h"
+#include "aqfq_layer.cuh"
+#include "aqfq_sm100_pair.cuh"
+
+namespace aqfq {
+namespace layer {
+
+constexpr int kT = 256;    // threads of a block that walks a row
+constexpr int kSms = 152;  // of a GB300: grids and the workspace's size; the results do not need it
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// sum over the block, the same value in every thread
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  __syncthreads();  // red is free
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) t += red[w];
+  return t;
+}
+
+// gamma / beta: columns [col, col + 8) of a vector of either type; NULL gives `def`
+__device__ __forceinline__ void load_param(const void* p, int pdtype, bool vec, int64_t col, int n,
+                                           float def, float (&v)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = def;
+  } else if (pdtype == AQFQ_BF16) {
+    load_row(static_cast<const bf16*>(p) + col, vec && n == 8, n, v);
+  } else {
+    load_row(static_cast<const float*>(p) + col, vec && n == 8, n, v);
+  }
+}
+
+// V parameters as pairs
+template <int V, int NV>
+__device__ __forceinline__ void params(const void* p, int pdtype, const int64_t (&col)[NV],
+                                       const bool (&in)[NV], float def, f2 (&v)[NV * V / 2]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = pair(def);
+  } else if (pdtype == AQFQ_BF16) {
+    Row<bf16, V, NV> w;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j]) w.load(j, static_cast<const bf16*>(p) + col[j]);
+      else w.zero(j);
+    }
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
+  } else {
+    Row<float, V, NV> w;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j]) w.load(j, static_cast<const float*>(p) + col[j]);
+      else w.zero(j);
+    }
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
+  }
+}
+// whether pair i's elements lie in the row (V = 1: each on its own)
+template <int V, int NV>
+__device__ __forceinline__ f2 masked(f2 v, int i, const bool (&in)[NV]) {
+  if constexpr (V == 8) return in[i / 4] ? v : 0ull;
+  else return mk2(in[2 * i] ? lo2(v) : 0.0f, in[2 * i + 1] ? hi2(v) : 0.0f);
+}
+
+// a lane's vector j of column sums to scratch, which the caller aligns to 8 bytes only
+template <int V>
+__device__ __forceinline__ void put_sums(float* p, const f2* v, int j) {
+  if constexpr (V == 1) {
+    put<float, 1>(p, v, j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) *reinterpret_cast<f2*>(p + 2 * i) = v[j * (V / 2) + i];
+  }
+}
+
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 200 * 1024;  // per SM
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+template <int G>
+__device__ __forceinline__ void group_sync(int grp) {
+  if constexpr (G == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * G) : "memory");
+}
+// pairs of V = 8 vectors of a row in shared memory
+// (MASK: zeros where the vector lies beyond the row)
+template <bool MASK, typename T, int NV>
+__device__ __forceinline__ void smem_pairs(const uint8_t* row, const int (&col)[NV], const bool (&in)[NV],
+                                           f2 (&v)[NV * 4]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + col[j] * int(sizeof(T)));
+    uint4 a = p[0];
+    if (MASK && !in[j]) a = make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(T) == 2) {
+      v[4 * j] = bf2(a.x), v[4 * j + 1] = bf2(a.y), v[4 * j + 2] = bf2(a.z), v[4 * j + 3] = bf2(a.w);
+    } else {
+      uint4 b = p[1];
+      if (MASK && !in[j]) b = make_uint4(0, 0, 0, 0);
+      v[4 * j] = mk2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[4 * j + 1] = mk2(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[4 * j + 2] = mk2(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[4 * j + 3] = mk2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+  }
+}
+
+// Loads on their way when a wait for row r gives up: the rows left, at most one per stage, and
+// after the first turn the stage of the row before r has not been refilled yet.
+__device__ __forceinline__ int64_t in_flight(int stages, bool first, int64_t r, int64_t step, int64_t rows) {
+  const int64_t left = (rows - r + step - 1) / step, most = first ? stages : stages - 1;
+  return left < most ? left : most;
+}
+
+struct RingArgs {
+  int stages, stage_bytes;  // per group
+  int row_bytes;            // of a tensor's row; a multiple of 16
+};
+
+// sums of two values over a group: half a warp carries each of them, so that five
+// exchanges serve both; the totals of every warp through red[2][G]
+template <int G>
+__device__ __forceinline__ void group_sum2(float (&s)[2], float* red, int grp) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane >= 16;
+  float t = (up ? s[1] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? s[0] : s[1], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  if constexpr (G == 1) {
+    s[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
+    s[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
+    group_sync<G>(grp);
+  } else {
+    if ((lane & 15) == 0) red[(up ? G : 0) + (threadIdx.x >> 5) % G] = t;
+    group_sync<G>(grp);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f2* p = reinterpret_cast<const f2*>(red + k * G);
+      f2 u = p[0];
+#pragma unroll
+      for (int w = 1; w < G / 2; ++w) u = add2(u, p[w]);
+      s[k] = lo2(u) + hi2(u);
+    }
+  }
+}
+
+// the ring's stages for `groups` groups in `bytes` of shared memory; fewer than 3: no ring
+inline RingArgs make_ring(int stage_bytes, int row_bytes, int groups, int bytes) {
+  RingArgs q;
+  q.stage_bytes = (stage_bytes + 127) / 128 * 128;
+  q.row_bytes = row_bytes;
+  q.stages = bytes / (groups * q.stage_bytes);
+  if (q.stages > kMaxStages) q.stages = kMaxStages;
+  return q;
+}
+
+template <typename K>
+inline cudaError_t ring_smem(DeviceOnce& once, K kernel) {
+  return once_per_device(once, [=] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  });
+}
+
+}  // namespace layer
+}  // namespace aqfq

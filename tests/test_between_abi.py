@@ -95,3 +95,75 @@ def test_rotary_binding_checks():
         aqfq.aqfq_rotary(q, pos, freqs, torch.empty_like(q))
     with pytest.raises(ValueError, match="heads"):
         aqfq.aqfq_rotary(q[0], pos, freqs, q)
+
+
+# ---- norms, gate and residual between two blocks ---------------------------------------
+
+def jfwd(L, dtype=0, x=A, ldx=64, f=2 * A, ldf=64, R=4, C=64, post=1, pd=0, gp=A, gate=A, gn=A, eps=1e-6,
+         h=3 * A, ldh=64, y=4 * A, ldy=64, rp=A, rq=A):
+    return L.aqfq_block_norm_fwd(dtype, x, ldx, f, ldf, R, C, post, pd, gp, gate, 1.0, gn, eps, h, ldh, y, ldy,
+                                 rp, rq, None)
+
+
+def test_block_norm_fwd_checks(L):
+    assert jfwd(L, dtype=2) == UNSUP and jfwd(L, pd=-1) == UNSUP
+    assert jfwd(L, C=0) == SHAPE and jfwd(L, C=-1) == SHAPE and jfwd(L, R=-1) == SHAPE
+    for ld in ("ldx", "ldf", "ldh", "ldy"):
+        assert jfwd(L, **{ld: 63}) == SHAPE
+    for eps in (-1.0, float("nan"), float("inf")):
+        assert jfwd(L, eps=eps) == SHAPE
+    assert jfwd(L, x=None, f=None, post=0, gp=None, gate=None, rp=None) == NULL
+    assert jfwd(L, h=None, y=None) == NULL
+    assert jfwd(L, y=None) == NULL and jfwd(L, y=None, gn=None) == NULL     # a norm that is not taken
+    assert jfwd(L, post=0) == UNSUP and jfwd(L, post=0, gp=None) == UNSUP and jfwd(L, post=0, rp=None) == UNSUP
+    assert jfwd(L, f=None) == NULL and jfwd(L, f=None, post=0, gp=None, rp=None) == NULL
+    for p in ("x", "f", "h", "y"):
+        assert jfwd(L, **{p: A + 1}) == ALIGN and jfwd(L, dtype=1, **{p: A + 2}) == ALIGN
+    for p in ("gp", "gate", "gn"):
+        assert jfwd(L, **{p: A + 1}) == ALIGN and jfwd(L, pd=1, **{p: A + 2}) == ALIGN
+    assert jfwd(L, rp=A + 2) == ALIGN and jfwd(L, rq=A + 2) == ALIGN
+    assert jfwd(L, R=0, x=None, f=None, h=None, y=None) == OK
+
+
+def jbwd(L, dtype=0, dy=A, lddy=64, dh=A, lddh=64, h=A, ldh=64, f=A, ldf=64, R=64, C=64, rp=A, rq=A, pd=0, gp=A,
+         gate=A, gn=A, dx=2 * A, lddx=64, df=3 * A, lddf=64, dgp=None, dga=None, dgn=None, ws=None, wsb=0):
+    return L.aqfq_block_norm_bwd(dtype, dy, lddy, dh, lddh, h, ldh, f, ldf, R, C, rp, rq, pd, gp, gate, 1.0, gn,
+                                 dx, lddx, df, lddf, dgp, dga, dgn, 0, ws, wsb, None)
+
+
+def test_block_norm_bwd_checks(L):
+    assert jbwd(L, dtype=3) == UNSUP and jbwd(L, pd=2) == UNSUP
+    assert jbwd(L, C=0) == SHAPE and jbwd(L, R=-1) == SHAPE
+    for ld in ("lddy", "lddh", "ldh", "ldf", "lddx", "lddf"):
+        assert jbwd(L, **{ld: 63}) == SHAPE
+    assert jbwd(L, dx=None, df=None) == NULL
+    assert jbwd(L, dy=None, dh=None) == NULL
+    assert jbwd(L, h=None) == NULL and jbwd(L, rq=None) == NULL
+    assert jbwd(L, dy=None) == NULL and jbwd(L, dy=None, gn=None, dgn=A, ws=A, wsb=1 << 20) == NULL
+    assert jbwd(L, f=None) == NULL and jbwd(L, f=None, df=None, rp=None, gp=None) == NULL
+    assert jbwd(L, f=None, df=None, rp=None, gp=None, gate=None, dga=A, ws=A, wsb=1 << 20) == NULL
+    assert jbwd(L, rp=None) == UNSUP and jbwd(L, rp=None, gp=None, dgp=A, ws=A, wsb=1 << 20) == UNSUP
+    for p in ("dy", "dh", "h", "f", "dx", "df"):
+        assert jbwd(L, **{p: A + 1}) == ALIGN
+    for p in ("gp", "gate", "gn"):
+        assert jbwd(L, **{p: A + 1}) == ALIGN
+    need = aqfq.aqfq_block_norm_bwd_workspace_bytes(64, 64)
+    assert need > 0
+    for p in ("dgp", "dga", "dgn"):
+        assert jbwd(L, **{p: A + 2}, ws=A, wsb=need) == ALIGN
+        assert jbwd(L, **{p: A}) == WS and jbwd(L, **{p: A}, ws=A, wsb=need - 1) == WS
+        assert jbwd(L, **{p: A}, ws=A + 4, wsb=need) == ALIGN
+    assert jbwd(L, R=0, dy=None, dh=None, h=None, f=None, rp=None, rq=None, dx=None, df=None) == OK
+    assert (aqfq.aqfq_block_norm_bwd_workspace_bytes(10 ** 7, 64)
+            == aqfq.aqfq_block_norm_bwd_workspace_bytes(10 ** 8, 64))
+    assert aqfq.aqfq_block_norm_bwd_workspace_bytes(-1, 64) == 0
+
+
+def test_block_norm_binding_checks():
+    t = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        aqfq.aqfq_block_norm_fwd(t, t, 1e-6, h=t)
+    with pytest.raises(ValueError, match="missing"):
+        aqfq.aqfq_block_norm_fwd(None, None, 1e-6, h=t)
+    with pytest.raises(ValueError, match="missing"):
+        aqfq.aqfq_block_norm_bwd(None, None, t, t, dx=t)
