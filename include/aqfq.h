@@ -470,7 +470,7 @@ aqfq_status aqfq_layernorm_bwd(int dtype, const void* dy, int64_t lddy, const vo
  *                kernel timed out (the output is then incomplete); never cleared
  * Limits: M, N, K < 2^30, the axis that is summed over at most 2^26, leading
  * dimensions of x, w and dy below 2^38. */
-enum { AQFQ_LINEAR_FWD = 0, AQFQ_LINEAR_DGRAD = 1, AQFQ_LINEAR_WGRAD = 2 };
+enum { AQFQ_LINEAR_FWD = 0, AQFQ_LINEAR_DGRAD = 1, AQFQ_LINEAR_WGRAD = 2, AQFQ_LINEAR_GATED = 3 };
 size_t aqfq_linear_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K);
 aqfq_status aqfq_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
                             int64_t N, int64_t K, int bias_dtype, const void* bias, int act,
@@ -582,6 +582,40 @@ aqfq_status aqfq_block_norm_bwd(int dtype, const void* dy, int64_t lddy, const v
                                 float* dgamma_post, float* dgate, float* dgamma_pre, int accumulate,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated feed-forward product, W [2N, K] gate's rows, then up's (a stack that is
+ * quantized as one weight), x [M, K] (BF16, products accumulated in FP32):
+ *   forward      g = x Wg^T, u = x Wu^T;  y = act(g) u (BF16 [M, N]); with gate and
+ *                up, g and u (unrounded) are also kept in 8 bits
+ *   gradient     through the next product W [N, K] (z = y W^T, dy [M, N] the
+ *                gradient of z) and the gate:  with s = dy W and g, u the kept values
+ *                dp[:, :K] = s u act'(g), dp[:, K:] = s act(g)  (BF16 [M, 2K])
+ *                y = act(g) u recomputed (BF16 [M, K], optional)
+ *                dp is then dy of aqfq_linear_dgrad and aqfq_linear_wgrad with the
+ *                stacked weight
+ *   gate, up     checkpoints of [M, N] (gradient: [M, K]) of one format and group, both
+ *                or (forward) neither
+ *   workspace    device, aqfq_gated_workspace_bytes(pass, M, N, K) bytes (pass
+ *                AQFQ_LINEAR_FWD or AQFQ_LINEAR_DGRAD), 16-byte aligned
+ * Everything else, the limits too, as for the linear products; 2N < 2^30. */
+size_t aqfq_gated_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K);
+aqfq_status aqfq_gated_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N,
+                           int64_t K, int act, void* y, int64_t ldy, const aqfq_ckpt8* gate,
+                           const aqfq_ckpt8* up, void* workspace, size_t workspace_bytes,
+                           int32_t* error_flag, void* stream);
+aqfq_status aqfq_gated_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t M,
+                             int64_t N, int64_t K, int act, const aqfq_ckpt8* gate,
+                             const aqfq_ckpt8* up, void* dp, int64_t lddp, void* y, int64_t ldy,
+                             void* workspace, size_t workspace_bytes, int32_t* error_flag,
+                             void* stream);
+
+/* The same gradient from the gradient dy [rows, cols] of y = act(g) u itself (where y
+ * is quantized before the next product):  dp[:, :cols] = dy u act'(g), dp[:, cols:] =
+ * dy act(g) [rows, 2 cols], y = act(g) u [rows, cols]; dp and y are of dtype, each may
+ * be NULL, not both (dy may be NULL without dp). */
+aqfq_status aqfq_ckpt8_gated_bwd(const aqfq_ckpt8* gate, const aqfq_ckpt8* up, int act, int dtype,
+                                 const void* dy, int64_t lddy, int64_t rows, int64_t cols, void* dp,
+                                 int64_t lddp, void* y, int64_t ldy, void* stream);
+
 /* Diagnostic (the pages have no counterpart): checks the bounded-wait path
  * that the GEMM's pipeline uses when a stage never arrives.  One thread waits
  * on an mbarrier phase that nothing completes, polling at most `polls` times
@@ -592,7 +626,8 @@ aqfq_status aqfq_selftest_wait_timeout(int32_t* flag, uint32_t polls, void* stre
 
 /* Diagnostics (host only, no counterpart in the pages): which kernel a size takes, so
  * that a test of a kernel can tell that its sizes reach it.
- * aqfq_selftest_linear_plan: plan[0] = 0 (empty sum), 1 (128 x 128 tiles, one CTA each)
+ * aqfq_selftest_linear_plan (AQFQ_LINEAR_GATED: aqfq_gated_fwd; the gradient of the gated
+ * product is cut as AQFQ_LINEAR_DGRAD): plan[0] = 0 (empty sum), 1 (128 x 128 tiles, one CTA each)
  * or 2 (256 x 256 tiles on pairs of CTAs); plan[1] = slices of the inner axis; plan[2] =
  * tiles of the last round that a second launch splits; plan[3] = into how many slices.
  * aqfq_selftest_layernorm_ring: warps per row of the ring kernel that serves aligned

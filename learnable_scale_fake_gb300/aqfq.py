@@ -25,7 +25,7 @@ SCALE_LEARNED, SCALE_DYNAMIC_BLOCK = 0, 1
 KD_KL, KD_RKL, KD_CAKLD, KD_MSE = 0, 1, 2, 3
 BF16, F32 = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
-LINEAR_FWD, LINEAR_DGRAD, LINEAR_WGRAD = 0, 1, 2
+LINEAR_FWD, LINEAR_DGRAD, LINEAR_WGRAD, LINEAR_GATED = 0, 1, 2, 3
 ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_PARTS = 0, 1, 2, 3
 
@@ -42,7 +42,8 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_layernorm_bwd_workspace_bytes", "aqfq_linear_fwd", "aqfq_linear_dgrad",
            "aqfq_linear_wgrad", "aqfq_linear_workspace_bytes",
            "aqfq_rotary", "aqfq_rotary_freqs", "aqfq_block_norm_fwd", "aqfq_block_norm_bwd",
-           "aqfq_block_norm_bwd_workspace_bytes",
+           "aqfq_block_norm_bwd_workspace_bytes", "aqfq_gated_fwd", "aqfq_gated_dgrad",
+           "aqfq_gated_workspace_bytes", "aqfq_ckpt8_gated_bwd",
            "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_selftest_linear_plan",
            "aqfq_selftest_layernorm_ring", "aqfq_status_string",
            "aqfq_version")
@@ -129,6 +130,11 @@ def lib():
                 "aqfq_block_norm_bwd": (i32, [i32, P, i64, P, i64, P, i64, P, i64, i64, i64, P, P, i32, P, P,
                                               f32, P, P, i64, P, i64, P, P, P, i32, P, sz, P]),
                 "aqfq_block_norm_bwd_workspace_bytes": (sz, [i64, i64]),
+                "aqfq_gated_fwd": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, i64, P, P, P, sz, P, P]),
+                "aqfq_gated_dgrad": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, P, P, i64, P, i64, P, sz, P,
+                                           P]),
+                "aqfq_gated_workspace_bytes": (sz, [i32, i64, i64, i64]),
+                "aqfq_ckpt8_gated_bwd": (i32, [P, P, i32, i32, P, i64, i64, i64, P, i64, P, i64, P]),
                 "aqfq_selftest_wait_timeout": (i32, [P, ctypes.c_uint32, P]),
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
                 "aqfq_selftest_linear_plan": (i32, [i32, i64, i64, i64, P]),
@@ -727,6 +733,62 @@ def aqfq_block_norm_bwd(dy, dh, h, f, rstd_post=None, rstd_pre=None, gamma_post=
         _stream_on(stream, dev))
     if st:
         _check("aqfq_block_norm_bwd", st)
+
+
+def aqfq_gated_workspace_bytes(kind, M, N, K) -> int:
+    """kind LINEAR_FWD (x [M, K], w [2N, K]) or LINEAR_DGRAD (dy [M, N], w [N, K])."""
+    return int(lib().aqfq_gated_workspace_bytes(int(kind), int(M), int(N), int(K)))
+
+
+def aqfq_gated_fwd(x, w, y, act=ACT_SILU, gate=None, up=None, workspace=None, error_flag=None, stream=None):
+    """y = act(x @ w[:N].T) * (x @ w[N:].T); gate and up keep the two products in 8 bits."""
+    px, ldx = _mat(x, "x", _BF)
+    dev = x.get_device()
+    M, K = x.shape
+    N = y.shape[1]
+    pw, ldw = _mat(w, "w", _BF, (2 * N, K), dev)
+    py, ldy = _mat(y, "y", _BF, (M, N), dev)
+    ws, wsb = _ws(workspace, dev)
+    st = (_lib or lib()).aqfq_gated_fwd(
+        px, ldx, pw, ldw, M, N, K, int(act), py, ldy, _ck(gate, M, N, dev), _ck(up, M, N, dev), ws, wsb,
+        _flag(error_flag, dev), _stream_on(stream, dev))
+    if st:
+        _check("aqfq_gated_fwd", st)
+
+
+def aqfq_gated_dgrad(dy, w, dp, gate, up, act=ACT_SILU, y=None, workspace=None, error_flag=None, stream=None):
+    """With s = dy @ w and g, u [M, K] kept in gate and up: dp = [s u act'(g), s act(g)] [M, 2K] and
+    y = act(g) u."""
+    pd, ldd = _mat(dy, "dy", _BF)
+    dev = dy.get_device()
+    M, N = dy.shape
+    K = w.shape[1]
+    pw, ldw = _mat(w, "w", _BF, (N, K), dev)
+    po, ldo = _mat(dp, "dp", _BF, (M, 2 * K), dev)
+    py, ldy = _mat(y, "y", _BF, (M, K), dev)
+    ws, wsb = _ws(workspace, dev)
+    st = (_lib or lib()).aqfq_gated_dgrad(
+        pd, ldd, pw, ldw, M, N, K, int(act), _ck(gate, M, K, dev), _ck(up, M, K, dev), po, ldo, py, ldy, ws,
+        wsb, _flag(error_flag, dev), _stream_on(stream, dev))
+    if st:
+        _check("aqfq_gated_dgrad", st)
+
+
+def aqfq_ckpt8_gated_bwd(gate, up, act, dy, dp=None, y=None, stream=None):
+    """dp = [dy u act'(g), dy act(g)] and y = act(g) u for the g, u [rows, cols] kept in gate and up; dy
+    may be None without dp."""
+    R, C = gate.size
+    dev = gate.device
+    a = dy if dy is not None else y if y is not None else dp
+    dt = _ROWS if a is None else (a.dtype,) if a.dtype in _ROWS else _ROWS
+    pd, ldd = _mat(dy, "dy", dt, (R, C), dev)
+    pp, ldp = _mat(dp, "dp", dt, (R, 2 * C), dev)
+    py, ldy = _mat(y, "y", dt, (R, C), dev)
+    st = (_lib or lib()).aqfq_ckpt8_gated_bwd(
+        _ck(gate, R, C, dev), _ck(up, R, C, dev), int(act), _dt(a), pd, ldd, R, C, pp, ldp, py, ldy,
+        _stream_on(stream, dev))
+    if st:
+        _check("aqfq_ckpt8_gated_bwd", st)
 
 
 def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:

@@ -254,6 +254,57 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
+// Gate and up kept in 8 bits: dg = dy u act'(g), du = dy act(g), y = act(g) u.
+template <typename T, int V, int ACT, int U>
+__global__ void __launch_bounds__(kWarps * 32)
+    gated_bwd_kernel(const Ckpt cg, const Ckpt cu, const T* dy, int64_t lddy, int64_t rows, int64_t cols, int lr,
+                     T* dg, T* du, int64_t lddp, T* y, int64_t ldy) {
+  constexpr int NV = Lane<V>::NV, P = NV * V / 2;
+  const Lane<V> l = lane_of<V>(lr, cols);
+  for (int64_t r = l.row; r < rows; r += l.step * U) {
+    Row<T, V, NV> raw[U];
+    CodeRow<V, NV> wg[U], wu[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t ru = r + k * l.step < rows ? r + k * l.step : rows - 1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (dg) raw[k].load(j, dy + ru * lddy + l.col[j]);
+        wg[k].load(j, cg, ru, cols, l.col[j]);
+        wu[k].load(j, cu, ru, cols, l.col[j]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t ru = r + k * l.step;
+      if (ru >= rows) break;
+      f2 g[P], u[P], d[P];
+      wg[k].values(cg.fmt, g);
+      wu[k].values(cu.fmt, u);
+#pragma unroll
+      for (int i = 0; i < P; ++i) d[i] = dg ? mul2(raw[k].pair_at(i), u[i]) : 0ull;
+      slope_all<ACT, sizeof(T) == 4>(g, d);  // g becomes act(g)
+      if (dg) {
+        f2 e[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) e[i] = mul2(raw[k].pair_at(i), g[i]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (l.in[j]) put<T, V>(dg + ru * lddp + l.col[j], d, j);
+          if (l.in[j]) put<T, V>(du + ru * lddp + l.col[j], e, j);
+        }
+      }
+      if (y) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) u[i] = mul2(u[i], g[i]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (l.in[j]) put<T, V>(y + ru * ldy + l.col[j], u, j);
+      }
+    }
+  }
+}
+
 // 32 columns x 32 slices per block: slice j adds the parts j, j + 32, ... in
 // order, then the slices are added pairwise.  At most ten parts per slice, all of
 // them under way at once.
@@ -487,4 +538,41 @@ extern "C" aqfq_status aqfq_ckpt8_act_bwd(const aqfq_ckpt8* ckpt, int act, int d
       launch_part_sums(part, nullptr, int(m.gy), cols, dbias, nullptr, accumulate, st) != cudaSuccess)
     return AQFQ_ERR_CUDA;
   return AQFQ_OK;
+}
+
+extern "C" aqfq_status aqfq_ckpt8_gated_bwd(const aqfq_ckpt8* gate, const aqfq_ckpt8* up, int act, int dtype,
+                                            const void* dy, int64_t lddy, int64_t rows, int64_t cols, void* dp,
+                                            int64_t lddp, void* y, int64_t ldy, void* stream) {
+  Ckpt cg = {}, cu = {};
+  if (!view_ok(rows, cols, cols) || (dy && !view_ok(rows, cols, lddy)) || (y && !view_ok(rows, cols, ldy)) ||
+      cols > 0x3FFFFFF8 || (dp && !view_ok(rows, 2 * cols, lddp)))
+    return AQFQ_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !act_ok(act)) return AQFQ_ERR_UNSUPPORTED;
+  aqfq_status s = make_ckpt(gate, rows, cols, cg);
+  if (s == AQFQ_OK) s = make_ckpt(up, rows, cols, cu);
+  if (s != AQFQ_OK) return s;
+  if (cg.fmt != cu.fmt || cg.lg != cu.lg) return AQFQ_ERR_UNSUPPORTED;
+  const bool any = rows > 0 && cols > 0;
+  if (any && ((!dp && !y) || (dp && !dy))) return AQFQ_ERR_NULL;
+  const int es = esize(dtype);
+  if (!al(dy, es) || !al(dp, es) || !al(y, es)) return AQFQ_ERR_ALIGN;
+  if (!any) return AQFQ_OK;
+  if (sm_count() <= 0) return AQFQ_ERR_CUDA;
+  const int vec = cols % 8 == 0 && rows_aligned<8>(dy, lddy, es) && rows_aligned<8>(dp, lddp, es) &&
+                          rows_aligned<8>(y, ldy, es) && al(cg.codes, 8) && al(cu.codes, 8)
+                      ? 8
+                      : 1;
+  const Map m = make_map(rows, cols, cg.lg, vec, 65535);
+  by_act(act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    by_type(dtype, vec, [&](auto t, auto v) {
+      using T = typename decltype(t)::type;
+      constexpr int V = decltype(v)::value;
+      T* out = static_cast<T*>(dp);
+      gated_bwd_kernel<T, V, ACT, kUB><<<dim3(m.gx, m.gy), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+          cg, cu, static_cast<const T*>(dy), lddy, rows, cols, m.lr, out, out ? out + cols : nullptr, lddp,
+          static_cast<T*>(y), ldy);
+    });
+  });
+  return done();
 }

@@ -4,11 +4,16 @@
 //   forward       y = act(p) (+ res),  p = x W^T + b   (p optionally kept in 8 bits)
 //   input grad    dx = (dy W) act'(p') (+ res)         (p' from its 8-bit checkpoint)
 //   weight grad   dw = dy^T x (+ dw)
+//   gated         y = act(g) u,  g = x Wg^T, u = x Wu^T  (g and u optionally kept in 8 bits)
+//   gated grad    with s = dy W: dg = s u act'(g), du = s act(g), y = act(g) u  (from the kept g, u)
 //
-// All three are out[r, c] = sum over k of A(r, k) B(c, k) with other strides:
+// All of them are out[r, c] = sum over k of A(r, k) B(c, k) with other strides:
 //   forward       r = m, c = n, k = k:  A = x (k contiguous), B = W (k contiguous)
 //   input grad    r = m, c = k, k = n:  A = dy (n contiguous), B = W (c contiguous)
 //   weight grad   r = n, c = k, k = m:  A = dy (r contiguous), B = x (c contiguous)
+// The gated product is the forward one with the rows of Wg and of Wu, 128 and 128, as the
+// columns of one tile, so that g and u of an output meet in one lane; the gated gradient is
+// the input gradient with another epilogue.
 //
 // Products of BF16 are exact in binary32 and their sums are held in it.  Over 3680 terms the
 // tensor cores' sums measured 4e-6 off (2-norm, relative), a blocked sum of FMAs 6e-7: far
@@ -25,7 +30,15 @@ namespace aqfq {
 namespace layer {
 namespace {
 
-enum Pass { P_FWD = AQFQ_LINEAR_FWD, P_DGRAD = AQFQ_LINEAR_DGRAD, P_WGRAD = AQFQ_LINEAR_WGRAD };
+enum Pass {
+  P_FWD = AQFQ_LINEAR_FWD,
+  P_DGRAD = AQFQ_LINEAR_DGRAD,
+  P_WGRAD = AQFQ_LINEAR_WGRAD,
+  P_GATED,        // forward, gate and up
+  P_GATED_DGRAD,  // input gradient through a gate
+};
+// whether the column operand's rows are the tile's columns (k contiguous)
+constexpr bool k_major(int pass) { return pass == P_FWD || pass == P_GATED; }
 
 // ---------------------------------------------------------------------------
 // epilogue of sums in memory: 16 lanes hold 128 columns of a row, a lane 8 of them, a
@@ -44,6 +57,11 @@ struct Epi {
   bool vec_out, vec_res, vec_bias, vec_codes;  // 8-element accesses are aligned
   bool wide;            // 16-element accesses (32 bytes) of out and res, 16 of codes
   Ckpt c;               // forward: written; input gradient: read
+  // gated passes: c and c2 are gate's and up's; the gradient has dg in out, du in out2 and
+  // act(g) u in hidden (may be NULL)
+  Ckpt c2;
+  bf16 *out2, *hidden;
+  int64_t ldh;
 };
 
 // columns of [col, col + V) that lie in the row
@@ -131,6 +149,67 @@ __device__ __forceinline__ void epilogue8(const Epi& e, int64_t r, bool in, int6
     store_row(static_cast<float*>(e.out) + r * e.ldo + col, e.vec_out && full, n, v);
   else
     store_row(static_cast<bf16*>(e.out) + r * e.ldo + col, e.vec_out && full, n, v);
+}
+
+// 8 codes and their values in row r, columns [col, col + 8)
+__device__ __forceinline__ void kept8(const Epi& e, const Ckpt& c, int64_t r, int64_t col, int n, float (&p)[8]) {
+  uint32_t w[2];
+  load_bytes<8>(c.codes + r * e.cols + col, e.vec_codes && n == 8, n, w);
+  const float s = c.scale[r * c.groups + (col >> c.lg)];
+  ckpt_values4(w[0], s, c.fmt, p);
+  ckpt_values4(w[1], s, c.fmt, p + 4);
+}
+// the gated gradient of 8 columns from their sums v
+__device__ __forceinline__ void gated_grad8(const Epi& e, int64_t r, bool in, int64_t col, float (&v)[8]) {
+  const int n = in_row<8>(e, col);
+  if (!in || n <= 0) return;
+  const bool vec = e.vec_out && n == 8;
+  float g[8], u[8], d[8];
+  kept8(e, e.c, r, col, n, g);
+  kept8(e, e.c2, r, col, n, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = v[i] * u[i];
+  slope_apply(e.act, g, d);  // g becomes act(g)
+  store_row(static_cast<bf16*>(e.out) + r * e.ldo + col, vec, n, d);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= g[i], u[i] *= g[i];
+  store_row(e.out2 + r * e.ldo + col, vec, n, v);
+  if (e.hidden) store_row(e.hidden + r * e.ldh + col, vec, n, u);
+}
+// the gated forward of 8 columns from the sums g and u; 16 lanes hold 128 columns of a row.
+// Every lane of the warp calls it.
+__device__ __forceinline__ void gated8(const Epi& e, int64_t r, bool in, int64_t col, float (&g)[8], float (&u)[8]) {
+  const int n = in_row<8>(e, col);
+  const bool full = n == 8;
+  in = in && n > 0;
+  if (e.c.codes) {
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = i < n ? g[i] : 0.0f, u[i] = i < n ? u[i] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Ckpt& c = k ? e.c2 : e.c;
+      const float(&v)[8] = k ? u : g;
+      uint32_t m = amax_bits(v);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+        if (o < 4 || o < (1 << (c.lg - 3))) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (in) {
+        const Divisor d = ckpt_divisor(m, c.fmt);
+        const f2 x[4] = {mk2(v[0], v[1]), mk2(v[2], v[3]), mk2(v[4], v[5]), mk2(v[6], v[7])};
+        uint32_t w[2];
+        ckpt_codes(x, d, c.fmt, w);
+        store_bytes<8>(c.codes + r * e.cols + col, e.vec_codes && full, n, w);
+        if ((int(col) & ((1 << c.lg) - 1)) == 0) c.scale[r * c.groups + (col >> c.lg)] = d.s;
+      }
+    }
+  }
+  if (!in) return;
+  act_apply(e.act, g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] *= u[i];
+  store_row(static_cast<bf16*>(e.out) + r * e.ldo + col, e.vec_out && full, n, g);
 }
 
 // Partial sums of 128 columns in shared memory: the 16-byte units of 4 columns with an
@@ -376,6 +455,9 @@ __device__ __forceinline__ void prefetch_inputs(const Epi& e, int64_t r, int64_t
   if (PASS == P_WGRAD) {
     const int es = e.out_dtype == AQFQ_F32 ? 4 : 2;
     if (e.accumulate) p = static_cast<const uint8_t*>(e.out) + (r * e.ldo + col) * es, q = p + n * es;
+  } else if (PASS == P_GATED_DGRAD) {
+    prefetch_l2(e.c.codes + r * e.cols + col);
+    prefetch_l2(e.c2.codes + r * e.cols + col);
   } else if (e.res) {
     p = reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + col), q = p + n * 2;
   }
@@ -402,7 +484,8 @@ __device__ __forceinline__ void prefetch_row(const Epi& e, int64_t r, int64_t c0
       prefetch_l2(static_cast<const uint8_t*>(e.out) + (r * e.ldo + c0) * es + at);
   } else {
     if (e.res && at < n * 2) prefetch_l2(reinterpret_cast<const uint8_t*>(e.res + r * e.ldr + c0) + at);
-    if (PASS == P_DGRAD && e.c.codes && lane == 8) prefetch_l2(e.c.codes + r * e.cols + c0);
+    if ((PASS == P_DGRAD || PASS == P_GATED_DGRAD) && e.c.codes && lane == 8) prefetch_l2(e.c.codes + r * e.cols + c0);
+    if (PASS == P_GATED_DGRAD && lane == 9) prefetch_l2(e.c2.codes + r * e.cols + c0);
   }
 }
 
@@ -585,6 +668,178 @@ __device__ __forceinline__ void epilogue_whole(const Epi& e, int64_t r, int64_t 
 }
 
 // ---------------------------------------------------------------------------
+// gated epilogues from tensor memory, a row per lane
+// ---------------------------------------------------------------------------
+template <int ACT, int V>
+__device__ __forceinline__ void act_of(const Epi& e, float (&v)[V]) {
+  if constexpr (ACT < 0) act_apply(e.act, v);
+  else act_all<ACT>(v);
+}
+template <int ACT, int V>
+__device__ __forceinline__ void slope_of(const Epi& e, float (&p)[V], float (&v)[V]) {
+  if constexpr (ACT < 0) slope_apply(e.act, p, v);
+  else slope_all<ACT>(p, v);
+}
+// n of 16 values as BF16 at p
+__device__ __forceinline__ void put16(bf16* p, int n, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
+  const Seg q = seg(p, n == 16);
+  st16(p, q.a32, q.a16, n, w);
+}
+__device__ __forceinline__ void put_codes16(const Epi& e, const Ckpt& c, int64_t r, int64_t cc, int n,
+                                            const Divisor& d, const float (&v)[16]) {
+  uint32_t w[4];
+  f2 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = mk2(v[2 * i], v[2 * i + 1]);
+  ckpt_codes(x, d, c.fmt, w);
+  store_codes16(c.codes + r * e.cols + cc, n, w);
+}
+
+// Forward: columns [col, col + 32) of row r, g and u at tg and tu.  The four warps of a
+// quarter of the rows hold a tile's 128 columns (`part` of them this one's); with kept
+// values they exchange their maxima through `most` ([2][4][128] floats; `at` the lane's row
+// of the tile) at the barrier `bar`, and read the sums twice instead of holding 64 registers
+// through it.  The four warps all call it.
+template <int ACT>
+__device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int64_t col, uint32_t tg,
+                                          uint32_t tu, float* most, int at, int part, int bar) {
+  uint32_t a[16], b[16];
+  float g[16], u[16];
+  const bool keep = e.c.codes != nullptr;
+  Divisor dg = {}, du = {};
+  if (keep) {
+    uint32_t mg = 0, mu = 0;
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      tmem_issue(tg + uint32_t(c * 16), a);
+      tmem_issue(tu + uint32_t(c * 16), b);
+      tmem_take(a, g);
+      tmem_take(b, u);
+      const int64_t left = e.cols - (col + c * 16);
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = i < left ? g[i] : 0.0f, u[i] = i < left ? u[i] : 0.0f;
+      }
+      mg = max(mg, amax_bits(g));
+      mu = max(mu, amax_bits(u));
+    }
+    int first = part;
+    if (e.c.lg > 5) {
+      most[part * 128 + at] = __uint_as_float(mg);
+      most[512 + part * 128 + at] = __uint_as_float(mu);
+      __syncwarp();
+      switch (bar) {  // constants: a barrier named in a register would reserve all sixteen
+        case 2: asm volatile("bar.sync 2, 128;" ::: "memory"); break;
+        case 3: asm volatile("bar.sync 3, 128;" ::: "memory"); break;
+        case 4: asm volatile("bar.sync 4, 128;" ::: "memory"); break;
+        default: asm volatile("bar.sync 5, 128;" ::: "memory"); break;
+      }
+      first = part & ~((1 << (e.c.lg - 5)) - 1);
+      for (int i = 0; i < (1 << (e.c.lg - 5)); ++i) {
+        mg = max(mg, __float_as_uint(most[(first + i) * 128 + at]));
+        mu = max(mu, __float_as_uint(most[512 + (first + i) * 128 + at]));
+      }
+    }
+    dg = ckpt_divisor(mg, e.c.fmt), du = ckpt_divisor(mu, e.c.fmt);
+    if (in && part == first && col < e.cols) {
+      const int64_t k = r * e.c.groups + (col >> e.c.lg);
+      e.c.scale[k] = dg.s, e.c2.scale[k] = du.s;
+    }
+  }
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int64_t cc = col + c * 16, left = e.cols - cc;
+    if (left <= 0) break;
+    const int n = left > 16 ? 16 : int(left);
+    tmem_issue(tg + uint32_t(c * 16), a);
+    tmem_issue(tu + uint32_t(c * 16), b);
+    tmem_take(a, g);
+    tmem_take(b, u);
+    if (keep && in) {
+      put_codes16(e, e.c, r, cc, n, dg, g);
+      put_codes16(e, e.c2, r, cc, n, du, u);
+    }
+    act_of<ACT>(e, g);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] *= u[i];
+    if (in) put16(static_cast<bf16*>(e.out) + r * e.ldo + cc, n, g);
+  }
+}
+
+// 16 kept gate and up values of a row
+struct GateCodes {
+  uint32_t g[4], u[4];
+  float sg, su;
+  __device__ __forceinline__ void load(const Epi& e, int64_t r, int64_t cc) {
+    const int64_t left = e.cols - cc;
+    const int n = left > 16 ? 16 : int(left);
+    one(e, e.c.codes + r * e.cols + cc, n, g);
+    one(e, e.c2.codes + r * e.cols + cc, n, u);
+    const int64_t k = r * e.c.groups + (cc >> e.c.lg);
+    sg = e.c.scale[k], su = e.c2.scale[k];
+  }
+  static __device__ __forceinline__ void one(const Epi& e, const uint8_t* p, int n, uint32_t (&w)[4]) {
+    if (seg(p, n == 16).a16) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if (e.vec_codes) {  // rows start at multiples of 8
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      const uint2 z = n > 8 ? *reinterpret_cast<const uint2*>(p + 8) : make_uint2(0, 0);
+      w[0] = x.x, w[1] = x.y, w[2] = z.x, w[3] = z.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) w[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+    }
+  }
+};
+
+// Gradient: columns [col, col + 16 NCH) of row r from their sums at taddr; the next 16
+// columns' kept values are on their way while 16 are computed.
+template <int ACT, int NCH>
+__device__ __forceinline__ void gated_grad_row(const Epi& e, int64_t r, bool in, int64_t col, uint32_t taddr) {
+  uint32_t t[16];
+  float v[16];
+  GateCodes cur = {};
+  if (in && col < e.cols) cur.load(e, r, col);
+#pragma unroll 1
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t cc = col + c * 16, left = e.cols - cc;
+    if (left <= 0) break;
+    const int n = left > 16 ? 16 : int(left);
+    tmem_issue(taddr + uint32_t(c * 16), t);
+    float p[16], u[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ckpt_values4(cur.g[i], cur.sg, e.c.fmt, p + 4 * i);
+      ckpt_values4(cur.u[i], cur.su, e.c.fmt, u + 4 * i);
+    }
+    if (in && c + 1 < NCH && left > 16) cur.load(e, r, cc + 16);
+    tmem_take(t, v);
+    if (in) {
+      float d[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d[i] = v[i] * u[i];
+      slope_of<ACT>(e, p, d);  // p becomes act(g)
+      put16(static_cast<bf16*>(e.out) + r * e.ldo + cc, n, d);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= p[i];
+      put16(e.out2 + r * e.ldo + cc, n, v);
+      if (e.hidden) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] *= p[i];
+        put16(e.hidden + r * e.ldh + cc, n, u);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // product on a pair of CTAs: tiles of 256 rows x BN columns, 64 of k per stage.
 // Each CTA loads 128 rows of A and BN / 2 of B by TMA; one thread of the leader
 // issues the MMAs for both (tcgen05, cta_group::2); the accumulators (128 rows
@@ -640,6 +895,7 @@ struct PairArgs {
   int first, count;  // the tiles of this launch
   int splits;        // slices of the inner axis
   int a_rows;        // rows of A per box (tile_kernel: fewer when there are fewer rows)
+  int up;            // gated product: the first row of up's weight
   int ksteps;        // 64-element steps of the inner axis
   float* part;       // [splits][rows][cols4] partial sums when splits > 1
   int64_t cols4;     // cols rounded up to 4
@@ -664,7 +920,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
   using C = Cfg<BN>;
-  constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+  constexpr bool A_MN = PASS == P_WGRAD, B_MN = !k_major(PASS);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -716,7 +972,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int sp = SPLIT ? slice : u / tiles;
       const int k0 = int(int64_t(a.ksteps) * sp / a.splits);
       const int k1 = int(int64_t(a.ksteps) * (sp + 1) / a.splits);
-      const int r0 = tr * kRows + int(rank) * kHalf, c0 = tc * BN + int(rank) * (BN / 2);
+      const int r0 = tr * kRows + int(rank) * kHalf;
+      // gated: the leader's half of the columns is gate's, the other one up's
+      const int c0 = PASS == P_GATED ? tc * (BN / 2) + int(rank) * a.up : tc * BN + int(rank) * (BN / 2);
       for (int k = k0; k < k1; ++k, ++it) {
         if (it >= C::STAGES && !mbar_wait_warp(&sh->empty[s], phase)) {
           ok = false;
@@ -811,9 +1069,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       tile_of(a, a.first + u % tiles, tr, tc);
       const int buf = n & 1;
       const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf + q * 32, r = r0 + lane;
-      const int64_t col = int64_t(tc) * BN + part * W;
-      const bool live = r0 < e.rows && col < e.cols, whole = !SPLIT && a.splits == 1;
-      const bool fast = whole_block<PASS>(e, r0, col);
+      const bool whole = !SPLIT && a.splits == 1;
+      // gated: 32 outputs of the tile's 128 per warp, or (partial sums) 64 of gate's or up's
+      const int64_t col = PASS == P_GATED ? int64_t(tc) * (BN / 2) + (whole ? part * (W / 2) : (part & 1) * W)
+                                          : int64_t(tc) * BN + part * W;
+      const bool live = r0 < e.rows && (col < e.cols || (PASS == P_GATED && whole));
+      const bool fast = PASS < P_GATED && whole_block<PASS>(e, r0, col);
       RowCodes<kChunks> codes;
       if (live && whole) {
         if (PASS == P_FWD && e.bias) {
@@ -857,7 +1118,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                   make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         } else if (a.splits > 1) {
-          float* dst = a.part + (int64_t(u / tiles) * e.rows + r) * a.cols4 + col;
+          const int64_t half = PASS == P_GATED ? a.cols4 / 2 : a.cols4;
+          float* dst = a.part + (int64_t(u / tiles) * e.rows + r) * a.cols4 + col +
+                       (PASS == P_GATED && part >= 2 ? half : 0);
           uint32_t t[16];
           float v[16];
 #pragma unroll 1
@@ -867,11 +1130,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (r < e.rows) {
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                if (col + c * 16 + i < a.cols4)
+                if (col + c * 16 + i < half)
                   *reinterpret_cast<float4*>(dst + c * 16 + i) =
                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
+        } else if constexpr (PASS == P_GATED) {
+          const uint32_t tg = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + part * (W / 2));
+          gated_row<ACT>(e, r, r < e.rows, col, tg, tg + BN / 2, sbias, q * 32 + lane, part, 2 + q);
+        } else if constexpr (PASS == P_GATED_DGRAD) {
+          gated_grad_row<ACT, W / 16>(e, r, r < e.rows, col, taddr);
         } else {
           if (fast) epilogue_whole<PASS, ACT>(e, r, col, taddr, mybias + int(col & 127), codes);
           else epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), codes);
@@ -890,7 +1158,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int64_t r0 = int64_t(tr) * kRows + int(rank) * kHalf;
     const int nrows = e.rows - r0 > kHalf ? kHalf : (e.rows > r0 ? int(e.rows - r0) : 0);
     const int half = warp & 1, row0 = nrows * slice / a.splits, rend = nrows * (slice + 1) / a.splits;
-    const int64_t c0 = int64_t(tc) * BN + half * (BN / 2), col = c0 + (lane & 15) * 8;
+    const int64_t c0 = PASS == P_GATED ? int64_t(tc) * (BN / 2) : int64_t(tc) * BN + half * (BN / 2);
+    const int64_t col = c0 + (lane & 15) * 8;
     float bias[8] = {};
     if (PASS == P_FWD) load_bias(e, col, bias);
     if (warp >= 2 && c0 < e.cols)
@@ -898,7 +1167,18 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         prefetch_row<PASS>(e, r0 + row, c0, lane & 15);
     __syncwarp();
     cluster_sync();  // every slice's partial sums are in shared memory
-    if (c0 < e.cols) {
+    if constexpr (PASS == P_GATED) {
+      // (a warp takes both halves of two rows: g and u of an output)
+#pragma unroll 1
+      for (int base = row0 + warp * 2; base < rend; base += 2 * NW) {
+        const int row = base + (lane >> 4);
+        const uint32_t at = smem_u32(smem) + uint32_t((row < kHalf ? row : base) * C::PSTRIDE + (lane & 15) * 4) * 4;
+        float g[8], v[8];
+        cluster_sum8(at, a.splits, rank, 2, g);
+        cluster_sum8(at + BN / 2 * 4, a.splits, rank, 2, v);
+        gated8(e, r0 + row, row < rend, col, g, v);
+      }
+    } else if (c0 < e.cols) {
 #pragma unroll 1
       for (int base = row0 + (warp >> 1) * 2; base < rend; base += NW) {
         const int row = base + (lane >> 4);
@@ -907,7 +1187,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         cluster_sum8(smem_u32(smem) + uint32_t((row < kHalf ? row : base) * C::PSTRIDE + half * (BN / 2) +
                                                (lane & 15) * 4) * 4,
                      a.splits, rank, 2, v);
-        epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
+        if constexpr (PASS == P_GATED_DGRAD) gated_grad8(e, r0 + row, row < rend, col, v);
+        else epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
       }
     }
   }
@@ -940,13 +1221,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
 constexpr int kWarpsC = 16;
-constexpr int kStagesC = 6;
-constexpr int kStrideC = kTile + 4;  // floats per row of partial sums
-constexpr size_t kSmemC = 1024 + size_t(kStagesC) * 2 * kABytes + 256;
-static_assert(size_t(kTile) * kStrideC * 4 <= size_t(kStagesC) * 2 * kABytes, "partial sums fit the stages");
+// (the gated product: 128 x 128 outputs, so that a group of 128 kept columns stays in one
+// tile, and 256 sums per row)
+template <bool GATED>
+struct CfgC {
+  static constexpr int COLS = GATED ? 2 * kTile : kTile;  // sums per row
+  static constexpr int STAGES = GATED ? 4 : 6;
+  static constexpr uint32_t STAGE = kABytes + COLS * kBK * 2;
+  static constexpr int STRIDE = COLS + 4;  // floats per row of partial sums
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 256;
+  static_assert(size_t(kTile) * STRIDE * 4 <= size_t(STAGES) * STAGE, "partial sums fit the stages");
+};
 
 struct __align__(8) CtaShared {
-  uint64_t full[kStagesC], empty[kStagesC];
+  uint64_t full[6], empty[6];
   uint64_t accum;
   uint32_t tmem;
   int32_t abort;
@@ -957,11 +1245,13 @@ template <int PASS>
 __global__ void __launch_bounds__(32 * kWarpsC, 1)
     tile_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const PairArgs a, const Epi e) {
-  constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+  constexpr bool A_MN = PASS == P_WGRAD, B_MN = !k_major(PASS), GATED = PASS == P_GATED;
+  using C = CfgC<GATED>;
+  constexpr int kStagesC = C::STAGES, kStrideC = C::STRIDE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  CtaShared* sh = reinterpret_cast<CtaShared*>(smem + kStagesC * 2 * kABytes);
+  CtaShared* sh = reinterpret_cast<CtaShared*>(smem + kStagesC * C::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slice = int(cluster_rank());
   const int tile = blockIdx.x / a.splits;
@@ -973,9 +1263,9 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
 
   auto load = [&](int k, int s) {
     if (elect_one()) {
-      uint8_t *da = smem + s * 2 * kABytes, *db = da + kABytes;
+      uint8_t *da = smem + s * C::STAGE, *db = da + kABytes;
       const int kk = (k0 + k) * kBK;
-      mbar_arrive_expect_tx(&sh->full[s], kABytes + (A_MN ? kABytes : uint32_t(a.a_rows * kBK * 2)));
+      mbar_arrive_expect_tx(&sh->full[s], C::STAGE - kABytes + (A_MN ? kABytes : uint32_t(a.a_rows * kBK * 2)));
       if constexpr (A_MN) {
         tma_load_2d(da, &ta, &sh->full[s], int(r0), kk);
         tma_load_2d(da + kABytes / 2, &ta, &sh->full[s], int(r0) + 64, kk);
@@ -987,6 +1277,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         tma_load_2d(db + kABytes / 2, &tb, &sh->full[s], int(c0) + 64, kk);
       } else {
         tma_load_2d(db, &tb, &sh->full[s], kk, int(c0));
+        if (GATED) tma_load_2d(db + kABytes, &tb, &sh->full[s], kk, a.up + int(c0));
       }
     }
     __syncwarp();
@@ -1005,7 +1296,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     // the first stages are on their way before the others have set up
     for (int k = 0; k < n && k < kStagesC; ++k) load(k, k);
   } else if (warp == 1) {
-    tmem_alloc(&sh->tmem, kTile);
+    tmem_alloc(&sh->tmem, C::COLS);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -1030,7 +1321,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     }
     if (lane == 0) sh->issued = k;
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile) | (A_MN ? kIdescTransA : 0) |
+    constexpr uint32_t idesc = idesc_bf16_f32(kTile, C::COLS) | (A_MN ? kIdescTransA : 0) |
                                (B_MN ? kIdescTransB : 0);
     const uint32_t base = smem_u32(smem);
     const uint64_t da0 = A_MN ? smem_desc_mn_sw128(base, 8192) : smem_desc_sw128(base);
@@ -1044,7 +1335,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         break;
       }
       tc_fence_after_sync();
-      const uint64_t da = da0 + ((s * 2 * kABytes) >> 4), db = db0 + ((s * 2 * kABytes) >> 4);
+      const uint64_t da = da0 + ((s * C::STAGE) >> 4), db = db0 + ((s * C::STAGE) >> 4);
       if (elect_one()) {
         tc_mma_f16(tmem, da, db, idesc, k > 0 ? 1u : 0u);
 #pragma unroll
@@ -1068,6 +1359,21 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     const int q = warp & 3;
     const int64_t r = r0 + q * 32 + lane, col = c0 + (warp >> 2) * 32;
     const bool live = q * 32 < nrows && col < e.cols, in = live && r < e.rows;  // live: uniform
+    if constexpr (PASS >= P_GATED) {
+      if (PASS == P_GATED_DGRAD && in) prefetch_inputs<PASS>(e, r, col, 32);
+      __syncwarp();
+      if (!mbar_wait_warp(&sh->accum, 0)) *abort = 1;
+      __syncwarp();
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
+      if (PASS == P_GATED) {
+        if (q * 32 < nrows)  // (all four warps of the quarter; the stages are consumed)
+          gated_row<-1>(e, r, r < e.rows, col, taddr, taddr + kTile, reinterpret_cast<float*>(smem), q * 32 + lane,
+                        warp >> 2, 2 + q);
+      } else if (live) {
+        gated_grad_row<-1, 2>(e, r, in, col, taddr);
+      }
+    } else {
     ChunkIn<PASS> add[2];
     RowCodes<2> codes;
     float bias[4][8];
@@ -1144,11 +1450,12 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v[c]);
       }
     }
+    }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 1) {
       tc_fence_after_sync();
-      tmem_dealloc(tmem, kTile);
+      tmem_dealloc(tmem, C::COLS);
     }
     if (warp == 0 && *abort) drain_loads(sh->full, kStagesC, sh->issued);
     if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
@@ -1169,18 +1476,19 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
   {
     const int q = warp & 3, part = warp >> 2;  // 32 rows x 32 columns
     if (q * 32 < nrows) {
-      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(part * 32);
-      float* dst = sums + (q * 32 + lane) * kStrideC;
+      constexpr int W = C::COLS / 4;
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(part * W);
+      float* dst = sums + (q * 32 + lane) * kStrideC + part * W / kTile * kTile;
       uint32_t t[16];
       float v[16];
       tmem_issue(taddr, t);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < W / 16; ++c) {
         tmem_take(t, v);
-        if (c < 1) tmem_issue(taddr + 16, t);
+        if (c + 1 < W / 16) tmem_issue(taddr + uint32_t((c + 1) * 16), t);
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(dst + unit_at((part * 32 + c * 16 + i) / 4) * 4) =
+          *reinterpret_cast<float4*>(dst + unit_at((part * W % kTile + c * 16 + i) / 4) * 4) =
               make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
@@ -1194,14 +1502,22 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
     const float* at = sums + (row < kTile ? row : base) * kStrideC + (lane & 15) * 4;
     float v[8];
     cluster_sum8(smem_u32(at), a.splits, 0, 1, v);
-    epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
+    if constexpr (PASS == P_GATED) {
+      float u[8];
+      cluster_sum8(smem_u32(at + kTile), a.splits, 0, 1, u);
+      gated8(e, r0 + row, row < rend, col, v, u);
+    } else if constexpr (PASS == P_GATED_DGRAD) {
+      gated_grad8(e, r0 + row, row < rend, col, v);
+    } else {
+      epilogue8<PASS>(e, r0 + row, row < rend, col, bias, v);
+    }
   }
   tc_fence_before_sync();
   __syncwarp();
   cluster_sync();  // the others have read this CTA's sums
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kTile);
+    tmem_dealloc(tmem, C::COLS);
   }
   if (warp == 0 && *abort) drain_loads(sh->full, kStagesC, sh->issued);
   if (threadIdx.x == 0 && *abort && a.err) atomicExch(a.err, 1);
@@ -1217,19 +1533,31 @@ __global__ void __launch_bounds__(256)
   float bias[8] = {};
   if (PASS == P_FWD) load_bias(e, col, bias);
   for (int64_t base = int64_t(blockIdx.y) * 16 + warp * 2; base < e.rows; base += int64_t(gridDim.y) * 16) {
-    const int64_t r = base + (lane >> 4);
-    float v[8] = {};
+    const int64_t r = base + (lane >> 4), half = PASS == P_GATED ? cols4 / 2 : cols4;
+    auto sum = [&](int64_t at, float(&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      if (r < e.rows && col + j < cols4) {
-        const float* p = part + r * cols4 + col + j;
-        for (int s = 0; s < splits; ++s) {
-          const float4 f = *reinterpret_cast<const float4*>(p + int64_t(s) * e.rows * cols4);
-          v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
+      for (int j = 0; j < 8; j += 4) {
+        v[j] = v[j + 1] = v[j + 2] = v[j + 3] = 0.0f;
+        if (r < e.rows && col + j < half) {
+          const float* p = part + r * cols4 + at + col + j;
+          for (int s = 0; s < splits; ++s) {
+            const float4 f = *reinterpret_cast<const float4*>(p + int64_t(s) * e.rows * cols4);
+            v[j] += f.x, v[j + 1] += f.y, v[j + 2] += f.z, v[j + 3] += f.w;
+          }
         }
       }
+    };
+    float v[8];
+    sum(0, v);
+    if constexpr (PASS == P_GATED) {
+      float u[8];
+      sum(half, u);
+      gated8(e, r, r < e.rows, col, v, u);
+    } else if constexpr (PASS == P_GATED_DGRAD) {
+      gated_grad8(e, r, r < e.rows, col, v);
+    } else {
+      epilogue8<PASS>(e, r, r < e.rows, col, bias, v);
     }
-    epilogue8<PASS>(e, r, r < e.rows, col, bias, v);
   }
 }
 
@@ -1308,15 +1636,16 @@ constexpr int64_t kMostScratch = int64_t(64) << 20;
 //     kernel and the partial sums' way to memory and back (weight gradients of many
 //     tokens: few tiles, a long sum).
 // (The same with and without a checkpoint, so that keeping one changes no sum.)
-Plan make_plan(int64_t rows, int64_t cols, int64_t depth) {
+// gated: a tile has half as many outputs per row, each with two sums.
+Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
   Plan p;
   p.nr = int((rows + kRows - 1) / kRows);
-  p.nc = int((cols + kBN - 1) / kBN);
+  p.nc = int(gated ? (cols + kBN / 2 - 1) / (kBN / 2) : (cols + kBN - 1) / kBN);
   p.ksteps = int((depth + kBK - 1) / kBK);
   p.splits = p.ksteps > 0 ? 1 : 0;
   p.small = false;
   p.a_rows = kHalf, p.tail = p.tail_splits = 0;
-  p.cols4 = (cols + 3) / 4 * 4;
+  p.cols4 = (cols + 3) / 4 * (gated ? 8 : 4);
   p.bytes = 0;
   if (p.ksteps == 0) return p;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
@@ -1402,13 +1731,14 @@ cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
                         cudaStream_t st) {
   static DeviceOnce once;
   const cudaError_t attr = once_per_device(once, [] {
-    return cudaFuncSetAttribute(tile_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemC));
+    return cudaFuncSetAttribute(tile_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(CfgC<PASS == P_GATED>::SMEM));
   });
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.nr * a.nc * a.splits));
   cfg.blockDim = dim3(32 * kWarpsC);
-  cfg.dynamicSmemBytes = kSmemC;
+  cfg.dynamicSmemBytes = CfgC<PASS == P_GATED>::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1421,7 +1751,7 @@ cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
 template <int PASS>
 aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi& e, void* workspace,
                     size_t workspace_bytes, int32_t* err, cudaStream_t st) {
-  const Plan p = make_plan(e.rows, e.cols, depth);
+  const Plan p = make_plan(e.rows, e.cols, depth, PASS == P_GATED);
   if (p.bytes > 0) {
     if (!workspace || workspace_bytes < p.bytes) return AQFQ_ERR_WORKSPACE;
     if (!al(workspace, 16)) return AQFQ_ERR_ALIGN;
@@ -1430,11 +1760,12 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
   if (p.splits > 0) {
     if (!encode_fn()) return AQFQ_ERR_CUDA;
     CUtensorMap ta, tb;
-    constexpr bool A_MN = PASS == P_WGRAD, B_MN = PASS != P_FWD;
+    constexpr bool A_MN = PASS == P_WGRAD, B_MN = !k_major(PASS);
     if (!encode(&ta, A, kBK, A_MN ? kBK : unsigned(p.a_rows)) ||
         !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
       return AQFQ_ERR_CUDA;
-    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, p.ksteps, part, p.cols4, err};
+    const int up = PASS == P_GATED ? int(e.cols) : 0;
+    PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, up, p.ksteps, part, p.cols4, err};
     cudaError_t r;
     a.count -= p.tail;
     if (p.small) {
@@ -1472,10 +1803,11 @@ bool operand_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
 }
 
 void finish_epi(Epi& e, int es) {
-  e.vec_out = rows_aligned<8>(e.out, e.ldo, es);
+  e.vec_out = rows_aligned<8>(e.out, e.ldo, es) && rows_aligned<8>(e.out2, e.ldo, es) &&
+              rows_aligned<8>(e.hidden, e.ldh, es);
   e.vec_res = rows_aligned<8>(e.res, e.ldr, 2);
   e.vec_bias = rows_aligned<8>(e.bias, 8, esize(e.bias_dtype));
-  e.vec_codes = rows_aligned<8>(e.c.codes, e.cols, 1);
+  e.vec_codes = rows_aligned<8>(e.c.codes, e.cols, 1) && rows_aligned<8>(e.c2.codes, e.cols, 1);
   e.wide = al(e.out, 32) && (e.ldo * es) % 32 == 0 && (!e.res || (al(e.res, 32) && e.ldr % 16 == 0)) &&
            (!e.c.codes || (al(e.c.codes, 16) && e.cols % 16 == 0));
 }
@@ -1505,6 +1837,7 @@ extern "C" aqfq_status aqfq_selftest_linear_plan(int pass, int64_t M, int64_t N,
     case AQFQ_LINEAR_FWD: p = make_plan(M, N, K); break;
     case AQFQ_LINEAR_DGRAD: p = make_plan(M, K, N); break;
     case AQFQ_LINEAR_WGRAD: p = make_plan(N, K, M); break;
+    case AQFQ_LINEAR_GATED: p = make_plan(M, N, K, true); break;
     default: return AQFQ_ERR_UNSUPPORTED;
   }
   plan[0] = p.ksteps == 0 ? 0 : p.small ? 1 : 2;
@@ -1590,4 +1923,70 @@ extern "C" aqfq_status aqfq_linear_wgrad(const void* dy, int64_t lddy, const voi
   finish_epi(e, esize(dtype));
   return product<P_WGRAD>({dy, N, M, lddy}, {x, K, M, ldx}, M, e, workspace, workspace_bytes,
                           error_flag, static_cast<cudaStream_t>(stream));
+}
+
+// gate's and up's checkpoint of one format and group
+static aqfq_status gate_and_up(const aqfq_ckpt8* gate, const aqfq_ckpt8* up, int64_t rows, int64_t cols, Epi& e) {
+  const aqfq_status s = make_ckpt(gate, rows, cols, e.c);
+  if (s != AQFQ_OK) return s;
+  const aqfq_status s2 = make_ckpt(up, rows, cols, e.c2);
+  if (s2 != AQFQ_OK) return s2;
+  return e.c.fmt == e.c2.fmt && e.c.lg == e.c2.lg ? AQFQ_OK : AQFQ_ERR_UNSUPPORTED;
+}
+
+extern "C" size_t aqfq_gated_workspace_bytes(int pass, int64_t M, int64_t N, int64_t K) {
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K)) return 0;
+  switch (pass) {
+    case AQFQ_LINEAR_FWD: return size_ok(2 * N) ? make_plan(M, N, K, true).bytes : 0;
+    case AQFQ_LINEAR_DGRAD: return make_plan(M, K, N).bytes;
+    default: return 0;
+  }
+}
+
+extern "C" aqfq_status aqfq_gated_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
+                                      int64_t N, int64_t K, int act, void* y, int64_t ldy,
+                                      const aqfq_ckpt8* gate, const aqfq_ckpt8* up, void* workspace,
+                                      size_t workspace_bytes, int32_t* error_flag, void* stream) {
+  if (!size_ok(M) || !size_ok(N) || !size_ok(2 * N) || !size_ok(K) || !view_ok(M, K, ldx) ||
+      !view_ok(2 * N, K, ldw) || !view_ok(M, N, ldy) || !inner_ok(K, ldx, ldw))
+    return AQFQ_ERR_SHAPE;
+  if (!act_ok(act)) return AQFQ_ERR_UNSUPPORTED;
+  Epi e = {};
+  if (gate || up) {
+    const aqfq_status s = gate_and_up(gate, up, M, N, e);
+    if (s != AQFQ_OK) return s;
+  }
+  if (M > 0 && N > 0 && (!y || (K > 0 && (!x || !w)))) return AQFQ_ERR_NULL;
+  if (!operand_ok(x, ldx, M, K) || !operand_ok(w, ldw, 2 * N, K) || !al(y, 2) || !al(error_flag, 4))
+    return AQFQ_ERR_ALIGN;
+  if (M == 0 || N == 0) return AQFQ_OK;
+  e.rows = M, e.cols = N;
+  e.out = y, e.ldo = ldy, e.out_dtype = AQFQ_BF16, e.act = act;
+  finish_epi(e, 2);
+  return product<P_GATED>({x, K, M, ldx}, {w, K, 2 * N, ldw}, K, e, workspace, workspace_bytes, error_flag,
+                          static_cast<cudaStream_t>(stream));
+}
+
+extern "C" aqfq_status aqfq_gated_dgrad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t M,
+                                        int64_t N, int64_t K, int act, const aqfq_ckpt8* gate,
+                                        const aqfq_ckpt8* up, void* dp, int64_t lddp, void* y, int64_t ldy,
+                                        void* workspace, size_t workspace_bytes, int32_t* error_flag,
+                                        void* stream) {
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K) || !view_ok(M, N, lddy) || !view_ok(N, K, ldw) ||
+      !view_ok(M, 2 * K, lddp) || (y && !view_ok(M, K, ldy)) || !inner_ok(N, lddy, ldw))
+    return AQFQ_ERR_SHAPE;
+  if (!act_ok(act)) return AQFQ_ERR_UNSUPPORTED;
+  Epi e = {};
+  const aqfq_status s = gate_and_up(gate, up, M, K, e);
+  if (s != AQFQ_OK) return s;
+  if (M > 0 && K > 0 && (!dp || (N > 0 && (!dy || !w)))) return AQFQ_ERR_NULL;
+  if (!operand_ok(dy, lddy, M, N) || !operand_ok(w, ldw, N, K) || !al(dp, 2) || !al(y, 2) || !al(error_flag, 4))
+    return AQFQ_ERR_ALIGN;
+  if (M == 0 || K == 0) return AQFQ_OK;
+  e.rows = M, e.cols = K;
+  e.out = dp, e.ldo = lddp, e.out_dtype = AQFQ_BF16, e.act = act;
+  e.out2 = static_cast<bf16*>(dp) + K, e.hidden = static_cast<bf16*>(y), e.ldh = ldy;
+  finish_epi(e, 2);
+  return product<P_GATED_DGRAD>({dy, N, M, lddy}, {w, K, N, ldw}, N, e, workspace, workspace_bytes, error_flag,
+                                static_cast<cudaStream_t>(stream));
 }

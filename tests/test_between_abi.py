@@ -167,3 +167,73 @@ def test_block_norm_binding_checks():
         aqfq.aqfq_block_norm_fwd(None, None, 1e-6, h=t)
     with pytest.raises(ValueError, match="missing"):
         aqfq.aqfq_block_norm_bwd(None, None, t, t, dx=t)
+
+
+# ---- gated product ---------------------------------------------------------------------
+
+def ck(fmt=aqfq.INT8, group=128, codes=7 * A, scale=8 * A):
+    return ctypes.byref(aqfq.Ckpt8(fmt, group, codes, scale))
+
+
+def gfwd(L, x=A, ldx=64, w=2 * A, ldw=64, M=4, N=32, K=64, act=4, y=3 * A, ldy=32, gate=None, up=None, ws=None,
+         wsb=0, err=None):
+    return L.aqfq_gated_fwd(x, ldx, w, ldw, M, N, K, act, y, ldy, gate, up, ws, wsb, err, None)
+
+
+def gdgrad(L, x=A, ldx=32, w=2 * A, ldw=64, M=4, N=32, K=64, act=4, gate="ok", up="ok", y=3 * A, ldy=128, h=None,
+           ldh=0, ws=None, wsb=0, err=None):
+    return L.aqfq_gated_dgrad(x, ldx, w, ldw, M, N, K, act, ck() if gate == "ok" else gate,
+                              ck() if up == "ok" else up, y, ldy, h, ldh, ws, wsb, err, None)
+
+
+def test_gated_checks(L):
+    for f in (gfwd, gdgrad):
+        assert f(L, x=None) == NULL and f(L, w=None) == NULL and f(L, y=None) == NULL
+        assert f(L, x=A + 8) == ALIGN and f(L, w=A + 2) == ALIGN and f(L, y=A + 1) == ALIGN
+        assert f(L, ldx=68) == ALIGN and f(L, ldw=68) == ALIGN
+        assert f(L, ldx=24) == SHAPE and f(L, ldw=56) == SHAPE and f(L, ldy=24) == SHAPE
+        assert f(L, M=-1) == SHAPE and f(L, N=1 << 30) == SHAPE and f(L, K=-8) == SHAPE
+        assert f(L, act=5) == UNSUP and f(L, act=-1) == UNSUP
+        assert f(L, err=A + 2) == ALIGN
+        assert f(L, gate=ck(), up=None) == NULL and f(L, gate=None, up=ck()) == NULL
+        assert f(L, gate=ck(group=16), up=ck(group=16)) == UNSUP
+        assert f(L, gate=ck(), up=ck(group=64)) == UNSUP
+        assert f(L, gate=ck(), up=ck(fmt=aqfq.FP8_E4M3)) == UNSUP
+        assert f(L, gate=ck(codes=None), up=ck()) == NULL
+    assert gfwd(L, N=1 << 29, ldy=1 << 29) == SHAPE               # 2N beyond the limit
+    assert gdgrad(L, ldy=64) == SHAPE                             # dp has 2K columns
+    assert gdgrad(L, gate=None, up=None) == NULL                  # the gradient needs what was kept
+    assert gdgrad(L, h=A, ldh=32) == SHAPE and gdgrad(L, h=A + 1, ldh=64) == ALIGN
+    need = aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_FWD, 70, 300, 33000)
+    big = dict(M=70, N=300, K=33000, ldx=33000, ldw=33000, ldy=300)
+    assert need > 0 and gfwd(L, **big) == WS and gfwd(L, ws=A, wsb=need - 1, **big) == WS
+    assert gfwd(L, ws=A + 8, wsb=need, **big) == ALIGN
+    assert gfwd(L, M=0, x=None, w=None, y=None) == OK and gfwd(L, N=0, x=None, w=None, y=None) == OK
+    none = ck(codes=None, scale=None)
+    assert gdgrad(L, M=0, x=None, w=None, y=None, gate=none, up=none) == OK
+    assert aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_WGRAD, 70, 300, 33000) == 0
+    assert aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_FWD, -1, 300, 33000) == 0
+
+
+def gbwd(L, gate="ok", up="ok", act=4, dtype=0, dy=A, lddy=64, R=4, C=64, dp=2 * A, lddp=128, y=3 * A, ldy=64):
+    return L.aqfq_ckpt8_gated_bwd(ck() if gate == "ok" else gate, ck() if up == "ok" else up, act, dtype, dy, lddy, R,
+                                  C, dp, lddp, y, ldy, None)
+
+
+def test_elementwise_gated_gradient_checks(L):
+    assert gbwd(L, gate=None) == NULL and gbwd(L, up=None) == NULL
+    assert gbwd(L, up=ck(group=32)) == UNSUP and gbwd(L, up=ck(fmt=aqfq.FP8_E4M3)) == UNSUP
+    assert gbwd(L, act=5) == UNSUP and gbwd(L, dtype=2) == UNSUP
+    assert gbwd(L, dp=None, y=None) == NULL and gbwd(L, dy=None) == NULL
+    for p in ("dy", "dp", "y"):
+        assert gbwd(L, **{p: A + 1}) == ALIGN
+    assert gbwd(L, lddy=63) == SHAPE and gbwd(L, lddp=127) == SHAPE and gbwd(L, ldy=63) == SHAPE
+    assert gbwd(L, R=-1) == SHAPE and gbwd(L, C=-1) == SHAPE
+    none = ck(codes=None, scale=None)
+    assert gbwd(L, gate=none, up=none, R=0, dy=None, dp=None, y=None) == OK
+
+
+def test_gated_binding_checks():
+    t = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        aqfq.aqfq_gated_fwd(t, t, t)
