@@ -630,10 +630,12 @@ aqfq_status aqfq_selftest_wait_timeout(int32_t* flag, uint32_t polls, void* stre
  * product is cut as AQFQ_LINEAR_DGRAD): plan[0] = 0 (empty sum), 1 (128 x 128 tiles, one CTA each)
  * or 2 (256 x 256 tiles on pairs of CTAs); plan[1] = slices of the inner axis; plan[2] =
  * tiles of the last round that a second launch splits; plan[3] = into how many slices.
- * aqfq_selftest_layernorm_ring: warps per row of the ring kernel that serves aligned
- * tensors of this size (backward: with x kept as a checkpoint, with dres), 0 if the
- * rows are held in registers or walked. */
+ * aqfq_selftest_layernorm_ring, aqfq_selftest_block_norm_ring: warps per row of the ring
+ * kernel that serves aligned tensors of this size (layer norm backward: with x kept as a
+ * checkpoint, with dres; block norm: with x, f and y or dy, backward with dh or without),
+ * 0 if the rows are held in registers or walked. */
 aqfq_status aqfq_selftest_linear_plan(int pass, int64_t M, int64_t N, int64_t K, int32_t* plan);
+int32_t aqfq_selftest_block_norm_ring(int backward, int dtype, int64_t rows, int64_t cols, int dh);
 int32_t aqfq_selftest_layernorm_ring(int backward, int dtype, int64_t rows, int64_t cols, int ckpt,
                                      int dres);
 

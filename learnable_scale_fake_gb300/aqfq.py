@@ -45,7 +45,7 @@ EXPORTS = ("aqfq_qdq_fwd", "aqfq_grouped_qdq", "aqfq_grouped_qdq_gemm", "aqfq_sc
            "aqfq_block_norm_bwd_workspace_bytes", "aqfq_gated_fwd", "aqfq_gated_dgrad",
            "aqfq_gated_workspace_bytes", "aqfq_ckpt8_gated_bwd",
            "aqfq_selftest_wait_timeout", "aqfq_selftest_grid_codes", "aqfq_selftest_linear_plan",
-           "aqfq_selftest_layernorm_ring", "aqfq_status_string",
+           "aqfq_selftest_layernorm_ring", "aqfq_selftest_block_norm_ring", "aqfq_status_string",
            "aqfq_version")
 
 
@@ -139,6 +139,7 @@ def lib():
                 "aqfq_selftest_grid_codes": (i32, [S, P, i64, P, P]),
                 "aqfq_selftest_linear_plan": (i32, [i32, i64, i64, i64, P]),
                 "aqfq_selftest_layernorm_ring": (i32, [i32, i32, i64, i64, i32, i32]),
+                "aqfq_selftest_block_norm_ring": (i32, [i32, i32, i64, i64, i32]),
                 "aqfq_status_string": (ctypes.c_char_p, [i32]),
                 "aqfq_version": (i32, []),
             }
@@ -804,6 +805,11 @@ def aqfq_selftest_layernorm_ring(backward, dtype, rows, cols, ckpt=False, dres=F
     """Warps per row of the ring kernel that serves aligned tensors of this size; 0: no ring."""
     return int(lib().aqfq_selftest_layernorm_ring(int(backward), _CODE[dtype], rows, cols, int(ckpt),
                                                   int(dres)))
+
+
+def aqfq_selftest_block_norm_ring(backward, dtype, rows, cols, dh=True) -> int:
+    """Warps per row of the ring kernel that serves aligned tensors of this size; 0: no ring."""
+    return int(lib().aqfq_selftest_block_norm_ring(int(backward), _CODE[dtype], rows, cols, int(dh)))
 
 
 def aqfq_status_string(status: int) -> str:

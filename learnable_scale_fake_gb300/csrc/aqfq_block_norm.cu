@@ -239,6 +239,128 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
 }
 
 // ---------------------------------------------------------------------------
+// Many rows: persistent blocks whose rows arrive by bulk asynchronous copies, as in the
+// layer norm (aqfq_norm.cu): a group of G warps owns a ring of stages, R rows of x and of f
+// each, a lane two vectors of 8 columns; after the barrier of a turn's first sum every warp
+// has read the stage before, which one thread then refills.  A wait gives up after about a
+// second; the rows left are then written as NaN.
+// ---------------------------------------------------------------------------
+template <typename T, int G, int NW, int MB, int R>
+__global__ void __launch_bounds__(32 * NW, MB)
+    join_fwd_ring(const T* x, const T* f, T* h, T* y, const FwdArgs a, const RingArgs q) {
+  constexpr int NG = NW / G, P = 8;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[NG][kMaxStages];
+  __shared__ __align__(8) float red[NG][2][2 * G];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / G, wr = warp % G;
+  uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < NG; ++g)
+      for (int i = 0; i < q.stages; ++i) sm100::mbar_init(&full[g][i], 1);
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t step = int64_t(gridDim.x) * NG * R;
+  int64_t r = (int64_t(blockIdx.x) * NG + grp) * R;
+  const bool loader = wr == 0 && lane == 0;
+  // a stage: R rows of f, R rows of x
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      uint64_t* bar = &full[grp][st];
+      const uint32_t dst = sm100::smem_u32(mine + st * q.stage_bytes), n = uint32_t(q.row_bytes);
+      const int rows = a.rows - row < R ? int(a.rows - row) : R;
+      sm100::mbar_arrive_expect_tx(bar, uint32_t(2 * rows) * n);
+      for (int k = 0; k < rows; ++k) {
+        bulk_load(dst + k * n, f + (row + k) * a.ldf, n, bar);
+        bulk_load(dst + (R + k) * n, x + (row + k) * a.ldx, n, bar);
+      }
+    }
+  };
+  if (loader)
+    for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
+  const float inv = 1.0f / float(a.cols);
+  int64_t col[2];
+  int cl[2];
+  bool in[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    col[j] = (wr * 64 + j * 32 + lane) * 8;
+    in[j] = col[j] < a.cols;
+    cl[j] = in[j] ? int(col[j]) : 0;
+  }
+  f2 c[P], g[P];
+  coefs<8, 2>(a.c, a.pdtype, col, in, c);
+  params<8, 2>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  int st = 0, prev = q.stages - 1;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (bool first = true; r < a.rows; r += step, first = false) {
+    if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
+      ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
+    }
+    const uint8_t* stage = mine + st * q.stage_bytes;
+    f2 v[R][P];
+    float s[2] = {};
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // (a second row that does not exist: whatever the stage held, not stored)
+      smem_pairs<true, T, 2>(stage + k * q.row_bytes, cl, in, v[k]);
+      if (!ok) v[k][0] = pair(__int_as_float(0x7FC00000));
+    }
+    if (a.post) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        f2 t = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) t = fma2(v[k][i], v[k][i], t);
+        s[k] = lo2(t) + hi2(t);
+      }
+      group_sum2<G>(s, red[grp][0], grp);
+      if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+#pragma unroll
+      for (int k = 0; k < R; ++k) s[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+      if (wr == 0 && lane < R && r + lane < a.rows && a.rstd_post) a.rstd_post[r + lane] = lane ? s[1] : s[0];
+    } else {
+      s[0] = s[1] = 1.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      f2 b[P], t = 0;
+      smem_pairs<false, T, 2>(stage + (R + k) * q.row_bytes, cl, in, b);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        v[k][i] = masked<8, 2>(fma2(mul2(v[k][i], pair(s[k])), c[i], b[i]), i, in);
+        t = fma2(v[k][i], v[k][i], t);
+      }
+      s[k] = lo2(t) + hi2(t);
+      if (h && r + k < a.rows) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (in[j]) put<T, 8>(h + (r + k) * a.ldh + col[j], v[k], j);
+      }
+    }
+    group_sum2<G>(s, red[grp][1], grp);
+    if (!a.post && loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+#pragma unroll
+    for (int k = 0; k < R; ++k) s[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+    if (wr == 0 && lane < R && r + lane < a.rows && a.rstd_pre) a.rstd_pre[r + lane] = lane ? s[1] : s[0];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (r + k >= a.rows) break;
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[k][i] = mul2(mul2(v[k][i], pair(s[k])), g[i]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (in[j]) put<T, 8>(y + (r + k) * a.ldy + col[j], v[k], j);
+    }
+    prev = st;
+    if (++st == q.stages) st = 0, phase ^= 1;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
 struct BwdArgs {
@@ -456,6 +578,174 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
   }
 }
 
+// Many rows: a ring as forward, one row of dy, h, f and (where there is one) dh per stage;
+// one reduction of three sums per row.
+template <typename T, int NV, int G>
+__global__ void __launch_bounds__(512, 1)
+    join_bwd_ring(const BwdIn<T> p, const BwdArgs a, const RingArgs q) {
+  constexpr int NG = 16 / G, P = NV * 4, C = 32 * G * NV * 8;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[NG][kMaxStages];
+  __shared__ float4 red[16][2];  // [warp][parity]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / G, wr = warp % G;
+  uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < NG; ++g)
+      for (int i = 0; i < q.stages; ++i) sm100::mbar_init(&full[g][i], 1);
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t step = int64_t(gridDim.x) * NG;
+  int64_t r = int64_t(blockIdx.x) * NG + grp;
+  const bool loader = wr == 0 && lane == 0;
+  const uint32_t n = uint32_t(q.row_bytes);
+  auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      uint64_t* bar = &full[grp][st];
+      const uint32_t dst = sm100::smem_u32(mine + st * q.stage_bytes);
+      sm100::mbar_arrive_expect_tx(bar, (p.dh ? 4 : 3) * n);
+      bulk_load(dst, p.dy + row * a.lddy, n, bar);
+      bulk_load(dst + n, p.h + row * a.ldh, n, bar);
+      bulk_load(dst + 2 * n, p.f + row * a.ldf, n, bar);
+      if (p.dh) bulk_load(dst + 3 * n, p.dh + row * a.lddh, n, bar);
+    }
+  };
+  if (loader)
+    for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
+  const float inv = 1.0f / float(a.cols);
+  int cl[NV];
+  int64_t col[NV];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    col[j] = (wr * NV * 32 + j * 32 + lane) * 8;
+    in[j] = col[j] < a.cols;
+    cl[j] = in[j] ? int(col[j]) : 0;
+  }
+  f2 g[P], c[P], ag[P] = {}, as[P] = {};
+  params<8, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  coefs<8, NV>(a.c, a.pdtype, col, in, c);
+  // the row's scalars are fetched one row ahead
+  float rh_n = 0.0f, rf_n = 1.0f;
+  auto scalars = [&](int64_t row) {
+    if (row < a.rows) {
+      rh_n = __ldg(a.rstd_pre + row);
+      if (a.post) rf_n = __ldg(a.rstd_post + row);
+    }
+  };
+  scalars(r);
+  int st = 0, prev = q.stages - 1, par = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (bool first = true; r < a.rows; r += step, first = false, par ^= 1) {
+    const float rh = rh_n, rf = rf_n;
+    scalars(r + step);
+    if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
+      ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
+    }
+    const uint8_t* stage = mine + st * q.stage_bytes;
+    f2 qq[P], hh[P], fh[P], t0 = 0, t1 = 0, t2 = 0;
+    {
+      f2 d[P];
+      smem_pairs<true, T, NV>(stage, cl, in, d);
+      smem_pairs<true, T, NV>(stage + n, cl, in, hh);
+      if (!ok) d[0] = hh[0] = pair(__int_as_float(0x7FC00000));
+      if (p.dh) {
+        smem_pairs<true, T, NV>(stage + 3 * n, cl, in, qq);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) qq[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        // zero beyond the row, also where a factor is infinite
+        hh[i] = masked<8, NV>(mul2(hh[i], pair(rh)), i, in);
+        ag[i] = fma2(d[i], hh[i], ag[i]);
+        const f2 u = mul2(d[i], g[i]);
+        qq[i] = masked<8, NV>(fma2(pair(rh), u, qq[i]), i, in);
+        t0 = fma2(u, hh[i], t0);
+      }
+    }
+    smem_pairs<true, T, NV>(stage + 2 * n, cl, in, fh);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      fh[i] = masked<8, NV>(mul2(fh[i], pair(rf)), i, in);
+      const f2 cf = mul2(c[i], fh[i]);
+      t1 = fma2(cf, qq[i], t1);
+      t2 = fma2(cf, hh[i], t2);
+    }
+    float s0 = lo2(t0) + hi2(t0), s1 = lo2(t1) + hi2(t1), s2 = lo2(t2) + hi2(t2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+      s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+    }
+    if constexpr (G > 1) {
+      if (lane == 0) red[warp][par] = make_float4(s0, s1, s2, 0.0f);
+      group_sync<G>(grp);
+      s0 = s1 = s2 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < G; ++w) {
+        const float4 t = red[grp * G + w][par];
+        s0 += t.x, s1 += t.y, s2 += t.z;
+      }
+    } else {
+      group_sync<G>(grp);
+    }
+    // every warp has read the row before this one
+    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+    const float m2 = rh * (s0 * inv);
+    const f2 n2 = pair(-m2), n3 = pair(a.post ? -fmaf(-m2, s2 * inv, s1 * inv) : 0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      qq[i] = fma2(n2, hh[i], qq[i]);
+      as[i] = fma2(qq[i], fh[i], as[i]);
+      fh[i] = mul2(pair(rf), fma2(fh[i], n3, mul2(c[i], qq[i])));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j] && p.dx) put<T, 8>(p.dx + r * a.lddx + col[j], qq, j);
+      if (in[j] && p.df) put<T, 8>(p.df + r * a.lddf + col[j], fh, j);
+    }
+    prev = st;
+    if (++st == q.stages) st = 0, phase ^= 1;
+  }
+  if (!a.pg && !a.ps) return;  // uniform over the grid
+  float* pg = a.pg ? a.pg + int64_t(blockIdx.x) * a.cols : nullptr;
+  float* ps = a.ps ? a.ps + int64_t(blockIdx.x) * a.cols : nullptr;
+  if constexpr (NG > 1) {
+    // group after group into shared memory (every copy has landed and been read), in order
+    float* sums = reinterpret_cast<float*>(ring);
+    __syncthreads();
+    for (int k = 0; k < NG; ++k) {
+      if (k == grp) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float2* p1 = reinterpret_cast<float2*>(sums + col[i / 4] + 2 * (i % 4));
+          float2* p2 = reinterpret_cast<float2*>(sums + C + col[i / 4] + 2 * (i % 4));
+          const float2 o = k ? *p1 : make_float2(0.0f, 0.0f), o2 = k ? *p2 : make_float2(0.0f, 0.0f);
+          *p1 = make_float2(o.x + lo2(ag[i]), o.y + hi2(ag[i]));
+          *p2 = make_float2(o2.x + lo2(as[i]), o2.y + hi2(as[i]));
+        }
+      }
+      __syncthreads();
+    }
+    for (int k = threadIdx.x; k < a.cols; k += blockDim.x) {
+      if (pg) pg[k] = sums[k];
+      if (ps) ps[k] = sums[C + k];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (in[j] && pg) put_sums<8>(pg + col[j], ag, j);
+      if (in[j] && ps) put_sums<8>(ps + col[j], as, j);
+    }
+  }
+}
+
 // The vectors' gradients from the parts of their column sums, in the parts' order: slices of
 // parts j, j + 32, ... by warp, then the slices in pairs.
 struct VecOut {
@@ -507,9 +797,52 @@ cudaError_t run_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaSt
   return cudaGetLastError();
 }
 
+template <typename T, int G, int NW, int MB, int R>
+cudaError_t run_fwd_ring(const T* x, const T* f, T* h, T* y, const FwdArgs& a, const RingArgs& q, cudaStream_t st) {
+  constexpr int NG = NW / G;
+  static DeviceOnce once;
+  auto kernel = join_fwd_ring<T, G, NW, MB, R>;
+  const cudaError_t attr = ring_smem(once, kernel);
+  if (attr != cudaSuccess) return attr;
+  int64_t blocks = (a.rows + R * NG - 1) / (R * NG);
+  if (blocks > MB * kSms) blocks = MB * kSms;
+  kernel<<<unsigned(blocks), 32 * NW, size_t(NG) * q.stages * q.stage_bytes, st>>>(x, f, h, y, a, q);
+  return cudaGetLastError();
+}
+
+// Warps per row of the ring that serves the forward pass, and rows per stage (0: no ring).
+// Enough rows that every group has several.
+int fwd_ring(int64_t rows, int64_t c, int esize, RingArgs& q, int& R) {
+  if (c % 8 != 0 || c <= 1024 || c > 8192) return 0;
+  const int G = c <= 2048 ? 4 : c <= 4096 ? 8 : 16;
+  const int nw = G == 16 ? 16 : 8, mb = G == 16 ? 1 : 2, row = int(c) * esize;
+  for (R = 2; R > 0; --R) {
+    q = make_ring(2 * R * row, row, nw / G, kRingBytes / mb);
+    if (q.stages >= 3) return rows >= int64_t(4) * R * kSms * mb * (nw / G) ? G : 0;
+  }
+  return 0;
+}
+int bwd_ring(int64_t rows, int64_t c, int esize, bool dh, RingArgs& q) {
+  // (binary32: half the columns per lane, else half as many stages would fit)
+  const int64_t lanes = esize == 4 ? 2 * c : c;
+  if (c % 8 != 0 || c <= 256 || lanes > 8192) return 0;
+  const int G = lanes <= 512 ? 1 : lanes <= 1024 ? 2 : lanes <= 2048 ? 4 : lanes <= 4096 ? 8 : 16;
+  const int row = int(c) * esize;
+  q = make_ring(row * (dh ? 4 : 3), row, 16 / G, kRingBytes);
+  return q.stages >= 3 && rows >= int64_t(4) * kSms * (16 / G) ? G : 0;
+}
+
 template <typename T>
 cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
+  if (a.vec && a.pvec && x && f && y) {
+    RingArgs q;
+    int R = 0;
+    const int G = fwd_ring(a.rows, c, sizeof(T), q, R);
+    if (G == 4) return R == 2 ? run_fwd_ring<T, 4, 8, 2, 2>(x, f, h, y, a, q, st) : run_fwd_ring<T, 4, 8, 2, 1>(x, f, h, y, a, q, st);
+    if (G == 8) return R == 2 ? run_fwd_ring<T, 8, 8, 2, 2>(x, f, h, y, a, q, st) : run_fwd_ring<T, 8, 8, 2, 1>(x, f, h, y, a, q, st);
+    if (G == 16) return R == 2 ? run_fwd_ring<T, 16, 16, 1, 2>(x, f, h, y, a, q, st) : run_fwd_ring<T, 16, 16, 1, 1>(x, f, h, y, a, q, st);
+  }
   const bool regs = a.rows <= 0x7FFFFFFF;  // the grid holds a block per (few) rows
   if (regs && a.vec && a.pvec && c % 8 == 0) {
     if (c <= 256) return run_fwd<T, 8, 1, 1, 2>(x, f, h, y, a, st);
@@ -544,10 +877,37 @@ cudaError_t run_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStream_
   return cudaGetLastError();
 }
 
+template <typename T, int NV, int G>
+cudaError_t run_bwd_ring(const BwdIn<T>& p, const BwdArgs& a, const RingArgs& q, int* parts, cudaStream_t st) {
+  constexpr int NG = 16 / G;
+  static DeviceOnce once;
+  const cudaError_t attr = ring_smem(once, join_bwd_ring<T, NV, G>);
+  if (attr != cudaSuccess) return attr;
+  int64_t blocks = (a.rows + NG - 1) / NG;
+  if (blocks > kSms) blocks = kSms;
+  *parts = int(blocks);
+  size_t smem = size_t(NG) * q.stages * q.stage_bytes;
+  if (NG > 1 && smem < size_t(2) * 32 * G * NV * 8 * 4) smem = size_t(2) * 32 * G * NV * 8 * 4;
+  join_bwd_ring<T, NV, G><<<unsigned(blocks), 512, smem, st>>>(p, a, q);
+  return cudaGetLastError();
+}
+
 // parts: the blocks that wrote column sums
 template <typename T>
 cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStream_t st) {
   const int64_t c = a.cols;
+  if (a.vec && a.pvec && p.dy && p.f) {
+    RingArgs q;
+    const int G = bwd_ring(a.rows, c, sizeof(T), p.dh != nullptr, q);
+    constexpr int NV = sizeof(T) == 4 ? 1 : 2;
+    if constexpr (NV == 2) {  // (binary32 rows of more than 256 columns take two warps)
+      if (G == 1) return run_bwd_ring<T, NV, 1>(p, a, q, parts, st);
+    }
+    if (G == 2) return run_bwd_ring<T, NV, 2>(p, a, q, parts, st);
+    if (G == 4) return run_bwd_ring<T, NV, 4>(p, a, q, parts, st);
+    if (G == 8) return run_bwd_ring<T, NV, 8>(p, a, q, parts, st);
+    if (G == 16) return run_bwd_ring<T, NV, 16>(p, a, q, parts, st);
+  }
   if (a.vec && a.pvec && c % 8 == 0) {
     if (c <= 256) return run_bwd<T, 8, 1, 1, true>(p, a, parts, st);
     if (c <= 512) return run_bwd<T, 8, 1, 2, true>(p, a, parts, st);
@@ -588,6 +948,13 @@ cudaError_t backward(const void* dy, const void* dh, const void* h, const void* 
 
 using namespace aqfq;
 using namespace aqfq::layer;
+
+extern "C" int32_t aqfq_selftest_block_norm_ring(int backward, int dtype, int64_t rows, int64_t cols, int dh) {
+  if (!view_ok(rows, cols, cols) || !dtype_ok(dtype)) return 0;
+  RingArgs q;
+  int R = 0;
+  return backward ? bwd_ring(rows, cols, esize(dtype), dh != 0, q) : fwd_ring(rows, cols, esize(dtype), q, R);
+}
 
 extern "C" aqfq_status aqfq_block_norm_fwd(int dtype, const void* x, int64_t ldx, const void* f,
                                            int64_t ldf, int64_t rows, int64_t cols, int post,

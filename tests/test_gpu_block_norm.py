@@ -189,6 +189,77 @@ def test_backward(dtype, pdtype, post):
             assert fx.intact() and fd.intact()
 
 
+# rows that the rings of shared memory serve: every number of warps per row, full and ragged
+# columns, a last stage with one row
+RINGS = [(2435, 4096, torch.bfloat16), (2433, 2600, torch.bfloat16), (4867, 2048, torch.bfloat16),
+         (4865, 1032, torch.bfloat16), (1217, 8192, torch.bfloat16), (1219, 4104, torch.bfloat16),
+         (1218, 4096, torch.float32), (4867, 1048, torch.float32), (613, 8192, torch.float32)]
+RINGS_BACK = [(1217, 4096, torch.bfloat16), (1220, 2056, torch.bfloat16), (2433, 2048, torch.bfloat16),
+              (4865, 1024, torch.bfloat16), (4870, 520, torch.bfloat16), (9730, 512, torch.bfloat16),
+              (9729, 264, torch.bfloat16), (609, 8192, torch.bfloat16), (610, 4104, torch.bfloat16),
+              (1219, 2048, torch.float32), (4867, 512, torch.float32), (2440, 1024, torch.float32),
+              (611, 4096, torch.float32)]
+
+
+@pytest.mark.parametrize("R,C,dtype", RINGS)
+def test_forward_from_a_ring(R, C, dtype):
+    G = aqfq.aqfq_selftest_block_norm_ring(False, dtype, R, C)
+    assert G == (4 if C <= 2048 else 8 if C <= 4096 else 16)
+    x, f, gpost, gate, gpre = inputs(R, C, 21, dtype, torch.bfloat16)
+    for post in (True, False):
+        fx, ff = Framed(R, C, dtype, 8, 8, x), Framed(R, C, dtype, 0, 0, f)
+        fh, fy = Framed(R, C, dtype, 16, 8), Framed(R, C, dtype, 0, 0)
+        rp, rq = (torch.full((R,), -1.0, device=DEV) for _ in range(2))
+        gp = gpost if post else None
+        kw = dict(post=post, gamma_post=None if gp is None else gp.to(DEV), gate=gate.to(DEV), alpha=0.5,
+                  gamma_pre=gpre.to(DEV), rstd_post=rp if post else None)
+        aqfq.aqfq_block_norm_fwd(fx.view, ff.view, EPS, h=fh.view, y=fy.view, rstd_pre=rq, **kw)
+        only = torch.empty(R, C, dtype=dtype, device=DEV)
+        aqfq.aqfq_block_norm_fwd(fx.view, ff.view, EPS, y=only, **kw)
+        torch.cuda.synchronize()
+        ref = forward64(x, f, post, gp, gate, 0.5, gpre, EPS, C)
+        check(fh.view, ref["h"], dtype, f"h {R}x{C}")
+        check(fy.view, ref["y"], dtype, f"y {R}x{C}")
+        check(rq, ref["rstd_pre"], None, "rstd_pre")
+        if post:
+            check(rp, ref["rstd_post"], None, "rstd_post")
+        assert fh.intact() and fy.intact() and torch.equal(only, fy.view)
+
+
+@pytest.mark.parametrize("R,C,dtype", RINGS_BACK)
+@pytest.mark.parametrize("post", [True, False])
+def test_backward_from_a_ring(R, C, dtype, post):
+    x, f, gpost, gate, gpre = inputs(R, C, 31, dtype, torch.float32)
+    gpost = gpost if post else None
+    ref = forward64(x, f, post, gpost, gate, 0.5, gpre, EPS, C)
+    h = ref["h"][0].to(dtype)
+    rq = ref["rstd_pre"][0].float().to(DEV)
+    rp = ref["rstd_post"][0].float().to(DEV) if post else None
+    dy, dh0 = (randn((R, C), 900 + k, dtype=torch.float32).to(dtype) for k in (0, 40))
+    for dh in (dh0, None):
+        G = aqfq.aqfq_selftest_block_norm_ring(True, dtype, R, C, dh is not None)
+        per = 512 if dtype == torch.bfloat16 else 256
+        assert G == next(g for g in (1, 2, 4, 8, 16) if C <= per * g)
+        fr = {n: None if t is None else Framed(R, C, dtype, 8 * k, 8, t)
+              for k, (n, t) in enumerate((("dy", dy), ("dh", dh), ("h", h), ("f", f)))}
+        fx, fd = Framed(R, C, dtype, 8, 8), Framed(R, C, dtype, 0, 0)
+        vec = torch.full((3, C), float("nan"), device=DEV)
+        view = lambda n: None if fr[n] is None else fr[n].view
+        aqfq.aqfq_block_norm_bwd(view("dy"), view("dh"), view("h"), view("f"), rstd_post=rp, rstd_pre=rq,
+                                 gamma_post=None if gpost is None else gpost.to(DEV), gate=gate.to(DEV), alpha=0.5,
+                                 gamma_pre=gpre.to(DEV), dx=fx.view, df=fd.view, dgate=vec[0],
+                                 dgamma_post=vec[1] if post else None, dgamma_pre=vec[2],
+                                 workspace=ws(aqfq.aqfq_block_norm_bwd_workspace_bytes(R, C)))
+        torch.cuda.synchronize()
+        want = bwd64(dy, dh, h, f, rp, rq, gpost, gate, 0.5, gpre, R, C)
+        check(fx.view, want["dx"], dtype, f"dx {R}x{C}")
+        check(fd.view, want["df"], dtype, f"df {R}x{C}")
+        for k, n in enumerate(("dgate", "dgamma_post", "dgamma_pre")):
+            if n != "dgamma_post" or post:
+                check(vec[k], want[n], None, f"{n} {R}x{C}")
+        assert fx.intact() and fd.intact()
+
+
 def test_parts_of_the_call():
     """Without a residual, without a block (a plain norm), h or y alone; the same bits as together."""
     R, C = 9, 640
