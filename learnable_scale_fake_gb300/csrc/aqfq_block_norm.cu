@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
 // ---------------------------------------------------------------------------
 // Many rows: persistent blocks whose rows arrive by bulk asynchronous copies, as in the
 // layer norm (aqfq_norm.cu): a group of G warps owns a ring of stages, R rows of x and of f
-// each, a lane two vectors of 8 columns; after the barrier of a turn's first sum every warp
-// has read the stage before, which one thread then refills.  A wait gives up after about a
-// second; the rows left are then written as NaN.
+// each, a lane two vectors of 8 columns; after the barrier of a turn's last sum every warp
+// has read the stage, which one thread then refills.  A wait gives up after about a second;
+// the rows left are then written as NaN.
 // ---------------------------------------------------------------------------
 template <typename T, int G, int NW, int MB, int R>
 __global__ void __launch_bounds__(32 * NW, MB)
@@ -292,13 +292,13 @@ __global__ void __launch_bounds__(32 * NW, MB)
   f2 c[P], g[P];
   coefs<8, 2>(a.c, a.pdtype, col, in, c);
   params<8, 2>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
-  int st = 0, prev = q.stages - 1;
+  int st = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (bool first = true; r < a.rows; r += step, first = false) {
+  for (; r < a.rows; r += step) {
     if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
-      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, true, r, step, a.rows));
     }
     const uint8_t* stage = mine + st * q.stage_bytes;
     f2 v[R][P];
@@ -318,7 +318,6 @@ __global__ void __launch_bounds__(32 * NW, MB)
         s[k] = lo2(t) + hi2(t);
       }
       group_sum2<G>(s, red[grp][0], grp);
-      if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
 #pragma unroll
       for (int k = 0; k < R; ++k) s[k] = rsqrtf(fmaf(s[k], inv, a.eps));
       if (wr == 0 && lane < R && r + lane < a.rows && a.rstd_post) a.rstd_post[r + lane] = lane ? s[1] : s[0];
@@ -342,7 +341,8 @@ __global__ void __launch_bounds__(32 * NW, MB)
       }
     }
     group_sum2<G>(s, red[grp][1], grp);
-    if (!a.post && loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
+    // every warp has read these rows
+    if (loader && ok) fetch(r + q.stages * step, st);
 #pragma unroll
     for (int k = 0; k < R; ++k) s[k] = rsqrtf(fmaf(s[k], inv, a.eps));
     if (wr == 0 && lane < R && r + lane < a.rows && a.rstd_pre) a.rstd_pre[r + lane] = lane ? s[1] : s[0];
@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(32 * NW, MB)
       for (int j = 0; j < 2; ++j)
         if (in[j]) put<T, 8>(y + (r + k) * a.ldy + col[j], v[k], j);
     }
-    prev = st;
     if (++st == q.stages) st = 0, phase ^= 1;
   }
 }
@@ -578,15 +577,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
   }
 }
 
-// Many rows: a ring as forward, one row of dy, h, f and (where there is one) dh per stage;
-// one reduction of three sums per row.
+// The totals of four values over a warp: at each of two steps a lane hands half of its values
+// to its partner and keeps the other half, so that six exchanges serve all of them.  Returns
+// the total of value lane / 8.
+__device__ __forceinline__ float warp_totals4(float v0, float v1, float v2, float v3) {
+  const int lane = threadIdx.x & 31;
+  const bool a = lane & 16, b = lane & 8;
+  const float x = (a ? v2 : v0) + __shfl_xor_sync(0xFFFFFFFFu, a ? v0 : v2, 16);
+  const float y = (a ? v3 : v1) + __shfl_xor_sync(0xFFFFFFFFu, a ? v1 : v3, 16);
+  float t = (b ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, b ? x : y, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  return t;
+}
+
+// 16 bytes of shared memory (volatile: the copies that fill them are not the compiler's)
+__device__ __forceinline__ uint4 lds128(uint32_t s) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(s) : "memory");
+  return x;
+}
+
+// Many rows: a ring as forward, one row of dy, h, f and (where there is one) dh per stage; one
+// reduction of three sums per row.  Lanes beyond the row read zeros and have zero factors, so
+// that nothing is masked.
+// (Two rows per turn: 8192 x 4096 in BF16 98 us instead of 80, the registers are full.)
 template <typename T, int NV, int G>
 __global__ void __launch_bounds__(512, 1)
     join_bwd_ring(const BwdIn<T> p, const BwdArgs a, const RingArgs q) {
   constexpr int NG = 16 / G, P = NV * 4, C = 32 * G * NV * 8;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[NG][kMaxStages];
-  __shared__ float4 red[16][2];  // [warp][parity]
+  __shared__ float4 red[2][16];  // [parity][warp]: three sums
+  __shared__ __align__(16) uint4 zeros[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp / G, wr = warp % G;
   uint8_t* mine = ring + size_t(grp) * q.stages * q.stage_bytes;
@@ -594,12 +617,15 @@ __global__ void __launch_bounds__(512, 1)
     for (int g = 0; g < NG; ++g)
       for (int i = 0; i < q.stages; ++i) sm100::mbar_init(&full[g][i], 1);
     sm100::fence_barrier_init();
+    zeros[0] = zeros[1] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
+  const uint32_t mine0 = sm100::smem_u32(mine);
   const int64_t step = int64_t(gridDim.x) * NG;
   int64_t r = int64_t(blockIdx.x) * NG + grp;
   const bool loader = wr == 0 && lane == 0;
   const uint32_t n = uint32_t(q.row_bytes);
+  // a stage: dy, h, f, dh
   auto fetch = [&](int64_t row, int st) {
     if (row < a.rows) {
       uint64_t* bar = &full[grp][st];
@@ -614,18 +640,38 @@ __global__ void __launch_bounds__(512, 1)
   if (loader)
     for (int i = 0; i < q.stages; ++i) fetch(r + i * step, i);
   const float inv = 1.0f / float(a.cols);
-  int cl[NV];
   int64_t col[NV];
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     col[j] = (wr * NV * 32 + j * 32 + lane) * 8;
     in[j] = col[j] < a.cols;
-    cl[j] = in[j] ? int(col[j]) : 0;
   }
   f2 g[P], c[P], ag[P] = {}, as[P] = {};
-  params<8, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  params<8, NV>(a.gamma_pre, a.pdtype, col, in, 0.0f, g);
+  if (!a.gamma_pre) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) g[i] = pair(1.0f);
+  }
   coefs<8, NV>(a.c, a.pdtype, col, in, c);
+  // this lane's pairs of the tensor at shared address `row`
+  const uint32_t nothing = sm100::smem_u32(zeros);
+  auto pairs = [&](uint32_t row, f2 (&v)[P]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint32_t s = in[j] ? row + uint32_t(col[j]) * uint32_t(sizeof(T)) : nothing;
+      const uint4 x = lds128(s);
+      if constexpr (sizeof(T) == 2) {
+        v[4 * j] = bf2(x.x), v[4 * j + 1] = bf2(x.y), v[4 * j + 2] = bf2(x.z), v[4 * j + 3] = bf2(x.w);
+      } else {
+        const uint4 z = lds128(s + 16);
+        v[4 * j] = mk2(__uint_as_float(x.x), __uint_as_float(x.y));
+        v[4 * j + 1] = mk2(__uint_as_float(x.z), __uint_as_float(x.w));
+        v[4 * j + 2] = mk2(__uint_as_float(z.x), __uint_as_float(z.y));
+        v[4 * j + 3] = mk2(__uint_as_float(z.z), __uint_as_float(z.w));
+      }
+    }
+  };
   // the row's scalars are fetched one row ahead
   float rh_n = 0.0f, rf_n = 1.0f;
   auto scalars = [&](int64_t row) {
@@ -635,82 +681,77 @@ __global__ void __launch_bounds__(512, 1)
     }
   };
   scalars(r);
-  int st = 0, prev = q.stages - 1, par = 0;
+  T* dx = p.dx ? p.dx + r * a.lddx : nullptr;
+  T* df = p.df ? p.df + r * a.lddf : nullptr;
+  const int64_t xstep = step * a.lddx, fstep = step * a.lddf;
+  int st = 0, par = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (bool first = true; r < a.rows; r += step, first = false, par ^= 1) {
+  for (; r < a.rows; r += step, par ^= 1) {
     const float rh = rh_n, rf = rf_n;
     scalars(r + step);
     if (ok && !sm100::mbar_test(&full[grp][st], phase)) {
       ok = sm100::mbar_wait_suspend(&full[grp][st], phase);
-      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, first, r, step, a.rows));
+      if (!ok && loader) sm100::drain_ring(full[grp], q.stages, st, phase, in_flight(q.stages, true, r, step, a.rows));
     }
-    const uint8_t* stage = mine + st * q.stage_bytes;
+    const uint32_t stage = mine0 + uint32_t(st * q.stage_bytes);
     f2 qq[P], hh[P], fh[P], t0 = 0, t1 = 0, t2 = 0;
     {
       f2 d[P];
-      smem_pairs<true, T, NV>(stage, cl, in, d);
-      smem_pairs<true, T, NV>(stage + n, cl, in, hh);
+      pairs(stage, d);
+      pairs(stage + n, hh);
       if (!ok) d[0] = hh[0] = pair(__int_as_float(0x7FC00000));
       if (p.dh) {
-        smem_pairs<true, T, NV>(stage + 3 * n, cl, in, qq);
+        pairs(stage + 3 * n, qq);
       } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) qq[i] = 0;
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        // zero beyond the row, also where a factor is infinite
-        hh[i] = masked<8, NV>(mul2(hh[i], pair(rh)), i, in);
+        const f2 rl = pair(in[i / 4] ? rh : 0.0f);
+        hh[i] = mul2(hh[i], rl);
         ag[i] = fma2(d[i], hh[i], ag[i]);
         const f2 u = mul2(d[i], g[i]);
-        qq[i] = masked<8, NV>(fma2(pair(rh), u, qq[i]), i, in);
+        qq[i] = fma2(rl, u, qq[i]);
         t0 = fma2(u, hh[i], t0);
       }
     }
-    smem_pairs<true, T, NV>(stage + 2 * n, cl, in, fh);
+    pairs(stage + 2 * n, fh);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      fh[i] = masked<8, NV>(mul2(fh[i], pair(rf)), i, in);
+      fh[i] = mul2(fh[i], pair(in[i / 4] ? rf : 0.0f));
       const f2 cf = mul2(c[i], fh[i]);
       t1 = fma2(cf, qq[i], t1);
       t2 = fma2(cf, hh[i], t2);
     }
-    float s0 = lo2(t0) + hi2(t0), s1 = lo2(t1) + hi2(t1), s2 = lo2(t2) + hi2(t2);
+    const float mine_sum = warp_totals4(lo2(t0) + hi2(t0), lo2(t1) + hi2(t1), lo2(t2) + hi2(t2), 0.0f);
+    if ((lane & 7) == 0) reinterpret_cast<float*>(&red[par][warp])[lane >> 3] = mine_sum;
+    group_sync<G>(grp);
+    // every warp has read the row
+    if (loader && ok) fetch(r + q.stages * step, st);
+    f2 s01 = 0, s2 = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
-      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
-      s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+    for (int w = 0; w < G; ++w) {
+      const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(&red[par][grp * G + w]);
+      s01 = add2(s01, t.x);
+      s2 = add2(s2, t.y);
     }
-    if constexpr (G > 1) {
-      if (lane == 0) red[warp][par] = make_float4(s0, s1, s2, 0.0f);
-      group_sync<G>(grp);
-      s0 = s1 = s2 = 0.0f;
-#pragma unroll
-      for (int w = 0; w < G; ++w) {
-        const float4 t = red[grp * G + w][par];
-        s0 += t.x, s1 += t.y, s2 += t.z;
-      }
-    } else {
-      group_sync<G>(grp);
-    }
-    // every warp has read the row before this one
-    if (loader && !first && ok) fetch(r + (q.stages - 1) * step, prev);
-    const float m2 = rh * (s0 * inv);
-    const f2 n2 = pair(-m2), n3 = pair(a.post ? -fmaf(-m2, s2 * inv, s1 * inv) : 0.0f);
+    const float m2 = rh * (lo2(s01) * inv);
+    const f2 n2 = pair(-m2), n3 = pair(a.post ? -fmaf(-m2, lo2(s2) * inv, hi2(s01) * inv) : 0.0f), rr = pair(rf);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       qq[i] = fma2(n2, hh[i], qq[i]);
       as[i] = fma2(qq[i], fh[i], as[i]);
-      fh[i] = mul2(pair(rf), fma2(fh[i], n3, mul2(c[i], qq[i])));
+      fh[i] = mul2(rr, fma2(fh[i], n3, mul2(c[i], qq[i])));
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (in[j] && p.dx) put<T, 8>(p.dx + r * a.lddx + col[j], qq, j);
-      if (in[j] && p.df) put<T, 8>(p.df + r * a.lddf + col[j], fh, j);
+      if (in[j] && dx) put<T, 8>(dx + col[j], qq, j);
+      if (in[j] && df) put<T, 8>(df + col[j], fh, j);
     }
-    prev = st;
+    if (dx) dx += xstep;
+    if (df) df += fstep;
     if (++st == q.stages) st = 0, phase ^= 1;
   }
   if (!a.pg && !a.ps) return;  // uniform over the grid
@@ -822,11 +863,11 @@ int fwd_ring(int64_t rows, int64_t c, int esize, RingArgs& q, int& R) {
   }
   return 0;
 }
+// A lane has 8 columns, 16 of rows wider than 4096 (with 16 throughout, 8192 x 4096 in BF16
+// took 90 us instead of 80: spilled registers, and binary32 rows had too few stages).
 int bwd_ring(int64_t rows, int64_t c, int esize, bool dh, RingArgs& q) {
-  // (binary32: half the columns per lane, else half as many stages would fit)
-  const int64_t lanes = esize == 4 ? 2 * c : c;
-  if (c % 8 != 0 || c <= 256 || lanes > 8192) return 0;
-  const int G = lanes <= 512 ? 1 : lanes <= 1024 ? 2 : lanes <= 2048 ? 4 : lanes <= 4096 ? 8 : 16;
+  if (c % 8 != 0 || c <= 256 || c > 8192) return 0;
+  const int G = c <= 512 ? 2 : c <= 1024 ? 4 : c <= 2048 ? 8 : 16;
   const int row = int(c) * esize;
   q = make_ring(row * (dh ? 4 : 3), row, 16 / G, kRingBytes);
   return q.stages >= 3 && rows >= int64_t(4) * kSms * (16 / G) ? G : 0;
@@ -899,14 +940,11 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
   if (a.vec && a.pvec && p.dy && p.f) {
     RingArgs q;
     const int G = bwd_ring(a.rows, c, sizeof(T), p.dh != nullptr, q);
-    constexpr int NV = sizeof(T) == 4 ? 1 : 2;
-    if constexpr (NV == 2) {  // (binary32 rows of more than 256 columns take two warps)
-      if (G == 1) return run_bwd_ring<T, NV, 1>(p, a, q, parts, st);
-    }
-    if (G == 2) return run_bwd_ring<T, NV, 2>(p, a, q, parts, st);
-    if (G == 4) return run_bwd_ring<T, NV, 4>(p, a, q, parts, st);
-    if (G == 8) return run_bwd_ring<T, NV, 8>(p, a, q, parts, st);
-    if (G == 16) return run_bwd_ring<T, NV, 16>(p, a, q, parts, st);
+    if (G > 0 && c > 4096) return run_bwd_ring<T, 2, 16>(p, a, q, parts, st);
+    if (G == 2) return run_bwd_ring<T, 1, 2>(p, a, q, parts, st);
+    if (G == 4) return run_bwd_ring<T, 1, 4>(p, a, q, parts, st);
+    if (G == 8) return run_bwd_ring<T, 1, 8>(p, a, q, parts, st);
+    if (G == 16) return run_bwd_ring<T, 1, 16>(p, a, q, parts, st);
   }
   if (a.vec && a.pvec && c % 8 == 0) {
     if (c <= 256) return run_bwd<T, 8, 1, 1, true>(p, a, parts, st);
