@@ -37,15 +37,41 @@ struct FwdArgs {
   bool vec, pvec;
 };
 
+// A lane's vectors of a row, all loads under way at once: a vector beyond the row reads the
+// row's first one instead (each behind a branch of its own, the 2-byte loads of 4096 x 5001
+// in BF16 waited for one another: 390 us forward), and masked() drops it.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void load_cols(Row<T, V, NV>& w, const T* p, const int64_t (&cl)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) w.load(j, p + cl[j]);
+}
+// a lane's pairs of a parameter vector (of any value beyond the row); NULL gives ones
 template <int V, int NV>
-__device__ __forceinline__ void coefs(const Coef& c, int pdtype, const int64_t (&col)[NV],
-                                      const bool (&in)[NV], f2 (&v)[NV * V / 2]) {
-  params<V, NV>(c.gate, pdtype, col, in, 1.0f, v);
+__device__ __forceinline__ void vector_pairs(const void* p, int pdtype, const int64_t (&cl)[NV],
+                                             f2 (&v)[NV * V / 2]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = pair(1.0f);
+  } else if (pdtype == AQFQ_BF16) {
+    Row<bf16, V, NV> w;
+    load_cols(w, static_cast<const bf16*>(p), cl);
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
+  } else {
+    Row<float, V, NV> w;
+    load_cols(w, static_cast<const float*>(p), cl);
+#pragma unroll
+    for (int i = 0; i < NV * V / 2; ++i) v[i] = w.pair_at(i);
+  }
+}
+template <int V, int NV>
+__device__ __forceinline__ void coefs(const Coef& c, int pdtype, const int64_t (&cl)[NV], f2 (&v)[NV * V / 2]) {
+  vector_pairs<V, NV>(c.gate, pdtype, cl, v);
 #pragma unroll
   for (int i = 0; i < NV * V / 2; ++i) v[i] = mul2(v[i], pair(c.alpha));
   if (c.gamma_post) {
     f2 g[NV * V / 2];
-    params<V, NV>(c.gamma_post, pdtype, col, in, 1.0f, g);
+    vector_pairs<V, NV>(c.gamma_post, pdtype, cl, g);
 #pragma unroll
     for (int i = 0; i < NV * V / 2; ++i) v[i] = mul2(v[i], g[i]);
   }
@@ -152,22 +178,26 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
   const float inv = 1.0f / float(a.cols);
   const int64_t r0 = (int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0)) * R;
   if (G == 1 && r0 >= a.rows) return;
-  int64_t col[NV];
+  int64_t col[NV], cl[NV];
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     col[j] = ((G == 1 ? 0 : int64_t(warp) * (NV * 32)) + j * 32 + lane) * V;
     in[j] = col[j] < a.cols;
+    cl[j] = in[j] ? col[j] : 0;
   }
   Row<T, V, NV> rx[R], rf[R];
+  if (f) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) load_cols(rf[k], f + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldf, cl);
+  }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    const int64_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
+    if (x) {
+      load_cols(rx[k], x + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldx, cl);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      rx[k].zero(j), rf[k].zero(j);
-      if (in[j] && f) rf[k].load(j, f + r * a.ldf + col[j]);
-      if (in[j] && x) rx[k].load(j, x + r * a.ldx + col[j]);
+      for (int j = 0; j < NV; ++j) rx[k].zero(j);
     }
   }
   f2 v[R][P];
@@ -178,7 +208,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
       f2 t = 0;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        v[k][i] = rf[k].pair_at(i);
+        v[k][i] = masked<V, NV>(rf[k].pair_at(i), i, in);
         t = fma2(v[k][i], v[k][i], t);
       }
       s[k] = lo2(t) + hi2(t);
@@ -193,7 +223,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
       }
     }
     f2 c[P];
-    coefs<V, NV>(a.c, a.pdtype, col, in, c);
+    coefs<V, NV>(a.c, a.pdtype, cl, c);
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -203,7 +233,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[k][i] = rx[k].pair_at(i);
+      for (int i = 0; i < P; ++i) v[k][i] = masked<V, NV>(rx[k].pair_at(i), i, in);
   }
   if (h) {
 #pragma unroll
@@ -224,7 +254,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
   }
   row_sums<R, G>(s, red[1]);
   f2 g[P];
-  params<V, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  vector_pairs<V, NV>(a.gamma_pre, a.pdtype, cl, g);
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     if (r0 + k >= a.rows) break;
@@ -289,9 +319,10 @@ __global__ void __launch_bounds__(32 * NW, MB)
     in[j] = col[j] < a.cols;
     cl[j] = in[j] ? int(col[j]) : 0;
   }
+  const int64_t cl64[2] = {cl[0], cl[1]};
   f2 c[P], g[P];
-  coefs<8, 2>(a.c, a.pdtype, col, in, c);
-  params<8, 2>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
+  coefs<8, 2>(a.c, a.pdtype, cl64, c);
+  vector_pairs<8, 2>(a.gamma_pre, a.pdtype, cl64, g);
   int st = 0;
   uint32_t phase = 0;
   bool ok = true;
@@ -453,18 +484,17 @@ struct JoinRow {
   Row<T, V, NV> dy, dh, h, f;
   float rh, rf;
   // r: a row that exists
-  __device__ __forceinline__ void load(const BwdIn<T>& p, const BwdArgs& a, int64_t r,
-                                       const int64_t (&col)[NV], const bool (&in)[NV]) {
+  __device__ __forceinline__ void load(const BwdIn<T>& p, const BwdArgs& a, int64_t r, const int64_t (&cl)[NV]) {
     rh = p.dy ? __ldg(a.rstd_pre + r) : 0.0f, rf = a.post ? __ldg(a.rstd_post + r) : 1.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      dy.zero(j), dh.zero(j), h.zero(j), f.zero(j);
-      if (in[j]) {
-        if (p.dy) dy.load(j, p.dy + r * a.lddy + col[j]), h.load(j, p.h + r * a.ldh + col[j]);
-        if (p.dh) dh.load(j, p.dh + r * a.lddh + col[j]);
-        if (p.f) f.load(j, p.f + r * a.ldf + col[j]);
-      }
+      if (!p.dy) dy.zero(j), h.zero(j);
+      if (!p.dh) dh.zero(j);
+      if (!p.f) f.zero(j);
     }
+    if (p.dy) load_cols(dy, p.dy + r * a.lddy, cl), load_cols(h, p.h + r * a.ldh, cl);
+    if (p.f) load_cols(f, p.f + r * a.ldf, cl);
+    if (p.dh) load_cols(dh, p.dh + r * a.lddh, cl);
   }
 };
 
@@ -480,24 +510,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ng = int(blockDim.x) / (32 * G), grp = warp / G, wr = warp % G;
   const float inv = 1.0f / float(a.cols);
-  int64_t col[NV];
+  int64_t col[NV], cl[NV];
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     col[j] = (int64_t(wr) * (NV * 32) + j * 32 + lane) * V;
     in[j] = col[j] < a.cols;
+    cl[j] = in[j] ? col[j] : 0;
   }
   f2 g[P], c[P], ag[P] = {}, as[P] = {};
-  params<V, NV>(a.gamma_pre, a.pdtype, col, in, 1.0f, g);
-  coefs<V, NV>(a.c, a.pdtype, col, in, c);
+  vector_pairs<V, NV>(a.gamma_pre, a.pdtype, cl, g);
+  coefs<V, NV>(a.c, a.pdtype, cl, c);
   const int64_t step = int64_t(gridDim.x) * ng;
   int64_t r = int64_t(blockIdx.x) * ng + grp;
   JoinRow<T, V, NV> cur;
-  if (r < a.rows) cur.load(p, a, r, col, in);
+  if (r < a.rows) cur.load(p, a, r, cl);
   int par = 0;
   for (; r < a.rows; r += step, par ^= 1) {
     JoinRow<T, V, NV> nxt;
-    if constexpr (PF) nxt.load(p, a, r + step < a.rows ? r + step : r, col, in);
+    if constexpr (PF) nxt.load(p, a, r + step < a.rows ? r + step : r, cl);
     const f2 rh = pair(cur.rh), rf = pair(cur.rf);
     f2 hh[P], fh[P], q[P], t0 = 0, t1 = 0, t2 = 0;
 #pragma unroll
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
       // zero beyond the row, also where a factor is infinite
       hh[i] = masked<V, NV>(mul2(cur.h.pair_at(i), rh), i, in);
       fh[i] = masked<V, NV>(mul2(cur.f.pair_at(i), rf), i, in);
-      const f2 d = cur.dy.pair_at(i), u = mul2(d, g[i]), cf = mul2(c[i], fh[i]);
+      const f2 d = masked<V, NV>(cur.dy.pair_at(i), i, in), u = mul2(d, g[i]), cf = mul2(c[i], fh[i]);
       ag[i] = fma2(d, hh[i], ag[i]);
       q[i] = masked<V, NV>(fma2(rh, u, cur.dh.pair_at(i)), i, in);
       t0 = fma2(u, hh[i], t0);
@@ -543,7 +574,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
       if (in[j] && p.df) put<T, V>(p.df + r * a.lddf + col[j], fh, j);
     }
     if constexpr (PF) cur = nxt;
-    else if (r + step < a.rows) cur.load(p, a, r + step, col, in);
+    else if (r + step < a.rows) cur.load(p, a, r + step, cl);
   }
   if (!a.pg && !a.ps) return;  // uniform over the grid
   float* pg = a.pg ? a.pg + int64_t(blockIdx.x) * a.cols : nullptr;
@@ -647,13 +678,16 @@ __global__ void __launch_bounds__(512, 1)
     col[j] = (wr * NV * 32 + j * 32 + lane) * 8;
     in[j] = col[j] < a.cols;
   }
-  f2 g[P], c[P], ag[P] = {}, as[P] = {};
-  params<8, NV>(a.gamma_pre, a.pdtype, col, in, 0.0f, g);
-  if (!a.gamma_pre) {
+  int64_t cl[NV];
 #pragma unroll
-    for (int i = 0; i < P; ++i) g[i] = pair(1.0f);
+  for (int j = 0; j < NV; ++j) cl[j] = in[j] ? col[j] : 0;
+  f2 g[P], c[P], ag[P] = {}, as[P] = {};
+  vector_pairs<8, NV>(a.gamma_pre, a.pdtype, cl, g);
+  coefs<8, NV>(a.c, a.pdtype, cl, c);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {  // finite beyond the row
+    if (!in[i / 4]) g[i] = c[i] = 0;
   }
-  coefs<8, NV>(a.c, a.pdtype, col, in, c);
   // this lane's pairs of the tensor at shared address `row`
   const uint32_t nothing = sm100::smem_u32(zeros);
   auto pairs = [&](uint32_t row, f2 (&v)[P]) {
@@ -864,10 +898,11 @@ int fwd_ring(int64_t rows, int64_t c, int esize, RingArgs& q, int& R) {
   return 0;
 }
 // A lane has 8 columns, 16 of rows wider than 4096 (with 16 throughout, 8192 x 4096 in BF16
-// took 90 us instead of 80: spilled registers, and binary32 rows had too few stages).
+// took 90 us instead of 80: spilled registers, and binary32 rows had too few stages).  Rows of
+// 1024 columns and fewer are as fast in registers: 16384 x 512 26.5 us against 27.1.
 int bwd_ring(int64_t rows, int64_t c, int esize, bool dh, RingArgs& q) {
-  if (c % 8 != 0 || c <= 256 || c > 8192) return 0;
-  const int G = c <= 512 ? 2 : c <= 1024 ? 4 : c <= 2048 ? 8 : 16;
+  if (c % 8 != 0 || c <= 1024 || c > 8192) return 0;
+  const int G = c <= 2048 ? 8 : 16;
   const int row = int(c) * esize;
   q = make_ring(row * (dh ? 4 : 3), row, 16 / G, kRingBytes);
   return q.stages >= 3 && rows >= int64_t(4) * kSms * (16 / G) ? G : 0;
@@ -941,8 +976,6 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
     RingArgs q;
     const int G = bwd_ring(a.rows, c, sizeof(T), p.dh != nullptr, q);
     if (G > 0 && c > 4096) return run_bwd_ring<T, 2, 16>(p, a, q, parts, st);
-    if (G == 2) return run_bwd_ring<T, 1, 2>(p, a, q, parts, st);
-    if (G == 4) return run_bwd_ring<T, 1, 4>(p, a, q, parts, st);
     if (G == 8) return run_bwd_ring<T, 1, 8>(p, a, q, parts, st);
     if (G == 16) return run_bwd_ring<T, 1, 16>(p, a, q, parts, st);
   }
@@ -959,6 +992,7 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
     if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(p, a, parts, st);
     if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(p, a, parts, st);
     if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(p, a, parts, st);
+    if (c <= 8192) return run_bwd<T, 1, 16, 16, false>(p, a, parts, st);
   }
   const int64_t blocks = a.rows < kSms ? a.rows : kSms;
   *parts = int(blocks);
