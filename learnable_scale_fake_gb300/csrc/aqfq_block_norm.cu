@@ -167,17 +167,21 @@ __device__ __forceinline__ void row_sums(float (&s)[R], float (&red)[R][G]) {
 
 // ---------------------------------------------------------------------------
 // Rows held in registers (columns as in the layer norm): a row belongs to G warps, a block
-// takes R rows (G = 1: each of its four warps does), whose loads are all under way first.
+// takes R rows at a time (G = 1: each of its four warps does), whose loads are all under way
+// first, and keeps its columns' parameters while it walks down the rows.
 // ---------------------------------------------------------------------------
+template <int V, int G>
+constexpr int rows_threads = G == 1 ? 128 : 32 * G;
+// threads of an SM: single elements leave more to wait for per byte
+template <int V, int G>
+constexpr int rows_blocks = (V == 1 ? 1024 : 512) / rows_threads<V, G>;
 template <typename T, int V, int NV, int G, int R>
-__global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
+__global__ void __launch_bounds__(rows_threads<V, G>, rows_blocks<V, G>)
     join_fwd_rows(const T* x, const T* f, T* h, T* y, const FwdArgs a) {
   constexpr int RB = G == 1 ? 4 : 1, P = NV * V / 2;
-  __shared__ float red[2][R][G];
+  __shared__ float red[2][2][R][G];  // [parity of the turn][sum]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv = 1.0f / float(a.cols);
-  const int64_t r0 = (int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0)) * R;
-  if (G == 1 && r0 >= a.rows) return;
   int64_t col[NV], cl[NV];
   bool in[NV];
 #pragma unroll
@@ -186,85 +190,91 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G)
     in[j] = col[j] < a.cols;
     cl[j] = in[j] ? col[j] : 0;
   }
-  Row<T, V, NV> rx[R], rf[R];
-  if (f) {
+  const bool writer = lane == 0 && (G == 1 || warp == 0);
+  f2 c[P], g[P];
+  int par = 0;
+  for (int64_t r0 = (int64_t(blockIdx.x) * RB + (G == 1 ? warp : 0)) * R, first = 1; r0 < a.rows;
+       r0 += int64_t(gridDim.x) * RB * R, first = 0, par ^= 1) {
+    Row<T, V, NV> rx[R], rf[R];
+    if (f) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) load_cols(rf[k], f + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldf, cl);
-  }
+      for (int k = 0; k < R; ++k) load_cols(rf[k], f + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldf, cl);
+    }
 #pragma unroll
-  for (int k = 0; k < R; ++k) {
-    if (x) {
-      load_cols(rx[k], x + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldx, cl);
+    for (int k = 0; k < R; ++k) {
+      if (x) {
+        load_cols(rx[k], x + (r0 + k < a.rows ? r0 + k : a.rows - 1) * a.ldx, cl);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) rx[k].zero(j);
+      }
+    }
+    if (first) {
+      if (f) coefs<V, NV>(a.c, a.pdtype, cl, c);
+      if (y) vector_pairs<V, NV>(a.gamma_pre, a.pdtype, cl, g);
+    }
+    f2 v[R][P];
+    float s[R], scale[R];
+    if (f) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        f2 t = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          v[k][i] = masked<V, NV>(rf[k].pair_at(i), i, in);
+          t = fma2(v[k][i], v[k][i], t);
+        }
+        s[k] = lo2(t) + hi2(t);
+        scale[k] = 1.0f;
+      }
+      if (a.post) {
+        row_sums<R, G>(s, red[par][0]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+          if (a.rstd_post && writer && r0 + k < a.rows) a.rstd_post[r0 + k] = scale[k];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          v[k][i] = masked<V, NV>(fma2(mul2(v[k][i], pair(scale[k])), c[i], rx[k].pair_at(i)), i, in);
     } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) rx[k].zero(j);
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[k][i] = masked<V, NV>(rx[k].pair_at(i), i, in);
     }
-  }
-  f2 v[R][P];
-  float s[R], scale[R];
-  if (f) {
+    if (h) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (r0 + k >= a.rows) break;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (in[j]) put<T, V>(h + (r0 + k) * a.ldh + col[j], v[k], j);
+      }
+    }
+    if (!y) continue;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       f2 t = 0;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        v[k][i] = masked<V, NV>(rf[k].pair_at(i), i, in);
-        t = fma2(v[k][i], v[k][i], t);
-      }
+      for (int i = 0; i < P; ++i) t = fma2(v[k][i], v[k][i], t);
       s[k] = lo2(t) + hi2(t);
-      scale[k] = 1.0f;
     }
-    if (a.post) {
-      row_sums<R, G>(s, red[0]);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
-        if (a.rstd_post && lane == 0 && (G == 1 || warp == 0) && r0 + k < a.rows) a.rstd_post[r0 + k] = scale[k];
-      }
-    }
-    f2 c[P];
-    coefs<V, NV>(a.c, a.pdtype, cl, c);
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        v[k][i] = masked<V, NV>(fma2(mul2(v[k][i], pair(scale[k])), c[i], rx[k].pair_at(i)), i, in);
-  } else {
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int i = 0; i < P; ++i) v[k][i] = masked<V, NV>(rx[k].pair_at(i), i, in);
-  }
-  if (h) {
+    row_sums<R, G>(s, red[par][1]);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       if (r0 + k >= a.rows) break;
+      scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
+      if (a.rstd_pre && writer) a.rstd_pre[r0 + k] = scale[k];
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[k][i] = mul2(mul2(v[k][i], pair(scale[k])), g[i]);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (in[j]) put<T, V>(h + (r0 + k) * a.ldh + col[j], v[k], j);
+        if (in[j]) put<T, V>(y + (r0 + k) * a.ldy + col[j], v[k], j);
     }
-  }
-  if (!y) return;
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    f2 t = 0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) t = fma2(v[k][i], v[k][i], t);
-    s[k] = lo2(t) + hi2(t);
-  }
-  row_sums<R, G>(s, red[1]);
-  f2 g[P];
-  vector_pairs<V, NV>(a.gamma_pre, a.pdtype, cl, g);
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    if (r0 + k >= a.rows) break;
-    scale[k] = rsqrtf(fmaf(s[k], inv, a.eps));
-    if (a.rstd_pre && lane == 0 && (G == 1 || warp == 0)) a.rstd_pre[r0 + k] = scale[k];
-#pragma unroll
-    for (int i = 0; i < P; ++i) v[k][i] = mul2(mul2(v[k][i], pair(scale[k])), g[i]);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (in[j]) put<T, V>(y + (r0 + k) * a.ldy + col[j], v[k], j);
   }
 }
 
@@ -867,8 +877,11 @@ __global__ void __launch_bounds__(1024)
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NV, int G, int R>
 cudaError_t run_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaStream_t st) {
-  constexpr int RB = G == 1 ? 4 * R : R;
-  join_fwd_rows<T, V, NV, G, R><<<unsigned((a.rows + RB - 1) / RB), G == 1 ? 128 : 32 * G, 0, st>>>(x, f, h, y, a);
+  constexpr int RB = G == 1 ? 4 * R : R, threads = rows_threads<V, G>;
+  // as many blocks as run at a time
+  int64_t blocks = (a.rows + RB - 1) / RB;
+  if (blocks > kSms * rows_blocks<V, G>) blocks = kSms * rows_blocks<V, G>;
+  join_fwd_rows<T, V, NV, G, R><<<unsigned(blocks), threads, 0, st>>>(x, f, h, y, a);
   return cudaGetLastError();
 }
 
@@ -919,21 +932,20 @@ cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cud
     if (G == 8) return R == 2 ? run_fwd_ring<T, 8, 8, 2, 2>(x, f, h, y, a, q, st) : run_fwd_ring<T, 8, 8, 2, 1>(x, f, h, y, a, q, st);
     if (G == 16) return R == 2 ? run_fwd_ring<T, 16, 16, 1, 2>(x, f, h, y, a, q, st) : run_fwd_ring<T, 16, 16, 1, 1>(x, f, h, y, a, q, st);
   }
-  const bool regs = a.rows <= 0x7FFFFFFF;  // the grid holds a block per (few) rows
-  if (regs && a.vec && a.pvec && c % 8 == 0) {
+  if (a.vec && a.pvec && c % 8 == 0) {
     if (c <= 256) return run_fwd<T, 8, 1, 1, 2>(x, f, h, y, a, st);
     if (c <= 512) return run_fwd<T, 8, 2, 1, 1>(x, f, h, y, a, st);
     if (c <= 1024) return run_fwd<T, 8, 2, 2, 2>(x, f, h, y, a, st);
     if (c <= 2048) return run_fwd<T, 8, 2, 4, 2>(x, f, h, y, a, st);
     if (c <= 4096) return run_fwd<T, 8, 2, 8, 2>(x, f, h, y, a, st);
     if (c <= 8192) return run_fwd<T, 8, 2, 16, 2>(x, f, h, y, a, st);
-  } else if (regs) {
-    if (c <= 256) return run_fwd<T, 1, 8, 1, 2>(x, f, h, y, a, st);
-    if (c <= 512) return run_fwd<T, 1, 8, 2, 2>(x, f, h, y, a, st);
-    if (c <= 1024) return run_fwd<T, 1, 8, 4, 2>(x, f, h, y, a, st);
-    if (c <= 2048) return run_fwd<T, 1, 8, 8, 2>(x, f, h, y, a, st);
-    if (c <= 4096) return run_fwd<T, 1, 8, 16, 2>(x, f, h, y, a, st);
-    if (c <= 8192) return run_fwd<T, 1, 16, 16, 1>(x, f, h, y, a, st);
+  } else {
+    if (c <= 256) return run_fwd<T, 1, 8, 1, 1>(x, f, h, y, a, st);
+    if (c <= 512) return run_fwd<T, 1, 8, 2, 1>(x, f, h, y, a, st);
+    if (c <= 1024) return run_fwd<T, 1, 8, 4, 1>(x, f, h, y, a, st);
+    if (c <= 2048) return run_fwd<T, 1, 8, 8, 1>(x, f, h, y, a, st);
+    if (c <= 4096) return run_fwd<T, 1, 8, 16, 1>(x, f, h, y, a, st);
+    if (c <= 8192) return run_fwd<T, 1, 8, 32, 1>(x, f, h, y, a, st);
   }
   const unsigned grid = unsigned(a.rows > 0x7FFFFFFF ? 0x7FFFFFFF : a.rows);
   join_fwd_walk<T><<<grid, kT, 0, st>>>(x, f, h, y, a);
