@@ -515,7 +515,7 @@ constexpr int kBwdThreads = 512;
 template <typename T, int V, int NV, int G, bool PF>
 __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p, const BwdArgs a) {
   constexpr int C = 32 * G * NV * V, P = NV * V / 2;
-  extern __shared__ float sums[];  // [2][C] when several rows share the block
+  extern __shared__ float sums[];  // [ng][2][C] when several rows share the block
   __shared__ float4 red[kBwdThreads / 32][2];  // [warp][parity]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ng = int(blockDim.x) / (32 * G), grp = warp / G, wr = warp % G;
@@ -590,24 +590,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) join_bwd_rows(const BwdIn<T> p
   float* pg = a.pg ? a.pg + int64_t(blockIdx.x) * a.cols : nullptr;
   float* ps = a.ps ? a.ps + int64_t(blockIdx.x) * a.cols : nullptr;
   if (ng > 1) {
-    // group after group into shared memory, in order
-    for (int k = 0; k < ng; ++k) {
-      if (k == grp) {
+    // every group's sums into shared memory, then added in the groups' order (one group after
+    // the other into one place: sixteen barriers, 16384 x 256 in BF16 19.4 us)
+    float* mine = sums + size_t(grp) * 2 * C;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int c0 = V == 8 ? int(col[i / 4]) + 2 * (i % 4) : int(col[2 * i % NV]);
-          const int c1 = V == 8 ? c0 + 1 : int(col[(2 * i + 1) % NV]);
-          sums[c0] = (k ? sums[c0] : 0.0f) + lo2(ag[i]);
-          sums[c1] = (k ? sums[c1] : 0.0f) + hi2(ag[i]);
-          sums[C + c0] = (k ? sums[C + c0] : 0.0f) + lo2(as[i]);
-          sums[C + c1] = (k ? sums[C + c1] : 0.0f) + hi2(as[i]);
-        }
-      }
-      __syncthreads();
+    for (int i = 0; i < P; ++i) {
+      const int c0 = V == 8 ? int(col[i / 4]) + 2 * (i % 4) : int(col[2 * i % NV]);
+      const int c1 = V == 8 ? c0 + 1 : int(col[(2 * i + 1) % NV]);
+      mine[c0] = lo2(ag[i]), mine[c1] = hi2(ag[i]);
+      mine[C + c0] = lo2(as[i]), mine[C + c1] = hi2(as[i]);
     }
+    __syncthreads();
     for (int k = threadIdx.x; k < a.cols; k += blockDim.x) {
-      if (pg) pg[k] = sums[k];
-      if (ps) ps[k] = sums[C + k];
+      float tg = 0.0f, ts = 0.0f;
+      for (int w = 0; w < ng; ++w) tg += sums[size_t(w) * 2 * C + k], ts += sums[size_t(w) * 2 * C + C + k];
+      if (pg) pg[k] = tg;
+      if (ps) ps[k] = ts;
     }
   } else {
 #pragma unroll
@@ -955,12 +953,13 @@ cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cud
 template <typename T, int V, int NV, int G, bool PF>
 cudaError_t run_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStream_t st) {
   constexpr int most = kBwdThreads / 32 / G, C = 32 * G * NV * V;
+  static_assert(most == 1 || most * 2 * C * 4 <= 32768, "shared memory without an attribute");
   int64_t ng = (a.rows + kSms - 1) / kSms;
   if (ng > most) ng = most;
   int64_t blocks = (a.rows + ng - 1) / ng;
   if (blocks > kSms) blocks = kSms;
   *parts = int(blocks);
-  const size_t smem = ng > 1 && (a.pg || a.ps) ? size_t(2) * C * 4 : 0;  // 32 KiB at most
+  const size_t smem = ng > 1 && (a.pg || a.ps) ? size_t(ng) * 2 * C * 4 : 0;  // 32 KiB at most
   join_bwd_rows<T, V, NV, G, PF><<<unsigned(blocks), unsigned(32 * G * ng), smem, st>>>(p, a);
   return cudaGetLastError();
 }
