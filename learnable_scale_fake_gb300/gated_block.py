@@ -1,0 +1,149 @@
+"""A gated feed-forward block with norms on both sides in scale-only training, run
+through the C ABI.  With the residual stream h and its norm n (of the join before):
+
+    f  = (act(n Wg_hat^T) * (n Wu_hat^T)) W2_hat^T
+    h' = h + alpha gate norm(f) gamma_post,   n' = norm(h') gamma_pre
+
+Wg and Wu are one stacked weight W1; W1_hat and W2_hat are the NVFP4 fake-quant of
+frozen BF16 weights, of which only the block scales train (gate and the norms'
+vectors get their gradients too).  Between the passes the block keeps h, h' and f,
+the two products of the gate in 8 bits and three floats per token; n and the hidden
+activation are recomputed.
+
+``python -m learnable_scale_fake_gb300.gated_block`` trains the scales of a small
+block against its unquantized self and prints the loss.
+(AngelSlim mcore_qad article, sections 1, 2.3 and 2.4: frozen weights, fake-quant in
+the forward, the gradient flows to the scales, stacked gate and up projections.)
+"""
+from __future__ import annotations
+
+import torch
+
+from . import aqfq
+
+SPEC = aqfq.qspec(aqfq.NVFP4, aqfq.PER_GROUP, group=16)
+
+
+class GatedBlock:
+    """tokens x hidden, hidden -> ff (twice) -> hidden; every buffer is made once.
+
+    w1 [2 ff, hidden] gate's rows, then up's; w2 [hidden, ff]; gamma_in: the norm that made
+    n from h; gamma_post, gate, gamma_pre, alpha: the join after the block.  ``fmt`` / ``group``: of the
+    8-bit checkpoints.  hidden and ff are multiples of 16."""
+
+    def __init__(self, w1, w2, gamma_in, gamma_post, gate, gamma_pre, tokens, alpha=1.0, act=aqfq.ACT_SILU,
+                 fmt=aqfq.INT8, group=128, eps=1e-6):
+        self.w1, self.w2 = w1, w2
+        self.gamma_in, self.gamma_post, self.gate, self.gamma_pre = gamma_in, gamma_post, gate, gamma_pre
+        self.alpha, self.act, self.eps = alpha, act, eps
+        hidden, ff = w2.shape
+        dev = w1.device
+
+        def new(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        def kept(cols):
+            return aqfq.ckpt8(fmt, group, new(tokens, cols, dtype=torch.uint8),
+                              new(tokens, -(-cols // group), dtype=torch.float32))
+
+        # learned block scales and tensor scales, initialised from the weights
+        self.s1, self.s2 = (new(w.numel() // 16, dtype=torch.float32) for w in (w1, w2))
+        self.g1, self.g2 = new(1, dtype=torch.float32), new(1, dtype=torch.float32)
+        aqfq.aqfq_scale_init(SPEC, w1, self.s1, self.g1)
+        aqfq.aqfq_scale_init(SPEC, w2, self.s2, self.g2)
+        self.ds1, self.ds2 = torch.empty_like(self.s1), torch.empty_like(self.s2)
+        self.w1_hat, self.w2_hat = torch.empty_like(w1), torch.empty_like(w2)
+        self.dw1, self.dw2 = torch.empty_like(w1), torch.empty_like(w2)
+        # what lives from the forward to the backward pass
+        self.kept_gate, self.kept_up = kept(ff), kept(ff)
+        self.f, self.h_out = new(tokens, hidden), new(tokens, hidden)
+        self.rstd_post, self.rstd_pre = (new(tokens, dtype=torch.float32) for _ in range(2))
+        # scratch within a pass, outputs
+        self.n, self.n_out, self.dn, self.dh = (new(tokens, hidden) for _ in range(4))
+        self.df = new(tokens, hidden)
+        self.y, self.dp = new(tokens, ff), new(tokens, 2 * ff)
+        self.dgamma_post, self.dgate, self.dgamma_pre = (new(hidden, dtype=torch.float32) for _ in range(3))
+        M = tokens
+        need = max([aqfq.aqfq_linear_workspace_bytes(k, M, n, c)
+                    for k in (aqfq.LINEAR_FWD, aqfq.LINEAR_DGRAD, aqfq.LINEAR_WGRAD)
+                    for n, c in ((2 * ff, hidden), (hidden, ff))]
+                   + [aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_FWD, M, ff, hidden),
+                      aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_DGRAD, M, hidden, ff),
+                      aqfq.aqfq_block_norm_bwd_workspace_bytes(M, hidden)])
+        self.workspace = new(max(need, 16), dtype=torch.uint8)
+        self.error = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def norm_in(self, h, out, stream=None):
+        """out = norm(h) gamma_in, as the join before the block gives it."""
+        aqfq.aqfq_block_norm_fwd(h, None, self.eps, y=out, gamma_pre=self.gamma_in, stream=stream)
+        return out
+
+    def forward(self, h, n, stream=None):
+        """(h', n') from the residual stream h and its norm n."""
+        kw = {"workspace": self.workspace, "error_flag": self.error, "stream": stream}
+        aqfq.aqfq_qdq_fwd(SPEC, self.w1, self.s1, self.g1, self.w1_hat, stream=stream)
+        aqfq.aqfq_qdq_fwd(SPEC, self.w2, self.s2, self.g2, self.w2_hat, stream=stream)
+        aqfq.aqfq_gated_fwd(n, self.w1_hat, self.y, act=self.act, gate=self.kept_gate, up=self.kept_up, **kw)
+        aqfq.aqfq_linear_fwd(self.y, self.w2_hat, self.f, **kw)
+        aqfq.aqfq_block_norm_fwd(h, self.f, self.eps, h=self.h_out, y=self.n_out, post=True,
+                                 gamma_post=self.gamma_post, gate=self.gate, alpha=self.alpha,
+                                 gamma_pre=self.gamma_pre, rstd_post=self.rstd_post, rstd_pre=self.rstd_pre,
+                                 stream=stream)
+        return self.h_out, self.n_out
+
+    def backward(self, h, dh_out, dn_out, stream=None):
+        """(dh, dn) from the gradients of h' and n' and the forward's h; dh lacks what flows through n.
+        The scale gradients are in ds1 and ds2, the vectors' in dgamma_post, dgate and dgamma_pre."""
+        kw = {"workspace": self.workspace, "error_flag": self.error, "stream": stream}
+        aqfq.aqfq_block_norm_bwd(dn_out, dh_out, self.h_out, self.f, rstd_post=self.rstd_post,
+                                 rstd_pre=self.rstd_pre, gamma_post=self.gamma_post, gate=self.gate,
+                                 alpha=self.alpha, gamma_pre=self.gamma_pre, dx=self.dh, df=self.df,
+                                 dgamma_post=self.dgamma_post, dgate=self.dgate, dgamma_pre=self.dgamma_pre,
+                                 workspace=self.workspace, stream=stream)
+        # through the second product and the gate; the hidden activation comes back on the way
+        aqfq.aqfq_gated_dgrad(self.df, self.w2_hat, self.dp, self.kept_gate, self.kept_up, act=self.act, y=self.y, **kw)
+        aqfq.aqfq_linear_wgrad(self.df, self.y, self.dw2, **kw)
+        aqfq.aqfq_scale_grad(SPEC, self.w2, self.dw2, self.s2, self.g2, dscale=self.ds2, stream=stream)
+        # through the first product; its input recomputed
+        self.norm_in(h, self.n, stream)
+        aqfq.aqfq_linear_wgrad(self.dp, self.n, self.dw1, **kw)
+        aqfq.aqfq_scale_grad(SPEC, self.w1, self.dw1, self.s1, self.g1, dscale=self.ds1, stream=stream)
+        aqfq.aqfq_linear_dgrad(self.dp, self.w1_hat, self.dn, **kw)
+        return self.dh, self.dn
+
+
+def random_block(hidden, ff, tokens, seed=0, dev="cuda", **kw):
+    g = torch.Generator(device=dev).manual_seed(seed)
+
+    def n(*shape, std=1.0):
+        return (torch.randn(shape, generator=g, device=dev) * std).bfloat16()
+
+    return GatedBlock(n(2 * ff, hidden, std=hidden ** -0.5), n(hidden, ff, std=ff ** -0.5),
+                      1 + n(hidden, std=0.1), 1 + n(hidden, std=0.1), 1 + n(hidden, std=0.3),
+                      1 + n(hidden, std=0.1), tokens, **kw)
+
+
+def main(steps=20, hidden=2048, ff=8192, tokens=4096, lr=3e-3):
+    block = random_block(hidden, ff, tokens)
+    h = torch.randn(tokens, hidden, device="cuda").bfloat16()
+    n = block.norm_in(h, torch.empty_like(h))
+    # the target: the same block with its weights as they are
+    y, f, target = torch.empty_like(block.y), torch.empty_like(h), torch.empty_like(h)
+    aqfq.aqfq_gated_fwd(n, block.w1, y, act=block.act, workspace=block.workspace)
+    aqfq.aqfq_linear_fwd(y, block.w2, f, workspace=block.workspace)
+    aqfq.aqfq_block_norm_fwd(h, f, block.eps, y=target, post=True, gamma_post=block.gamma_post, gate=block.gate,
+                             alpha=block.alpha, gamma_pre=block.gamma_pre)
+    opt = torch.optim.Adam([block.s1, block.s2], lr=lr * float(block.s1.mean()))
+    for i in range(steps):
+        diff = block.forward(h, n)[1].float() - target.float()
+        loss = diff.square().mean()
+        block.backward(h, None, (diff * (2.0 / diff.numel())).bfloat16())
+        block.s1.grad, block.s2.grad = block.ds1, block.ds2
+        opt.step()
+        if i % 5 == 0 or i == steps - 1:
+            print(f"step {i:3d}  loss {loss.item():.6f}")
+    assert int(block.error.item()) == 0, "a pipeline wait timed out"
+
+
+if __name__ == "__main__":
+    main()
