@@ -62,6 +62,7 @@ struct Epi {
   Ckpt c2;
   bf16 *out2, *hidden;
   int64_t ldh;
+  bool staged;  // they may be stored by the tensor memory accelerator
 };
 
 // columns of [col, col + V) that lie in the row
@@ -834,8 +835,29 @@ __device__ __forceinline__ f2 act_and_slope(int act, f2 x, f2& d) {
   }
 }
 
-// Gradient: columns [col, col + 16 NCH) of row r from their sums at taddr, pair by pair: each
-// pair's three results are packed before the next one's.
+// Gradient of 16 columns from their sums, pair by pair: each pair's three results are packed
+// before the next one's.  c: chunk of the kept values.
+template <int ACT, int NCH>
+__device__ __forceinline__ void gated_grad16(const Epi& e, const GateRow<NCH>& kept, int c, const float (&s)[16],
+                                             uint32_t (&wg)[8], uint32_t (&wu)[8], uint32_t (&wh)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f2 g[2], u[2];
+    ckpt_values4(kept.g[c][i], kept.sg[c / 2], e.c.fmt, g);
+    ckpt_values4(kept.u[c][i], kept.su[c / 2], e.c.fmt, u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f2 v = mk2(s[4 * i + 2 * k], s[4 * i + 2 * k + 1]);
+      f2 d;
+      const f2 a = act_and_slope<ACT>(e.act, g[k], d);
+      wg[2 * i + k] = pack2(mul2(mul2(v, u[k]), d));
+      wu[2 * i + k] = pack2(mul2(v, a));
+      wh[2 * i + k] = pack2(mul2(u[k], a));
+    }
+  }
+}
+
+// Columns [col, col + 16 NCH) of row r from their sums at taddr.
 template <int ACT, int NCH>
 __device__ __forceinline__ void gated_grad_row(const Epi& e, int64_t r, bool in, int64_t col, uint32_t taddr,
                                                const GateRow<NCH>& kept) {
@@ -852,21 +874,7 @@ __device__ __forceinline__ void gated_grad_row(const Epi& e, int64_t r, bool in,
     tmem_issue(taddr + uint32_t(c * 16), t);
     tmem_take(t, s);
     if (in) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f2 g[2], u[2];
-        ckpt_values4(kept.g[c][i], kept.sg[c / 2], e.c.fmt, g);
-        ckpt_values4(kept.u[c][i], kept.su[c / 2], e.c.fmt, u);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const f2 v = mk2(s[4 * i + 2 * k], s[4 * i + 2 * k + 1]);
-          f2 d;
-          const f2 a = act_and_slope<ACT>(e.act, g[k], d);
-          wg[2 * i + k] = pack2(mul2(mul2(v, u[k]), d));
-          wu[2 * i + k] = pack2(mul2(v, a));
-          wh[2 * i + k] = pack2(mul2(u[k], a));
-        }
-      }
+      gated_grad16<ACT>(e, kept, c, s, wg, wu, wh);
       const Seg sg = seg(pg + c * 16, n == 16), su = seg(pu + c * 16, n == 16);
       st16(pg + c * 16, sg.a32, sg.a16, n, wg);
       st16(pu + c * 16, su.a32, su.a16, n, wu);
@@ -875,6 +883,64 @@ __device__ __forceinline__ void gated_grad_row(const Epi& e, int64_t r, bool in,
         st16(ph + c * 16, sh.a32, sh.a16, n, wh);
       }
     }
+  }
+}
+
+// The outputs of the gated gradient as the tensor memory accelerator stores them: boxes of 32
+// rows x 16 columns, rows of 32 bytes in the 32-byte swizzle.
+template <int PASS>
+struct OutMaps {};
+template <>
+struct OutMaps<P_GATED_DGRAD> {
+  CUtensorMap out[3];  // dg, du, act(g) u
+};
+constexpr int kBoxCols = 16;
+constexpr uint32_t kBoxBytes = 32 * kBoxCols * 2;
+
+// The same for a warp's 32 rows from r0 on (r0 and col exist) through its 3 KiB of shared memory
+// at `stage`: a row per lane written to global memory in pieces of 32 bytes costs the load/store
+// unit a pass per row (half of its time); here it writes whole units of shared memory, conflict-free
+// by the swizzle (unit u of row r at u ^ (r / 4 % 2)), and the accelerator cuts off what lies
+// beyond the last row or column.
+template <int ACT, int NCH>
+__device__ __forceinline__ void gated_grad_staged(const Epi& e, const OutMaps<P_GATED_DGRAD>& m, int64_t r0,
+                                                  int lane, int64_t col, uint32_t taddr,
+                                                  const GateRow<NCH>& kept, uint32_t stage) {
+  const bool in = r0 + lane < e.rows;
+  const uint32_t row = stage + uint32_t(lane * 32), x = uint32_t(lane >> 2) & 1;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if (col + c * 16 >= e.cols) break;
+    uint32_t t[16], w[3][8];
+    float s[16];
+    // the boxes before these have been read
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    tmem_issue(taddr + uint32_t(c * 16), t);
+    tmem_take(t, s);
+    if (in) {
+      gated_grad16<ACT>(e, kept, c, s, w[0], w[1], w[2]);
+#pragma unroll
+      for (int o = 0; o < 3; ++o)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + o * kBoxBytes + ((uint32_t(i) ^ x) << 4)),
+                       "r"(w[o][4 * i]), "r"(w[o][4 * i + 1]), "r"(w[o][4 * i + 2]), "r"(w[o][4 * i + 3])
+                       : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int o = 0; o < 3; ++o)
+        if (o < 2 || e.hidden)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                           reinterpret_cast<uint64_t>(&m.out[o])),
+                       "r"(int(col) + c * 16), "r"(int(r0)), "r"(stage + o * kBoxBytes)
+                       : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    __syncwarp();
   }
 }
 
@@ -908,17 +974,21 @@ constexpr int kRows = 256, kHalf = 128, kBK = 64;
 constexpr int kThreadsP = 64 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
-template <int BN>
+// STAGED: five stages (with four the plain input gradient took 85 us instead of 75), and the epilogue warps' outputs on their way to memory
+template <int BN, bool STAGED>
 struct Cfg {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = STAGED ? 5 : 6;
   static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
   static constexpr uint32_t STAGE = kABytes + B_BYTES;
-  static constexpr uint32_t BIAS = kEpiWarps * 128 * 4;  // the 128 columns around a warp's
+  static constexpr uint32_t BIAS = STAGED ? kEpiWarps * 3 * kBoxBytes  // three boxes of each warp
+                                          : kEpiWarps * 128 * 4;       // the 128 columns around a warp's
   static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + BIAS + 256;
   // a split tile's partial sums (one row per 16-byte odd stride) reuse the stages
   static constexpr int PSTRIDE = BN + 4;
-  static_assert(size_t(kHalf) * PSTRIDE * 4 <= size_t(STAGES) * STAGE, "partial sums fit the stages");
+  static_assert(STAGED || size_t(kHalf) * PSTRIDE * 4 <= size_t(STAGES) * STAGE, "partial sums fit the stages");
 };
+// which kernels stage their outputs
+constexpr bool is_staged(int pass, bool split) { return pass == P_GATED_DGRAD && !split; }
 
 struct __align__(8) PairShared {
   uint64_t full[6], empty[6];  // TMA bytes of both CTAs (leader) / MMA commit
@@ -957,8 +1027,8 @@ __device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& tr, int& 
 template <int PASS, int ACT, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsP, 1)
     pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                const PairArgs a, const Epi e) {
-  using C = Cfg<BN>;
+                const __grid_constant__ OutMaps<PASS> outs, const PairArgs a, const Epi e) {
+  using C = Cfg<BN, is_staged(PASS, SPLIT)>;
   constexpr bool A_MN = PASS == P_WGRAD, B_MN = !k_major(PASS);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1180,7 +1250,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           const uint32_t tg = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + part * (W / 2));
           gated_row<ACT>(e, r, r < e.rows, col, tg, tg + BN / 2, sbias, q * 32 + lane, part, 2 + q);
         } else if constexpr (PASS == P_GATED_DGRAD) {
-          gated_grad_row<ACT, W / 16>(e, r, r < e.rows, col, taddr, gates);
+          if constexpr (is_staged(PASS, SPLIT)) {
+            if (e.staged)
+              gated_grad_staged<ACT, W / 16>(e, outs, r0, lane, col, taddr, gates,
+                                             smem_u32(sbias) + uint32_t(warp - 2) * 3 * kBoxBytes);
+            else
+              gated_grad_row<ACT, W / 16>(e, r, r < e.rows, col, taddr, gates);
+          }
         } else {
           if (fast) epilogue_whole<PASS, ACT>(e, r, col, taddr, mybias + int(col & 127), codes);
           else epilogue_row<PASS, ACT>(e, r, r < e.rows, col, taddr, mybias + int(col & 127), codes);
@@ -1190,6 +1266,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       __syncwarp();
       if (!SPLIT && lane == 0) mbar_arrive_cluster(peer_addr(smem_u32(&sh->tempty[buf]), lead));
     }
+    // the boxes' shared memory has been read and their rows written
+    if (is_staged(PASS, SPLIT) && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   if constexpr (SPLIT) {
     // this CTA's rows of the tile; a warp takes half the columns of two rows per turn
@@ -1725,14 +1804,38 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
   return p;
 }
 
+// the boxes of the outputs (OutMaps); false: one of them cannot be described
+bool encode_outs(const Epi& e, OutMaps<P_GATED_DGRAD>& m) {
+  void* const base[3] = {e.out, e.out2, e.hidden};
+  const int64_t ld[3] = {e.ldo, e.ldo, e.ldh};
+  for (int o = 0; o < 3; ++o) {
+    if (!base[o]) continue;
+    if (!al(base[o], 16) || ld[o] % 8 != 0) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(e.cols), cuuint64_t(e.rows)};
+    const int64_t row = e.rows > 1 ? ld[o] : (e.cols + 7) / 8 * 8;  // a single row has no stride
+    const cuuint64_t strides[1] = {cuuint64_t(row) * 2};
+    const cuuint32_t box[2] = {kBoxCols, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    if (strides[0] >= (cuuint64_t(1) << 40) ||
+        encode_fn()(&m.out[o], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base[o], dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
+}
+
 template <int PASS, int ACT, bool SPLIT>
-cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, const Epi& e,
+cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, Epi e,
                         cudaStream_t st) {
+  using C = Cfg<kBN, is_staged(PASS, SPLIT)>;
+  OutMaps<PASS> outs = {};
+  if constexpr (is_staged(PASS, SPLIT)) e.staged = a.splits == 1 && encode_outs(e, outs);
   auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
   static DeviceOnce once;
   const cudaError_t attr = once_per_device(once, [&] {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kBN>::SMEM));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
     if (e != cudaSuccess || !SPLIT) return e;
     // more than 8 CTAs per cluster
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1743,13 +1846,13 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   const int csize = SPLIT ? 2 * a.splits : 2;
   cfg.gridDim = dim3(SPLIT ? unsigned(tiles * csize) : 2 * unsigned(units < kPairs ? units : kPairs));
   cfg.blockDim = dim3(kThreadsP);
-  cfg.dynamicSmemBytes = Cfg<kBN>::SMEM;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = unsigned(csize), at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, a, e);
+  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, outs, a, e);
 }
 
 template <int PASS>

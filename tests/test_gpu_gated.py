@@ -85,12 +85,13 @@ def check_grad(s, dp, y, g, u, act, what):
         close(y, ref, u.abs() * ea + r * ref.abs(), f"y {what}")
 
 
-def check_dgrad(M, N, K, act, form, seed=0, div=8.0, hidden=True):
+def check_dgrad(M, N, K, act, form, seed=0, div=8.0, hidden=True, place=None):
+    """place: (pad, offset) of dp and y; by the seed if None."""
     dy, w = ints((M, N), 5 + seed, 1), ints((N, K), 6 + seed, 1) / div
     (cg, *g), (cu, *u) = two_ckpt(M, K, *form, seed=8 + seed)
     fd, fw = operand(dy, seed), operand(w, seed + 1)
-    fo = Framed(M, 2 * K, torch.bfloat16, seed % 3, seed % 2)
-    fy = Framed(M, K, torch.bfloat16, (seed + 1) % 3, seed % 2)
+    po, py = (place, place) if place else ((seed % 3, seed % 2), ((seed + 1) % 3, seed % 2))
+    fo, fy = Framed(M, 2 * K, torch.bfloat16, *po), Framed(M, K, torch.bfloat16, *py)
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     aqfq.aqfq_gated_dgrad(fd.view, fw.view, fo.view, cg, cu, act=ACTS[act], y=fy.view if hidden else None,
                           workspace=ws(aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_DGRAD, M, N, K)), error_flag=err)
@@ -135,6 +136,16 @@ def test_gradient_on_pairs(act, form):
     for i, (M, K, N) in enumerate([(2048, 2560, 264), (2050, 2568, 200), (2303, 2509, 136)]):
         assert aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_DGRAD, M, N, K)["kernel"] == "pair"
         check_dgrad(M, N, K, act, form, seed=i)
+
+
+@pytest.mark.parametrize("act", NAMES)
+@pytest.mark.parametrize("place", [(0, 0), (8, 8), (24, 16), (4, 0)])
+def test_gradient_stored_in_boxes(act, place):
+    """Outputs that allow 16-byte rows go to memory in boxes of 32 x 32, ragged ones cut off (the last
+    place does not allow them); nothing around them is written."""
+    for i, (M, K, N) in enumerate([(2048, 2560, 200), (2050, 2568, 136), (2303, 2520, 72)]):
+        assert aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_DGRAD, M, N, K)["kernel"] == "pair"
+        check_dgrad(M, N, K, act, FORMS[i], seed=i, hidden=i != 1, place=place)
 
 
 def tails():
