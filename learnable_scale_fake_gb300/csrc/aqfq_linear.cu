@@ -673,13 +673,22 @@ __device__ __forceinline__ void act_of(const Epi& e, float (&v)[V]) {
   if constexpr (ACT < 0) act_apply(e.act, v);
   else act_all<ACT>(v);
 }
-// n of 16 values as BF16 at p
+// n of 16 BF16 at p; rows that start at multiples of 4 elements take 8-byte stores (1500 x 1100 x
+// 1000 by single elements 23.8 us, 1500 x 1104 x 1000 13.7)
+__device__ __forceinline__ void put16(bf16* p, int n, const uint32_t (&w)[8]) {
+  const Seg q = seg(p, n == 16);
+  if (!q.a16 && n == 16 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st_64(p + 4 * i, w[2 * i], w[2 * i + 1]);
+  } else {
+    st16(p, q.a32, q.a16, n, w);
+  }
+}
 __device__ __forceinline__ void put16(bf16* p, int n, const float (&v)[16]) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i + 1], v[2 * i]);
-  const Seg q = seg(p, n == 16);
-  st16(p, q.a32, q.a16, n, w);
+  put16(p, n, w);
 }
 __device__ __forceinline__ void put_codes16(const Epi& e, const Ckpt& c, int64_t r, int64_t cc, int n,
                                             const Divisor& d, const float (&v)[16]) {
@@ -875,13 +884,9 @@ __device__ __forceinline__ void gated_grad_row(const Epi& e, int64_t r, bool in,
     tmem_take(t, s);
     if (in) {
       gated_grad16<ACT>(e, kept, c, s, wg, wu, wh);
-      const Seg sg = seg(pg + c * 16, n == 16), su = seg(pu + c * 16, n == 16);
-      st16(pg + c * 16, sg.a32, sg.a16, n, wg);
-      st16(pu + c * 16, su.a32, su.a16, n, wu);
-      if (ph) {
-        const Seg sh = seg(ph + c * 16, n == 16);
-        st16(ph + c * 16, sh.a32, sh.a16, n, wh);
-      }
+      put16(pg + c * 16, n, wg);
+      put16(pu + c * 16, n, wu);
+      if (ph) put16(ph + c * 16, n, wh);
     }
   }
 }
@@ -1770,7 +1775,11 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
   p.bytes = 0;
   if (p.ksteps == 0) return p;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
-  if (small <= kClustersC[1] && p.ksteps < 512) {
+  // (gated: a tile of one CTA loads 48 KiB per step where a CTA of a pair loads 32, so pairs serve
+  // products that fill half the SMs without slices: 1000 x 1544 x 776 10.9 us against 11.8, 1500 x 1104
+  // x 1000 12.2 against 13.7; with slices tile_kernel stays, 1024 x 768 x 2048 13.3 us against 14.8)
+  const bool pairs = gated && rows > kTile && small > kClustersC[2];
+  if (small <= kClustersC[1] && p.ksteps < 512 && !pairs) {
     p.small = true;
     // zero rows that only the fill would write cost as much as loaded ones (1 row, 4096 x
     // 4096: 12.9 us with boxes of 128 rows, 9.4 us with 8); rows past the box stay unread

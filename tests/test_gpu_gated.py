@@ -130,6 +130,15 @@ def test_forward_on_pairs(act, form):
         check_fwd(M, N, K, act, form, seed=i)
 
 
+@pytest.mark.parametrize("size,kernel", [((1000, 1544, 264), "pair"), ((500, 1000, 136), "tile"),
+                                         ((129, 9600, 72), "pair"), ((128, 9728, 136), "tile")])
+def test_both_kernels_near_the_border(size, kernel):
+    plan = aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_GATED, *size)
+    assert plan["kernel"] == kernel and plan["splits"] <= 2
+    for i, form in enumerate([None] + FORMS):
+        check_fwd(*size, NAMES[i], form, seed=i)
+
+
 @pytest.mark.parametrize("act", NAMES)
 @pytest.mark.parametrize("form", FORMS)
 def test_gradient_on_pairs(act, form):
