@@ -1500,82 +1500,82 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
         gated_grad_row<-1, 2>(e, r, in, col, taddr, gates);
       }
     } else {
-    ChunkIn<PASS> add[2];
-    RowCodes<2> codes;
-    float bias[4][8];
-    if (in) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (col + c * 16 < e.cols) add[c].load(e, r, col + c * 16);
-      if (PASS == P_DGRAD && e.c.codes) codes.load(e, r, col);
-      if (PASS == P_FWD) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load_bias(e, col + i * 8, bias[i]);
-      }
-    }
-    __syncwarp();
-    if (!mbar_wait_warp(&sh->accum, 0)) *abort = 1;
-    __syncwarp();
-    tc_fence_after_sync();
-    float v[2][16];
-    if (live) {
-      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
-      uint32_t t[16];
-      tmem_issue(taddr, t);
-      tmem_take(t, v[0]);
-      tmem_issue(taddr + 16, t);
-      tmem_take(t, v[1]);
-    }
-    if (PASS == P_FWD && in) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i / 16][i % 16] += bias[i / 8][i % 8];
-    }
-    if (PASS == P_FWD && e.c.codes) {  // uniform over the grid
-      // a group is this warp's 32 columns, or those of two or four neighbouring warps too
-      float* most = reinterpret_cast<float*>(smem);  // [4][128]; the stages are consumed
-      uint32_t m = 0;
+      ChunkIn<PASS> add[2];
+      RowCodes<2> codes;
+      float bias[4][8];
       if (in) {
-        const int64_t left = e.cols - col;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = i < left ? v[i / 16][i % 16] : 0.0f;
-        m = max(amax_bits(v[0]), amax_bits(v[1]));
+        for (int c = 0; c < 2; ++c)
+          if (col + c * 16 < e.cols) add[c].load(e, r, col + c * 16);
+        if (PASS == P_DGRAD && e.c.codes) codes.load(e, r, col);
+        if (PASS == P_FWD) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_bias(e, col + i * 8, bias[i]);
+        }
       }
-      const int part = warp >> 2, at = q * 32 + lane;
-      most[part * 128 + at] = __uint_as_float(m);
-      __syncthreads();
+      __syncwarp();
+      if (!mbar_wait_warp(&sh->accum, 0)) *abort = 1;
+      __syncwarp();
+      tc_fence_after_sync();
+      float v[2][16];
+      if (live) {
+        const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
+        uint32_t t[16];
+        tmem_issue(taddr, t);
+        tmem_take(t, v[0]);
+        tmem_issue(taddr + 16, t);
+        tmem_take(t, v[1]);
+      }
+      if (PASS == P_FWD && in) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i / 16][i % 16] += bias[i / 8][i % 8];
+      }
+      if (PASS == P_FWD && e.c.codes) {  // uniform over the grid
+        // a group is this warp's 32 columns, or those of two or four neighbouring warps too
+        float* most = reinterpret_cast<float*>(smem);  // [4][128]; the stages are consumed
+        uint32_t m = 0;
+        if (in) {
+          const int64_t left = e.cols - col;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = i < left ? v[i / 16][i % 16] : 0.0f;
+          m = max(amax_bits(v[0]), amax_bits(v[1]));
+        }
+        const int part = warp >> 2, at = q * 32 + lane;
+        most[part * 128 + at] = __uint_as_float(m);
+        __syncthreads();
+        if (in) {
+          const int first = part & ~((1 << (e.c.lg - 5)) - 1);
+          for (int i = 0; i < (1 << (e.c.lg - 5)); ++i)
+            m = max(m, __float_as_uint(most[(first + i) * 128 + at]));
+          const Divisor d = ckpt_divisor(m, e.c.fmt);
+          if (part == first) e.c.scale[r * e.c.groups + (col >> e.c.lg)] = d.s;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int64_t left = e.cols - (col + c * 16);
+            uint32_t w[4];
+            f2 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = mk2(v[c][2 * i], v[c][2 * i + 1]);
+            ckpt_codes(x, d, e.c.fmt, w);
+            if (left > 0) store_codes16(e.c.codes + r * e.cols + col + c * 16, left > 16 ? 16 : int(left), w);
+          }
+        }
+      }
       if (in) {
-        const int first = part & ~((1 << (e.c.lg - 5)) - 1);
-        for (int i = 0; i < (1 << (e.c.lg - 5)); ++i)
-          m = max(m, __float_as_uint(most[(first + i) * 128 + at]));
-        const Divisor d = ckpt_divisor(m, e.c.fmt);
-        if (part == first) e.c.scale[r * e.c.groups + (col >> e.c.lg)] = d.s;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int64_t left = e.cols - (col + c * 16);
-          uint32_t w[4];
-          f2 x[8];
+          if (left <= 0) continue;
+          if (PASS == P_FWD) act_apply(e.act, v[c]);
+          if (PASS == P_DGRAD && e.c.codes) {
+            float p[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mk2(v[c][2 * i], v[c][2 * i + 1]);
-          ckpt_codes(x, d, e.c.fmt, w);
-          if (left > 0) store_codes16(e.c.codes + r * e.cols + col + c * 16, left > 16 ? 16 : int(left), w);
+            for (int i = 0; i < 4; ++i) ckpt_values4(codes.w[c][i], codes.scale[0], e.c.fmt, p + 4 * i);
+            slope_apply(e.act, p, v[c]);
+          }
+          finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v[c]);
         }
       }
-    }
-    if (in) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int64_t left = e.cols - (col + c * 16);
-        if (left <= 0) continue;
-        if (PASS == P_FWD) act_apply(e.act, v[c]);
-        if (PASS == P_DGRAD && e.c.codes) {
-          float p[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ckpt_values4(codes.w[c][i], codes.scale[0], e.c.fmt, p + 4 * i);
-          slope_apply(e.act, p, v[c]);
-        }
-        finish_chunk<PASS>(e, r, col + c * 16, left > 16 ? 16 : int(left), add[c], v[c]);
-      }
-    }
     }
     tc_fence_before_sync();
     __syncthreads();
