@@ -700,12 +700,12 @@ __device__ __forceinline__ void put_codes16(const Epi& e, const Ckpt& c, int64_t
   store_codes16(c.codes + r * e.cols + cc, n, w);
 }
 
-// Forward: columns [col, col + 32) of row r, g and u at tg and tu.  The four warps of a
-// quarter of the rows hold a tile's 128 columns (`part` of them this one's); with kept
+// Forward: columns [col, col + 16 NCH) of row r, g and u at tg and tu.  The four warps of a
+// quarter of the rows hold a tile's 64 NCH columns (`part` of them this one's); with kept
 // values they exchange their maxima through `most` ([2][4][128] floats; `at` the lane's row
 // of the tile) at the barrier `bar`, and read the sums twice instead of holding 64 registers
 // through it.  The four warps all call it.
-template <int ACT>
+template <int ACT, int NCH>
 __device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int64_t col, uint32_t tg,
                                           uint32_t tu, float* most, int at, int part, int bar) {
   uint32_t a[16], b[16];
@@ -715,7 +715,7 @@ __device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int6
   if (keep) {
     uint32_t mg = 0, mu = 0;
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < NCH; ++c) {
       tmem_issue(tg + uint32_t(c * 16), a);
       tmem_issue(tu + uint32_t(c * 16), b);
       tmem_take(a, g);
@@ -729,7 +729,8 @@ __device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int6
       mu = max(mu, amax_bits(u));
     }
     int first = part;
-    if (e.c.lg > 5) {
+    constexpr int LG = NCH == 2 ? 5 : 4;  // columns of a warp
+    if (e.c.lg > LG) {
       most[part * 128 + at] = __uint_as_float(mg);
       most[512 + part * 128 + at] = __uint_as_float(mu);
       __syncwarp();
@@ -739,8 +740,8 @@ __device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int6
         case 4: asm volatile("bar.sync 4, 128;" ::: "memory"); break;
         default: asm volatile("bar.sync 5, 128;" ::: "memory"); break;
       }
-      first = part & ~((1 << (e.c.lg - 5)) - 1);
-      for (int i = 0; i < (1 << (e.c.lg - 5)); ++i) {
+      first = part & ~((1 << (e.c.lg - LG)) - 1);
+      for (int i = 0; i < (1 << (e.c.lg - LG)); ++i) {
         mg = max(mg, __float_as_uint(most[(first + i) * 128 + at]));
         mu = max(mu, __float_as_uint(most[512 + (first + i) * 128 + at]));
       }
@@ -752,7 +753,7 @@ __device__ __forceinline__ void gated_row(const Epi& e, int64_t r, bool in, int6
     }
   }
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < NCH; ++c) {
     const int64_t cc = col + c * 16, left = e.cols - cc;
     if (left <= 0) break;
     const int n = left > 16 ? 16 : int(left);
@@ -982,7 +983,7 @@ constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 // STAGED: five stages (with four the plain input gradient took 85 us instead of 75), and the epilogue warps' outputs on their way to memory
 template <int BN, bool STAGED>
 struct Cfg {
-  static constexpr int STAGES = STAGED ? 5 : 6;
+  static constexpr int STAGES = STAGED && BN == 256 ? 5 : 6;
   static constexpr uint32_t B_BYTES = BN / 2 * kBK * 2;
   static constexpr uint32_t STAGE = kABytes + B_BYTES;
   static constexpr uint32_t BIAS = STAGED ? kEpiWarps * 3 * kBoxBytes  // three boxes of each warp
@@ -992,6 +993,9 @@ struct Cfg {
   static constexpr int PSTRIDE = BN + 4;
   static_assert(STAGED || size_t(kHalf) * PSTRIDE * 4 <= size_t(STAGES) * STAGE, "partial sums fit the stages");
 };
+// Tiles of half as many columns (the gated forward of a product that would fill few pairs; the gated
+// gradient is faster on small tiles: 512 x 2048 x 768 10.0 us against 13.8).
+constexpr int kNarrow = 128;
 // which kernels stage their outputs
 constexpr bool is_staged(int pass, bool split) { return pass == P_GATED_DGRAD && !split; }
 
@@ -1190,7 +1194,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const bool live = r0 < e.rows && (col < e.cols || (PASS == P_GATED && whole));
       const bool fast = PASS < P_GATED && whole_block<PASS>(e, r0, col);
       RowCodes<kChunks> codes;
-      GateRow<kChunks> gates;  // (each is held by its own pass only)
+      GateRow<BN / (kEpiWarps / 4) / 16> gates;  // (each is held by its own pass only)
       if (live && whole) {
         if (PASS == P_FWD && e.bias) {
           float b[4];
@@ -1253,7 +1257,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
         } else if constexpr (PASS == P_GATED) {
           const uint32_t tg = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 256 + part * (W / 2));
-          gated_row<ACT>(e, r, r < e.rows, col, tg, tg + BN / 2, sbias, q * 32 + lane, part, 2 + q);
+          gated_row<ACT, W / 32>(e, r, r < e.rows, col, tg, tg + BN / 2, sbias, q * 32 + lane, part, 2 + q);
         } else if constexpr (PASS == P_GATED_DGRAD) {
           if constexpr (is_staged(PASS, SPLIT)) {
             if (e.staged)
@@ -1494,7 +1498,7 @@ __global__ void __launch_bounds__(32 * kWarpsC, 1)
       const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t((warp >> 2) * 32);
       if (PASS == P_GATED) {
         if (q * 32 < nrows)  // (all four warps of the quarter; the stages are consumed)
-          gated_row<-1>(e, r, r < e.rows, col, taddr, taddr + kTile, reinterpret_cast<float*>(smem), q * 32 + lane,
+          gated_row<-1, 2>(e, r, r < e.rows, col, taddr, taddr + kTile, reinterpret_cast<float*>(smem), q * 32 + lane,
                         warp >> 2, 2 + q);
       } else if (live) {
         gated_grad_row<-1, 2>(e, r, in, col, taddr, gates);
@@ -1736,6 +1740,7 @@ struct Plan {
   int tail, tail_splits;  // last tiles that a second launch splits (0: none)
   int64_t cols4;
   size_t bytes;   // scratch
+  bool narrow;    // pairs on tiles of half as many columns
 };
 
 constexpr int kPairs = 76;  // SM pairs
@@ -1762,8 +1767,9 @@ constexpr int64_t kMostScratch = int64_t(64) << 20;
 //     kernel and the partial sums' way to memory and back (weight gradients of many
 //     tokens: few tiles, a long sum).
 // (The same with and without a checkpoint, so that keeping one changes no sum.)
-// gated: a tile has half as many outputs per row, each with two sums.
-Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
+// gated: a tile has half as many outputs per row, each with two sums.  narrow: half tiles may be
+// taken (not with kept groups of 128, which they cut, so that such a call may add in another order).
+Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false, bool narrow = false) {
   Plan p;
   p.nr = int((rows + kRows - 1) / kRows);
   p.nc = int(gated ? (cols + kBN / 2 - 1) / (kBN / 2) : (cols + kBN - 1) / kBN);
@@ -1773,6 +1779,7 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
   p.a_rows = kHalf, p.tail = p.tail_splits = 0;
   p.cols4 = (cols + 3) / 4 * (gated ? 8 : 4);
   p.bytes = 0;
+  p.narrow = false;
   if (p.ksteps == 0) return p;
   const int64_t small = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
   // (gated: a tile of one CTA loads 48 KiB per step where a CTA of a pair loads 32, so pairs serve
@@ -1791,6 +1798,15 @@ Plan make_plan(int64_t rows, int64_t cols, int64_t depth, bool gated = false) {
     // 1032, five steps: 5.5 us in one slice, 7.3 in five; nine steps 6.9 and 7.8; sixteen
     // steps, 300 x 1000 x 1000, 10.9 and 8.0); few rows are joined quickly
     if (rows > 64 && p.ksteps <= 10) sp = 1;
+    // (gated: slices are joined by two sums per output; pairs on half tiles need none: 512 x 768 x 2048
+    // 10.9 us against 13.5 in five slices, 1024 x 768 x 2048 11.7 against 13.3 in two, 300 x 2000 x 1000
+    // 10.2 against 12.8; longer sums are faster in slices, 256 x 768 x 8192 19.5 us against 31.5)
+    const int64_t half = (rows + kRows - 1) / kRows * ((cols + kNarrow / 2 - 1) / (kNarrow / 2));
+    if (narrow && gated && sp > 1 && rows > kTile && half <= kPairs && p.ksteps <= 32) {
+      p.small = false, p.narrow = true;
+      p.nr = int((rows + kRows - 1) / kRows), p.nc = int(half / p.nr);
+      return p;
+    }
     p.splits = sp;
     return p;
   }
@@ -1834,13 +1850,13 @@ bool encode_outs(const Epi& e, OutMaps<P_GATED_DGRAD>& m) {
   return true;
 }
 
-template <int PASS, int ACT, bool SPLIT>
+template <int PASS, int ACT, bool SPLIT, int BN = kBN>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& a, Epi e,
                         cudaStream_t st) {
-  using C = Cfg<kBN, is_staged(PASS, SPLIT)>;
+  using C = Cfg<BN, is_staged(PASS, SPLIT)>;
   OutMaps<PASS> outs = {};
   if constexpr (is_staged(PASS, SPLIT)) e.staged = a.splits == 1 && encode_outs(e, outs);
-  auto kernel = pair_kernel<PASS, ACT, kBN, SPLIT>;
+  auto kernel = pair_kernel<PASS, ACT, BN, SPLIT>;
   static DeviceOnce once;
   const cudaError_t attr = once_per_device(once, [&] {
     const cudaError_t e =
@@ -1905,7 +1921,7 @@ cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
 template <int PASS>
 aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi& e, void* workspace,
                     size_t workspace_bytes, int32_t* err, cudaStream_t st) {
-  const Plan p = make_plan(e.rows, e.cols, depth, PASS == P_GATED);
+  const Plan p = make_plan(e.rows, e.cols, depth, PASS == P_GATED, !e.c.codes || e.c.lg < 7);
   if (p.bytes > 0) {
     if (!workspace || workspace_bytes < p.bytes) return AQFQ_ERR_WORKSPACE;
     if (!al(workspace, 16)) return AQFQ_ERR_ALIGN;
@@ -1916,7 +1932,7 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     CUtensorMap ta, tb;
     constexpr bool A_MN = PASS == P_WGRAD, B_MN = !k_major(PASS);
     if (!encode(&ta, A, kBK, A_MN ? kBK : unsigned(p.a_rows)) ||
-        !encode(&tb, B, kBK, B_MN ? kBK : kHalf))
+        !encode(&tb, B, kBK, B_MN ? kBK : p.narrow ? kNarrow / 2 : kHalf))
       return AQFQ_ERR_CUDA;
     const int up = PASS == P_GATED ? int(e.cols) : 0;
     PairArgs a = {p.nr, p.nc, 0, p.nr * p.nc, p.splits, p.a_rows, up, p.ksteps, part, p.cols4, err};
@@ -1924,6 +1940,9 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     a.count -= p.tail;
     if (p.small) {
       r = launch_tile<PASS>(ta, tb, a, e, st);
+    } else if (p.narrow) {
+      if constexpr (PASS == P_GATED) r = launch_pair<PASS, -1, false, kNarrow>(ta, tb, a, e, st);
+      else r = cudaErrorInvalidValue;  // (never planned)
     } else if (p.splits > 1) {  // finish_kernel has the epilogue
       r = launch_pair<PASS, AQFQ_ACT_NONE, false>(ta, tb, a, e, st);
     } else {
@@ -1991,10 +2010,10 @@ extern "C" aqfq_status aqfq_selftest_linear_plan(int pass, int64_t M, int64_t N,
     case AQFQ_LINEAR_FWD: p = make_plan(M, N, K); break;
     case AQFQ_LINEAR_DGRAD: p = make_plan(M, K, N); break;
     case AQFQ_LINEAR_WGRAD: p = make_plan(N, K, M); break;
-    case AQFQ_LINEAR_GATED: p = make_plan(M, N, K, true); break;
+    case AQFQ_LINEAR_GATED: p = make_plan(M, N, K, true, true); break;
     default: return AQFQ_ERR_UNSUPPORTED;
   }
-  plan[0] = p.ksteps == 0 ? 0 : p.small ? 1 : 2;
+  plan[0] = p.ksteps == 0 ? 0 : p.small ? 1 : p.narrow ? 3 : 2;
   plan[1] = p.splits, plan[2] = p.tail, plan[3] = p.tail_splits;
   return AQFQ_OK;
 }

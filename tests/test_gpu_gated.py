@@ -131,10 +131,13 @@ def test_forward_on_pairs(act, form):
 
 
 @pytest.mark.parametrize("size,kernel", [((1000, 1544, 264), "pair"), ((500, 1000, 136), "tile"),
-                                         ((129, 9600, 72), "pair"), ((128, 9728, 136), "tile")])
-def test_both_kernels_near_the_border(size, kernel):
-    plan = aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_GATED, *size)
-    assert plan["kernel"] == kernel and plan["splits"] <= 2
+                                         ((129, 9600, 72), "pair"), ((128, 9728, 136), "tile"),
+                                         ((129, 65, 2048), "narrow pair"), ((512, 768, 2048), "narrow pair"),
+                                         ((700, 1500, 712), "narrow pair"), ((1023, 1149, 1000), "narrow pair"),
+                                         ((128, 768, 2048), "tile"), ((512, 768, 2056), "tile")])
+def test_each_kernel_near_the_borders(size, kernel):
+    """(Half tiles: 64 outputs, of which a group of 128 takes two: kept so, the small tiles serve them.)"""
+    assert aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_GATED, *size)["kernel"] == kernel
     for i, form in enumerate([None] + FORMS):
         check_fwd(*size, NAMES[i], form, seed=i)
 
