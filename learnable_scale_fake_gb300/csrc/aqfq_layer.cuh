@@ -485,9 +485,10 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, bool vec, int n, ui
 // ---------------------------------------------------------------------------
 // A lane's share of a row: NV vectors of V consecutive elements, kept as they are
 // in memory until all loads are under way.  V = 8 where rows allow 16-byte
-// accesses (16 BF16 where they allow 32-byte ones); V = 1 (neighbouring lanes on
-// neighbouring columns) where they do not.  In arithmetic the E = NV V elements are E / 2 pairs: neighbours within a vector
-// (V = 8, 16), or the same lane's elements of vectors 2k and 2k + 1 (V = 1).
+// accesses (16 BF16 where they allow 32-byte ones); V = 2 (the norms between blocks)
+// or 1 (neighbouring lanes on neighbouring columns) where they do not.  In arithmetic
+// the E = NV V elements are E / 2 pairs: neighbours within a vector (V > 1), or the
+// same lane's elements of vectors 2k and 2k + 1 (V = 1).
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NV>
 struct Row {
@@ -497,6 +498,13 @@ struct Row {
     if constexpr (V == 1) {
       if constexpr (sizeof(T) == 2) w[j][0] = __ldg(reinterpret_cast<const uint16_t*>(p));
       else w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (V == 2) {
+      if constexpr (sizeof(T) == 2) {
+        w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        w[j][0] = u.x, w[j][1] = u.y;
+      }
     } else if constexpr (V == 16) {
       static_assert(sizeof(T) == 2, "32 bytes");
       ld_stream(p, w[j]);
@@ -517,6 +525,8 @@ struct Row {
                             : mk2(__uint_as_float(a), __uint_as_float(b));
     } else if constexpr (sizeof(T) == 2) {
       return bf2(w[i / W][i % W]);
+    } else if constexpr (V == 2) {
+      return mk2(__uint_as_float(w[i][0]), __uint_as_float(w[i][1]));
     } else {
       return mk2(__uint_as_float(w[i / 4][2 * (i % 4)]), __uint_as_float(w[i / 4][2 * (i % 4) + 1]));
     }
@@ -527,6 +537,9 @@ template <typename T, int V>
 __device__ __forceinline__ void put(T* p, const f2* v, int j) {
   if constexpr (V == 1) {
     from_f(j & 1 ? hi2(v[j / 2]) : lo2(v[j / 2]), *p);
+  } else if constexpr (V == 2) {
+    if constexpr (sizeof(T) == 2) st_32(p, pack2(v[j]));
+    else st_64(p, uint32_t(v[j]), uint32_t(v[j] >> 32));
   } else if constexpr (V == 16) {
     const f2* q = v + 8 * j;
     const uint32_t w[8] = {pack2(q[0]), pack2(q[1]), pack2(q[2]), pack2(q[3]),

@@ -75,6 +75,7 @@ __device__ __forceinline__ void params(const void* p, int pdtype, const int64_t 
 template <int V, int NV>
 __device__ __forceinline__ f2 masked(f2 v, int i, const bool (&in)[NV]) {
   if constexpr (V == 8) return in[i / 4] ? v : 0ull;
+  else if constexpr (V == 2) return in[i] ? v : 0ull;
   else return mk2(in[2 * i] ? lo2(v) : 0.0f, in[2 * i + 1] ? hi2(v) : 0.0f);
 }
 

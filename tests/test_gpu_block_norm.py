@@ -17,7 +17,9 @@ from learnable_scale_fake_gb300 import aqfq
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(1, 1), (1, 2048), (3, 7), (5, 8), (64, 100), (2, 255), (300, 256), (33, 1003), (7, 2056),
-          (1000, 768), (701, 512), (5, 5000), (3, 8192), (2, 20000), (160, 9001)]
+          (1000, 768), (701, 512), (5, 5000), (3, 8192), (2, 20000), (160, 9001),
+          # rows that allow accesses of two elements only
+          (300, 6), (333, 250), (77, 510), (40, 1018), (3, 2002), (160, 4090), (155, 8190)]
 EPS = 1e-6
 
 
@@ -70,7 +72,7 @@ def check(got, ref, dtype, what):
     close(got, want, tol, what)
 
 
-LAYOUTS = ((0, 0), (8, 8), (3, 1))
+LAYOUTS = ((0, 0), (8, 8), (3, 1), (2, 2))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -162,7 +164,7 @@ def test_backward(dtype, pdtype, post):
         if i % 7 == 5:
             dy = gpre = None
         base = randn((3, C), 77 + i, 3.0, torch.float32)
-        pad, off = LAYOUTS[i % 3]
+        pad, off = LAYOUTS[i % 4]
         for acc in (False, True):
             fr = {n: None if t is None else Framed(R, C, dtype, pad, off, t)
                   for n, t in (("dy", dy), ("dh", dh), ("h", h), ("f", f))}
@@ -201,7 +203,8 @@ RINGS_BACK = [(1217, 4096, torch.bfloat16), (1220, 2056, torch.bfloat16), (2433,
 MANY_BACK = [(4865, 1024, torch.bfloat16), (4871, 520, torch.bfloat16), (9731, 512, torch.bfloat16),
              (9729, 264, torch.bfloat16), (4867, 512, torch.float32), (2440, 1024, torch.float32),
              (2000, 1003, torch.bfloat16), (3001, 333, torch.float32), (700, 4001, torch.bfloat16), (333, 5001, torch.bfloat16),
-             (157, 8191, torch.float32)]
+             (157, 8191, torch.float32), (2000, 1002, torch.bfloat16), (3001, 334, torch.float32),
+             (700, 4002, torch.bfloat16), (333, 5002, torch.bfloat16)]
 
 
 @pytest.mark.parametrize("R,C,dtype", RINGS)
@@ -398,3 +401,33 @@ def test_captured_and_on_another_stream(R, C):
     torch.cuda.synchronize()
     for o in out[1:]:
         assert all(torch.equal(p, q) for p, q in zip(out[0][:9], o[:9]))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^22 elements apart, 1300 of them: the last start beyond 2^33 bytes and 2^32
+    elements.  The results of packed rows, which the other tests hold to the formulas."""
+    R, ld, dt = 1300, 1 << 22, torch.bfloat16
+    whole = torch.empty(R * ld, dtype=dt, device=DEV)
+    for C in (2048, 512, 250, 251, 9001):
+        names = ("x", "f", "dy", "dh", "h", "y", "dx", "df")
+        far = {n: whole.as_strided((R, C), (ld, 1), 16384 * k) for k, n in enumerate(names)}
+        near = {n: randn((R, C), 900 + k, 1.0, dt).to(DEV) for k, n in enumerate(names)}
+        for n in names:
+            far[n].copy_(near[n])
+        g = randn((C,), 950, 1.0, torch.float32).to(DEV)
+        out = []
+        for t in (far, near):
+            rp, rq = (torch.empty(R, device=DEV) for _ in range(2))
+            sums = torch.empty(3, C, device=DEV)
+            ws = torch.empty(aqfq.aqfq_block_norm_bwd_workspace_bytes(R, C), dtype=torch.uint8, device=DEV)
+            aqfq.aqfq_block_norm_fwd(t["x"], t["f"], EPS, h=t["h"], y=t["y"], post=True, gamma_post=g, gate=g,
+                                     alpha=0.5, gamma_pre=g, rstd_post=rp, rstd_pre=rq)
+            aqfq.aqfq_block_norm_bwd(t["dy"], t["dh"], t["h"], t["f"], rstd_post=rp, rstd_pre=rq, gamma_post=g,
+                                     gate=g, alpha=0.5, gamma_pre=g, dx=t["dx"], df=t["df"], dgamma_post=sums[0],
+                                     dgate=sums[1], dgamma_pre=sums[2], workspace=ws)
+            out.append((rp, rq, sums))
+        torch.cuda.synchronize()
+        for a, b in zip(*out):
+            assert torch.equal(a, b), C
+        for n in ("h", "y", "dx", "df"):
+            assert torch.equal(far[n], near[n]), (n, C)
