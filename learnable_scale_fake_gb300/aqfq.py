@@ -746,7 +746,7 @@ def aqfq_gated_fwd(x, w, y, act=ACT_SILU, gate=None, up=None, workspace=None, er
     px, ldx = _mat(x, "x", _BF)
     dev = x.get_device()
     M, K = x.shape
-    N = y.shape[1]
+    N = w.shape[0] // 2
     pw, ldw = _mat(w, "w", _BF, (2 * N, K), dev)
     py, ldy = _mat(y, "y", _BF, (M, N), dev)
     ws, wsb = _ws(workspace, dev)
@@ -793,8 +793,8 @@ def aqfq_ckpt8_gated_bwd(gate, up, act, dy, dp=None, y=None, stream=None):
 
 
 def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:
-    """How the product is cut: kernel ("empty", "tile", "pair" or "narrow pair"), slices of the inner axis, tiles
-    of the last round that a second launch splits, and into how many slices."""
+    """How the product is cut: kernel ("empty", "tile", "pair" or "narrow pair"), slices of the
+    inner axis, tiles of the last round that a second launch splits, and into how many slices."""
     plan = (ctypes.c_int32 * 4)()
     _check("aqfq_selftest_linear_plan", lib().aqfq_selftest_linear_plan(int(kind), M, N, K, plan))
     return {"kernel": ("empty", "tile", "pair", "narrow pair")[plan[0]], "splits": plan[1], "tail": plan[2],

@@ -952,6 +952,7 @@ cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cud
     if (c <= 1024) return run_fwd<T, 2, 4, 4, 1>(x, f, h, y, a, st);
     if (c <= 2048) return run_fwd<T, 2, 4, 8, 1>(x, f, h, y, a, st);
     if (c <= 4096) return run_fwd<T, 2, 4, 16, 1>(x, f, h, y, a, st);
+    if (c <= 6144) return run_fwd<T, 2, 4, 24, 1>(x, f, h, y, a, st);
     if (c <= 8192) return run_fwd<T, 2, 4, 32, 1>(x, f, h, y, a, st);
   } else {
     if (c <= 256) return run_fwd<T, 1, 8, 1, 1>(x, f, h, y, a, st);
@@ -959,6 +960,7 @@ cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cud
     if (c <= 1024) return run_fwd<T, 1, 8, 4, 1>(x, f, h, y, a, st);
     if (c <= 2048) return run_fwd<T, 1, 8, 8, 1>(x, f, h, y, a, st);
     if (c <= 4096) return run_fwd<T, 1, 8, 16, 1>(x, f, h, y, a, st);
+    if (c <= 6144) return run_fwd<T, 1, 8, 24, 1>(x, f, h, y, a, st);
     if (c <= 8192) return run_fwd<T, 1, 8, 32, 1>(x, f, h, y, a, st);
   }
   const unsigned grid = unsigned(a.rows > 0x7FFFFFFF ? 0x7FFFFFFF : a.rows);
@@ -1019,14 +1021,16 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
     if (c <= 512) return run_bwd<T, 2, 4, 2, true>(p, a, parts, st);
     if (c <= 1024) return run_bwd<T, 2, 4, 4, true>(p, a, parts, st);
     if (c <= 2048) return run_bwd<T, 2, 4, 8, true>(p, a, parts, st);
-    if (c <= 4096) return run_bwd<T, 2, 4, 16, true>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 2, 4, 16, false>(p, a, parts, st);
+    if (c <= 6144) return run_bwd<T, 2, 6, 16, false>(p, a, parts, st);
     if (c <= 8192) return run_bwd<T, 2, 8, 16, false>(p, a, parts, st);
   } else {
     if (c <= 128) return run_bwd<T, 1, 4, 1, true>(p, a, parts, st);
     if (c <= 512) return run_bwd<T, 1, 4, 4, true>(p, a, parts, st);
     if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(p, a, parts, st);
     if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(p, a, parts, st);
-    if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 1, 8, 16, false>(p, a, parts, st);
+    if (c <= 6144) return run_bwd<T, 1, 12, 16, false>(p, a, parts, st);
     if (c <= 8192) return run_bwd<T, 1, 16, 16, false>(p, a, parts, st);
   }
   const int64_t blocks = a.rows < kSms ? a.rows : kSms;

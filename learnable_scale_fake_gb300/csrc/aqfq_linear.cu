@@ -980,7 +980,8 @@ constexpr int kRows = 256, kHalf = 128, kBK = 64;
 constexpr int kThreadsP = 64 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kHalf * kBK * 2;  // 16 KiB per CTA and stage
 
-// STAGED: five stages (with four the plain input gradient took 85 us instead of 75), and the epilogue warps' outputs on their way to memory
+// STAGED: five stages (with four the plain input gradient took 85 us instead of 75), and the
+// epilogue warps' outputs on their way to memory
 template <int BN, bool STAGED>
 struct Cfg {
   static constexpr int STAGES = STAGED && BN == 256 ? 5 : 6;
