@@ -927,6 +927,10 @@ int bwd_ring(int64_t rows, int64_t c, int esize, bool dh, RingArgs& q) {
 // against 99.6 and 137 against 208; 4096 x 334 5.8 against 8.0 and 11.8 against 14.8;
 // 65536 x 6 15.8 against 35.8 and 22.5 against 28.1.  Binary32 20000 x 250 16.4 against 16.8
 // and 26.3 against 45.3, 4096 x 4094 47.4 against 51.9 and 90.2 against 95.4.
+// Widths beyond 4096 in two steps: lanes that own no column cost as much as others.  4096 x 5001
+// single elements forward 75 us, 91 with lanes for 8192 columns, backward 138 and 192; 4096 x
+// 5002 62 and 75, 91 and 117.  The next row's loads stay ahead of this row up to 4096 columns
+// (4096 x 4094 53.7 us, without 82.4); beyond, they spill (4096 x 5001 168 us).
 template <typename T>
 cudaError_t launch_fwd(const T* x, const T* f, T* h, T* y, const FwdArgs& a, cudaStream_t st) {
   const int64_t c = a.cols;
@@ -1021,7 +1025,7 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
     if (c <= 512) return run_bwd<T, 2, 4, 2, true>(p, a, parts, st);
     if (c <= 1024) return run_bwd<T, 2, 4, 4, true>(p, a, parts, st);
     if (c <= 2048) return run_bwd<T, 2, 4, 8, true>(p, a, parts, st);
-    if (c <= 4096) return run_bwd<T, 2, 4, 16, false>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 2, 4, 16, true>(p, a, parts, st);
     if (c <= 6144) return run_bwd<T, 2, 6, 16, false>(p, a, parts, st);
     if (c <= 8192) return run_bwd<T, 2, 8, 16, false>(p, a, parts, st);
   } else {
@@ -1029,7 +1033,7 @@ cudaError_t launch_bwd(const BwdIn<T>& p, const BwdArgs& a, int* parts, cudaStre
     if (c <= 512) return run_bwd<T, 1, 4, 4, true>(p, a, parts, st);
     if (c <= 1024) return run_bwd<T, 1, 4, 8, true>(p, a, parts, st);
     if (c <= 2048) return run_bwd<T, 1, 4, 16, true>(p, a, parts, st);
-    if (c <= 4096) return run_bwd<T, 1, 8, 16, false>(p, a, parts, st);
+    if (c <= 4096) return run_bwd<T, 1, 8, 16, true>(p, a, parts, st);
     if (c <= 6144) return run_bwd<T, 1, 12, 16, false>(p, a, parts, st);
     if (c <= 8192) return run_bwd<T, 1, 16, 16, false>(p, a, parts, st);
   }
