@@ -13,6 +13,8 @@
 // fifteen packed ones per pair keep the issue slots 60 % busy), with GELU, the recomputed
 // activation and the bias gradient 86 us (5.4).  FP32 from INT8: pack 55 us (6.2), unpack 70
 // (4.8), with GELU 71, the gradient with GELU, activation and bias gradient 143 (6.1).
+// The gradient through a gate moves 2 + 2 + 4 bytes, 2 more with the product: with SiLU 110-114 us
+// (5.9-6.1 TB/s).
 #include <type_traits>
 
 #include "aqfq_internal.h"

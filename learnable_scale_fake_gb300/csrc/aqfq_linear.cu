@@ -962,14 +962,15 @@ __device__ __forceinline__ void gated_grad_staged(const Epi& e, const OutMaps<P_
 //               (with two per quarter the forward with GELU and checkpoint took 192 us at
 //               8192 x 4096 x 4096, with four 167 us).  Five of the eighteen warps share a
 //               quarter of the SM, which leaves 96 registers a thread, and spilled ones go to
-//               L2 beside 200 KB of shared memory: 8 to 28 bytes in the forward kernels and
-//               in the input gradient with GELU or tanh GELU, 248 and 116 in the forward's
-//               and the input gradient's split tail, none in the other kernels but 16 in the
-//               weight gradient's split tail.
+//               L2 beside 200 KB of shared memory: 12 to 24 bytes in the forward kernels and
+//               in the input gradient with an activation other than ReLU, 4 in the gated
+//               gradient with GELU, none in the other kernels but the split tails: 244
+//               (forward), 112 (input gradient), 320 and 116 (gated).
 // At 8192 x 4096 x 4096 (plain library products beside: 137-152, 147-156 and 155-168 us):
 // forward with GELU 146-153 us, with a checkpoint too 160-167 us, input gradient 142-167 us,
 // weight gradient 152-175 us; two runs differ by so much with the clock under the power
-// limit.  The MMAs run 81 to 89 % of the time; the rest is the first loads, the last tile's
+// limit.  Gated: forward 4096 x 8192 x 2048 with SiLU 142-144 us, with gate and up kept 155-157;
+// gradient 4096 x 2048 x 8192 with act(g) u 102 us, 93 without (plain input gradient 75).  The MMAs run 81 to 89 % of the time; the rest is the first loads, the last tile's
 // epilogue and tiles that do not divide evenly among 76 pairs.
 // Every wait is bounded; on a timeout the pair drains, frees its tensor memory,
 // raises the caller's flag and returns.
