@@ -746,7 +746,7 @@ def aqfq_gated_fwd(x, w, y, act=ACT_SILU, gate=None, up=None, workspace=None, er
     px, ldx = _mat(x, "x", _BF)
     dev = x.get_device()
     M, K = x.shape
-    N = w.shape[0] // 2
+    N = y.shape[-1]
     pw, ldw = _mat(w, "w", _BF, (2 * N, K), dev)
     py, ldy = _mat(y, "y", _BF, (M, N), dev)
     ws, wsb = _ws(workspace, dev)
