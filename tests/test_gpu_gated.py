@@ -328,3 +328,27 @@ def test_two_streams_and_a_replayed_graph():
         assert all(torch.equal(p, q) for p, q in zip(b[0][1], outs))
         for c, d in zip(b[0][0], cks):
             assert torch.equal(c[1], d[1]) and torch.equal(c[2], d[2])
+
+
+@pytest.mark.parametrize("N,K", [(264, 512), (2000, 512), (8192, 256)])
+def test_offsets_beyond_32_bits(N, K):
+    """Rows 2^24 elements apart, 300 of them: the last start beyond 2^33 bytes and 2^32 elements.
+    The results of packed rows, which the other tests hold to the formulas."""
+    M, ld = 300, 1 << 24
+    whole = torch.empty(M * ld, dtype=torch.bfloat16, device=DEV)
+    widths = {"x": K, "y": N, "dz": 136, "dp": 2 * N, "hidden": N, "dy": N, "dp2": 2 * N, "hidden2": N}
+    near = {n: randn((M, c), 60 + i, 1.0).to(DEV) for i, (n, c) in enumerate(widths.items())}
+    far = {n: whole.as_strided((M, c), (ld, 1), 65536 * i) for i, (n, c) in enumerate(widths.items())}
+    for n in widths:
+        far[n].copy_(near[n])
+    w, w2 = randn((2 * N, K), 70, K ** -0.5).to(DEV), randn((136, N), 71, 0.1).to(DEV)
+    for t in (far, near):
+        (g, *_), (u, *_) = new_ckpt(M, N, "int8", 64), new_ckpt(M, N, "int8", 64)
+        aqfq.aqfq_gated_fwd(t["x"], w, t["y"], gate=g, up=u,
+                            workspace=ws(aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_FWD, M, N, K)))
+        aqfq.aqfq_gated_dgrad(t["dz"], w2, t["dp"], g, u, y=t["hidden"],
+                              workspace=ws(aqfq.aqfq_gated_workspace_bytes(aqfq.LINEAR_DGRAD, M, 136, N)))
+        aqfq.aqfq_ckpt8_gated_bwd(g, u, aqfq.ACT_SILU, t["dy"], dp=t["dp2"], y=t["hidden2"])
+        torch.cuda.synchronize()
+    for n in ("y", "dp", "hidden", "dp2", "hidden2"):
+        assert torch.equal(far[n], near[n]), n
