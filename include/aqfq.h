@@ -626,9 +626,10 @@ aqfq_status aqfq_selftest_wait_timeout(int32_t* flag, uint32_t polls, void* stre
 
 /* Diagnostics (host only, no counterpart in the pages): which kernel a size takes, so
  * that a test of a kernel can tell that its sizes reach it.
- * aqfq_selftest_linear_plan (AQFQ_LINEAR_GATED: aqfq_gated_fwd without kept groups of 128; the
+ * aqfq_selftest_linear_plan (AQFQ_LINEAR_GATED: aqfq_gated_fwd without kept values; the
  * gated gradient is cut as AQFQ_LINEAR_DGRAD): plan[0] = 0 (empty sum), 1 (128 x 128 tiles,
- * one CTA each), 2 (256 x 256 tiles on pairs of CTAs) or 3 (256 x 128 tiles on pairs);
+ * one CTA each), 2 (256 x 256 tiles on pairs of CTAs), 3 (256 x 128 tiles on pairs) or 4 (few
+ * rows, the weight streamed through registers);
  * plan[1] = slices of the inner axis; plan[2] = tiles of the last round that a second launch
  * splits; plan[3] = into how many slices.
  * aqfq_selftest_layernorm_ring, aqfq_selftest_block_norm_ring: warps per row of the ring

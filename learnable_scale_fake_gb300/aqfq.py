@@ -793,11 +793,11 @@ def aqfq_ckpt8_gated_bwd(gate, up, act, dy, dp=None, y=None, stream=None):
 
 
 def aqfq_selftest_linear_plan(kind, M, N, K) -> dict:
-    """How the product is cut: kernel ("empty", "tile", "pair" or "narrow pair"), slices of the
+    """How the product is cut: kernel ("empty", "tile", "pair", "narrow pair" or "few rows"), slices of the
     inner axis, tiles of the last round that a second launch splits, and into how many slices."""
     plan = (ctypes.c_int32 * 4)()
     _check("aqfq_selftest_linear_plan", lib().aqfq_selftest_linear_plan(int(kind), M, N, K, plan))
-    return {"kernel": ("empty", "tile", "pair", "narrow pair")[plan[0]], "splits": plan[1], "tail": plan[2],
+    return {"kernel": ("empty", "tile", "pair", "narrow pair", "few rows")[plan[0]], "splits": plan[1], "tail": plan[2],
             "tail_splits": plan[3]}
 
 

@@ -21,6 +21,7 @@
 #include <cuda.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "aqfq_internal.h"
 #include "aqfq_layer.cuh"
@@ -1694,6 +1695,137 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
+// gated product of a few rows: the weight is streamed once, straight into the fragments of
+// register matrix products (16 weight rows x 16 of k by 8 rows of x).  A warp owns 8 outputs of
+// every row of x: their gate's rows are the fragment's first eight, up's the other eight, so that
+// g and u of an output meet in one lane.  The order of k within a fragment is free as long as
+// both operands share it: a lane takes 16 consecutive bytes of a row for two products.
+// `slices` warps of a block share the outputs, each a run of the inner axis; their sums meet in
+// the slices' order.
+// Bound by memory: the weight once, for one row as for eight.  Loads of tiles into shared memory,
+// their products and the joining of slices over a cluster are as many round trips before the
+// end: 1 x 768 x 2048 3.4 us (in tiles 7.1), 1 x 1536 x 4096 7.2 (11.0), 1 x 768 x 8192 7.2
+// (12.7), 1 x 8192 x 2048 12.2 (15.1; 5.5 TB/s), 1 x 14336 x 4096 41 (42; 5.7 TB/s).  Four steps
+// under way instead of eight: 14.8 at 768 x 8192, 45.7 at 14336 x 4096.  Dot products with packed
+// multiply-adds are as fast for a row or two (2.8, 6.9, 6.9, 16.2, 38.6), but take 20 us for eight rows
+// at 1536 x 4096.
+// ---------------------------------------------------------------------------
+constexpr int kWarpsF = 16;
+constexpr int kStepF = 32;  // of k: four lanes with 8 elements each
+
+// sums += 16 x 16 weights (gate's 8 rows and up's) by 8 rows of x, from 4 bytes of k each
+__device__ __forceinline__ void mma_few(float (&c)[4], uint32_t g0, uint32_t u0, uint32_t g1, uint32_t u1,
+                                        uint32_t x0, uint32_t x1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(g0), "r"(u0), "r"(g1), "r"(u1), "r"(x0), "r"(x1));
+}
+
+// RT: eights of rows of x
+template <int RT>
+__global__ void __launch_bounds__(32 * kWarpsF, 1)
+    few_rows_kernel(const bf16* x, int64_t ldx, const bf16* w, int64_t ldw, int64_t depth, int slices,
+                    const Epi e) {
+  constexpr int U = RT == 1 ? 8 : 4;  // most steps under way
+  __shared__ float4 part[RT][kWarpsF][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 2, kq = lane & 3;
+  const int slice = warp % slices;
+  const int64_t col = (int64_t(blockIdx.x) * (kWarpsF / slices) + warp / slices) * 8 + grp;
+  // (rows and columns that are not there: of others, not stored)
+  const bf16* wg = w + (col < e.cols ? col : e.cols - 1) * ldw;
+  const bf16* wu = wg + e.cols * ldw;
+  const bf16* xr[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) xr[r] = x + (grp + 8 * r < e.rows ? grp + 8 * r : 0) * ldx;
+  float c[RT][4] = {};
+  auto products = [&](const uint32_t (&g)[4], const uint32_t (&u)[4], const uint32_t (&b)[RT][4]) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      mma_few(c[r], g[0], u[0], g[1], u[1], b[r][0], b[r][1]);
+      mma_few(c[r], g[2], u[2], g[3], u[3], b[r][2], b[r][3]);
+    }
+  };
+  // N steps from step s on; MASK: vectors from `vectors` on and steps from `end` on are zeros
+  const int64_t vectors = depth / 8, steps = (depth + kStepF - 1) / kStepF;
+  auto block = [&](int64_t s, int64_t end, auto count, auto masked) {
+    constexpr int N = decltype(count)::value;
+    constexpr bool MASK = decltype(masked)::value;
+    uint32_t g[N][4], u[N][4], b[N][RT][4];
+    bool in[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t v = (s + j) * 4 + kq;
+      in[j] = !MASK || (s + j < end && v < vectors);
+      const int64_t at = (in[j] ? v : 0) * 8;  // (there is a first one)
+      ld_stream_v4(wg + at, g[j][0], g[j][1], g[j][2], g[j][3]);
+      ld_stream_v4(wu + at, u[j][0], u[j][1], u[j][2], u[j][3]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(xr[r] + at));
+        b[j][r][0] = q.x, b[j][r][1] = q.y, b[j][r][2] = q.z, b[j][r][3] = q.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (MASK) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[j][i] = in[j] ? g[j][i] : 0u, u[j][i] = in[j] ? u[j][i] : 0u;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) b[j][r][i] = in[j] ? b[j][r][i] : 0u;
+        }
+      }
+      products(g[j], u[j], b[j]);
+    }
+  };
+  const int64_t s0 = steps * slice / slices, s1 = steps * (slice + 1) / slices;
+  const int64_t whole = s1 < vectors / 4 ? s1 : vectors / 4;  // steps of whole vectors only
+  int64_t s = s0;
+  using Most = std::integral_constant<int, U>;
+  using Few = std::integral_constant<int, 4>;
+  for (; s + U <= whole; s += U) block(s, s1, Most(), std::false_type());
+  for (; s + 4 <= whole; s += 4) block(s, s1, Few(), std::false_type());
+  for (; s < s1; s += 4) block(s, s1, Few(), std::true_type());
+  const int left = int(depth & 7);  // elements after the last whole vector
+  if (left && slice == slices - 1) {
+    uint32_t g[4] = {}, u[4] = {}, b[RT][4] = {};
+    if (kq == 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i) {
+        if (i < left) {
+          const int64_t at = vectors * 8 + i;
+          g[i / 2] |= uint32_t(wg[at].b) << (16 * (i & 1));
+          u[i / 2] |= uint32_t(wu[at].b) << (16 * (i & 1));
+#pragma unroll
+          for (int r = 0; r < RT; ++r) b[r][i / 2] |= uint32_t(xr[r][at].b) << (16 * (i & 1));
+        }
+      }
+    }
+    __syncwarp();
+    products(g, u, b);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) part[r][warp][lane] = make_float4(c[r][0], c[r][1], c[r][2], c[r][3]);
+  __syncthreads();
+  if (slice != 0 || col >= e.cols) return;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float4 t = part[r][warp][lane];
+    for (int k = 1; k < slices; ++k) {
+      const float4 o = part[r][warp + k][lane];
+      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+    }
+    float g[2] = {t.x, t.y};
+    act_apply(e.act, g);
+    const int64_t row = 8 * r + 2 * kq;
+    bf16* y = static_cast<bf16*>(e.out) + row * e.ldo + col;
+    if (row < e.rows) from_f(g[0] * t.z, y[0]);
+    if (row + 1 < e.rows) from_f(g[1] * t.w, y[e.ldo]);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1919,6 +2051,33 @@ cudaError_t launch_tile(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   return cudaLaunchKernelEx(&cfg, tile_kernel<PASS>, ta, tb, a, e);
 }
 
+// Up to 16 rows without kept values; rows from 17 on take tiles (16 x 768 x 2048 4.6 us against 7.5
+// in tiles, 16 x 8192 x 2048 13.3 against 16.0, 16 x 14336 x 4096 41.5 against 42.3).
+constexpr int kFewRows = 16;
+bool few_rows(int64_t rows, int64_t depth) { return rows <= kFewRows && depth >= 8; }
+// Warps that share 8 outputs: by the steps of the busiest SM, a block per SM at a time, each with
+// about four steps' worth of start and joining.
+int few_slices(int64_t cols, int64_t depth) {
+  const int64_t units = (cols + 7) / 8, steps = (depth + kStepF - 1) / kStepF;
+  int slices = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kWarpsF && s <= steps; s *= 2) {
+    const int64_t blocks = (units * s + kWarpsF - 1) / kWarpsF, rounds = (blocks + 2 * kPairs - 1) / (2 * kPairs);
+    const int64_t cost = rounds * ((steps + s - 1) / s + 4);
+    if (cost < best) best = cost, slices = s;
+  }
+  return slices;
+}
+cudaError_t launch_few(const Operand& x, const Operand& w, int64_t depth, const Epi& e, cudaStream_t st) {
+  const int slices = few_slices(e.cols, depth);
+  const int64_t units = (e.cols + 7) / 8;
+  const unsigned blocks = unsigned((units * slices + kWarpsF - 1) / kWarpsF);
+  const bf16 *px = static_cast<const bf16*>(x.p), *pw = static_cast<const bf16*>(w.p);
+  if (e.rows <= 8) few_rows_kernel<1><<<blocks, 32 * kWarpsF, 0, st>>>(px, x.ld, pw, w.ld, depth, slices, e);
+  else few_rows_kernel<2><<<blocks, 32 * kWarpsF, 0, st>>>(px, x.ld, pw, w.ld, depth, slices, e);
+  return cudaGetLastError();
+}
+
 // out[r, c] = epilogue(sum over k of A(r, k) B(c, k)); A, B as stored
 template <int PASS>
 aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi& e, void* workspace,
@@ -1928,6 +2087,8 @@ aqfq_status product(const Operand& A, const Operand& B, int64_t depth, const Epi
     if (!workspace || workspace_bytes < p.bytes) return AQFQ_ERR_WORKSPACE;
     if (!al(workspace, 16)) return AQFQ_ERR_ALIGN;
   }
+  if (PASS == P_GATED && few_rows(e.rows, depth) && !e.c.codes)
+    return launch_few(A, B, depth, e, st) == cudaSuccess ? AQFQ_OK : AQFQ_ERR_CUDA;
   float* part = static_cast<float*>(workspace);
   if (p.splits > 0) {
     if (!encode_fn()) return AQFQ_ERR_CUDA;
@@ -2017,6 +2178,8 @@ extern "C" aqfq_status aqfq_selftest_linear_plan(int pass, int64_t M, int64_t N,
   }
   plan[0] = p.ksteps == 0 ? 0 : p.small ? 1 : p.narrow ? 3 : 2;
   plan[1] = p.splits, plan[2] = p.tail, plan[3] = p.tail_splits;
+  if (pass == AQFQ_LINEAR_GATED && few_rows(M, K))
+    plan[0] = 4, plan[1] = few_slices(N, K), plan[2] = plan[3] = 0;
   return AQFQ_OK;
 }
 

@@ -352,3 +352,44 @@ def test_offsets_beyond_32_bits(N, K):
         torch.cuda.synchronize()
     for n in ("y", "dp", "hidden", "dp2", "hidden2"):
         assert torch.equal(far[n], near[n]), n
+
+
+# rows, outputs and inner axes that fill nothing evenly; one to sixteen slices
+FEW = [(1, 8, 8), (1, 1, 9), (1, 768, 2048), (2, 13, 15), (3, 2000, 31), (5, 7, 8200), (7, 8192, 264), (8, 136, 1000),
+       (8, 264, 520), (9, 520, 1003), (13, 20000, 64), (15, 1001, 129), (16, 1536, 768), (16, 33, 4104)]
+
+
+@pytest.mark.parametrize("size", FEW, ids=["x".join(map(str, s)) for s in FEW])
+def test_few_rows(size):
+    assert aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_GATED, *size)["kernel"] == "few rows"
+    for i, act in enumerate(NAMES):
+        check_fwd(*size, act, None, seed=i)
+
+
+def test_what_few_rows_are():
+    plan = lambda *s: aqfq.aqfq_selftest_linear_plan(aqfq.LINEAR_GATED, *s)
+    assert plan(17, 768, 2048)["kernel"] == "tile" and plan(16, 768, 7)["kernel"] == "tile"
+    assert {plan(1, n, k)["splits"] for n in (8, 768, 2048, 8192, 20000) for k in (32, 64, 768, 2048)} == {1, 2, 4, 8, 16}
+    check_fwd(17, 768, 2048, "silu", None)
+    check_fwd(16, 768, 7, "silu", None)
+
+
+def test_few_rows_stay_apart():
+    """A row or a column that is not finite leaves the others' bits alone; NaN behind the inner axis
+    and behind the last row is not read into them."""
+    M, N, K = 5, 100, 77
+    framed = operand(randn((M, K), 1), 1), operand(randn((2 * N, K), 2, K ** -0.5), 1)
+    for f in framed:
+        f.whole[f.mask] = float("nan")
+    x, w = (f.view for f in framed)
+    y, z = (torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    aqfq.aqfq_gated_fwd(x, w, y)
+    x[2] = float("inf")
+    w[7, 3] = float("nan")
+    w[N + 9, 76] = float("inf")
+    aqfq.aqfq_gated_fwd(x, w, z)
+    torch.cuda.synchronize()
+    rows, cols = [0, 1, 3, 4], [c for c in range(N) if c not in (7, 9)]
+    assert y.isfinite().all()
+    assert torch.equal(y[rows][:, cols], z[rows][:, cols])
+    assert not z[2].isfinite().any() and z[:, 7].isnan().all() and not z[:, 9].isfinite().any()
