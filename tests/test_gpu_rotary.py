@@ -21,7 +21,9 @@ LAYOUTS = {"half": aqfq.ROTARY_HALF, "interleaved": aqfq.ROTARY_INTERLEAVED}
 # T, heads of q, heads of k (0: none), D, rot
 SHAPES = [(1, 32, 8, 128, 128), (7, 3, 1, 64, 64), (33, 5, 0, 80, 42), (5, 2, 2, 81, 40), (300, 9, 3, 96, 48),
           (1, 1, 0, 2, 2), (4, 1, 1, 1, 0), (17, 40, 8, 16, 8), (3, 2, 1, 256, 256), (2, 3, 0, 7, 4),
-          (2000, 6, 2, 64, 32), (2, 1, 1, 4096, 4094), (3, 0, 2, 32, 32), (0, 4, 2, 32, 32)]
+          (2000, 6, 2, 64, 32), (2, 1, 1, 4096, 4094), (3, 0, 2, 32, 32), (0, 4, 2, 32, 32),
+          # two elements at a time by halves in BF16
+          (9, 5, 2, 128, 44), (300, 3, 1, 80, 36), (2, 17, 0, 12, 4), (5, 2, 2, 96, 92)]
 
 
 def rotated(x, pos, freqs, layout, mscale, transposed):
